@@ -425,6 +425,119 @@ orthros_status orthros_attn_bwd(const orthros_bf16 *q_raw, const orthros_bf16 *k
                                 int Hkv, int d, int window, float scale, void *workspace,
                                 size_t ws_bytes, int32_t *dev_err, void *stream);
 
+/*
+ * The 8-bit KV cache (the paper has no counterpart; a serving form of the layer's cache).
+ * A row, the d values of one KV head at one position, is held as d codes and one exponent e
+ * and stands for code * 2^e:
+ *   k8, v8        [B, L_max, Hkv, d] codes, one byte each, dense: e4m3 bits
+ *                 (ORTHROS_KV_E4M3) or int8 (ORTHROS_KV_INT8), 16-byte aligned
+ *   k_exp, v_exp  [B, Hkv, L_max] int8, dense, 16-byte aligned; L_max a multiple of 16
+ * A row x is written with the smallest whole e for which max|x| 2^-e is at most 448 (e4m3) or
+ * 127 (int8), clamped to [-126, 127] (0 for a row of zeros), and codes x 2^-e rounded to
+ * nearest even.  Scaling by a power of two is exact, so the codes do not depend on the
+ * implementation, and a value read back is exact in bf16 (except below bf16's smallest, and
+ * that a value whose code rounds up to 2^128 reads back as infinite).  A value that is not finite sets ORTHROS_DEVERR_RANGE where it is written: it does not count
+ * for e, its e4m3 code is NaN, its int8 code the end of the range on its side (0 for a NaN).
+ */
+#define ORTHROS_KV_E4M3 0
+#define ORTHROS_KV_INT8 1
+
+/*
+ * Writes prompt rows into an 8-bit cache: rows 0 .. rows[b]-1 of k[b], v[b] go to cache rows
+ * start[b] .. start[b]+rows[b]-1; no other cache row is written.
+ *   k, v   [B, T, Hkv, d] bf16 (batch stride kv_bstride, 0 = T*Hkv*d)
+ *   start  [B] int32 device, or NULL (0 for every sequence)
+ *   rows   [B] int32 device, each in [0, T], or NULL (T for every sequence)
+ * A sequence with start < 0 or rows outside [0, T] is not written and sets
+ * ORTHROS_DEVERR_POSITION; one whose rows do not fit below L_max is not written and sets
+ * ORTHROS_DEVERR_CACHE_FULL.  cache_len is the caller's to set.
+ */
+orthros_status orthros_kv_quantize(const orthros_bf16 *k, const orthros_bf16 *v, const int32_t *start,
+                                   const int32_t *rows, uint8_t *k8, uint8_t *v8, int8_t *k_exp,
+                                   int8_t *v_exp, int B, int T, int Hkv, int d, int L_max, int code,
+                                   int64_t kv_bstride, int32_t *dev_err, void *stream);
+
+/*
+ * Reads cache rows start[b] .. start[b]+rows[b]-1 back as bf16 rows 0 .. rows[b]-1 of k[b], v[b]
+ * (e.g. the window in front of the next prompt chunk, or a cache for orthros_xattn_fwd); rows
+ * behind them are left as they are.  Arguments and errors as orthros_kv_quantize.
+ */
+orthros_status orthros_kv_dequantize(const uint8_t *k8, const uint8_t *v8, const int8_t *k_exp,
+                                     const int8_t *v_exp, const int32_t *start, const int32_t *rows,
+                                     orthros_bf16 *k, orthros_bf16 *v, int B, int T, int Hkv, int d,
+                                     int L_max, int code, int64_t kv_bstride, int32_t *dev_err,
+                                     void *stream);
+
+/*
+ * Bytes of device workspace orthros_decode_step_q8 needs, zero-filled once before its first use
+ * and left ready for the next step (not for two steps in flight).  Returns 0 for invalid sizes.
+ */
+size_t orthros_decode_q8_workspace_size(int B, int L_max, int Hq, int Hkv, int d);
+
+/*
+ * orthros_decode_step over an 8-bit cache: k_new, v_new are written as codes to cache row
+ * p = cache_len[b], both streams attend over the rows' values (the new one's too, as a later
+ * step will read it), and cache_len[b] becomes p + 1.  Accumulation and softmax are fp32.  The
+ * contents of rows at or beyond the old cache_len do not matter.  Other arguments and errors as
+ * orthros_decode_step.
+ */
+orthros_status orthros_decode_step_q8(const orthros_bf16 *q_new, const orthros_bf16 *qc_new,
+                                      const orthros_bf16 *k_new, const orthros_bf16 *v_new,
+                                      uint8_t *k8, uint8_t *v8, int8_t *k_exp, int8_t *v_exp,
+                                      int32_t *cache_len, int L_max, int code, const float *alpha,
+                                      const float *beta, const float *alpha_c, const float *beta_c,
+                                      orthros_bf16 *o, orthros_bf16 *oc, int B, int Hq, int Hkv, int d,
+                                      int window, float scale, void *workspace, size_t ws_bytes,
+                                      int32_t *dev_err, void *stream);
+
+/*
+ * Bytes of device workspace orthros_decode_step_prefix needs, zero-filled once before its first
+ * use and left ready for the next step (not for two steps in flight).  Returns 0 for invalid
+ * sizes.
+ */
+size_t orthros_decode_prefix_workspace_size(int B, int P, int L_max, int Hq, int Hkv, int d);
+
+/*
+ * orthros_decode_step for a batch whose sequences share one prompt prefix of P >= 1 rows:
+ *   k_prefix, v_prefix [P, Hkv, d] bf16, dense; read, never written
+ *   k_cache, v_cache   [B, L_max, Hkv, d], the rows behind the prefix, cache_len[b] of them
+ * Sequence b's positions are the prefix rows 0 .. P-1 and then its own rows: the new token goes
+ * to own row cache_len[b] (position P + cache_len[b]), its copy attends over the prefix and every
+ * own row, and the base token's window reaches back into the prefix where the own rows do not
+ * fill it.  The prefix is read once for the whole batch.  P + L_max must stay below 2^31.
+ * Other arguments, results and errors as orthros_decode_step.
+ */
+orthros_status orthros_decode_step_prefix(const orthros_bf16 *q_new, const orthros_bf16 *qc_new,
+                                          const orthros_bf16 *k_new, const orthros_bf16 *v_new,
+                                          const orthros_bf16 *k_prefix, const orthros_bf16 *v_prefix,
+                                          int P, orthros_bf16 *k_cache, orthros_bf16 *v_cache,
+                                          int32_t *cache_len, int L_max, const float *alpha,
+                                          const float *beta, const float *alpha_c, const float *beta_c,
+                                          orthros_bf16 *o, orthros_bf16 *oc, int B, int Hq, int Hkv,
+                                          int d, int window, float scale, void *workspace,
+                                          size_t ws_bytes, int32_t *dev_err, void *stream);
+
+/* Bytes of device workspace orthros_xattn_prefix_fwd needs.  Returns 0 for invalid sizes. */
+size_t orthros_xattn_prefix_workspace_size(int B, int T_out, int P, int T_kv, int Hq, int Hkv, int d);
+
+/*
+ * orthros_xattn_fwd for a batch whose sequences share one prompt prefix of P >= 1 rows
+ * (k_prefix, v_prefix [P, Hkv, d] bf16, dense): copy i of sequence b attends over the whole
+ * prefix and its sequence's own rows 0 .. pos[b, i] (k, v [B, T_kv, Hkv, d]; pos counts own rows,
+ * each in [0, T_kv), so the copy's position is P + pos).  The prefix is read once for all copies
+ * of the batch.  A copy whose position is out of range gets a zero output and sets
+ * ORTHROS_DEVERR_POSITION.  workspace: orthros_xattn_prefix_workspace_size(...) bytes, 256-byte
+ * aligned, contents need not be initialised.  Other arguments as orthros_xattn_fwd.
+ */
+orthros_status orthros_xattn_prefix_fwd(const orthros_bf16 *qc_raw, const int32_t *pos,
+                                        const orthros_bf16 *k_prefix, const orthros_bf16 *v_prefix,
+                                        int P, const orthros_bf16 *k, const orthros_bf16 *v,
+                                        const float *alpha_c, const float *beta_c, orthros_bf16 *oc,
+                                        int B, int T_out, int T_kv, int Hq, int Hkv, int d, float scale,
+                                        int64_t qc_bstride, int64_t kv_bstride, int64_t oc_bstride,
+                                        void *workspace, size_t ws_bytes, int32_t *dev_err,
+                                        void *stream);
+
 #ifdef __cplusplus
 }
 #endif

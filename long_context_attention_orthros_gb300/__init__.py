@@ -14,6 +14,11 @@ CUDA kernels.  PyTorch provides device memory and the current stream.
 * :func:`swa_bwd`      -- gradient of the base stream (Eq. (4) and its scale-offset)
 * :func:`xattn_bwd`    -- gradient of the output copies (Eq. (5)), added into dK / dV
 * :func:`attn_bwd`     -- both streams' gradient of a layer in one call, dK / dV written once
+* :func:`kv_quantize`, :func:`kv_dequantize` -- prompt rows written into an 8-bit KV cache
+  (:func:`kv_cache_q8`) and read back as bf16
+* :func:`decode_step_q8` -- the decode step over an 8-bit cache
+* :func:`xattn_prefix_fwd`, :func:`decode_step_prefix` -- the copies' attention and the decode
+  step for a batch that shares a prompt prefix
 
 If the library is missing these functions raise; there is no fallback.
 """
@@ -25,8 +30,15 @@ from ._binding import (  # noqa: F401
     OrthrosError,
     attn_bwd,
     attn_bwd_workspace_size,
+    decode_prefix_workspace_size,
+    decode_q8_workspace_size,
     decode_step,
+    decode_step_prefix,
+    decode_step_q8,
     decode_workspace_size,
+    kv_cache_q8,
+    kv_dequantize,
+    kv_quantize,
     lib,
     library_path,
     prefill_fwd,
@@ -39,5 +51,7 @@ from ._binding import (  # noqa: F401
     xattn_bwd,
     xattn_bwd_workspace_size,
     xattn_fwd,
+    xattn_prefix_fwd,
+    xattn_prefix_workspace_size,
     xattn_workspace_size,
 )

@@ -116,6 +116,50 @@ bool swa_tc_supported(int D, int G, int window);
 cudaError_t launch_swa_tc(int D, int G, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                           const CUtensorMap &o, const SwaParams &p, int num_sms, cudaStream_t stream);
 
+// prompt rows written into, or read back from, the 8-bit cache
+struct KvQ8Params {
+    orthros_bf16 *k, *v;        // [B, T, Hkv, d], batch stride kv_bstride (inputs of the write)
+    uint8_t *k8, *v8;           // codes [B, L_max, Hkv, d]
+    int8_t *k_exp, *v_exp;      // exponents [B, Hkv, L_max]
+    const int32_t *start, *rows;  // [B] or NULL (0 and T)
+    long long kv_bstride;
+    int32_t *dev_err;
+    int B, T, Hkv, L_max;
+};
+cudaError_t launch_kv_quantize(int D, int code, const KvQ8Params &p, cudaStream_t stream);
+cudaError_t launch_kv_dequantize(int D, int code, const KvQ8Params &p, cudaStream_t stream);
+
+// one decode step over the 8-bit cache, or over a shared prefix and each sequence's own bf16 cache
+struct ServeParams {
+    const orthros_bf16 *q_new, *qc_new, *k_new, *v_new;
+    const orthros_bf16 *k_prefix, *v_prefix;  // [P, Hkv, d] (prefix form)
+    void *k_cache, *v_cache;                  // bf16, or codes, [B, L_max, Hkv, d]
+    int8_t *k_exp, *v_exp;                    // [B, Hkv, L_max] (8-bit form)
+    int32_t *cache_len;
+    const float *alpha, *beta, *alpha_c, *beta_c;
+    orthros_bf16 *o, *oc;
+    float *part_o;
+    float2 *part_ml;
+    int *cnt_bh;
+    int *cnt_b;
+    int32_t *dev_err;
+    int B, Hq, Hkv, L_max, window, P, nsplit, n_part;
+    float qscale;
+};
+size_t serve_workspace_bytes(int B, int P, int L_max, int Hq, int Hkv, int D);
+// code: ORTHROS_KV_E4M3 / ORTHROS_KV_INT8, or -1 for bf16 caches behind a shared prefix
+cudaError_t launch_serve(int D, int code, ServeParams p, void *workspace, cudaStream_t stream);
+
+// output copies over a shared prefix [P, Hkv, d] and their own rows: p as for launch_xattn
+struct XattnPrefixParams {
+    XattnParams x;
+    const orthros_bf16 *k_prefix, *v_prefix, *k, *v;
+    long long kv_bstride;
+    int P;
+};
+size_t xattn_prefix_workspace_bytes(int B, int T_out, int P, int T_kv, int Hq, int Hkv, int D);
+cudaError_t launch_xattn_prefix(int D, XattnPrefixParams p, void *workspace, cudaStream_t stream);
+
 size_t xattn_workspace_bytes(int B, int T_out, int T_kv, int Hq, int Hkv, int D);
 // ctas > 0: at most 8 copy rows per (batch, KV head) run on exactly `ctas` CTAs of one SM each
 cudaError_t launch_xattn(int D, const CUtensorMap &k, const CUtensorMap &v, XattnParams p, void *workspace,

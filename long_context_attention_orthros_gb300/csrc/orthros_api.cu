@@ -736,3 +736,244 @@ orthros_status orthros_attn_bwd(const orthros_bf16 *q_raw, const orthros_bf16 *k
 }
 
 }  // extern "C"
+
+namespace {
+
+orthros_status kv_q8_setup(const void *k, const void *v, const void *k8, const void *v8, const void *k_exp,
+                           const void *v_exp, const int32_t *start, const int32_t *rows, int B, int T, int Hkv, int d,
+                           int L_max, int code, int64_t kv_bstride, int32_t *dev_err, orthros::KvQ8Params &p)
+{
+    if (B < 1 || T < 0 || Hkv < 1 || L_max < 1 || L_max % 16 != 0)
+        return ORTHROS_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || (code != ORTHROS_KV_E4M3 && code != ORTHROS_KV_INT8))
+        return ORTHROS_ERR_UNSUPPORTED;
+    if (!aligned16(k8) || !aligned16(v8) || !aligned16(k_exp) || !aligned16(v_exp) ||
+        (T > 0 && (!aligned16(k) || !aligned16(v))))
+        return ORTHROS_ERR_INVALID_ARG;
+    long long ks = kv_bstride;
+    if (!resolve_bstride(ks, static_cast<long long>(T) * Hkv * d))
+        return ORTHROS_ERR_INVALID_ARG;
+    p.k = static_cast<orthros_bf16 *>(const_cast<void *>(k));
+    p.v = static_cast<orthros_bf16 *>(const_cast<void *>(v));
+    p.k8 = static_cast<uint8_t *>(const_cast<void *>(k8));
+    p.v8 = static_cast<uint8_t *>(const_cast<void *>(v8));
+    p.k_exp = static_cast<int8_t *>(const_cast<void *>(k_exp));
+    p.v_exp = static_cast<int8_t *>(const_cast<void *>(v_exp));
+    p.start = start;
+    p.rows = rows;
+    p.kv_bstride = ks;
+    p.dev_err = dev_err;
+    p.B = B;
+    p.T = T;
+    p.Hkv = Hkv;
+    p.L_max = L_max;
+    return ORTHROS_OK;
+}
+
+// sizes that the decode steps over an 8-bit cache (P = 0) or behind a prefix take
+bool serve_sizes_ok(int B, int P, int L_max, int Hkv)
+{
+    return B >= 1 && P >= 0 && L_max >= 1 && static_cast<long long>(P) + L_max < 0x7fffffffLL &&
+           static_cast<long long>(B) * Hkv <= 65535;
+}
+
+}  // namespace
+
+extern "C" {
+
+orthros_status orthros_kv_quantize(const orthros_bf16 *k, const orthros_bf16 *v, const int32_t *start,
+                                   const int32_t *rows, uint8_t *k8, uint8_t *v8, int8_t *k_exp, int8_t *v_exp, int B,
+                                   int T, int Hkv, int d, int L_max, int code, int64_t kv_bstride, int32_t *dev_err,
+                                   void *stream)
+{
+    orthros::KvQ8Params p{};
+    const orthros_status st = kv_q8_setup(k, v, k8, v8, k_exp, v_exp, start, rows, B, T, Hkv, d, L_max, code,
+                                          kv_bstride, dev_err, p);
+    if (st != ORTHROS_OK || T == 0)
+        return st;
+    const cudaError_t e = orthros::launch_kv_quantize(d, code, p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
+}
+
+orthros_status orthros_kv_dequantize(const uint8_t *k8, const uint8_t *v8, const int8_t *k_exp, const int8_t *v_exp,
+                                     const int32_t *start, const int32_t *rows, orthros_bf16 *k, orthros_bf16 *v, int B,
+                                     int T, int Hkv, int d, int L_max, int code, int64_t kv_bstride, int32_t *dev_err,
+                                     void *stream)
+{
+    orthros::KvQ8Params p{};
+    const orthros_status st = kv_q8_setup(k, v, k8, v8, k_exp, v_exp, start, rows, B, T, Hkv, d, L_max, code,
+                                          kv_bstride, dev_err, p);
+    if (st != ORTHROS_OK || T == 0)
+        return st;
+    const cudaError_t e = orthros::launch_kv_dequantize(d, code, p, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
+}
+
+size_t orthros_decode_q8_workspace_size(int B, int L_max, int Hq, int Hkv, int d)
+{
+    if ((d != 64 && d != 128) || !heads_ok(Hq, Hkv) || !serve_sizes_ok(B, 0, L_max, Hkv) || L_max % 16 != 0)
+        return 0;
+    return orthros::serve_workspace_bytes(B, 0, L_max, Hq, Hkv, d);
+}
+
+orthros_status orthros_decode_step_q8(const orthros_bf16 *q_new, const orthros_bf16 *qc_new, const orthros_bf16 *k_new,
+                                      const orthros_bf16 *v_new, uint8_t *k8, uint8_t *v8, int8_t *k_exp,
+                                      int8_t *v_exp, int32_t *cache_len, int L_max, int code, const float *alpha,
+                                      const float *beta, const float *alpha_c, const float *beta_c, orthros_bf16 *o,
+                                      orthros_bf16 *oc, int B, int Hq, int Hkv, int d, int window, float scale,
+                                      void *workspace, size_t ws_bytes, int32_t *dev_err, void *stream)
+{
+    if (!aligned16(q_new) || !aligned16(qc_new) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k8) ||
+        !aligned16(v8) || !aligned16(k_exp) || !aligned16(v_exp) || !cache_len || !aligned16(alpha) ||
+        !aligned16(beta) || !aligned16(alpha_c) || !aligned16(beta_c) || !aligned16(o) || !aligned16(oc) ||
+        window < 1 || !std::isfinite(scale) || L_max % 16 != 0)
+        return ORTHROS_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || !heads_ok(Hq, Hkv) || (code != ORTHROS_KV_E4M3 && code != ORTHROS_KV_INT8))
+        return ORTHROS_ERR_UNSUPPORTED;
+    if (!serve_sizes_ok(B, 0, L_max, Hkv))
+        return ORTHROS_ERR_INVALID_ARG;
+    const size_t need = orthros::serve_workspace_bytes(B, 0, L_max, Hq, Hkv, d);
+    if (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return ORTHROS_ERR_WORKSPACE;
+    orthros::ServeParams p{};
+    p.q_new = q_new;
+    p.qc_new = qc_new;
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.k_cache = k8;
+    p.v_cache = v8;
+    p.k_exp = k_exp;
+    p.v_exp = v_exp;
+    p.cache_len = cache_len;
+    p.alpha = alpha;
+    p.beta = beta;
+    p.alpha_c = alpha_c;
+    p.beta_c = beta_c;
+    p.o = o;
+    p.oc = oc;
+    p.dev_err = dev_err;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.L_max = L_max;
+    p.window = window;
+    p.qscale = scale * kLog2e;
+    const cudaError_t e = orthros::launch_serve(d, code, p, workspace, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
+}
+
+size_t orthros_decode_prefix_workspace_size(int B, int P, int L_max, int Hq, int Hkv, int d)
+{
+    if ((d != 64 && d != 128) || !heads_ok(Hq, Hkv) || P < 1 || !serve_sizes_ok(B, P, L_max, Hkv))
+        return 0;
+    return orthros::serve_workspace_bytes(B, P, L_max, Hq, Hkv, d);
+}
+
+orthros_status orthros_decode_step_prefix(const orthros_bf16 *q_new, const orthros_bf16 *qc_new,
+                                          const orthros_bf16 *k_new, const orthros_bf16 *v_new,
+                                          const orthros_bf16 *k_prefix, const orthros_bf16 *v_prefix, int P,
+                                          orthros_bf16 *k_cache, orthros_bf16 *v_cache, int32_t *cache_len, int L_max,
+                                          const float *alpha, const float *beta, const float *alpha_c,
+                                          const float *beta_c, orthros_bf16 *o, orthros_bf16 *oc, int B, int Hq,
+                                          int Hkv, int d, int window, float scale, void *workspace, size_t ws_bytes,
+                                          int32_t *dev_err, void *stream)
+{
+    if (!aligned16(q_new) || !aligned16(qc_new) || !aligned16(k_new) || !aligned16(v_new) || !aligned16(k_prefix) ||
+        !aligned16(v_prefix) || !aligned16(k_cache) || !aligned16(v_cache) || !cache_len || !aligned16(alpha) ||
+        !aligned16(beta) || !aligned16(alpha_c) || !aligned16(beta_c) || !aligned16(o) || !aligned16(oc) || P < 1 ||
+        window < 1 || !std::isfinite(scale))
+        return ORTHROS_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || !heads_ok(Hq, Hkv))
+        return ORTHROS_ERR_UNSUPPORTED;
+    if (!serve_sizes_ok(B, P, L_max, Hkv))
+        return ORTHROS_ERR_INVALID_ARG;
+    const size_t need = orthros::serve_workspace_bytes(B, P, L_max, Hq, Hkv, d);
+    if (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return ORTHROS_ERR_WORKSPACE;
+    orthros::ServeParams p{};
+    p.q_new = q_new;
+    p.qc_new = qc_new;
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.k_prefix = k_prefix;
+    p.v_prefix = v_prefix;
+    p.P = P;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.cache_len = cache_len;
+    p.alpha = alpha;
+    p.beta = beta;
+    p.alpha_c = alpha_c;
+    p.beta_c = beta_c;
+    p.o = o;
+    p.oc = oc;
+    p.dev_err = dev_err;
+    p.B = B;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.L_max = L_max;
+    p.window = window;
+    p.qscale = scale * kLog2e;
+    const cudaError_t e = orthros::launch_serve(d, -1, p, workspace, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
+}
+
+size_t orthros_xattn_prefix_workspace_size(int B, int T_out, int P, int T_kv, int Hq, int Hkv, int d)
+{
+    if ((d != 64 && d != 128) || !heads_ok(Hq, Hkv) || P < 1 || T_out < 0 || !serve_sizes_ok(B, P, T_kv, Hkv))
+        return 0;
+    return T_out == 0 ? 256 : orthros::xattn_prefix_workspace_bytes(B, T_out, P, T_kv, Hq, Hkv, d);
+}
+
+orthros_status orthros_xattn_prefix_fwd(const orthros_bf16 *qc_raw, const int32_t *pos, const orthros_bf16 *k_prefix,
+                                        const orthros_bf16 *v_prefix, int P, const orthros_bf16 *k,
+                                        const orthros_bf16 *v, const float *alpha_c, const float *beta_c,
+                                        orthros_bf16 *oc, int B, int T_out, int T_kv, int Hq, int Hkv, int d,
+                                        float scale, int64_t qc_bstride, int64_t kv_bstride, int64_t oc_bstride,
+                                        void *workspace, size_t ws_bytes, int32_t *dev_err, void *stream)
+{
+    if (T_out < 0 || P < 1 || !std::isfinite(scale))
+        return ORTHROS_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || !heads_ok(Hq, Hkv))
+        return ORTHROS_ERR_UNSUPPORTED;
+    if (!serve_sizes_ok(B, P, T_kv, Hkv))
+        return ORTHROS_ERR_INVALID_ARG;
+    if (T_out == 0)
+        return ORTHROS_OK;
+    if (!aligned16(qc_raw) || !pos || !aligned16(k_prefix) || !aligned16(v_prefix) || !aligned16(k) || !aligned16(v) ||
+        !aligned16(alpha_c) || !aligned16(beta_c) || !aligned16(oc))
+        return ORTHROS_ERR_INVALID_ARG;
+    long long qs = qc_bstride, ks = kv_bstride, os = oc_bstride;
+    if (!resolve_bstride(qs, static_cast<long long>(T_out) * Hq * d) ||
+        !resolve_bstride(ks, static_cast<long long>(T_kv) * Hkv * d) ||
+        !resolve_bstride(os, static_cast<long long>(T_out) * Hq * d))
+        return ORTHROS_ERR_INVALID_ARG;
+    const size_t need = orthros::xattn_prefix_workspace_bytes(B, T_out, P, T_kv, Hq, Hkv, d);
+    if (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return ORTHROS_ERR_WORKSPACE;
+    orthros::XattnPrefixParams p{};
+    p.x.qc = qc_raw;
+    p.x.pos = pos;
+    p.x.alpha_c = alpha_c;
+    p.x.beta_c = beta_c;
+    p.x.oc = oc;
+    p.x.dev_err = dev_err;
+    p.x.qc_bstride = qs;
+    p.x.oc_bstride = os;
+    p.x.B = B;
+    p.x.T_out = T_out;
+    p.x.T_kv = T_kv;
+    p.x.Hq = Hq;
+    p.x.Hkv = Hkv;
+    p.x.qscale = scale * kLog2e;
+    p.k_prefix = k_prefix;
+    p.v_prefix = v_prefix;
+    p.k = k;
+    p.v = v;
+    p.kv_bstride = ks;
+    p.P = P;
+    const cudaError_t e = orthros::launch_xattn_prefix(d, p, workspace, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
+}
+
+}  // extern "C"
