@@ -129,41 +129,62 @@ struct KvQ8Params {
 cudaError_t launch_kv_quantize(int D, int code, const KvQ8Params &p, cudaStream_t stream);
 cudaError_t launch_kv_dequantize(int D, int code, const KvQ8Params &p, cudaStream_t stream);
 
+// attention of all rows of a batch over one shared prefix [P, Hkv, d]: partials in slots
+// (split, b, KV head, copy * G + head).  k, v maps with boxes of 64 x 1 x 64.
+struct PrefixAttnParams {
+    const orthros_bf16 *qc;  // [B, T_out, Hq, d], batch stride qc_bstride
+    const int32_t *pos;      // [B, T_out] own positions (a copy outside [0, T_kv) takes no key), or NULL
+    const float *alpha_c, *beta_c;
+    float *part_o;
+    float2 *part_ml;
+    int32_t *dev_err;
+    long long qc_bstride;
+    int B, T_out, T_kv, P, Hq, Hkv;
+    int chunk;  // keys of a split, set by the launcher
+    float qscale;
+};
+int prefix_attn_parts(long long copies, int P, int Hq, int Hkv);
+cudaError_t launch_prefix_attn(int D, const CUtensorMap &k, const CUtensorMap &v, PrefixAttnParams p,
+                               cudaStream_t stream);
+
 // one decode step over the 8-bit cache, or over a shared prefix and each sequence's own bf16 cache
 struct ServeParams {
     const orthros_bf16 *q_new, *qc_new, *k_new, *v_new;
-    const orthros_bf16 *k_prefix, *v_prefix;  // [P, Hkv, d] (prefix form)
-    void *k_cache, *v_cache;                  // bf16, or codes, [B, L_max, Hkv, d]
-    int8_t *k_exp, *v_exp;                    // [B, Hkv, L_max] (8-bit form)
+    void *k_cache, *v_cache;  // bf16, or codes, [B, L_max, Hkv, d]
+    int8_t *k_exp, *v_exp;    // [B, Hkv, L_max] (8-bit form)
     int32_t *cache_len;
     const float *alpha, *beta, *alpha_c, *beta_c;
     orthros_bf16 *o, *oc;
-    float *part_o;
-    float2 *part_ml;
-    int *cnt_bh;
-    int *cnt_b;
+    float *part_o;            // [2 * CTAs][G][D]
+    float2 *part_ml;          // [2 * CTAs][G]
+    int *cnt_bh;              // [B * Hkv][2]
+    int *cnt_all;
+    float *pre_o;             // the prefix kernel's partials (prefix form)
+    float2 *pre_ml;
     int32_t *dev_err;
-    int B, Hq, Hkv, L_max, window, P, nsplit, n_part;
+    int B, Hq, Hkv, L_max, window;
+    int P, n_part;            // prefix rows (0: 8-bit form) and splits
     float qscale;
 };
 size_t serve_workspace_bytes(int B, int P, int L_max, int Hq, int Hkv, int D);
-// code: ORTHROS_KV_E4M3 / ORTHROS_KV_INT8, or -1 for bf16 caches behind a shared prefix
-cudaError_t launch_serve(int D, int code, ServeParams p, void *workspace, cudaStream_t stream);
+// code: ORTHROS_KV_E4M3 / ORTHROS_KV_INT8, or -1 for bf16 caches behind a shared prefix; maps: the
+// cache's K and V, then the prefix's (boxes of 64 x 1 x 64; the 8-bit cache's d x 1 x 64)
+cudaError_t launch_serve(int D, int code, const CUtensorMap *maps, ServeParams p, void *workspace,
+                         cudaStream_t stream);
 
-// output copies over a shared prefix [P, Hkv, d] and their own rows: p as for launch_xattn
-struct XattnPrefixParams {
-    XattnParams x;
-    const orthros_bf16 *k_prefix, *v_prefix, *k, *v;
-    long long kv_bstride;
-    int P;
-};
+// output copies over a shared prefix and their own rows; maps: own K and V, the prefix's K and V
 size_t xattn_prefix_workspace_bytes(int B, int T_out, int P, int T_kv, int Hq, int Hkv, int D);
-cudaError_t launch_xattn_prefix(int D, XattnPrefixParams p, void *workspace, cudaStream_t stream);
+cudaError_t launch_xattn_prefix(int D, const CUtensorMap *maps, XattnParams p, int P, void *workspace,
+                                cudaStream_t stream);
 
 size_t xattn_workspace_bytes(int B, int T_out, int T_kv, int Hq, int Hkv, int D);
 // ctas > 0: at most 8 copy rows per (batch, KV head) run on exactly `ctas` CTAs of one SM each
 cudaError_t launch_xattn(int D, const CUtensorMap &k, const CUtensorMap &v, XattnParams p, void *workspace,
                          cudaStream_t stream, int ctas = 0);
+// the split-KV kernels alone: every row's xattn_parts() partials at p.part_o / p.part_ml
+int xattn_parts(int B, int T_out, int T_kv, int Hq, int Hkv);
+cudaError_t launch_xattn_partials(int D, const CUtensorMap &k, const CUtensorMap &v, XattnParams p,
+                                  cudaStream_t stream);
 // merge split partials [n_part][B*Hkv][R][D] into the copy outputs
 cudaError_t launch_xattn_combine(int D, const XattnParams &p, cudaStream_t stream);
 // many copies per (batch, KV head) (T_out * G >= 256): tcgen05 flash kernel over key blocks of

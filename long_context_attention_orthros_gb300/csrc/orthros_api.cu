@@ -770,6 +770,24 @@ orthros_status kv_q8_setup(const void *k, const void *v, const void *k8, const v
     return ORTHROS_OK;
 }
 
+// 4-D view {d, Hkv, L_max, B} of an 8-bit cache's codes, boxes of {d, 1, 64, 1}, rows swizzled
+// within their own d bytes
+bool make_map_q8(CUtensorMap *m, const void *base, int d, int Hkv, int L_max, int B)
+{
+    EncodeTiledFn fn = encode_fn();
+    if (!fn)
+        return false;
+    const cuuint64_t row = static_cast<cuuint64_t>(Hkv) * d;
+    cuuint64_t dims[4] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(Hkv), static_cast<cuuint64_t>(L_max),
+                          static_cast<cuuint64_t>(B)};
+    cuuint64_t strides[3] = {static_cast<cuuint64_t>(d), row, row * L_max};
+    cuuint32_t box[4] = {static_cast<cuuint32_t>(d), 1u, 64u, 1u};
+    cuuint32_t estr[4] = {1u, 1u, 1u, 1u};
+    return fn(m, CU_TENSOR_MAP_DATA_TYPE_UINT8, 4, const_cast<void *>(base), dims, strides, box, estr,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, d == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 // sizes that the decode steps over an 8-bit cache (P = 0) or behind a prefix take
 bool serve_sizes_ok(int B, int P, int L_max, int Hkv)
 {
@@ -858,7 +876,12 @@ orthros_status orthros_decode_step_q8(const orthros_bf16 *q_new, const orthros_b
     p.L_max = L_max;
     p.window = window;
     p.qscale = scale * kLog2e;
-    const cudaError_t e = orthros::launch_serve(d, code, p, workspace, static_cast<cudaStream_t>(stream));
+    CUtensorMap m[4];
+    if (!make_map_q8(&m[0], k8, d, Hkv, L_max, B) || !make_map_q8(&m[1], v8, d, Hkv, L_max, B))
+        return ORTHROS_ERR_CUDA;
+    m[2] = m[0];  // no prefix
+    m[3] = m[1];
+    const cudaError_t e = orthros::launch_serve(d, code, m, p, workspace, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
 }
 
@@ -895,8 +918,6 @@ orthros_status orthros_decode_step_prefix(const orthros_bf16 *q_new, const orthr
     p.qc_new = qc_new;
     p.k_new = k_new;
     p.v_new = v_new;
-    p.k_prefix = k_prefix;
-    p.v_prefix = v_prefix;
     p.P = P;
     p.k_cache = k_cache;
     p.v_cache = v_cache;
@@ -914,7 +935,12 @@ orthros_status orthros_decode_step_prefix(const orthros_bf16 *q_new, const orthr
     p.L_max = L_max;
     p.window = window;
     p.qscale = scale * kLog2e;
-    const cudaError_t e = orthros::launch_serve(d, -1, p, workspace, static_cast<cudaStream_t>(stream));
+    CUtensorMap m[4];
+    const long long cs = static_cast<long long>(L_max) * Hkv * d, ps = static_cast<long long>(P) * Hkv * d;
+    if (!make_map(&m[0], k_cache, d, Hkv, L_max, B, cs, 1, 64) || !make_map(&m[1], v_cache, d, Hkv, L_max, B, cs, 1, 64) ||
+        !make_map(&m[2], k_prefix, d, Hkv, P, 1, ps, 1, 64) || !make_map(&m[3], v_prefix, d, Hkv, P, 1, ps, 1, 64))
+        return ORTHROS_ERR_CUDA;
+    const cudaError_t e = orthros::launch_serve(d, -1, m, p, workspace, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
 }
 
@@ -951,28 +977,27 @@ orthros_status orthros_xattn_prefix_fwd(const orthros_bf16 *qc_raw, const int32_
     const size_t need = orthros::xattn_prefix_workspace_bytes(B, T_out, P, T_kv, Hq, Hkv, d);
     if (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
         return ORTHROS_ERR_WORKSPACE;
-    orthros::XattnPrefixParams p{};
-    p.x.qc = qc_raw;
-    p.x.pos = pos;
-    p.x.alpha_c = alpha_c;
-    p.x.beta_c = beta_c;
-    p.x.oc = oc;
-    p.x.dev_err = dev_err;
-    p.x.qc_bstride = qs;
-    p.x.oc_bstride = os;
-    p.x.B = B;
-    p.x.T_out = T_out;
-    p.x.T_kv = T_kv;
-    p.x.Hq = Hq;
-    p.x.Hkv = Hkv;
-    p.x.qscale = scale * kLog2e;
-    p.k_prefix = k_prefix;
-    p.v_prefix = v_prefix;
-    p.k = k;
-    p.v = v;
-    p.kv_bstride = ks;
-    p.P = P;
-    const cudaError_t e = orthros::launch_xattn_prefix(d, p, workspace, static_cast<cudaStream_t>(stream));
+    XattnParams p{};
+    p.qc = qc_raw;
+    p.pos = pos;
+    p.alpha_c = alpha_c;
+    p.beta_c = beta_c;
+    p.oc = oc;
+    p.dev_err = dev_err;
+    p.qc_bstride = qs;
+    p.oc_bstride = os;
+    p.B = B;
+    p.T_out = T_out;
+    p.T_kv = T_kv;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.qscale = scale * kLog2e;
+    CUtensorMap m[4];
+    const long long ps = static_cast<long long>(P) * Hkv * d;
+    if (!make_map(&m[0], k, d, Hkv, T_kv, B, ks, 1, 64) || !make_map(&m[1], v, d, Hkv, T_kv, B, ks, 1, 64) ||
+        !make_map(&m[2], k_prefix, d, Hkv, P, 1, ps, 1, 64) || !make_map(&m[3], v_prefix, d, Hkv, P, 1, ps, 1, 64))
+        return ORTHROS_ERR_CUDA;
+    const cudaError_t e = orthros::launch_xattn_prefix(d, m, p, P, workspace, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
 }
 

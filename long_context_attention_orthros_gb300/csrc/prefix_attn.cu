@@ -1,0 +1,274 @@
+// prefix_attn.cu -- attention of every query row of a batch over one shared prompt prefix, computed
+// once for all: rows (sequence b, copy i, head of the KV head's group) lie end to end, so each K/V
+// byte of the prefix serves the whole batch.  Results are partials (max, sum, unnormalised o) per
+// split of the prefix's keys, in the layout the combine kernel and the decode step join with
+// the sequences' own rows:  slot (split, b, KV head, copy * G + head).
+//
+// Grid (split, KV head x row tile).  A CTA streams its keys through a TMA ring (64-key blocks, one
+// producer warp); four warps run the online softmax on warp MMAs, RG groups of 16 rows with
+// 4 / RG warps sharing a group's keys and merging in shared memory.
+#include "kernels.cuh"
+#include "xattn.cuh"
+
+namespace orthros {
+
+template <int D>
+struct PaCfg {
+    static constexpr int KB = 64;
+    static constexpr int SLAB = KB * 128;
+    static constexpr int KV_BYTES = KB * D * 2;
+    static constexpr int STAGE_BYTES = 2 * KV_BYTES;
+    static constexpr int STAGES = 3;
+    static constexpr int CWARPS = 4;
+    static constexpr int THREADS = (CWARPS + 1) * 32;
+    static constexpr int BAR_OFF = STAGES * STAGE_BYTES;
+    static constexpr int SMEM = BAR_OFF + 2 * STAGES * 8 + 1024;
+    static_assert(STAGES * STAGE_BYTES >= CWARPS * 16 * (D + 2) * 4, "the warps' merge reuses the ring");
+};
+
+struct PaRow {
+    const orthros_bf16 *q;  // NULL: no such row, or a copy whose position is out of range
+    long long slot;         // of split 0; -1: no such row
+    int head;
+};
+
+template <int G>
+__device__ __forceinline__ PaRow pa_row(const PrefixAttnParams &p, long long row, int g, int D)
+{
+    PaRow r = {nullptr, -1, g * G};
+    const long long bi = row / G;
+    if (bi >= static_cast<long long>(p.B) * p.T_out)
+        return r;
+    const int b = static_cast<int>(bi / p.T_out), i = static_cast<int>(bi % p.T_out), h = static_cast<int>(row % G);
+    r.head = g * G + h;
+    r.slot = (static_cast<long long>(b) * p.Hkv + g) * p.T_out * G + static_cast<long long>(i) * G + h;
+    if (p.pos == nullptr || (p.pos[bi] >= 0 && p.pos[bi] < p.T_kv))
+        r.q = p.qc + b * p.qc_bstride + (static_cast<long long>(i) * p.Hq + r.head) * D;
+    return r;
+}
+
+template <int D, int G, int RG>
+__global__ void __launch_bounds__(PaCfg<D>::THREADS)
+    prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                       const PrefixAttnParams p)
+{
+    using C = PaCfg<D>;
+    constexpr int KL = C::CWARPS / RG;  // warps that share a group's keys
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_s = smem_u32(smem_raw);
+    const uint32_t pad = ((raw_s + 1023u) & ~1023u) - raw_s;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t sbase = raw_s + pad;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
+    uint64_t *empty = full + C::STAGES;
+    const int split = blockIdx.x, g = blockIdx.y % p.Hkv;
+    const long long row0 = static_cast<long long>(blockIdx.y / p.Hkv) * 16 * RG;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::STAGES; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&empty[s], C::CWARPS);
+        }
+        fence_barrier_init();
+    }
+    // what the kernels before wrote first, then a dependent grid may start beside this one
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __syncthreads();
+    const int js = split * p.chunk, je = min(js + p.chunk, p.P);
+    const int nblk = je > js ? (je - js + C::KB - 1) / C::KB : 0;
+
+    if (warp == C::CWARPS) {
+        if (lane != 0)
+            return;
+        tma_prefetch_desc(&kmap);
+        tma_prefetch_desc(&vmap);
+        for (int i = 0; i < nblk; ++i) {
+            const int s = i % C::STAGES;
+            if (i >= C::STAGES && !mbar_wait(&empty[s], static_cast<uint32_t>(((i / C::STAGES) - 1) & 1))) {
+                record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+                return;
+            }
+            uint8_t *dst = smem + s * C::STAGE_BYTES;
+            mbar_arrive_expect_tx(&full[s], C::STAGE_BYTES);
+#pragma unroll
+            for (int sl = 0; sl < D / 64; ++sl) {
+                tma_load_4d(dst + sl * C::SLAB, &kmap, &full[s], sl * 64, g, js + i * C::KB, 0);
+                tma_load_4d(dst + C::KV_BYTES + sl * C::SLAB, &vmap, &full[s], sl * 64, g, js + i * C::KB, 0);
+            }
+        }
+        return;
+    }
+
+    const int rg = warp / KL, kl = warp % KL;
+    const int gr = lane >> 2, qd = (lane & 3) * 2;
+    const PaRow rows[2] = {pa_row<G>(p, row0 + rg * 16 + gr, g, D), pa_row<G>(p, row0 + rg * 16 + gr + 8, g, D)};
+    WarpRows16<D> st;
+#pragma unroll
+    for (int kt = 0; kt < D / 16; ++kt)
+#pragma unroll
+        for (int r = 0; r < 4; ++r) {
+            const PaRow &row = rows[r & 1];
+            uint32_t hi = 0, lo = 0;
+            if (row.q != nullptr)
+                load_q_pair(row.q, p.alpha_c + row.head * D, p.beta_c + row.head * D,
+                            kt * 16 + qd + ((r & 2) ? 8 : 0), p.qscale, hi, lo);
+            st.qa[kt][r] = hi;
+            st.ql[kt][r] = lo;
+        }
+    st.reset();
+    bool ok = true;
+    for (int i = 0; i < nblk; ++i) {
+        const int s = i % C::STAGES;
+        if (ok && !mbar_wait(&full[s], static_cast<uint32_t>((i / C::STAGES) & 1)))
+            ok = false;
+        const uint32_t kbase = sbase + s * C::STAGE_BYTES;
+#pragma unroll
+        for (int c = kl; c < 4; c += KL) {
+            const int j0 = js + i * C::KB + c * 16;
+            if (ok && j0 < je)
+                st.step(kbase, C::SLAB, kbase + C::KV_BYTES, C::SLAB, c * 16, j0, je - 1, je - 1, j0 + 15 < je);
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&empty[s]);
+    }
+    if (!ok && lane == 0)
+        record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+    st.finish_sums();
+
+    // the KL warps of a group, scaled to their common max, summed through shared memory
+    float *os = reinterpret_cast<float *>(smem);  // [CWARPS][16][D]; the ring is free once all are here
+    float *ms = os + C::CWARPS * 16 * D, *ls = ms + C::CWARPS * 16;
+    named_barrier(1, C::CWARPS * 32);
+#pragma unroll
+    for (int half = 0; half < 2; ++half) {
+        const int r = warp * 16 + gr + 8 * half;
+        if ((lane & 3) == 0) {
+            ms[r] = half ? st.mB : st.mA;
+            ls[r] = half ? st.lB : st.lA;
+        }
+#pragma unroll
+        for (int i = 0; i < D / 8; ++i)
+            *reinterpret_cast<float2 *>(os + r * D + 8 * i + qd) = make_float2(st.o[i][2 * half], st.o[i][2 * half + 1]);
+    }
+    named_barrier(1, C::CWARPS * 32);
+    const float NEG_INF = -__int_as_float(0x7f800000);
+    const long long BHR = static_cast<long long>(p.B) * p.Hkv * p.T_out * G;
+    for (int e = threadIdx.x; e < 16 * RG * (D / 4); e += C::CWARPS * 32) {
+        const int r = e / (D / 4), d4 = 4 * (e % (D / 4));
+        const PaRow row = pa_row<G>(p, row0 + r, g, D);
+        if (row.slot < 0)
+            continue;
+        const int w0 = (r / 16) * KL;
+        float M = NEG_INF, L = 0.f;
+#pragma unroll
+        for (int w = 0; w < KL; ++w)
+            M = fmaxf(M, ms[(w0 + w) * 16 + r % 16]);
+        float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < KL; ++w) {
+            const int x = (w0 + w) * 16 + r % 16;
+            if (ms[x] == NEG_INF)
+                continue;
+            const float f = fast_exp2(ms[x] - M);
+            L += f * ls[x];
+            const float4 y = *reinterpret_cast<const float4 *>(os + x * D + d4);
+            a.x += f * y.x;
+            a.y += f * y.y;
+            a.z += f * y.z;
+            a.w += f * y.w;
+        }
+        if (row.q == nullptr) {  // a copy without a position takes no key
+            M = NEG_INF;
+            L = 0.f;
+        }
+        const long long slot = split * BHR + row.slot;
+        *reinterpret_cast<float4 *>(p.part_o + slot * D + d4) = a;
+        if (d4 == 0)
+            p.part_ml[slot] = make_float2(M, L);
+    }
+}
+
+// ------------------------------------------------------------------ host side
+
+struct PaPlan {
+    int rg, tiles, splits, chunk;
+};
+
+// two CTAs on each of 152 SMs in one wave, at least 256 keys a split
+static PaPlan pa_plan(long long copies, int P, int Hq, int Hkv)
+{
+    PaPlan pl;
+    const long long R = copies * (Hq / Hkv);
+    pl.rg = R <= 16 ? 1 : (R <= 32 ? 2 : 4);
+    const long long tiles = (R + 16 * pl.rg - 1) / (16 * pl.rg);
+    pl.tiles = static_cast<int>(tiles);
+    long long splits = 304 / (tiles * Hkv);
+    const long long most = (static_cast<long long>(P) + 255) / 256;
+    splits = splits > most ? most : splits;
+    splits = splits < 1 ? 1 : splits;
+    const long long chunk = ((P + splits - 1) / splits + 63) / 64 * 64;
+    pl.chunk = static_cast<int>(chunk);
+    pl.splits = static_cast<int>((P + chunk - 1) / chunk);
+    return pl;
+}
+
+int prefix_attn_parts(long long copies, int P, int Hq, int Hkv) { return pa_plan(copies, P, Hq, Hkv).splits; }
+
+template <int D, int G, int RG>
+static cudaError_t launch_pa(const CUtensorMap &k, const CUtensorMap &v, const PrefixAttnParams &p, const PaPlan &pl,
+                             cudaStream_t stream)
+{
+    auto kern = prefix_attn_kernel<D, G, RG>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PaCfg<D>::SMEM);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(pl.splits, static_cast<unsigned>(pl.tiles) * p.Hkv);
+    cfg.blockDim = dim3(PaCfg<D>::THREADS);
+    cfg.dynamicSmemBytes = PaCfg<D>::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, k, v, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+template <int D, int G>
+static cudaError_t launch_pa_t(const CUtensorMap &k, const CUtensorMap &v, const PrefixAttnParams &p, const PaPlan &pl,
+                               cudaStream_t stream)
+{
+    return pl.rg == 1 ? launch_pa<D, G, 1>(k, v, p, pl, stream)
+                      : pl.rg == 2 ? launch_pa<D, G, 2>(k, v, p, pl, stream) : launch_pa<D, G, 4>(k, v, p, pl, stream);
+}
+
+cudaError_t launch_prefix_attn(int D, const CUtensorMap &k, const CUtensorMap &v, PrefixAttnParams p,
+                               cudaStream_t stream)
+{
+    const PaPlan pl = pa_plan(static_cast<long long>(p.B) * p.T_out, p.P, p.Hq, p.Hkv);
+    if (static_cast<long long>(pl.tiles) * p.Hkv > 65535)
+        return cudaErrorInvalidValue;
+    p.chunk = pl.chunk;
+    const int G = p.Hq / p.Hkv;
+#define ORTHROS_PA_CASE(DD, GG) \
+    if (D == DD && G == GG)     \
+        return launch_pa_t<DD, GG>(k, v, p, pl, stream);
+    ORTHROS_PA_CASE(128, 1)
+    ORTHROS_PA_CASE(128, 2)
+    ORTHROS_PA_CASE(128, 4)
+    ORTHROS_PA_CASE(128, 8)
+    ORTHROS_PA_CASE(128, 16)
+    ORTHROS_PA_CASE(64, 1)
+    ORTHROS_PA_CASE(64, 2)
+    ORTHROS_PA_CASE(64, 4)
+    ORTHROS_PA_CASE(64, 8)
+    ORTHROS_PA_CASE(64, 16)
+#undef ORTHROS_PA_CASE
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace orthros

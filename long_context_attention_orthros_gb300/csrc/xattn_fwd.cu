@@ -793,8 +793,7 @@ static cudaError_t launch_partial_keys(const CUtensorMap &k, const CUtensorMap &
     return cudaGetLastError();
 }
 
-cudaError_t launch_xattn(int D, const CUtensorMap &k, const CUtensorMap &v, XattnParams p,
-                         void *workspace, cudaStream_t stream, int ctas)
+static XattnPlan xattn_apply_plan(XattnParams &p)
 {
     const XattnPlan pl = xattn_plan(p.B, p.T_out, p.T_kv, p.Hq, p.Hkv);
     p.G = p.Hq / p.Hkv;
@@ -804,6 +803,31 @@ cudaError_t launch_xattn(int D, const CUtensorMap &k, const CUtensorMap &v, Xatt
     p.chunk = pl.chunk;
     p.n_part = pl.n_part;
     p.direct = pl.direct;
+    return pl;
+}
+
+int xattn_parts(int B, int T_out, int T_kv, int Hq, int Hkv)
+{
+    return xattn_plan(B, T_out, T_kv, Hq, Hkv).n_part;
+}
+
+cudaError_t launch_xattn_partials(int D, const CUtensorMap &k, const CUtensorMap &v, XattnParams p,
+                                  cudaStream_t stream)
+{
+    const XattnPlan pl = xattn_apply_plan(p);
+    p.direct = 0;
+    p.lse = nullptr;
+    if (pl.keys)
+        return D == 128 ? launch_partial_keys<128>(k, v, p, stream) : launch_partial_keys<64>(k, v, p, stream);
+    if (D == 128)
+        return pl.WK == 4 ? launch_partial<128, 4>(k, v, p, stream) : launch_partial<128, 1>(k, v, p, stream);
+    return pl.WK == 4 ? launch_partial<64, 4>(k, v, p, stream) : launch_partial<64, 1>(k, v, p, stream);
+}
+
+cudaError_t launch_xattn(int D, const CUtensorMap &k, const CUtensorMap &v, XattnParams p,
+                         void *workspace, cudaStream_t stream, int ctas)
+{
+    const XattnPlan pl = xattn_apply_plan(p);
     if (!pl.direct) {
         const size_t rows = static_cast<size_t>(pl.n_part) * p.B * p.Hkv * p.R;
         const size_t o_bytes = (rows * D * sizeof(float) + 255) / 256 * 256;
