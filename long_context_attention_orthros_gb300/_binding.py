@@ -492,23 +492,54 @@ def decode_step(q_new, qc_new, k_new, v_new, k_cache, v_cache, cache_len, alpha,
 
 _CODES = {torch.float8_e4m3fn: 0, torch.int8: 1}  # ORTHROS_KV_E4M3, ORTHROS_KV_INT8
 
+# The calls below are made once a token and layer, so what they cost on the host counts: a
+# tensor is checked with as few attribute reads as will do, and its address goes to ctypes as
+# a plain integer.
+
+
+def _addr(t, dev: int):
+    """Device address of a tensor that has to live on device `dev` (or None)."""
+    if t is None:
+        return None
+    if t.get_device() != dev:
+        raise OrthrosError(f"tensor arguments must be CUDA tensors on the call's device (got {t.device})")
+    return t.data_ptr()
+
+
+def _expect(t, name: str, dtype, shape) -> None:
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
+        raise OrthrosError(f"{name} must be a contiguous {dtype} CUDA tensor {shape}")
+
+
+def _invoke(name: str, dev: int, *args) -> None:
+    """Call an entry point on device `dev` and its current stream (the last argument of each)."""
+    fn = getattr(_lib or lib(), name)
+    if torch.cuda.current_device() == dev:
+        st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    else:
+        with torch.cuda.device(dev):
+            st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
+    if st != 0:
+        _check(st, name)
+
+
+def _device_of(t, name: str) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise OrthrosError(f"{name} must be a CUDA tensor")
+    return dev
+
 
 def _cache_q8(k8, v8, k_exp, v_exp):
     """Check the four tensors of an 8-bit cache; return (B, L_max, Hkv, d, code)."""
-    if k8.dtype not in _CODES or not k8.is_cuda or k8.dim() != 4 or not k8.is_contiguous():
+    code = _CODES.get(k8.dtype)
+    if code is None or k8.dim() != 4 or not k8.is_contiguous():
         raise OrthrosError("k8 must be a contiguous float8_e4m3fn or int8 CUDA tensor [B, L_max, Hkv, d]")
-    B, L_max, Hkv, d = k8.shape
-    if v8.dtype != k8.dtype or not v8.is_cuda or v8.shape != k8.shape or not v8.is_contiguous():
-        raise OrthrosError("v8 must match k8")
-    for t, nm in ((k_exp, "k_exp"), (v_exp, "v_exp")):
-        if t.dtype != torch.int8 or not t.is_cuda or tuple(t.shape) != (B, Hkv, L_max) or not t.is_contiguous():
-            raise OrthrosError(f"{nm} must be a contiguous int8 CUDA tensor [B, Hkv, L_max]")
-    return B, L_max, Hkv, d, _CODES[k8.dtype]
-
-
-def _per_sequence(t, name: str, B: int) -> None:
-    if t is not None and (t.dtype != torch.int32 or not t.is_cuda or tuple(t.shape) != (B,) or not t.is_contiguous()):
-        raise OrthrosError(f"{name} must be a contiguous int32 CUDA tensor [B]")
+    B, L_max, Hkv, d = shape = k8.shape
+    _expect(v8, "v8", k8.dtype, shape)
+    _expect(k_exp, "k_exp", torch.int8, (B, Hkv, L_max))
+    _expect(v_exp, "v_exp", torch.int8, (B, Hkv, L_max))
+    return B, L_max, Hkv, d, code
 
 
 def kv_cache_q8(B, L_max, Hkv, d, device, dtype=torch.float8_e4m3fn):
@@ -521,41 +552,42 @@ def kv_cache_q8(B, L_max, Hkv, d, device, dtype=torch.float8_e4m3fn):
     return codes[0], codes[1], exps[0], exps[1]
 
 
+def _kv_pair(k, v, B, Hkv, d) -> int:
+    """Check bf16 rows [B, T, Hkv, d] that go into, or come out of, a cache; return their batch stride."""
+    ks = _bf16_rows(k, "k")
+    if _bf16_rows(v, "v") != ks or v.shape != k.shape:
+        raise OrthrosError("k and v must have the same shape and strides")
+    if k.shape[0] != B or k.shape[2] != Hkv or k.shape[3] != d:
+        raise OrthrosError("k does not match the cache")
+    return ks
+
+
 def kv_quantize(k, v, k8, v8, k_exp, v_exp, start=None, rows=None, dev_err=None):
     """Write rows 0..rows[b]-1 (default all T) of k, v [B, T, Hkv, d] into the 8-bit cache at rows
     start[b].. (default 0): codes k8, v8 [B, L_max, Hkv, d] (float8_e4m3fn or int8) and exponents
     k_exp, v_exp int8 [B, Hkv, L_max]; a row stands for code * 2^exponent."""
     B, L_max, Hkv, d, code = _cache_q8(k8, v8, k_exp, v_exp)
-    _kv_rows_q8(k, v, k8, B, Hkv, d)
-    _per_sequence(start, "start", B)
-    _per_sequence(rows, "rows", B)
-    with torch.cuda.device(k8.device):
-        st = lib().orthros_kv_quantize(_ptr(k), _ptr(v), _ptr(start), _ptr(rows), _ptr(k8), _ptr(v8), _ptr(k_exp),
-                                       _ptr(v_exp), B, k.shape[1], Hkv, d, L_max, code, _bf16_rows(k, "k"),
-                                       _ptr(dev_err), _stream(k8.device))
-    _check(st, "orthros_kv_quantize")
+    ks = _kv_pair(k, v, B, Hkv, d)
+    for t, nm in ((start, "start"), (rows, "rows")):
+        if t is not None:
+            _expect(t, nm, torch.int32, (B,))
+    dev = _device_of(k8, "k8")
+    a = [_addr(t, dev) for t in (k, v, start, rows, k8, v8, k_exp, v_exp, dev_err)]
+    _invoke("orthros_kv_quantize", dev, *a[:8], B, k.shape[1], Hkv, d, L_max, code, ks, a[8])
 
 
 def kv_dequantize(k8, v8, k_exp, v_exp, k, v, start=None, rows=None, dev_err=None):
     """Read cache rows start[b].. (default 0) back as bf16 into rows 0..rows[b]-1 (default all T) of
     k, v [B, T, Hkv, d]; rows behind them are left as they are.  Returns (k, v)."""
     B, L_max, Hkv, d, code = _cache_q8(k8, v8, k_exp, v_exp)
-    _kv_rows_q8(k, v, k8, B, Hkv, d)
-    _per_sequence(start, "start", B)
-    _per_sequence(rows, "rows", B)
-    with torch.cuda.device(k8.device):
-        st = lib().orthros_kv_dequantize(_ptr(k8), _ptr(v8), _ptr(k_exp), _ptr(v_exp), _ptr(start), _ptr(rows),
-                                         _ptr(k), _ptr(v), B, k.shape[1], Hkv, d, L_max, code, _bf16_rows(k, "k"),
-                                         _ptr(dev_err), _stream(k8.device))
-    _check(st, "orthros_kv_dequantize")
+    ks = _kv_pair(k, v, B, Hkv, d)
+    for t, nm in ((start, "start"), (rows, "rows")):
+        if t is not None:
+            _expect(t, nm, torch.int32, (B,))
+    dev = _device_of(k8, "k8")
+    a = [_addr(t, dev) for t in (k8, v8, k_exp, v_exp, start, rows, k, v, dev_err)]
+    _invoke("orthros_kv_dequantize", dev, *a[:8], B, k.shape[1], Hkv, d, L_max, code, ks, a[8])
     return k, v
-
-
-def _kv_rows_q8(k, v, k8, B, Hkv, d) -> None:
-    if _bf16_rows(k, "k") != _bf16_rows(v, "v") or v.shape != k.shape:
-        raise OrthrosError("k and v must have the same shape and strides")
-    if k.shape[0] != B or k.shape[2] != Hkv or k.shape[3] != d:
-        raise OrthrosError("k does not match the cache")
 
 
 def decode_q8_workspace_size(B, L_max, Hq, Hkv, d) -> int:
@@ -567,22 +599,25 @@ def decode_q8_workspace(B, L_max, Hq, Hkv, d, device) -> torch.Tensor:
     return torch.zeros(max(decode_q8_workspace_size(B, L_max, Hq, Hkv, d), 256), dtype=torch.uint8, device=device)
 
 
-def _decode_args(q_new, qc_new, k_new, v_new, cache_len, alpha, beta, alpha_c, beta_c, o, oc, B, Hkv, d, device):
+def _decode_args(q_new, qc_new, k_new, v_new, cache_len, vectors, o, oc, B, Hkv, d):
     """Check what the decode steps share; return (o, oc, Hq)."""
     Hq = q_new.shape[1]
+    rows, new, vec, bf16 = (B, Hq, d), (B, Hkv, d), (Hq, d), torch.bfloat16
+    _expect(q_new, "q_new", bf16, rows)
+    _expect(qc_new, "qc_new", bf16, rows)
+    _expect(k_new, "k_new", bf16, new)
+    _expect(v_new, "v_new", bf16, new)
+    _expect(cache_len, "cache_len", torch.int32, (B,))
+    for t, nm in zip(vectors, ("alpha", "beta", "alpha_c", "beta_c")):
+        _expect(t, nm, torch.float32, vec)
     if o is None:
-        o = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=device)
+        o = torch.empty_like(q_new)
+    else:
+        _expect(o, "o", bf16, rows)
     if oc is None:
-        oc = torch.empty((B, Hq, d), dtype=torch.bfloat16, device=device)
-    for t, nm, shp in ((q_new, "q_new", (B, Hq, d)), (qc_new, "qc_new", (B, Hq, d)), (k_new, "k_new", (B, Hkv, d)),
-                       (v_new, "v_new", (B, Hkv, d)), (o, "o", (B, Hq, d)), (oc, "oc", (B, Hq, d))):
-        if t.dtype != torch.bfloat16 or not t.is_cuda or tuple(t.shape) != shp or not t.is_contiguous():
-            raise OrthrosError(f"{nm} must be a contiguous bf16 CUDA tensor {shp}")
-    if cache_len is None:
-        raise OrthrosError("cache_len must be an int32 CUDA tensor [B]")
-    _per_sequence(cache_len, "cache_len", B)
-    for t, nm in ((alpha, "alpha"), (beta, "beta"), (alpha_c, "alpha_c"), (beta_c, "beta_c")):
-        _vec(t, nm, Hq, d)
+        oc = torch.empty_like(q_new)
+    else:
+        _expect(oc, "oc", bf16, rows)
     return o, oc, Hq
 
 
@@ -592,29 +627,22 @@ def decode_step_q8(q_new, qc_new, k_new, v_new, k8, v8, k_exp, v_exp, cache_len,
     int8 [B, Hkv, L_max]): the new row is written as codes and both streams attend over the rows'
     values.  Returns (o, oc)."""
     B, L_max, Hkv, d, code = _cache_q8(k8, v8, k_exp, v_exp)
-    o, oc, Hq = _decode_args(q_new, qc_new, k_new, v_new, cache_len, alpha, beta, alpha_c, beta_c, o, oc, B, Hkv, d,
-                             k8.device)
+    dev = _device_of(k8, "k8")
+    o, oc, Hq = _decode_args(q_new, qc_new, k_new, v_new, cache_len, (alpha, beta, alpha_c, beta_c), o, oc, B, Hkv, d)
     if workspace is None:
         workspace = decode_q8_workspace(B, L_max, Hq, Hkv, d, k8.device)
-    with torch.cuda.device(k8.device):
-        st = lib().orthros_decode_step_q8(_ptr(q_new), _ptr(qc_new), _ptr(k_new), _ptr(v_new), _ptr(k8), _ptr(v8),
-                                          _ptr(k_exp), _ptr(v_exp), _ptr(cache_len), L_max, code, _ptr(alpha),
-                                          _ptr(beta), _ptr(alpha_c), _ptr(beta_c), _ptr(o), _ptr(oc), B, Hq, Hkv, d,
-                                          int(window), _scale(scale, d), _ptr(workspace),
-                                          workspace.numel() * workspace.element_size(), _ptr(dev_err),
-                                          _stream(k8.device))
-    _check(st, "orthros_decode_step_q8")
+    a = [_addr(t, dev) for t in (q_new, qc_new, k_new, v_new, k8, v8, k_exp, v_exp, cache_len, alpha, beta, alpha_c,
+                                 beta_c, o, oc, workspace, dev_err)]
+    _invoke("orthros_decode_step_q8", dev, *a[:9], L_max, code, *a[9:15], B, Hq, Hkv, d, int(window),
+            _scale(scale, d), a[15], workspace.nbytes, a[16])
     return o, oc
 
 
 def _prefix_rows(k_prefix, v_prefix, Hkv, d) -> int:
-    for t, nm in ((k_prefix, "k_prefix"), (v_prefix, "v_prefix")):
-        if (t.dtype != torch.bfloat16 or not t.is_cuda or t.dim() != 3 or tuple(t.shape[1:]) != (Hkv, d) or
-                not t.is_contiguous()):
-            raise OrthrosError(f"{nm} must be a contiguous bf16 CUDA tensor [P, Hkv, d]")
-    if v_prefix.shape != k_prefix.shape:
-        raise OrthrosError("k_prefix and v_prefix must have the same shape")
-    return k_prefix.shape[0]
+    P = k_prefix.shape[0]
+    _expect(k_prefix, "k_prefix", torch.bfloat16, (P, Hkv, d))
+    _expect(v_prefix, "v_prefix", torch.bfloat16, (P, Hkv, d))
+    return P
 
 
 def decode_prefix_workspace_size(B, P, L_max, Hq, Hkv, d) -> int:
@@ -632,23 +660,18 @@ def decode_step_prefix(q_new, qc_new, k_new, v_new, k_prefix, v_prefix, k_cache,
     """decode_step for a batch that shares the prompt prefix k_prefix, v_prefix [P, Hkv, d]: sequence
     b's rows are the prefix and then its own cache_len[b] rows of k_cache, v_cache
     [B, L_max, Hkv, d].  Returns (o, oc)."""
-    B, L_max, Hkv, d = k_cache.shape
-    for t, nm in ((k_cache, "k_cache"), (v_cache, "v_cache")):
-        if t.dtype != torch.bfloat16 or not t.is_cuda or t.shape != k_cache.shape or not t.is_contiguous():
-            raise OrthrosError(f"{nm} must be a contiguous bf16 CUDA tensor [B, L_max, Hkv, d]")
+    B, L_max, Hkv, d = shape = k_cache.shape
+    _expect(k_cache, "k_cache", torch.bfloat16, shape)
+    _expect(v_cache, "v_cache", torch.bfloat16, shape)
     P = _prefix_rows(k_prefix, v_prefix, Hkv, d)
-    o, oc, Hq = _decode_args(q_new, qc_new, k_new, v_new, cache_len, alpha, beta, alpha_c, beta_c, o, oc, B, Hkv, d,
-                             k_cache.device)
+    dev = _device_of(k_cache, "k_cache")
+    o, oc, Hq = _decode_args(q_new, qc_new, k_new, v_new, cache_len, (alpha, beta, alpha_c, beta_c), o, oc, B, Hkv, d)
     if workspace is None:
         workspace = decode_prefix_workspace(B, P, L_max, Hq, Hkv, d, k_cache.device)
-    with torch.cuda.device(k_cache.device):
-        st = lib().orthros_decode_step_prefix(_ptr(q_new), _ptr(qc_new), _ptr(k_new), _ptr(v_new), _ptr(k_prefix),
-                                              _ptr(v_prefix), P, _ptr(k_cache), _ptr(v_cache), _ptr(cache_len), L_max,
-                                              _ptr(alpha), _ptr(beta), _ptr(alpha_c), _ptr(beta_c), _ptr(o), _ptr(oc),
-                                              B, Hq, Hkv, d, int(window), _scale(scale, d), _ptr(workspace),
-                                              workspace.numel() * workspace.element_size(), _ptr(dev_err),
-                                              _stream(k_cache.device))
-    _check(st, "orthros_decode_step_prefix")
+    a = [_addr(t, dev) for t in (q_new, qc_new, k_new, v_new, k_prefix, v_prefix, k_cache, v_cache, cache_len, alpha,
+                                 beta, alpha_c, beta_c, o, oc, workspace, dev_err)]
+    _invoke("orthros_decode_step_prefix", dev, *a[:6], P, *a[6:9], L_max, *a[9:15], B, Hq, Hkv, d, int(window),
+            _scale(scale, d), a[15], workspace.nbytes, a[16])
     return o, oc
 
 
@@ -663,30 +686,23 @@ def xattn_prefix_fwd(qc_raw, pos, k_prefix, v_prefix, k, v, alpha_c, beta_c, sca
     [B, T_kv, Hkv, d].  qc_raw [B, T_out, Hq, d]; pos int32 [B, T_out]."""
     B, T_kv, Hkv, d = k.shape
     T_out, Hq = qc_raw.shape[1], qc_raw.shape[2]
-    qs = _bf16_rows(qc_raw, "qc_raw")
-    ks = _bf16_rows(k, "k")
-    if _bf16_rows(v, "v") != ks or v.shape != k.shape:
-        raise OrthrosError("k and v must have the same shape and strides")
-    if qc_raw.shape[0] != B or qc_raw.shape[3] != d:
+    ks = _kv_pair(k, v, B, Hkv, d)
+    if qc_raw.shape != (B, T_out, Hq, d):
         raise OrthrosError("qc_raw shape does not match k")
+    qs = _bf16_rows(qc_raw, "qc_raw")
     P = _prefix_rows(k_prefix, v_prefix, Hkv, d)
-    if pos.dtype != torch.int32 or tuple(pos.shape) != (B, T_out) or not pos.is_contiguous():
-        raise OrthrosError("pos must be a contiguous int32 tensor [B, T_out]")
-    _vec(alpha_c, "alpha_c", Hq, d)
-    _vec(beta_c, "beta_c", Hq, d)
+    _expect(pos, "pos", torch.int32, (B, T_out))
+    _expect(alpha_c, "alpha_c", torch.float32, (Hq, d))
+    _expect(beta_c, "beta_c", torch.float32, (Hq, d))
+    dev = _device_of(k, "k")
     if out is None:
         out = torch.empty((B, T_out, Hq, d), dtype=torch.bfloat16, device=k.device)
-    if tuple(out.shape) != (B, T_out, Hq, d):
+    elif out.shape != (B, T_out, Hq, d):
         raise OrthrosError("out shape does not match qc_raw")
-    os_ = _bf16_rows(out, "out")
     if workspace is None:
         workspace = torch.empty(max(xattn_prefix_workspace_size(B, T_out, P, T_kv, Hq, Hkv, d), 256),
                                 dtype=torch.uint8, device=k.device)
-    with torch.cuda.device(k.device):
-        st = lib().orthros_xattn_prefix_fwd(_ptr(qc_raw), _ptr(pos), _ptr(k_prefix), _ptr(v_prefix), P, _ptr(k),
-                                            _ptr(v), _ptr(alpha_c), _ptr(beta_c), _ptr(out), B, T_out, T_kv, Hq, Hkv,
-                                            d, _scale(scale, d), qs, ks, os_, _ptr(workspace),
-                                            workspace.numel() * workspace.element_size(), _ptr(dev_err),
-                                            _stream(k.device))
-    _check(st, "orthros_xattn_prefix_fwd")
+    a = [_addr(t, dev) for t in (qc_raw, pos, k_prefix, v_prefix, k, v, alpha_c, beta_c, out, workspace, dev_err)]
+    _invoke("orthros_xattn_prefix_fwd", dev, *a[:4], P, *a[4:9], B, T_out, T_kv, Hq, Hkv, d, _scale(scale, d), qs, ks,
+            _bf16_rows(out, "out"), a[9], workspace.nbytes, a[10])
     return out
