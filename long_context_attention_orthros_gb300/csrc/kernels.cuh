@@ -155,8 +155,8 @@ struct ServeParams {
     int32_t *cache_len;
     const float *alpha, *beta, *alpha_c, *beta_c;
     orthros_bf16 *o, *oc;
-    float *part_o;            // [2 * CTAs][G][D]
-    float2 *part_ml;          // [2 * CTAs][G]
+    float *part_o;            // [2 * CTAs (+ B * Hkv behind a prefix)][G][D]
+    float2 *part_ml;
     int *cnt_bh;              // [B * Hkv][2]
     int *cnt_all;
     float *pre_o;             // the prefix kernel's partials (prefix form)

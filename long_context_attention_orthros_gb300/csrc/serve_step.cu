@@ -10,11 +10,14 @@
 // is a run of 64-key blocks; laid end to end they form one list of W blocks, and CTA c of n takes
 // blocks floor(c W / n) .. floor((c + 1) W / n) - 1, whatever sequence they belong to: a ragged
 // batch loads every SM alike.  A CTA's blocks arrive by TMA through a ring that runs on across
-// segment borders (one producer warp), four warps take 16 keys of a block each, with the G query
+// segment borders (one producer warp); a segment counts a few places more than its blocks, for
+// what its start and end cost.  Four warps take 16 keys of a block each (or 32 of
+// every other block), with the G query
 // rows of a KV head on the MMA's N side, and their results meet in shared memory.  A segment that
 // one CTA holds whole is written out at once; otherwise each CTA writes one partial (max, sum,
-// o) and the last to arrive joins them (a counter, no spin).  Partials are bounded by the grid
-// (two a CTA: one segment can run in from the CTA before, one can run out), not by the batch.
+// o), goes on, and when it has run out of blocks counts itself in: the last to finish a segment
+// joins its partials (a counter, no spin).  Partials are bounded by the grid (two a CTA: one
+// segment can run in from the CTA before, one can run out).
 //
 // The block that holds row p is patched in shared memory by the warp that owns the rows: the
 // new row goes in, rows behind it (whatever the cache holds there) become zeros.  The last CTA
@@ -33,26 +36,51 @@ namespace orthros {
 
 constexpr int SERVE_CTAS = 304;  // two on each of 152 SMs
 
+// a segment whose partials have to be joined, kept until the CTA has run out of blocks
+struct Join {
+    int bh, base, c0, parts;  // own parts: CTAs c0 .. c0 + parts - 1
+    int last;                 // this CTA was the last of them to finish
+    int pad;
+};
+constexpr int MAX_JOINS = 32;
+
 template <int D, int G, int CODE>
 struct SvCfg {
     static constexpr bool Q8 = CODE >= 0;
     static constexpr int KB = 64;
     static constexpr int KV_BYTES = KB * D * (Q8 ? 1 : 2);
     static constexpr int SLAB = KB * 128;  // bf16: one 64-wide slab
-    static constexpr int SCR_ROWS = 4 * G;
-    static constexpr int SCR_BYTES = SCR_ROWS * (D + 3) * 4;  // four warps' o, max, sum, exponent
+    // A step of 16 keys is a chain of some 300 dependent instructions.  In the 8-bit form a warp
+    // takes 32 keys at once, two independent chains, and the warps take blocks by pairs.
+    static constexpr int KT = Q8 && G <= 8 ? 2 : 1;
+    static constexpr int CWARPS = 4;
+    static constexpr int GROUP = 4 / KT;  // warps that share a block
+    static constexpr int SCR_ROWS = CWARPS * G;
+    static constexpr int SCR_BYTES = SCR_ROWS * (D + 3) * 4;  // the warps' o, max, sum, exponent
     static constexpr int LIMIT = 112 * 1024 - 2048;            // two CTAs share an SM
-    static constexpr int FIT = (LIMIT - SCR_BYTES) / (2 * KV_BYTES + 2 * KB);
+    // a segment's queries, its alpha and beta and the new K and V row come through buffers of their
+    // own, as many segments ahead
+    static constexpr int HB = G <= 8 ? 2 : 1;
+    static constexpr int HDR_NEW = G * D * (2 + 4 + 4);
+    static constexpr int HDR_BYTES = HDR_NEW + 2 * D * 2;
+    static constexpr int FIT = (LIMIT - SCR_BYTES - HB * HDR_BYTES) / (2 * KV_BYTES + 2 * KB);
     static constexpr int STAGES = FIT < 2 ? 2 : (FIT > 8 ? 8 : FIT);
     static constexpr int EXP_OFF = STAGES * 2 * KV_BYTES;
-    static constexpr int SCR_OFF = EXP_OFF + STAGES * 2 * KB;
+    static constexpr int HDR_OFF = EXP_OFF + STAGES * 2 * KB;
+    static constexpr int SCR_OFF = HDR_OFF + HB * HDR_BYTES;
     static constexpr int BAR_OFF = SCR_OFF + SCR_BYTES;
-    static constexpr int FLAG_OFF = BAR_OFF + 2 * STAGES * 8;
+    static constexpr int JOIN_OFF = BAR_OFF + (2 * STAGES + 2 * HB) * 8;
+    static constexpr int FLAG_OFF = JOIN_OFF + MAX_JOINS * static_cast<int>(sizeof(Join));
     static constexpr int SMEM = FLAG_OFF + 16 + 1024;
-    static constexpr int CWARPS = 4;
+    static_assert(HDR_OFF % 16 == 0 && SCR_OFF % 16 == 0 && BAR_OFF % 8 == 0 && JOIN_OFF % 8 == 0, "alignment");
     static constexpr int CTHREADS = CWARPS * 32;
     static constexpr int THREADS = CTHREADS + 32;
 };
+
+// What a segment costs beside its blocks (its queries' loads, the warps' and the CTAs' joins), in
+// blocks: every segment begins with so many empty places in the list, so that a CTA with many
+// short segments gets fewer blocks.
+constexpr int SEG_COST = 4;
 
 // what a sequence's cache_len makes of it
 struct SeqPlan {
@@ -64,10 +92,10 @@ struct SeqPlan {
     int lo_p, lo;  // first prefix row and first own row of the window
 };
 
-__device__ __forceinline__ SeqPlan seq_plan(const ServeParams &p, int b)
+__device__ __forceinline__ SeqPlan seq_plan(const ServeParams &p, int len)
 {
     SeqPlan s;
-    s.p = __ldcg(p.cache_len + b);
+    s.p = len;
     s.full = s.p < 0 || s.p >= p.L_max;
     s.npb = s.pb0 = s.ob0 = s.lo_p = s.lo = 0;
     s.nc = s.nb = 1;
@@ -87,11 +115,12 @@ __device__ __forceinline__ SeqPlan seq_plan(const ServeParams &p, int b)
     return s;
 }
 
-// a position in the list of blocks: block r of segment (b, g, base)
+// a position in the list: place r of segment (b, g, base), which holds block r - SEG_COST
 struct Cursor {
     int b, g, base, r;
     SeqPlan s;
     __device__ __forceinline__ int blocks() const { return base ? s.nb : s.nc; }
+    __device__ __forceinline__ int places() const { return SEG_COST + blocks(); }
     __device__ __forceinline__ void next_segment(const ServeParams &p)
     {
         r = 0;
@@ -103,36 +132,47 @@ struct Cursor {
         if (++g == p.Hkv) {
             g = 0;
             if (++b < p.B)
-                s = seq_plan(p, b);
+                s = seq_plan(p, __ldcg(p.cache_len + b));
         }
     }
 };
 
-// Called by a whole warp: W, and the cursor of block `it0(W)`.
-__device__ __forceinline__ long long plan_total(const ServeParams &p)
+__device__ __forceinline__ long long seq_places(const ServeParams &p, int len)
 {
-    const int lane = threadIdx.x & 31;
-    long long w = 0;
-    for (int b = lane; b < p.B; b += 32) {
-        const SeqPlan s = seq_plan(p, b);
-        w += static_cast<long long>(s.nc + s.nb) * p.Hkv;
-    }
-#pragma unroll
-    for (int off = 16; off > 0; off >>= 1)
-        w += __shfl_xor_sync(0xffffffffu, w, off);
-    return w;
+    const SeqPlan s = seq_plan(p, len);
+    return static_cast<long long>(s.nc + s.nb + 2 * SEG_COST) * p.Hkv;
 }
 
-__device__ __forceinline__ Cursor plan_locate(const ServeParams &p, long long it)
+// Called by a whole warp: CTA c of at most n takes places it0 .. it1 - 1 of the list's W, and its
+// cursor stands at it0.  Up to 32 sequences the lengths are read once.
+struct Share {
+    long long W, n, it0, it1;
+    Cursor cur;
+};
+
+__device__ __forceinline__ Share plan_share(const ServeParams &p, long long c, long long n)
 {
     const int lane = threadIdx.x & 31;
-    Cursor c;
-    c.b = 0;
+    Share sh;
+    int len = lane < p.B ? __ldcg(p.cache_len + lane) : 0;
+    long long w = lane < p.B ? seq_places(p, len) : 0, W = w;
+    for (int b = lane + 32; b < p.B; b += 32)
+        W += seq_places(p, __ldcg(p.cache_len + b));
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1)
+        W += __shfl_xor_sync(0xffffffffu, W, off);
+    sh.W = W;
+    sh.n = n < W ? n : W;
+    sh.it0 = c < sh.n ? c * W / sh.n : W;
+    sh.it1 = c < sh.n ? (c + 1) * W / sh.n : W;
+    sh.cur = Cursor{};
+    if (sh.it0 >= sh.it1)
+        return sh;
+    long long it = sh.it0;
     for (int b0 = 0; b0 < p.B; b0 += 32) {
-        long long w = 0;
-        if (b0 + lane < p.B) {
-            const SeqPlan s = seq_plan(p, b0 + lane);
-            w = static_cast<long long>(s.nc + s.nb) * p.Hkv;
+        if (b0 > 0) {
+            len = b0 + lane < p.B ? __ldcg(p.cache_len + b0 + lane) : 0;
+            w = b0 + lane < p.B ? seq_places(p, len) : 0;
         }
         long long inc = w;
 #pragma unroll
@@ -145,18 +185,18 @@ __device__ __forceinline__ Cursor plan_locate(const ServeParams &p, long long it
         if (here != 0) {
             const int f = __ffs(here) - 1;
             it -= __shfl_sync(0xffffffffu, inc - w, f);
-            c.b = b0 + f;
+            sh.cur.b = b0 + f;
+            sh.cur.s = seq_plan(p, __shfl_sync(0xffffffffu, len, f));
             break;
         }
         it -= __shfl_sync(0xffffffffu, inc, 31);
     }
-    c.s = seq_plan(p, c.b);
-    const int per = c.s.nc + c.s.nb;
-    c.g = static_cast<int>(it / per);
-    c.r = static_cast<int>(it % per);
-    c.base = c.r >= c.s.nc;
-    c.r -= c.base ? c.s.nc : 0;
-    return c;
+    const int per = sh.cur.s.nc + sh.cur.s.nb + 2 * SEG_COST;
+    sh.cur.g = static_cast<int>(it / per);
+    sh.cur.r = static_cast<int>(it % per);
+    sh.cur.base = sh.cur.r >= sh.cur.s.nc + SEG_COST;
+    sh.cur.r -= sh.cur.base ? sh.cur.s.nc + SEG_COST : 0;
+    return sh;
 }
 
 struct ServeMaps {
@@ -177,6 +217,8 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
     const uint32_t sbase = raw_s + pad;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
     uint64_t *empty = full + C::STAGES;
+    uint64_t *hfull = empty + C::STAGES, *hempty = hfull + C::HB;
+    Join *joins = reinterpret_cast<Join *>(smem + C::JOIN_OFF);
     int *s_flag = reinterpret_cast<int *>(smem + C::FLAG_OFF);
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float NEG_INF = -__int_as_float(0x7f800000);
@@ -184,7 +226,11 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
-            mbar_init(&empty[s], C::CWARPS);
+            mbar_init(&empty[s], C::GROUP);
+        }
+        for (int s = 0; s < C::HB; ++s) {
+            mbar_init(&hfull[s], 1);
+            mbar_init(&hempty[s], C::CWARPS);
         }
         fence_barrier_init();
     }
@@ -194,13 +240,10 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     if constexpr (Q8)
         asm volatile("griddepcontrol.wait;" ::: "memory");
-    const long long W = plan_total(p);
-    const long long n = gridDim.x < W ? gridDim.x : W;  // CTAs with work (every one then has a block)
     const long long c = blockIdx.x;
-    const long long it0 = c < n ? c * W / n : W, it1 = c < n ? (c + 1) * W / n : W;
-    Cursor cur{};
-    if (it0 < it1)
-        cur = plan_locate(p, it0);
+    const Share sh = plan_share(p, c, gridDim.x);
+    const long long W = sh.W, n = sh.n, it0 = sh.it0, it1 = sh.it1;
+    Cursor cur = sh.cur;
     __syncthreads();  // barriers are set up, and every warp has read cache_len
 
     if (warp == C::CWARPS) {
@@ -208,14 +251,40 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
         if (lane != 0)
             return;
         long long i = 0;
-        for (long long it = it0; it < it1; ++it, ++i) {
+        int segs = 0;
+        bool header = true;
+        for (long long it = it0; it < it1; ++it) {
+            if (cur.r < SEG_COST) {
+                ++cur.r;
+                continue;
+            }
+            if (header) {  // the segment's queries
+                const int hb = segs % C::HB;
+                if (segs >= C::HB && !mbar_wait(&hempty[hb], static_cast<uint32_t>((segs / C::HB - 1) & 1))) {
+                    record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+                    return;
+                }
+                uint8_t *h = smem + C::HDR_OFF + hb * C::HDR_BYTES;
+                const long long go = static_cast<long long>(cur.g) * G * D;
+                mbar_arrive_expect_tx(&hfull[hb], C::HDR_BYTES);
+                bulk_load(h, (cur.base ? p.q_new : p.qc_new) + static_cast<long long>(cur.b) * p.Hq * D + go, G * D * 2,
+                          &hfull[hb]);
+                bulk_load(h + G * D * 2, (cur.base ? p.alpha : p.alpha_c) + go, G * D * 4, &hfull[hb]);
+                bulk_load(h + G * D * 6, (cur.base ? p.beta : p.beta_c) + go, G * D * 4, &hfull[hb]);
+                const long long no = (static_cast<long long>(cur.b) * p.Hkv + cur.g) * D;
+                bulk_load(h + C::HDR_NEW, p.k_new + no, D * 2, &hfull[hb]);
+                bulk_load(h + C::HDR_NEW + D * 2, p.v_new + no, D * 2, &hfull[hb]);
+                header = false;
+                ++segs;
+            }
             const int s = static_cast<int>(i % C::STAGES);
             if (i >= C::STAGES && !mbar_wait(&empty[s], static_cast<uint32_t>(((i / C::STAGES) - 1) & 1))) {
                 record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
                 return;
             }
-            const bool pre = cur.base && cur.r < cur.s.npb;
-            const int blk = cur.base ? (pre ? cur.s.pb0 + cur.r : cur.s.ob0 + cur.r - cur.s.npb) : cur.r;
+            const int r = cur.r - SEG_COST;
+            const bool pre = cur.base && r < cur.s.npb;
+            const int blk = cur.base ? (pre ? cur.s.pb0 + r : cur.s.ob0 + r - cur.s.npb) : r;
             const int j0 = blk * C::KB;
             uint8_t *dst = smem + s * 2 * C::KV_BYTES;
             if constexpr (Q8) {
@@ -237,8 +306,11 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
                     tma_load_4d(dst + C::KV_BYTES + sl * C::SLAB, mv, &full[s], sl * 64, cur.g, j0, bb);
                 }
             }
-            if (++cur.r == cur.blocks() && it + 1 < it1)
+            ++i;
+            if (++cur.r == cur.places() && it + 1 < it1) {
                 cur.next_segment(p);
+                header = true;
+            }
         }
         return;
     }
@@ -248,37 +320,151 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
     float *os = reinterpret_cast<float *>(smem + C::SCR_OFF);  // [CWARPS][G][D]
     float *ms = os + C::CWARPS * G * D, *ls = ms + C::CWARPS * G;
     int *es = reinterpret_cast<int *>(ls + C::CWARPS * G);
-    bool ok = true, joined_prefix = false, bad = false;
+    bool ok = true, bad = false;
     long long i = 0;
-    for (long long it = it0; it < it1;) {
-        const int b = cur.b, g = cur.g, seg_blocks = cur.blocks();
-        const SeqPlan sp = cur.s;
-        const int m = static_cast<int>(seg_blocks - cur.r < it1 - it ? seg_blocks - cur.r : it1 - it);
-        const orthros_bf16 *q = (cur.base ? p.q_new : p.qc_new) + (static_cast<long long>(b) * p.Hq + g * G) * D;
-        const float *al = (cur.base ? p.alpha : p.alpha_c) + g * G * D, *be = (cur.base ? p.beta : p.beta_c) + g * G * D;
-        typename std::conditional<Q8, WarpQ8<D, NT, Q8 ? CODE : 0>, WarpKeys16<D, NT, false>>::type st;
-        if constexpr (Q8) {
-            st.load_q(q, al, be, G, p.qscale);
-        } else {
-#pragma unroll
-            for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                for (int kt = 0; kt < D / 16; ++kt)
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const int row = 8 * nt + (lane >> 2);
-                        uint32_t hi = 0, lo = 0;
-                        if (row < G)
-                            load_q_pair(q + row * D, al + row * D, be + row * D, kt * 16 + 2 * (lane & 3) + 8 * hf,
-                                        p.qscale, hi, lo);
-                        st.qb[nt][kt][hf] = hi;
-                        st.ql[nt][kt][hf] = lo;
-                    }
+    int segs = 0, njoin = 0;
+    // Joins the segments on the list: each counts this CTA in (after its partials: the barrier orders
+    // them before the fence), and those that it was the last to finish are joined, a warp a row.
+    // At the end of the CTA's work only, so that no wait for memory stands between two segments.
+    auto join_all = [&](bool final) {
+        named_barrier(1, C::CTHREADS);
+        if (t < njoin) {
+            Join &j = joins[t];
+            int *cnt = p.cnt_bh + 2LL * j.bh + j.base;
+            __threadfence();
+            const int last = j.parts == 1 || atomicAdd(cnt, 1) == j.parts - 1;
+            __threadfence();
+            j.last = last;
+            if (last)
+                *cnt = 0;
         }
+        if (final && t == C::CTHREADS - 1)  // every warp of this CTA has read cache_len for the last time
+            s_flag[0] = atomicAdd(p.cnt_all, 1) == static_cast<int>(gridDim.x) - 1;
+        if constexpr (!Q8) {
+            // the prefix kernel's partials; and the step has ended only when that kernel has
+            asm volatile("griddepcontrol.wait;" ::: "memory");
+        }
+        named_barrier(1, C::CTHREADS);
+        const long long BH = static_cast<long long>(p.B) * p.Hkv;
+        for (int x = warp; x < njoin * G; x += C::CWARPS) {
+            const Join j = joins[x / G];
+            const int row = x % G;
+            if (!j.last)
+                continue;
+            // parts: the CTAs' own, then (a copy behind a prefix) the prefix splits'
+            const int nq = j.parts + (!Q8 && !j.base ? p.n_part : 0);
+            auto slot_of = [&](int q) -> long long {
+                return q < j.parts ? (j.parts == 1 ? 2LL * gridDim.x + j.bh : 2LL * (j.c0 + q) + (q == 0 ? 1 : 0)) * G + row
+                                   : ((q - j.parts) * BH + j.bh) * G + row;
+            };
+            auto ml_of = [&](int q) -> float2 {
+                return q >= nq ? make_float2(NEG_INF, 0.f) : __ldcg((q < j.parts ? p.part_ml : p.pre_ml) + slot_of(q));
+            };
+            const float2 ml0 = ml_of(lane);
+            float M = ml0.x, L = 0.f;
+            for (int q = lane + 32; q < nq; q += 32)
+                M = fmaxf(M, ml_of(q).x);
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+            constexpr int E = D / 32;
+            float a[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                a[e] = 0.f;
+            for (int q0 = 0; q0 < nq; q0 += 32) {
+                const float2 ml = q0 == 0 ? ml0 : ml_of(q0 + lane);
+                const float w = ml.x == NEG_INF ? 0.f : fast_exp2(ml.x - M);
+                L += w * ml.y;
+                const int nn = min(32, nq - q0);
+#pragma unroll 16
+                for (int k = 0; k < nn; ++k) {
+                    const float wk = __shfl_sync(0xffffffffu, w, k);
+                    const float *src = (q0 + k < j.parts ? p.part_o : p.pre_o) + slot_of(q0 + k) * D + lane * E;
+                    if constexpr (E == 4) {
+                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(src));
+                        a[0] = fmaf(wk, y.x, a[0]);
+                        a[1] = fmaf(wk, y.y, a[1]);
+                        a[2] = fmaf(wk, y.z, a[2]);
+                        a[3] = fmaf(wk, y.w, a[3]);
+                    } else {
+                        const float2 y = __ldcg(reinterpret_cast<const float2 *>(src));
+                        a[0] = fmaf(wk, y.x, a[0]);
+                        a[1] = fmaf(wk, y.y, a[1]);
+                    }
+                }
+            }
+#pragma unroll
+            for (int off = 16; off > 0; off >>= 1)
+                L += __shfl_xor_sync(0xffffffffu, L, off);
+            const float inv = L > 0.f ? 1.f / L : 0.f;
+            orthros_bf16 *orow = (j.base ? p.o : p.oc) +
+                                 (static_cast<long long>(j.bh / p.Hkv) * p.Hq + (j.bh % p.Hkv) * G + row) * D + lane * E;
+#pragma unroll
+            for (int e = 0; e < E; e += 2)
+                *reinterpret_cast<uint32_t *>(orow + e) = pack_bf16x2(a[e] * inv, a[e + 1] * inv);
+        }
+        njoin = 0;
+        named_barrier(1, C::CTHREADS);  // the list may be filled again
+    };
+    for (long long it = it0; it < it1;) {
+        const int b = cur.b, g = cur.g, seg_places = cur.places();
+        const SeqPlan sp = cur.s;
+        const int places = static_cast<int>(seg_places - cur.r < it1 - it ? seg_places - cur.r : it1 - it);
+        const int first = max(cur.r - SEG_COST, 0), m = cur.r + places - SEG_COST - first;  // blocks first .. first + m - 1
+        if (m <= 0) {  // the CTA's last places are a segment's empty ones
+            it += places;
+            continue;
+        }
+        typename std::conditional<Q8, WarpQ8<D, NT, Q8 ? CODE : 0>, WarpKeys16<D, NT, false>>::type st;
+        {
+            const int hb = segs % C::HB;
+            if (ok && !mbar_wait(&hfull[hb], static_cast<uint32_t>((segs / C::HB) & 1)))
+                ok = false;
+            const orthros_bf16 *q = reinterpret_cast<const orthros_bf16 *>(smem + C::HDR_OFF + hb * C::HDR_BYTES);
+            const float *al = reinterpret_cast<const float *>(q + G * D), *be = al + G * D;
+            if constexpr (Q8) {
+                st.load_q(q, al, be, G, p.qscale);
+            } else {
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                    for (int kt = 0; kt < D / 16; ++kt)
+#pragma unroll
+                        for (int hf = 0; hf < 2; ++hf) {
+                            const int row = 8 * nt + (lane >> 2), d = row * D + kt * 16 + 2 * (lane & 3) + 8 * hf;
+                            uint32_t hi = 0, lo = 0;
+                            if (row < G) {
+                                const float2 x = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(q + d));
+                                const float2 a = *reinterpret_cast<const float2 *>(al + d);
+                                const float2 c2 = *reinterpret_cast<const float2 *>(be + d);
+                                split_q_pair(fmaf(x.x, a.x, c2.x) * p.qscale, fmaf(x.y, a.y, c2.y) * p.qscale, hi, lo);
+                            }
+                            st.qb[nt][kt][hf] = hi;
+                            st.ql[nt][kt][hf] = lo;
+                        }
+            }
+        }
+        // the new rows as this lane takes them: lanes 0 .. 15 of K's, 16 .. 31 of V's, D / 16 values each
+        const int kv = lane >> 4;
+        uint32_t fresh_w[D / 32];
+        {
+            const uint32_t *src = reinterpret_cast<const uint32_t *>(smem + C::HDR_OFF + (segs % C::HB) * C::HDR_BYTES +
+                                                                     C::HDR_NEW) + lane * (D / 32);
+#pragma unroll
+            for (int e = 0; e < D / 32; ++e)
+                fresh_w[e] = src[e];
+        }
+        __syncwarp();
+        if (lane == 0)
+            mbar_arrive(&hempty[segs % C::HB]);
+        ++segs;
         st.reset();
         for (int x = 0; x < m; ++x, ++i) {
+            if (C::KT == 2 && (i & 1) != (warp >> 1))
+                continue;  // the other pair's block
             const int s = static_cast<int>(i % C::STAGES);
-            const int r = cur.r + x;
+            const int r = first + x;
             const bool pre = cur.base && r < sp.npb;
             const int blk = cur.base ? (pre ? sp.pb0 + r : sp.ob0 + r - sp.npb) : r;
             // the block's rows that count: lo .. hi
@@ -286,90 +472,86 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
             const int hi = (pre ? p.P - 1 : sp.p) - blk * C::KB;
             if (ok && !mbar_wait(&full[s], static_cast<uint32_t>((i / C::STAGES) & 1)))
                 ok = false;
-            const int r0 = warp * 16;
-            if (ok && !sp.full && r0 <= hi && r0 + 15 >= lo) {
+            constexpr int WK = 16 * C::KT;  // this warp's keys: rows r0 .. r0 + WK - 1 of the block
+            const int r0 = (warp % C::GROUP) * WK;
+            if (ok && !sp.full && r0 <= hi && r0 + WK - 1 >= lo) {
                 uint8_t *kb = smem + s * 2 * C::KV_BYTES, *vb = kb + C::KV_BYTES;
                 int8_t *ke = reinterpret_cast<int8_t *>(smem + C::EXP_OFF + s * 2 * C::KB), *ve = ke + C::KB;
-                const bool whole = lo <= r0 && r0 + 15 < (pre ? hi + 1 : hi);  // row p itself is patched in
+                const bool whole = lo <= r0 && r0 + WK - 1 < (pre ? hi + 1 : hi);  // row p itself is patched in
                 if (!whole) {
                     // V rows that do not count become zeros (their weight is zero, but they may hold
                     // anything), and the new row is put where it belongs
-                    for (int rr = r0; rr < r0 + 16; ++rr) {
-                        const bool fresh = !pre && rr == hi;
-                        if (rr >= lo && rr <= hi && !fresh)
+                    constexpr int CH = D * (Q8 ? 1 : 2) / 16;  // 16-byte chunks of a row
+#pragma unroll 1
+                    for (int e = lane; e < WK * CH; e += 32) {
+                        const int rr = r0 + e / CH, c16 = e % CH;
+                        if (rr >= lo && rr <= hi)
                             continue;
+                        uint8_t *to;
                         if constexpr (Q8) {
-                            if (!fresh) {
-                                if (lane < D / 16)
-                                    *reinterpret_cast<uint4 *>(vb + q8_offset<D>(rr, lane)) = make_uint4(0, 0, 0, 0);
-                                if (lane == 0)
-                                    ve[rr] = -127;
-                                continue;
+                            to = vb + q8_offset<D>(rr, c16);
+                            if (c16 == 0)
+                                ve[rr] = -127;
+                        } else {
+                            to = vb + (c16 / 8) * C::SLAB + sw128_offset(rr, c16 % 8);
+                        }
+                        *reinterpret_cast<uint4 *>(to) = make_uint4(0, 0, 0, 0);
+                    }
+                    if (!pre && hi >= r0 && hi < r0 + WK) {
+                        const long long row = (static_cast<long long>(b) * p.L_max + sp.p) * p.Hkv + g;
+                        if constexpr (Q8) {
+                            constexpr int E = D / 16;
+                            float f[E], amax = 0.f;
+#pragma unroll
+                            for (int e = 0; e < E; ++e) {
+                                const float2 two = unpack_bf16x2(fresh_w[e / 2]);
+                                f[e] = (e & 1) ? two.y : two.x;
+                                if (fabsf(f[e]) < __int_as_float(0x7f800000))
+                                    amax = fmaxf(amax, fabsf(f[e]));
+                                else
+                                    bad = true;
                             }
 #pragma unroll
-                            for (int kv = 0; kv < 2; ++kv) {
-                                // lane l holds values E l .. E l + E - 1
-                                constexpr int E = D / 32;
-                                const orthros_bf16 *src =
-                                    (kv ? p.v_new : p.k_new) + (static_cast<long long>(b) * p.Hkv + g) * D + E * lane;
-                                float f[E], amax = 0.f;
+                            for (int off = 8; off > 0; off >>= 1)
+                                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+                            const int ex = q8_exponent<Q8 ? CODE : 0>(amax);
+                            const float sd = q8_pow2(-ex);
+                            uint32_t w[E / 4];
 #pragma unroll
-                                for (int e = 0; e < E; ++e) {
-                                    f[e] = __uint_as_float(static_cast<uint32_t>(src[e]) << 16);
-                                    if (fabsf(f[e]) < __int_as_float(0x7f800000))
-                                        amax = fmaxf(amax, fabsf(f[e]));
-                                    else
-                                        bad = true;
-                                }
+                            for (int e = 0; e < E; e += 4)
+                                w[e / 4] = q8_codes2<Q8 ? CODE : 0>(f[e] * sd, f[e + 1] * sd) |
+                                           q8_codes2<Q8 ? CODE : 0>(f[e + 2] * sd, f[e + 3] * sd) << 16;
+                            const int d = E * (lane & 15);
+                            uint8_t *to = (kv ? vb : kb) + q8_offset<D>(hi, d / 16) + d % 16;
+                            uint8_t *cache = static_cast<uint8_t *>(kv ? p.v_cache : p.k_cache) + row * D + d;
 #pragma unroll
-                                for (int off = 16; off > 0; off >>= 1)
-                                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-                                const int ex = q8_exponent<Q8 ? CODE : 0>(amax);
-                                const float sd = q8_pow2(-ex);
-                                uint32_t w[E / 2];
-#pragma unroll
-                                for (int e = 0; e < E; e += 2)
-                                    w[e / 2] = q8_codes2<Q8 ? CODE : 0>(f[e] * sd, f[e + 1] * sd);
-                                uint8_t *to = (kv ? vb : kb) + q8_offset<D>(rr, E * lane / 16) + E * lane % 16;
-                                uint8_t *cache = static_cast<uint8_t *>(kv ? p.v_cache : p.k_cache) +
-                                                 ((static_cast<long long>(b) * p.L_max + sp.p) * p.Hkv + g) * D + E * lane;
-#pragma unroll
-                                for (int e = 0; e < E / 2; ++e) {
-                                    reinterpret_cast<uint16_t *>(to)[e] = static_cast<uint16_t>(w[e]);
-                                    if (!cur.base)
-                                        reinterpret_cast<uint16_t *>(cache)[e] = static_cast<uint16_t>(w[e]);
-                                }
-                                if (lane == 0) {
-                                    (kv ? ve : ke)[rr] = static_cast<int8_t>(ex);
-                                    if (!cur.base)
-                                        (kv ? p.v_exp : p.k_exp)[(static_cast<long long>(b) * p.Hkv + g) * p.L_max +
-                                                                 sp.p] = static_cast<int8_t>(ex);
-                                }
+                            for (int e = 0; e < E / 4; ++e) {
+                                reinterpret_cast<uint32_t *>(to)[e] = w[e];
+                                if (!cur.base)
+                                    reinterpret_cast<uint32_t *>(cache)[e] = w[e];
+                            }
+                            if ((lane & 15) == 0) {
+                                (kv ? ve : ke)[hi] = static_cast<int8_t>(ex);
+                                if (!cur.base)
+                                    (kv ? p.v_exp : p.k_exp)[(static_cast<long long>(b) * p.Hkv + g) * p.L_max + sp.p] =
+                                        static_cast<int8_t>(ex);
                             }
                         } else {
-                            const int sl = lane / 8, c8 = lane % 8;  // 16-byte chunk of the row
-                            if (lane < D / 8) {
-                                const long long off = (static_cast<long long>(b) * p.Hkv + g) * D + lane * 8;
-                                uint4 kn = make_uint4(0, 0, 0, 0), vn = kn;
-                                if (fresh) {
-                                    kn = *reinterpret_cast<const uint4 *>(p.k_new + off);
-                                    vn = *reinterpret_cast<const uint4 *>(p.v_new + off);
-                                    *reinterpret_cast<uint4 *>(kb + sl * C::SLAB + sw128_offset(rr, c8)) = kn;
-                                    if (!cur.base) {
-                                        const long long row =
-                                            ((static_cast<long long>(b) * p.L_max + sp.p) * p.Hkv + g) * D + lane * 8;
-                                        *reinterpret_cast<uint4 *>(static_cast<orthros_bf16 *>(p.k_cache) + row) = kn;
-                                        *reinterpret_cast<uint4 *>(static_cast<orthros_bf16 *>(p.v_cache) + row) = vn;
-                                    }
-                                }
-                                *reinterpret_cast<uint4 *>(vb + sl * C::SLAB + sw128_offset(rr, c8)) = vn;
+                            const int d = (D / 16) * (lane & 15);
+                            uint8_t *to = (kv ? vb : kb) + (d / 64) * C::SLAB + sw128_offset(hi, d % 64 / 8) + d % 8 * 2;
+                            orthros_bf16 *cache = static_cast<orthros_bf16 *>(kv ? p.v_cache : p.k_cache) + row * D + d;
+#pragma unroll
+                            for (int e = 0; e < D / 32; ++e) {
+                                reinterpret_cast<uint32_t *>(to)[e] = fresh_w[e];
+                                if (!cur.base)
+                                    reinterpret_cast<uint32_t *>(cache)[e] = fresh_w[e];
                             }
                         }
                     }
                     __syncwarp();
                 }
                 if constexpr (Q8) {
-                    st.step(kb, vb, ke, ve, r0, whole, lo, hi);
+                    st.template step<C::KT>(kb, vb, ke, ve, r0, whole, lo, hi);
                 } else {
                     const uint32_t ks = sbase + s * 2 * C::KV_BYTES;
                     int lim[NT][2];
@@ -415,11 +597,13 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
             }
         named_barrier(1, C::CTHREADS);
         // segment bounds in the list, and who else has a share
-        const long long s0 = it - cur.r, s1 = s0 + seg_blocks;
+        const long long s0 = it - cur.r + SEG_COST, s1 = it - cur.r + seg_places;
         const long long c0 = ((s0 + 1) * n - 1) / W, c1 = (s1 * n - 1) / W;  // owners of its first and last block
         const bool joins_prefix = !Q8 && !cur.base && !sp.full;
         const bool alone = c0 == c1 && !joins_prefix;
-        const long long slot = 2 * c + (c == c0 ? 1 : 0);  // a segment that began before this CTA: slot 0
+        // one slot for a segment that began before this CTA, one for one that runs out of it, and one
+        // for each copy that only the prefix has to be joined with
+        const long long slot = c0 == c1 ? 2LL * gridDim.x + static_cast<long long>(b) * p.Hkv + g : 2 * c + (c == c0 ? 1 : 0);
         orthros_bf16 *out = (cur.base ? p.o : p.oc) + (static_cast<long long>(b) * p.Hq + g * G) * D;
         for (int e = t; e < G * (D / 4); e += C::CTHREADS) {
             const int row = e / (D / 4), d4 = 4 * (e % (D / 4));
@@ -456,104 +640,22 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
         if (sp.full && !cur.base && g == 0 && t == 0)
             record_error(p.dev_err, ORTHROS_DEVERR_CACHE_FULL);
         if (!alone) {
-            int *cnt = p.cnt_bh + (static_cast<long long>(b) * p.Hkv + g) * 2 + cur.base;
-            __threadfence();
-            named_barrier(1, C::CTHREADS);
             if (t == 0)
-                s_flag[0] = c0 == c1 || atomicAdd(cnt, 1) == static_cast<int>(c1 - c0);
-            named_barrier(1, C::CTHREADS);
-            if (s_flag[0]) {
-                __threadfence();
-                if (t == 0)
-                    *cnt = 0;
-                if (joins_prefix && !joined_prefix) {
-                    asm volatile("griddepcontrol.wait;" ::: "memory");
-                    joined_prefix = true;
-                }
-                // part q: own partials c0 .. c1, then the prefix splits
-                const int nown = static_cast<int>(c1 - c0) + 1, nq = nown + (joins_prefix ? p.n_part : 0);
-                const long long BH = static_cast<long long>(p.B) * p.Hkv;
-                for (int row = warp; row < G; row += C::CWARPS) {
-                    auto index = [&](int qi) -> long long {
-                        return qi < nown ? (2 * (c0 + qi) + (qi == 0 ? 1 : 0)) * G + row : 0;
-                    };
-                    auto prefix_index = [&](int qi) -> long long {
-                        return (static_cast<long long>(qi - nown) * BH + static_cast<long long>(b) * p.Hkv + g) * G + row;
-                    };
-                    auto ml_of = [&](int qi) -> float2 {
-                        return qi < nown ? __ldcg(p.part_ml + index(qi)) : __ldcg(p.pre_ml + prefix_index(qi));
-                    };
-                    float M = NEG_INF, L = 0.f;
-                    for (int qi = lane; qi < nq; qi += 32)
-                        M = fmaxf(M, ml_of(qi).x);
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1)
-                        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-                    constexpr int E = D / 32;
-                    float a[E];
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        a[e] = 0.f;
-                    for (int q0 = 0; q0 < nq; q0 += 32) {
-                        float w = 0.f;
-                        if (q0 + lane < nq) {
-                            const float2 ml = ml_of(q0 + lane);
-                            w = ml.x == NEG_INF ? 0.f : fast_exp2(ml.x - M);
-                            L += w * ml.y;
-                        }
-                        const int nn = min(32, nq - q0);
-#pragma unroll 8
-                        for (int k = 0; k < nn; ++k) {
-                            const float wk = __shfl_sync(0xffffffffu, w, k);
-                            const int qi = q0 + k;
-                            const float *src =
-                                (qi < nown ? p.part_o + index(qi) * D : p.pre_o + prefix_index(qi) * D) + lane * E;
-                            if constexpr (E == 4) {
-                                const float4 y = __ldcg(reinterpret_cast<const float4 *>(src));
-                                a[0] = fmaf(wk, y.x, a[0]);
-                                a[1] = fmaf(wk, y.y, a[1]);
-                                a[2] = fmaf(wk, y.z, a[2]);
-                                a[3] = fmaf(wk, y.w, a[3]);
-                            } else {
-                                const float2 y = __ldcg(reinterpret_cast<const float2 *>(src));
-                                a[0] = fmaf(wk, y.x, a[0]);
-                                a[1] = fmaf(wk, y.y, a[1]);
-                            }
-                        }
-                    }
-#pragma unroll
-                    for (int off = 16; off > 0; off >>= 1)
-                        L += __shfl_xor_sync(0xffffffffu, L, off);
-                    const float inv = L > 0.f ? 1.f / L : 0.f;
-#pragma unroll
-                    for (int e = 0; e < E; e += 2)
-                        *reinterpret_cast<uint32_t *>(out + row * D + lane * E + e) =
-                            pack_bf16x2(a[e] * inv, a[e + 1] * inv);
-                }
-            }
+                joins[njoin] = {b * p.Hkv + g, cur.base, static_cast<int>(c0), static_cast<int>(c1 - c0) + 1, 0, 0};
+            if (++njoin == MAX_JOINS)
+                join_all(false);
         }
-        it += m;
-        cur.r += m;
-        if (cur.r == seg_blocks && it < it1)
+        it += places;
+        cur.r += places;
+        if (cur.r == seg_places && it < it1)
             cur.next_segment(p);
-    }
-    if constexpr (!Q8) {
-        // the step has ended only when the prefix kernel has, whether or not a partial was joined
-        if (!joined_prefix)
-            asm volatile("griddepcontrol.wait;" ::: "memory");
     }
     if (bad)
         record_error(p.dev_err, ORTHROS_DEVERR_RANGE);
     if (!ok && lane == 0)
         record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
-
-    // ---- the last CTA of the grid advances the lengths (every one has read them by now)
-    named_barrier(1, C::CTHREADS);
-    if (t == 0) {
-        __threadfence();
-        s_flag[0] = atomicAdd(p.cnt_all, 1) == static_cast<int>(gridDim.x) - 1;
-    }
-    named_barrier(1, C::CTHREADS);
+    join_all(true);
+    // the last CTA of the grid advances the lengths: every one has read them by now
     if (s_flag[0]) {
         for (int b = t; b < p.B; b += C::CTHREADS) {
             const int len = __ldcg(p.cache_len + b);
@@ -580,7 +682,7 @@ static ServeLayout serve_layout(int B, int P, int L_max, int Hq, int Hkv, int D)
     ServeLayout l;
     l.ctas = static_cast<int>(most < SERVE_CTAS ? most : SERVE_CTAS);
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
-    const size_t slots = 2 * static_cast<size_t>(l.ctas) * G;
+    const size_t slots = (2 * static_cast<size_t>(l.ctas) + (P > 0 ? BH : 0)) * G;
     l.part_ml = up(slots * D * sizeof(float));
     l.cnt = l.part_ml + up(slots * sizeof(float2));
     l.pre_o = l.cnt + up((2 * BH + 1) * sizeof(int));

@@ -1,5 +1,5 @@
-// warp_q8.cuh -- a warp's online softmax over 16 keys at a time of an 8-bit cache, for up to
-// 8 * NT query rows that share one KV head, on warp MMAs in fp16:
+// warp_q8.cuh -- a warp's online softmax over 16 or 32 keys at a time of an 8-bit cache, for up
+// to 8 * NT query rows that share one KV head, on warp MMAs in fp16:
 //   S^T = K q^T (16 keys x rows),  O^T += V^T P^T.
 // Codes turn into fp16 in registers (exactly), so shared memory is read once, 16 bytes a lane:
 // the order of d inside an MMA's k (and m) is free as long as both operands agree, and a lane
@@ -67,7 +67,7 @@ struct WarpQ8 {
         E = -256;
     }
 
-    // query rows row0 .. of x [rows][D] with the scale-offset; rows at or beyond n are zeros
+    // query rows of x [n][D] with the scale-offset (all three in shared memory); rows from n on are zeros
     __device__ __forceinline__ void load_q(const orthros_bf16 *x, const float *alpha, const float *beta, int n,
                                            float qscale)
     {
@@ -84,8 +84,8 @@ struct WarpQ8 {
                     f[s][i] = 0.f;
                 if (row < n) {
                     const uint2 u = *reinterpret_cast<const uint2 *>(x + row * D + d);
-                    const float4 al = __ldg(reinterpret_cast<const float4 *>(alpha + row * D + d));
-                    const float4 be = __ldg(reinterpret_cast<const float4 *>(beta + row * D + d));
+                    const float4 al = *reinterpret_cast<const float4 *>(alpha + row * D + d);
+                    const float4 be = *reinterpret_cast<const float4 *>(beta + row * D + d);
                     const float2 a = unpack_bf16x2(u.x), b = unpack_bf16x2(u.y);
                     f[s][0] = fmaf(a.x, al.x, be.x) * qscale;
                     f[s][1] = fmaf(a.y, al.y, be.y) * qscale;
@@ -114,77 +114,91 @@ struct WarpQ8 {
         }
     }
 
-    // Keys at rows r0 .. r0 + 15 of the staged block (K codes at kb, V codes at vb, both exponents
-    // in shared memory).  Unless whole, only rows lo .. hi of the block count; V rows that do not
-    // count must hold finite codes and an exponent no larger than the others'.
+    // Keys at rows r0 .. r0 + 16 KT - 1 of the staged block (K codes at kb, V codes at vb, both
+    // exponents in shared memory).  Unless whole, only rows lo .. hi of the block count; V rows
+    // that do not count must hold finite codes and an exponent no larger than the others'.
+    template <int KT>
     __device__ __forceinline__ void step(const uint8_t *kb, const uint8_t *vb, const int8_t *ke, const int8_t *ve, int r0,
                                          bool whole, int lo, int hi)
     {
         const int lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
         const float NEG_INF = -__int_as_float(0x7f800000);
-        uint4 ka[D / 64], kc[D / 64];
+        uint4 ka[KT][D / 64], kc[KT][D / 64];
+        float kf[KT][2];
+        int v[KT][2], vmax = -256;
 #pragma unroll
-        for (int c = 0; c < D / 64; ++c) {
-            ka[c] = *reinterpret_cast<const uint4 *>(kb + q8_offset<D>(r0 + gq, t + 4 * c));
-            kc[c] = *reinterpret_cast<const uint4 *>(kb + q8_offset<D>(r0 + gq + 8, t + 4 * c));
+        for (int j = 0; j < KT; ++j) {
+#pragma unroll
+            for (int c = 0; c < D / 64; ++c) {
+                ka[j][c] = *reinterpret_cast<const uint4 *>(kb + q8_offset<D>(r0 + 16 * j + gq, t + 4 * c));
+                kc[j][c] = *reinterpret_cast<const uint4 *>(kb + q8_offset<D>(r0 + 16 * j + gq + 8, t + 4 * c));
+            }
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                kf[j][i] = q8_pow2(ke[r0 + 16 * j + gq + 8 * i]);
+                v[j][i] = ve[r0 + 16 * j + gq + 8 * i];
+                vmax = max(vmax, v[j][i]);
+            }
         }
-        const float kf[2] = {q8_pow2(ke[r0 + gq]), q8_pow2(ke[r0 + gq + 8])};
-        const int v0 = ve[r0 + gq], v1 = ve[r0 + gq + 8];
-        float s[NT][4], s2[NT][4];
+        float s[KT][NT][4], s2[KT][NT][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                s[nt][e] = s2[nt][e] = 0.f;
-#pragma unroll
-        for (int k = 0; k < D / 16; ++k) {
-            const uint4 ua = ka[k >> 2], uc = kc[k >> 2];
-            const uint32_t wa = (k & 3) == 0 ? ua.x : (k & 3) == 1 ? ua.y : (k & 3) == 2 ? ua.z : ua.w;
-            const uint32_t wc = (k & 3) == 0 ? uc.x : (k & 3) == 1 ? uc.y : (k & 3) == 2 ? uc.z : uc.w;
-            const uint32_t a[4] = {q8_half2<CODE>(wa, false), q8_half2<CODE>(wc, false), q8_half2<CODE>(wa, true),
-                                   q8_half2<CODE>(wc, true)};
+        for (int j = 0; j < KT; ++j)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt)
-                mma_16816_f16((k & 1) ? s2[nt] : s[nt], a, qb[nt][k][0], qb[nt][k][1]);
-        }
-        // s[nt][e]: key gq + 8 (e >> 1), row 8 nt + 2 t + (e & 1)
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    s[j][nt][e] = s2[j][nt][e] = 0.f;
+#pragma unroll
+        for (int k = 0; k < D / 16; ++k)
+#pragma unroll
+            for (int j = 0; j < KT; ++j) {
+                const uint4 ua = ka[j][k >> 2], uc = kc[j][k >> 2];
+                const uint32_t wa = (k & 3) == 0 ? ua.x : (k & 3) == 1 ? ua.y : (k & 3) == 2 ? ua.z : ua.w;
+                const uint32_t wc = (k & 3) == 0 ? uc.x : (k & 3) == 1 ? uc.y : (k & 3) == 2 ? uc.z : uc.w;
+                const uint32_t a[4] = {q8_half2<CODE>(wa, false), q8_half2<CODE>(wc, false), q8_half2<CODE>(wa, true),
+                                       q8_half2<CODE>(wc, true)};
+#pragma unroll
+                for (int nt = 0; nt < NT; ++nt)
+                    mma_16816_f16((k & 1) ? s2[j][nt] : s[j][nt], a, qb[nt][k][0], qb[nt][k][1]);
+            }
+        // s[j][nt][e]: key 16 j + gq + 8 (e >> 1), row 8 nt + 2 t + (e & 1)
         bool raise = false;
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
+        for (int j = 0; j < KT; ++j)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                s[nt][e] = (s[nt][e] + s2[nt][e]) * qf[nt][e & 1] * kf[e >> 1];
-                if (!whole) {
-                    const int j = r0 + gq + 8 * (e >> 1);
-                    if (j < lo || j > hi)
-                        s[nt][e] = NEG_INF;
+            for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    s[j][nt][e] = (s[j][nt][e] + s2[j][nt][e]) * qf[nt][e & 1] * kf[j][e >> 1];
+                    if (!whole) {
+                        const int x = r0 + 16 * j + gq + 8 * (e >> 1);
+                        if (x < lo || x > hi)
+                            s[j][nt][e] = NEG_INF;
+                    }
+                    raise |= s[j][nt][e] > m[nt][e & 1] + 8.f;
                 }
-                raise |= s[nt][e] > m[nt][e & 1] + 8.f;
-            }
-        // the largest V exponent met so far
-        const int emax = __reduce_max_sync(0xffffffffu, max(v0, v1));
-        float oscale = 1.f;
-        if (emax > E) {
-            oscale = fast_exp2(static_cast<float>(E - emax));
+        raise |= vmax > E;
+        // rare: a row's maximum, or the largest V exponent met so far, goes up
+        if (__any_sync(0xffffffffu, raise)) {
+            const int emax = max(E, __reduce_max_sync(0xffffffffu, vmax));
+            const float oscale = fast_exp2(static_cast<float>(E - emax));
             E = emax;
-        }
-        raise = __any_sync(0xffffffffu, raise);
-        if (raise || oscale != 1.f) {
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
                 float c[2] = {oscale, oscale};
-                if (raise) {
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        float mx = fmaxf(s[nt][i], s[nt][2 + i]);
+                for (int i = 0; i < 2; ++i) {
+                    float mx = NEG_INF;
 #pragma unroll
-                        for (int off = 4; off < 32; off <<= 1)
-                            mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                        const float n = fmaxf(m[nt][i], mx), f = n == NEG_INF ? 1.f : fast_exp2(m[nt][i] - n);
-                        m[nt][i] = n;
-                        l[nt][i] *= f;
-                        c[i] *= f;
-                    }
+                    for (int j = 0; j < KT; ++j)
+                        mx = fmaxf(mx, fmaxf(s[j][nt][i], s[j][nt][2 + i]));
+#pragma unroll
+                    for (int off = 4; off < 32; off <<= 1)
+                        mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                    const float n = fmaxf(m[nt][i], mx), f = n == NEG_INF ? 1.f : fast_exp2(m[nt][i] - n);
+                    m[nt][i] = n;
+                    l[nt][i] *= f;
+                    c[i] *= f;
                 }
 #pragma unroll
                 for (int mt = 0; mt < D / 16; ++mt) {
@@ -195,48 +209,55 @@ struct WarpQ8 {
                 }
             }
         }
-        const float vf[2] = {q8_pow2(max(v0 - E + 6, -126)), q8_pow2(max(v1 - E + 6, -126))};
-        uint32_t pb[NT][2];
+        uint32_t pb[KT][NT][2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-            const float u0 = m[nt][0] == NEG_INF ? 0.f : m[nt][0], u1 = m[nt][1] == NEG_INF ? 0.f : m[nt][1];
-            const float p0 = fast_exp2(s[nt][0] - u0), p1 = fast_exp2(s[nt][1] - u1);
-            const float p2 = fast_exp2(s[nt][2] - u0), p3 = fast_exp2(s[nt][3] - u1);
-            l[nt][0] += p0 + p2;
-            l[nt][1] += p1 + p3;
-            const __half2 h0 = __floats2half2_rn(p0 * vf[0], p1 * vf[0]), h1 = __floats2half2_rn(p2 * vf[1], p3 * vf[1]);
-            pb[nt][0] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&h0));
-            pb[nt][1] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&h1));
-        }
-        // V: four keys, D / 8 bytes each
-        uint32_t w[4][D / 32];
+        for (int j = 0; j < KT; ++j) {
+            const float vf[2] = {q8_pow2(max(v[j][0] - E + 6, -126)), q8_pow2(max(v[j][1] - E + 6, -126))};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const int r = r0 + 2 * t + (i & 1) + 8 * (i >> 1);
-            if constexpr (D == 128) {
-                const uint4 u = *reinterpret_cast<const uint4 *>(vb + q8_offset<D>(r, gq));
-                w[i][0] = u.x;
-                w[i][1] = u.y;
-                w[i][2] = u.z;
-                w[i][3] = u.w;
-            } else {
-                const uint2 u = *reinterpret_cast<const uint2 *>(vb + q8_offset<D>(r, gq >> 1) + 8 * (gq & 1));
-                w[i][0] = u.x;
-                w[i][1] = u.y;
+            for (int nt = 0; nt < NT; ++nt) {
+                const float u0 = m[nt][0] == NEG_INF ? 0.f : m[nt][0], u1 = m[nt][1] == NEG_INF ? 0.f : m[nt][1];
+                const float p0 = fast_exp2(s[j][nt][0] - u0), p1 = fast_exp2(s[j][nt][1] - u1);
+                const float p2 = fast_exp2(s[j][nt][2] - u0), p3 = fast_exp2(s[j][nt][3] - u1);
+                l[nt][0] += p0 + p2;
+                l[nt][1] += p1 + p3;
+                const __half2 h0 = __floats2half2_rn(p0 * vf[0], p1 * vf[0]);
+                const __half2 h1 = __floats2half2_rn(p2 * vf[1], p3 * vf[1]);
+                pb[j][nt][0] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&h0));
+                pb[j][nt][1] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&h1));
             }
         }
+        // V: four keys of every 16, D / 8 bytes each
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c)
+        for (int j = 0; j < KT; ++j) {
+            uint32_t w[4][D / 32];
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                const uint32_t x = __byte_perm(w[0][c], w[1][c], hf ? 0x7362 : 0x5140);
-                const uint32_t y = __byte_perm(w[2][c], w[3][c], hf ? 0x7362 : 0x5140);
-                const uint32_t a[4] = {q8_half2<CODE>(x, false), q8_half2<CODE>(x, true), q8_half2<CODE>(y, false),
-                                       q8_half2<CODE>(y, true)};
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-                    mma_16816_f16(o[nt][2 * c + hf], a, pb[nt][0], pb[nt][1]);
+            for (int i = 0; i < 4; ++i) {
+                const int r = r0 + 16 * j + 2 * t + (i & 1) + 8 * (i >> 1);
+                if constexpr (D == 128) {
+                    const uint4 u = *reinterpret_cast<const uint4 *>(vb + q8_offset<D>(r, gq));
+                    w[i][0] = u.x;
+                    w[i][1] = u.y;
+                    w[i][2] = u.z;
+                    w[i][3] = u.w;
+                } else {
+                    const uint2 u = *reinterpret_cast<const uint2 *>(vb + q8_offset<D>(r, gq >> 1) + 8 * (gq & 1));
+                    w[i][0] = u.x;
+                    w[i][1] = u.y;
+                }
             }
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c)
+#pragma unroll
+                for (int hf = 0; hf < 2; ++hf) {
+                    const uint32_t x = __byte_perm(w[0][c], w[1][c], hf ? 0x7362 : 0x5140);
+                    const uint32_t y = __byte_perm(w[2][c], w[3][c], hf ? 0x7362 : 0x5140);
+                    const uint32_t a[4] = {q8_half2<CODE>(x, false), q8_half2<CODE>(x, true), q8_half2<CODE>(y, false),
+                                           q8_half2<CODE>(y, true)};
+#pragma unroll
+                    for (int nt = 0; nt < NT; ++nt)
+                        mma_16816_f16(o[nt][2 * c + hf], a, pb[j][nt][0], pb[j][nt][1]);
+                }
+        }
     }
 
     __device__ __forceinline__ void finish_sums()
