@@ -143,6 +143,8 @@ struct PrefixAttnParams {
     int chunk;  // keys of a split, set by the launcher
     float qscale;
 };
+cudaError_t launch_prefix_tc(int D, bool rows2, const CUtensorMap &k, const CUtensorMap &v, const PrefixAttnParams &p,
+                             int splits, int tiles, cudaStream_t stream);
 int prefix_attn_parts(long long copies, int P, int Hq, int Hkv);
 cudaError_t launch_prefix_attn(int D, const CUtensorMap &k, const CUtensorMap &v, PrefixAttnParams p,
                                cudaStream_t stream);

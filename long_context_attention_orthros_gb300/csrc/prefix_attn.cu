@@ -8,6 +8,7 @@
 // producer warp); four warps run the online softmax on warp MMAs, RG groups of 16 rows with
 // 4 / RG warps sharing a group's keys and merging in shared memory.
 #include "kernels.cuh"
+#include "prefix_rows.cuh"
 #include "xattn.cuh"
 
 namespace orthros {
@@ -25,27 +26,6 @@ struct PaCfg {
     static constexpr int SMEM = BAR_OFF + 2 * STAGES * 8 + 1024;
     static_assert(STAGES * STAGE_BYTES >= CWARPS * 16 * (D + 2) * 4, "the warps' merge reuses the ring");
 };
-
-struct PaRow {
-    const orthros_bf16 *q;  // NULL: no such row, or a copy whose position is out of range
-    long long slot;         // of split 0; -1: no such row
-    int head;
-};
-
-template <int G>
-__device__ __forceinline__ PaRow pa_row(const PrefixAttnParams &p, long long row, int g, int D)
-{
-    PaRow r = {nullptr, -1, g * G};
-    const long long bi = row / G;
-    if (bi >= static_cast<long long>(p.B) * p.T_out)
-        return r;
-    const int b = static_cast<int>(bi / p.T_out), i = static_cast<int>(bi % p.T_out), h = static_cast<int>(row % G);
-    r.head = g * G + h;
-    r.slot = (static_cast<long long>(b) * p.Hkv + g) * p.T_out * G + static_cast<long long>(i) * G + h;
-    if (p.pos == nullptr || (p.pos[bi] >= 0 && p.pos[bi] < p.T_kv))
-        r.q = p.qc + b * p.qc_bstride + (static_cast<long long>(i) * p.Hq + r.head) * D;
-    return r;
-}
 
 template <int D, int G, int RG>
 __global__ void __launch_bounds__(PaCfg<D>::THREADS)
@@ -102,13 +82,13 @@ __global__ void __launch_bounds__(PaCfg<D>::THREADS)
 
     const int rg = warp / KL, kl = warp % KL;
     const int gr = lane >> 2, qd = (lane & 3) * 2;
-    const PaRow rows[2] = {pa_row<G>(p, row0 + rg * 16 + gr, g, D), pa_row<G>(p, row0 + rg * 16 + gr + 8, g, D)};
+    const PrefixRow rows[2] = {prefix_row<G>(p, row0 + rg * 16 + gr, g, D), prefix_row<G>(p, row0 + rg * 16 + gr + 8, g, D)};
     WarpRows16<D> st;
 #pragma unroll
     for (int kt = 0; kt < D / 16; ++kt)
 #pragma unroll
         for (int r = 0; r < 4; ++r) {
-            const PaRow &row = rows[r & 1];
+            const PrefixRow &row = rows[r & 1];
             uint32_t hi = 0, lo = 0;
             if (row.q != nullptr)
                 load_q_pair(row.q, p.alpha_c + row.head * D, p.beta_c + row.head * D,
@@ -157,7 +137,7 @@ __global__ void __launch_bounds__(PaCfg<D>::THREADS)
     const long long BHR = static_cast<long long>(p.B) * p.Hkv * p.T_out * G;
     for (int e = threadIdx.x; e < 16 * RG * (D / 4); e += C::CWARPS * 32) {
         const int r = e / (D / 4), d4 = 4 * (e % (D / 4));
-        const PaRow row = pa_row<G>(p, row0 + r, g, D);
+        const PrefixRow row = prefix_row<G>(p, row0 + r, g, D);
         if (row.slot < 0)
             continue;
         const int w0 = (r / 16) * KL;
@@ -193,28 +173,34 @@ __global__ void __launch_bounds__(PaCfg<D>::THREADS)
 // ------------------------------------------------------------------ host side
 
 struct PaPlan {
-    int rg, tiles, splits, chunk;
+    int tc;     // 0: warp MMAs; 1: tensor memory, one tile of rows; 2: two tiles
+    int rg, tiles, splits, chunk, parts;
 };
 
-// two CTAs on each of 152 SMs in one wave, at least 256 keys a split
+// warp MMAs: two CTAs on each of 152 SMs in one wave, at least 256 keys a split; tensor memory: one
+// CTA an SM, at least 512 keys a split
 static PaPlan pa_plan(long long copies, int P, int Hq, int Hkv)
 {
     PaPlan pl;
     const long long R = copies * (Hq / Hkv);
+    pl.tc = R <= 16 ? 0 : (R <= 128 ? 1 : 2);
     pl.rg = R <= 16 ? 1 : (R <= 32 ? 2 : 4);
-    const long long tiles = (R + 16 * pl.rg - 1) / (16 * pl.rg);
+    const int rows = pl.tc ? 128 * pl.tc : 16 * pl.rg, ctas = pl.tc ? 152 : 304, keys = pl.tc ? 512 : 256;
+    const long long tiles = (R + rows - 1) / rows;
     pl.tiles = static_cast<int>(tiles);
-    long long splits = 304 / (tiles * Hkv);
-    const long long most = (static_cast<long long>(P) + 255) / 256;
+    long long splits = ctas / (tiles * Hkv);
+    const long long most = (static_cast<long long>(P) + keys - 1) / keys;
     splits = splits > most ? most : splits;
     splits = splits < 1 ? 1 : splits;
-    const long long chunk = ((P + splits - 1) / splits + 63) / 64 * 64;
+    const int unit = pl.tc ? 128 : 64;
+    const long long chunk = ((P + splits - 1) / splits + unit - 1) / unit * unit;
     pl.chunk = static_cast<int>(chunk);
     pl.splits = static_cast<int>((P + chunk - 1) / chunk);
+    pl.parts = pl.splits * (pl.tc == 1 ? 2 : 1);
     return pl;
 }
 
-int prefix_attn_parts(long long copies, int P, int Hq, int Hkv) { return pa_plan(copies, P, Hq, Hkv).splits; }
+int prefix_attn_parts(long long copies, int P, int Hq, int Hkv) { return pa_plan(copies, P, Hq, Hkv).parts; }
 
 template <int D, int G, int RG>
 static cudaError_t launch_pa(const CUtensorMap &k, const CUtensorMap &v, const PrefixAttnParams &p, const PaPlan &pl,
@@ -253,6 +239,8 @@ cudaError_t launch_prefix_attn(int D, const CUtensorMap &k, const CUtensorMap &v
     if (static_cast<long long>(pl.tiles) * p.Hkv > 65535)
         return cudaErrorInvalidValue;
     p.chunk = pl.chunk;
+    if (pl.tc)
+        return launch_prefix_tc(D, pl.tc == 2, k, v, p, pl.splits, pl.tiles, stream);
     const int G = p.Hq / p.Hkv;
 #define ORTHROS_PA_CASE(DD, GG) \
     if (D == DD && G == GG)     \

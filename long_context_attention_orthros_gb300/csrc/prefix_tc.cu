@@ -1,0 +1,535 @@
+// prefix_tc.cu -- attention of every query row of a batch over one shared prompt prefix on the
+// 5th-generation tensor cores (tcgen05 + tensor memory): the form of prefix_attn.cu for more rows
+// than its warp MMAs keep up with.  Rows, partials and slots are those of prefix_attn.cu.
+//
+// A CTA takes a range of the prefix's keys and runs two softmax streams over it, so that one
+// stream's MMAs run while the other's exponentials do:
+//   ROWS2: tiles of 128 rows each, A and B; every pair of 64-key blocks serves both (R > 128);
+//   KEYS2: one tile of 128 rows; the streams take pairs of key blocks in turn, each with its own
+//          maximum, sum and O (its own partial), and the ring is one pair deeper.
+// Per pair of blocks (128 keys) and stream:
+//   S = q K^T   one N = 128 product per 16 of d, fp16, fp32 accumulators in tensor memory.  A q row is
+//               scaled by a power of two to a largest value in [2^14, 2^15) before it is rounded (the
+//               factor comes back in the exponent's FMA); K is converted from bf16 in shared memory,
+//               a key row whose largest |k| reaches 65520 by an exact 2^-e first and its logits
+//               multiplied back by 2^e;
+//   softmax     a thread a row; the running maximum is raised only when it grows by more than 8
+//               (log2 units); P <= 256 as bf16 over S;
+//   O += P V    bf16, fp32 accumulators in tensor memory.
+// At the end O, the maximum and the sum leave as the stream's partial, unnormalised.
+//
+// Roles (512 threads, one CTA an SM):
+//   warp 0        TMA producer of K/V blocks
+//   warp 1        allocates tensor memory; lane 0 issues every tcgen05.mma
+//   warps 2-3     convert each landed K block to fp16 (with warps 12-15)
+//   warps 4-7     softmax and partial of stream 0; a warp without a row only keeps step
+//   warps 8-11    the same for stream 1
+//   warps 12-15   queries from global memory to fp16 tiles, then K conversion
+// Tensor memory: S of stream t at 128 t; O at 256 + D t.  Every mbarrier wait is bounded; a timeout
+// records ORTHROS_DEVERR_TIMEOUT and all roles drain to the common exit.
+#include <cuda_fp16.h>
+
+#include "common.cuh"
+#include "kernels.cuh"
+#include "prefix_rows.cuh"
+#include "tc.cuh"
+
+namespace orthros {
+
+template <int D, bool ROWS2>
+struct PtCfg {
+    static constexpr int KB = 64;
+    static constexpr int SLABS = D / 64;
+    static constexpr int TILES = ROWS2 ? 2 : 1;
+    static constexpr int Q_SLAB = 128 * 128;
+    static constexpr int Q_BYTES = SLABS * Q_SLAB;
+    static constexpr int PAIR_SLAB = 128 * 128;             // 128 keys of one 64-wide slab
+    static constexpr int PAIR_BYTES = SLABS * PAIR_SLAB;    // K, or V, of a pair
+    static constexpr int PAIRS = ROWS2 ? 2 : 3;
+    static constexpr int SLOTS = 2 * PAIRS;                 // 64-key blocks of the ring
+    static constexpr int K_OFF = 0;
+    static constexpr int V_OFF = PAIRS * PAIR_BYTES;
+    static constexpr int Q_OFF = 2 * PAIRS * PAIR_BYTES;
+    static constexpr int KEXP_OFF = Q_OFF + TILES * Q_BYTES;   // int8 [SLOTS][KB]: key row shift
+    static constexpr int KFLAG_OFF = KEXP_OFF + SLOTS * KB;    // uint8 [SLOTS][8]
+    static constexpr int QSC_OFF = KFLAG_OFF + SLOTS * 8;      // int8 [TILES][128]: query row shift
+    static constexpr int BAR_OFF = QSC_OFF + TILES * 128;
+    static constexpr int NBARS = 3 * SLOTS + 10;
+    static constexpr int HOLD_OFF = BAR_OFF + NBARS * 8;
+    static constexpr int USED = HOLD_OFF + 16 + 1024;
+    static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;  // one CTA an SM: it takes all of tensor memory
+    static_assert(SMEM <= 232448, "shared memory budget");
+    static constexpr uint32_t TM_S = 0, TM_O = 256;
+    static constexpr int CPR = D / 8;       // 16-byte chunks of a query row
+    static constexpr int RPP = 128 / CPR;   // rows one pass of 128 threads covers
+    static constexpr int CONV_THREADS = 192;
+};
+
+template <int D, int G, bool ROWS2>
+__global__ void __launch_bounds__(512, 1)
+    prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
+                     const PrefixAttnParams p)
+{
+    using C = PtCfg<D, ROWS2>;
+    extern __shared__ uint8_t smem_raw[];
+    const uint32_t raw_s = smem_u32(smem_raw);
+    const uint32_t pad = ((raw_s + 1023u) & ~1023u) - raw_s;
+    uint8_t *smem = smem_raw + pad;
+    const uint32_t sbase = raw_s + pad;
+    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);  // [SLOTS] K/V block landed
+    uint64_t *kconv = full + C::SLOTS;     // [SLOTS] K block converted
+    uint64_t *empty = kconv + C::SLOTS;    // [SLOTS] block released (MMA commit)
+    uint64_t *q_full = empty + C::SLOTS;   // [2] query tile prepared
+    uint64_t *s_full = q_full + 2;         // [2] S of a pair complete
+    uint64_t *p_full = s_full + 2;         // [2] P written
+    uint64_t *o_done = p_full + 2;         // [2] O += P V of a pair complete
+    uint64_t *o_final = o_done + 2;        // [2] of the stream's last pair
+    int8_t *kexp = reinterpret_cast<int8_t *>(smem + C::KEXP_OFF);
+    int8_t *qexp = reinterpret_cast<int8_t *>(smem + C::QSC_OFF);
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::HOLD_OFF);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int split = blockIdx.x, g = blockIdx.y;
+    const long long row_base = static_cast<long long>(blockIdx.z) * 128 * C::TILES;
+    const long long R = static_cast<long long>(p.B) * p.T_out * G;
+    if (threadIdx.x == 0) {
+        for (int s = 0; s < C::SLOTS; ++s) {
+            mbar_init(&full[s], 1);
+            mbar_init(&kconv[s], C::CONV_THREADS / 32);
+            mbar_init(&empty[s], 1);
+            reinterpret_cast<uint64_t *>(smem + C::KFLAG_OFF)[s] = 0;
+        }
+        for (int t = 0; t < 2; ++t) {
+            mbar_init(&q_full[t], 4);
+            mbar_init(&s_full[t], 1);
+            mbar_init(&p_full[t], 4);
+            mbar_init(&o_done[t], 1);
+            mbar_init(&o_final[t], 1);
+        }
+        fence_barrier_init();
+    }
+    if (warp == 1)
+        tmem_alloc(tmem_holder, 512);
+    tc_fence_before();
+    // what the kernels before wrote first, then a dependent grid may start beside this one
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = *tmem_holder;
+    const int js = split * p.chunk, je = min(js + p.chunk, p.P);
+    const int nkb = (je - js + C::KB - 1) / C::KB;  // at least 1: the plan has no empty split
+    const int npair = (nkb + 1) / 2;
+    auto pairs_of = [&](int t) { return ROWS2 ? npair : (npair - t + 1) / 2; };  // of stream t
+    auto pair_at = [&](int t, int u) { return ROWS2 ? u : 2 * u + t; };           // its u-th
+
+    if (warp == 0) {
+        // ------------------------------------------------------------------ producer
+        if (lane == 0) {
+            tma_prefetch_desc(&kmap);
+            tma_prefetch_desc(&vmap);
+            for (int j = 0; j < 2 * npair; ++j) {
+                const int s = j % C::SLOTS;
+                if (j >= C::SLOTS && !mbar_wait(&empty[s], static_cast<uint32_t>(((j / C::SLOTS) - 1) & 1))) {
+                    record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+                    break;
+                }
+                const int at = (s / 2) * C::PAIR_BYTES + (s % 2) * C::KB * 128;
+                mbar_arrive_expect_tx(&full[s], 2 * C::SLABS * C::KB * 128);
+#pragma unroll
+                for (int sl = 0; sl < C::SLABS; ++sl) {
+                    tma_load_4d(smem + C::K_OFF + at + sl * C::PAIR_SLAB, &kmap, &full[s], sl * 64, g, js + j * C::KB, 0);
+                    tma_load_4d(smem + C::V_OFF + at + sl * C::PAIR_SLAB, &vmap, &full[s], sl * 64, g, js + j * C::KB, 0);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t IDESC_QK = umma_idesc(128, 128, false, false);
+            constexpr uint32_t IDESC_PV = umma_idesc(128, D, true, true);
+            bool ok = mbar_wait(&q_full[0], 0) && (!ROWS2 || mbar_wait(&q_full[1], 0));
+            auto issue_s = [&](int t, int u) -> bool {
+                const int pp = pair_at(t, u), s0 = (2 * pp) % C::SLOTS;
+                const uint32_t ph = static_cast<uint32_t>(((2 * pp) / C::SLOTS) & 1);
+                if (!ROWS2 || t == 0)  // the pair's blocks landed and converted
+                    for (int h = 0; h < 2; ++h)
+                        if (!(mbar_wait(&full[s0 + h], ph) && mbar_wait(&kconv[s0 + h], ph)))
+                            return false;
+                // S overwrites the P that the stream's last P V reads
+                if (u >= 1 && !mbar_wait(&o_done[t], static_cast<uint32_t>((u - 1) & 1)))
+                    return false;
+                tc_fence_after();
+                const uint64_t kdesc = umma_desc_sw128(sbase + C::K_OFF + (s0 / 2) * C::PAIR_BYTES, 16, 1024);
+                const uint64_t qdesc = umma_desc_sw128(sbase + C::Q_OFF + (ROWS2 ? t : 0) * C::Q_BYTES, 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t off = static_cast<uint32_t>((kk >> 2) * C::PAIR_SLAB + (kk & 3) * 32) >> 4;
+                    static_assert(C::PAIR_SLAB == C::Q_SLAB, "one offset serves both operands");
+                    umma_ss(tbase + C::TM_S + 128 * t, qdesc + off, kdesc + off, IDESC_QK, kk != 0);
+                }
+                umma_commit(&s_full[t]);
+                return true;
+            };
+            auto issue_pv = [&](int t, int u) -> bool {
+                if (!mbar_wait(&p_full[t], static_cast<uint32_t>(u & 1)))
+                    return false;
+                tc_fence_after();
+                const int s0 = (2 * pair_at(t, u)) % C::SLOTS;
+                const uint64_t vdesc = umma_desc_sw128(sbase + C::V_OFF + (s0 / 2) * C::PAIR_BYTES, C::PAIR_SLAB, 1024);
+#pragma unroll
+                for (int kk = 0; kk < 8; ++kk)
+                    umma_ts(tbase + C::TM_O + D * t, tbase + C::TM_S + 128 * t + 8 * kk,
+                            vdesc + static_cast<uint64_t>(kk * (2048 >> 4)), IDESC_PV, (u > 0 || kk > 0) ? 1u : 0u);
+                umma_commit(&o_done[t]);
+                if (u == pairs_of(t) - 1)
+                    umma_commit(&o_final[t]);
+                if (!ROWS2 || t == 1) {  // everything that reads the pair has been issued
+                    umma_commit(&empty[s0]);
+                    umma_commit(&empty[s0 + 1]);
+                }
+                return true;
+            };
+            for (int t = 0; t < 2; ++t)
+                ok = ok && (pairs_of(t) == 0 || issue_s(t, 0));
+            for (int u = 0; u < pairs_of(0) && ok; ++u)
+                for (int t = 0; t < 2 && ok; ++t) {
+                    if (u >= pairs_of(t))
+                        continue;
+                    // ROWS2: S_A of the next pair goes out before P V of B; the pair B still reads stays
+                    ok = issue_pv(t, u) && (u + 1 >= pairs_of(t) || issue_s(t, u + 1));
+                }
+            if (!ok)
+                record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+        }
+    } else if (warp < 4 || warp >= 12) {
+        // ------------------------------------------------------------------ query prep + K converters
+        bool ok = true, bad = false;
+        if (warp >= 12) {
+            const int tid = threadIdx.x - 384;  // 0 .. 127
+            const int cr = tid % C::CPR, r0 = tid / C::CPR;
+            constexpr int SETS = (C::RPP % G == 0) ? 1 : 2;  // heads a thread meets (G = 16 at D = 128: two)
+            static_assert((SETS * C::RPP) % G == 0, "a thread's heads repeat every SETS passes");
+            float al[SETS][8], be[SETS][8];
+#pragma unroll
+            for (int x = 0; x < SETS; ++x) {
+                const int h = g * G + (r0 + x * C::RPP) % G;
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    al[x][e] = __ldg(p.alpha_c + h * D + 8 * cr + e) * p.qscale;
+                    be[x][e] = __ldg(p.beta_c + h * D + 8 * cr + e) * p.qscale;
+                }
+            }
+            for (int t = 0; t < C::TILES; ++t) {
+                uint8_t *qb = smem + C::Q_OFF + t * C::Q_BYTES + (cr / 8) * C::Q_SLAB;
+#pragma unroll
+                for (int jr = 0; jr < 128 / C::RPP; ++jr) {
+                    const int r = r0 + jr * C::RPP;
+                    const PrefixRow row = prefix_row<G>(p, row_base + t * 128 + r, g, D);
+                    uint4 raw = make_uint4(0, 0, 0, 0);
+                    if (row.q != nullptr)
+                        raw = __ldg(reinterpret_cast<const uint4 *>(row.q + 8 * cr));
+                    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
+                    float f[8], amax = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = ffma2(unpack_bf16x2(w[e]),
+                                               make_float2(al[jr % SETS][2 * e], al[jr % SETS][2 * e + 1]),
+                                               make_float2(be[jr % SETS][2 * e], be[jr % SETS][2 * e + 1]));
+                        f[2 * e] = row.q != nullptr ? y.x : 0.f;
+                        f[2 * e + 1] = row.q != nullptr ? y.y : 0.f;
+                        amax = fmax3(amax, fabsf(f[2 * e]), fabsf(f[2 * e + 1]));
+                    }
+#pragma unroll
+                    for (int off = 1; off < C::CPR; off <<= 1)
+                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+                    int sh = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
+                    sh = amax == 0.f ? 0 : (sh < -126 ? -126 : sh);
+                    const float sd = exp2i(-sh);
+                    uint32_t o4[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __half2 hv = __floats2half2_rn(f[2 * e] * sd, f[2 * e + 1] * sd);
+                        o4[e] = *reinterpret_cast<const uint32_t *>(&hv);
+                    }
+                    *reinterpret_cast<uint4 *>(qb + sw128_offset(r, cr % 8)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+                    if (cr == 0)
+                        qexp[t * 128 + r] = static_cast<int8_t>(sh);
+                }
+                fence_proxy_async_smem();  // the MMA reads q through the async proxy
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&q_full[t]);
+            }
+        }
+        // K conversion: 8 consecutive lanes a key row, rows cid / 8 + 24 it of a block
+        const int cid = warp < 4 ? threadIdx.x - 64 : threadIdx.x - 384 + 64;  // 0 .. 191
+        const int cw = cid >> 5;
+        constexpr int ITS = (C::KB * 8 + C::CONV_THREADS - 1) / C::CONV_THREADS;
+        const int nrows = cid + (ITS - 1) * C::CONV_THREADS < C::KB * 8 ? ITS : ITS - 1;  // warp-uniform
+        for (int j = 0; j < 2 * npair && ok; ++j) {
+            const int s = j % C::SLOTS;
+            if (!(ok = mbar_wait(&full[s], static_cast<uint32_t>((j / C::SLOTS) & 1))))
+                break;
+            uint8_t *blk = smem + C::K_OFF + (s / 2) * C::PAIR_BYTES + (s % 2) * C::KB * 128;
+            uint4 u[ITS][C::SLABS];
+            bool big = false;
+#pragma unroll
+            for (int it = 0; it < ITS; ++it)
+                if (it < nrows) {
+#pragma unroll
+                    for (int sl = 0; sl < C::SLABS; ++sl) {
+                        u[it][sl] = *reinterpret_cast<const uint4 *>(blk + sl * C::PAIR_SLAB + ((cid >> 3) + 24 * it) * 128 +
+                                                                     (cid & 7) * 16);
+                        big |= !(bf16x8_absmax(u[it][sl]) < 65520.f);
+                    }
+                }
+            const bool wany = __any_sync(0xffffffffu, big);
+            if (!wany) {
+#pragma unroll
+                for (int it = 0; it < ITS; ++it)
+                    if (it < nrows) {
+#pragma unroll
+                        for (int sl = 0; sl < C::SLABS; ++sl)
+                            *reinterpret_cast<uint4 *>(blk + sl * C::PAIR_SLAB + ((cid >> 3) + 24 * it) * 128 +
+                                                       (cid & 7) * 16) = k_to_fp16(u[it][sl]);
+                    }
+            } else {
+                shift_key_rows<C::SLABS>(blk, C::PAIR_SLAB, 0, cid >> 3, C::CONV_THREADS / 8, nrows, cid & 7,
+                                         kexp + s * C::KB, bad);
+            }
+            if (lane == 0)
+                smem[C::KFLAG_OFF + s * 8 + cw] = wany ? 1 : 0;
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&kconv[s]);
+        }
+        if (bad)
+            record_error(p.dev_err, ORTHROS_DEVERR_RANGE);
+        if (!ok && lane == 0)
+            record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+    } else {
+        // ------------------------------------------------------------------ softmax + partials
+        const int t = (warp - 4) >> 2;  // stream
+        const int tile = ROWS2 ? t : 0, rw = warp & 3, r = rw * 32 + lane;
+        const long long row_i = row_base + tile * 128 + r;
+        const bool work = row_base + tile * 128 + rw * 32 < R;  // the warp has a row
+        const PrefixRow row = prefix_row<G>(p, row_i, g, D);
+        const uint32_t s_lane = tbase + (static_cast<uint32_t>(rw * 32) << 16) + C::TM_S + 128 * t;
+        const uint32_t o_col = tbase + (static_cast<uint32_t>(rw * 32) << 16) + C::TM_O + D * t;
+        const float NEG_INF = -__int_as_float(0x7f800000);
+        const int nu = pairs_of(t);
+        bool ok = mbar_wait(&q_full[tile], 0), range_bad = false;
+        const float qf = exp2i(qexp[tile * 128 + r]);  // logit = S qf
+        const float2 qf2 = make_float2(qf, qf);
+        float m = NEG_INF, l = 0.f;
+        for (int u = 0; u < nu && ok; ++u) {
+            const int pp = pair_at(t, u);
+            if (!(ok = mbar_wait(&s_full[t], static_cast<uint32_t>(u & 1))))
+                break;
+            tc_fence_after();
+            if (work) {
+                float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+                for (int hh = 0; hh < 2 && ok; ++hh) {
+                    const int j = 2 * pp + hh, ks = j % C::SLOTS;
+                    const uint32_t s_col = s_lane + 64 * hh;
+                    const int nvalid = je - 1 - (js + j * C::KB);  // column c is a key iff c <= nvalid
+                    uint32_t va[32], vb[32];
+                    tmem_ld32(s_col, va);
+                    tmem_ld32(s_col + 32, vb);
+                    // the block's conversion completed before its S was issued: this test succeeds and
+                    // orders the flag read after the converters' writes
+                    const uint32_t kph = static_cast<uint32_t>((j / C::SLOTS) & 1);
+                    const bool seen = mbar_test_wait(&kconv[ks], kph);
+                    const uint64_t kf = *reinterpret_cast<const volatile uint64_t *>(smem + C::KFLAG_OFF + ks * 8);
+                    tmem_wait_ld();
+                    if (!seen || kf != 0) {
+                        if (!(ok = mbar_wait(&kconv[ks], kph)))
+                            break;
+                        const uint64_t kf2 = *reinterpret_cast<const volatile uint64_t *>(smem + C::KFLAG_OFF + ks * 8);
+                        uint32_t kw = 0;
+#pragma unroll
+                        for (int cw = 0; cw < C::CONV_THREADS / 32; ++cw)
+                            kw |= (((kf2 >> (8 * cw)) & 0xffu) ? 1u : 0u) << cw;
+                        if (kw != 0) {  // logits of shifted key rows times 2^e (rare), in tensor memory
+                            unshift_chunk32(s_col, kexp + ks * C::KB, 0, kw, 24, 4, range_bad);
+                            unshift_chunk32(s_col + 32, kexp + ks * C::KB, 32, kw, 24, 4, range_bad);
+                            tmem_ld32(s_col, va);
+                            tmem_ld32(s_col + 32, vb);
+                            tmem_wait_ld();
+                        }
+                    }
+                    if (nvalid < C::KB - 1) {
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            if (e > nvalid)
+                                va[e] = __float_as_uint(NEG_INF);
+                            if (32 + e > nvalid)
+                                vb[e] = __float_as_uint(NEG_INF);
+                        }
+                    }
+                    float m4[4] = {NEG_INF, NEG_INF, NEG_INF, NEG_INF};
+#pragma unroll
+                    for (int e = 0; e < 32; e += 2) {
+                        m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(va[e]), __uint_as_float(va[e + 1]));
+                        m4[(e >> 1) & 3] = fmax3(m4[(e >> 1) & 3], __uint_as_float(vb[e]), __uint_as_float(vb[e + 1]));
+                    }
+                    const float mb = fmaxf(fmaxf(m4[0], m4[1]), fmaxf(m4[2], m4[3])) * qf;
+                    const bool raise = mb > m + 8.f;
+                    if (__any_sync(0xffffffffu, raise)) {
+                        const float f = raise ? fast_exp2(m - mb) : 1.f;  // m = -inf before the first key: 0
+                        if (u > 0) {
+                            // O holds the stream's pairs before u: their P V completed before S of u was issued
+                            if (!(ok = mbar_wait(&o_done[t], static_cast<uint32_t>((u - 1) & 1))))
+                                break;
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 32) {
+                                uint32_t w[32];
+                                tmem_ld32(o_col + c, w);
+                                tmem_wait_ld();
+#pragma unroll
+                                for (int e = 0; e < 32; ++e)
+                                    w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+                                tmem_st32(o_col + c, w);
+                            }
+                        }
+                        if (hh == 1) {  // P of the first half was taken against the old maximum
+                            tmem_wait_st();
+                            uint32_t w[32];
+                            tmem_ld32(s_lane, w);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) {
+                                const float2 pq = unpack_bf16x2(w[e]);
+                                w[e] = pack_bf16x2(pq.x * f, pq.y * f);
+                            }
+                            tmem_st32(s_lane, w);
+                            l2[0].x *= f;
+                            l2[0].y *= f;
+                            l2[1].x *= f;
+                            l2[1].y *= f;
+                        }
+                        if (raise) {
+                            l *= f;
+                            m = mb;
+                        }
+                    }
+                    const float uo = m == NEG_INF ? 0.f : m;
+                    const float2 nm = make_float2(-uo, -uo);
+#pragma unroll
+                    for (int hq = 0; hq < 2; ++hq) {
+                        const uint32_t *v = hq ? vb : va;
+                        uint32_t pw[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const float2 d = ffma2(make_float2(__uint_as_float(v[2 * e]), __uint_as_float(v[2 * e + 1])), qf2, nm);
+                            const float2 y = make_float2(fast_exp2(d.x), fast_exp2(d.y));
+                            l2[e & 1] = fadd2(l2[e & 1], y);
+                            pw[e] = pack_bf16x2(y.x, y.y);
+                        }
+                        tmem_st16(s_lane + 32 * hh + 16 * hq, pw);
+                    }
+                }
+                if (!ok)
+                    break;
+                l += (l2[0].x + l2[0].y) + (l2[1].x + l2[1].y);
+                tmem_wait_st();
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&p_full[t]);
+        }
+        // ---- the stream's partial: a thread a row
+        if (ok && work) {
+            const bool store = row.slot >= 0, valid = row.q != nullptr && nu > 0;
+            const long long part = ROWS2 ? split : 2 * split + t;
+            const long long slot = part * R * p.Hkv + row.slot;
+            if (store)
+                p.part_ml[slot] = valid ? make_float2(m, l) : make_float2(NEG_INF, 0.f);
+            if (nu > 0 && !(ok = mbar_wait(&o_final[t], 0)))
+                record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+            if (ok) {
+                tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < D; c += 32) {
+                    uint32_t v[32];
+                    if (nu > 0) {
+                        tmem_ld32(o_col + c, v);
+                        tmem_wait_ld();
+                    }
+                    if (store) {
+#pragma unroll
+                        for (int e = 0; e < 32; e += 8) {
+                            const uint4 a = valid ? make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]) : make_uint4(0, 0, 0, 0);
+                            const uint4 b = valid ? make_uint4(v[e + 4], v[e + 5], v[e + 6], v[e + 7]) : make_uint4(0, 0, 0, 0);
+                            st_global_v8(p.part_o + slot * D + c + e, a, b);
+                        }
+                    }
+                }
+            }
+        }
+        if (range_bad)
+            record_error(p.dev_err, ORTHROS_DEVERR_RANGE);
+        if (!ok && lane == 0)
+            record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+    }
+
+    // ---------------------------------------------------------------------- teardown
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tbase, 512);
+    }
+}
+
+template <int D, int G, bool ROWS2>
+static cudaError_t launch_ptc(const CUtensorMap &k, const CUtensorMap &v, const PrefixAttnParams &p, int splits, int tiles,
+                              cudaStream_t stream)
+{
+    using C = PtCfg<D, ROWS2>;
+    auto kern = prefix_tc_kernel<D, G, ROWS2>;
+    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess)
+        return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(splits, p.Hkv, tiles);
+    cfg.blockDim = dim3(512);
+    cfg.dynamicSmemBytes = C::SMEM;
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, kern, k, v, p);
+    return e == cudaSuccess ? cudaGetLastError() : e;
+}
+
+cudaError_t launch_prefix_tc(int D, bool rows2, const CUtensorMap &k, const CUtensorMap &v, const PrefixAttnParams &p,
+                             int splits, int tiles, cudaStream_t stream)
+{
+    const int G = p.Hq / p.Hkv;
+#define ORTHROS_PTC_CASE(DD, GG)                                                         \
+    if (D == DD && G == GG)                                                              \
+        return rows2 ? launch_ptc<DD, GG, true>(k, v, p, splits, tiles, stream)          \
+                     : launch_ptc<DD, GG, false>(k, v, p, splits, tiles, stream);
+    ORTHROS_PTC_CASE(128, 1)
+    ORTHROS_PTC_CASE(128, 2)
+    ORTHROS_PTC_CASE(128, 4)
+    ORTHROS_PTC_CASE(128, 8)
+    ORTHROS_PTC_CASE(128, 16)
+    ORTHROS_PTC_CASE(64, 1)
+    ORTHROS_PTC_CASE(64, 2)
+    ORTHROS_PTC_CASE(64, 4)
+    ORTHROS_PTC_CASE(64, 8)
+    ORTHROS_PTC_CASE(64, 16)
+#undef ORTHROS_PTC_CASE
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace orthros
