@@ -57,14 +57,17 @@ struct SvCfg {
     static constexpr int GROUP = 4 / KT;  // warps that share a block
     static constexpr int SCR_ROWS = CWARPS * G;
     static constexpr int SCR_BYTES = SCR_ROWS * (D + 3) * 4;  // the warps' o, max, sum, exponent
-    static constexpr int LIMIT = 112 * 1024 - 2048;            // two CTAs share an SM
-    // a segment's queries, its alpha and beta and the new K and V row come through buffers of their
-    // own, as many segments ahead
-    static constexpr int HB = G <= 8 ? 2 : 1;
+    static constexpr int LIMIT = 113 * 1024 - 2048;            // two CTAs share an SM
+    // a segment's queries, its alpha and beta and the new K and V row come through a buffer of their
+    // own, free again once the segment has begun
+    static constexpr int HB = 1;
     static constexpr int HDR_NEW = G * D * (2 + 4 + 4);
     static constexpr int HDR_BYTES = HDR_NEW + 2 * D * 2;
     static constexpr int FIT = (LIMIT - SCR_BYTES - HB * HDR_BYTES) / (2 * KV_BYTES + 2 * KB);
-    static constexpr int STAGES = FIT < 2 ? 2 : (FIT > 8 ? 8 : FIT);
+    // A slot of the ring always holds blocks of the same warps (a multiple of KT stages): warps that
+    // skipped one of a slot's phases could take the phase before it for the one they wait for.
+    static constexpr int STAGES = FIT < 2 ? 2 : (FIT > 8 ? 8 : FIT / KT * KT);
+    static_assert(STAGES % KT == 0, "a slot belongs to one group of warps");
     static constexpr int EXP_OFF = STAGES * 2 * KV_BYTES;
     static constexpr int HDR_OFF = EXP_OFF + STAGES * 2 * KB;
     static constexpr int SCR_OFF = HDR_OFF + HB * HDR_BYTES;
@@ -72,6 +75,7 @@ struct SvCfg {
     static constexpr int JOIN_OFF = BAR_OFF + (2 * STAGES + 2 * HB) * 8;
     static constexpr int FLAG_OFF = JOIN_OFF + MAX_JOINS * static_cast<int>(sizeof(Join));
     static constexpr int SMEM = FLAG_OFF + 16 + 1024;
+    static_assert(SMEM <= 232448, "shared memory budget");
     static_assert(HDR_OFF % 16 == 0 && SCR_OFF % 16 == 0 && BAR_OFF % 8 == 0 && JOIN_OFF % 8 == 0, "alignment");
     static constexpr int CTHREADS = CWARPS * 32;
     static constexpr int THREADS = CTHREADS + 32;
@@ -376,21 +380,31 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
                 const float2 ml = q0 == 0 ? ml0 : ml_of(q0 + lane);
                 const float w = ml.x == NEG_INF ? 0.f : fast_exp2(ml.x - M);
                 L += w * ml.y;
-                const int nn = min(32, nq - q0);
-#pragma unroll 16
-                for (int k = 0; k < nn; ++k) {
-                    const float wk = __shfl_sync(0xffffffffu, w, k);
-                    const float *src = (q0 + k < j.parts ? p.part_o : p.pre_o) + slot_of(q0 + k) * D + lane * E;
-                    if constexpr (E == 4) {
-                        const float4 y = __ldcg(reinterpret_cast<const float4 *>(src));
-                        a[0] = fmaf(wk, y.x, a[0]);
-                        a[1] = fmaf(wk, y.y, a[1]);
-                        a[2] = fmaf(wk, y.z, a[2]);
-                        a[3] = fmaf(wk, y.w, a[3]);
-                    } else {
-                        const float2 y = __ldcg(reinterpret_cast<const float2 *>(src));
-                        a[0] = fmaf(wk, y.x, a[0]);
-                        a[1] = fmaf(wk, y.y, a[1]);
+                // eight parts' loads in flight; past the end the last part with a weight of zero
+                for (int k0 = 0; k0 < min(32, nq - q0); k0 += 8) {
+                    float y[8][E];
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int q = min(q0 + k0 + k, nq - 1);
+                        const float *src = (q < j.parts ? p.part_o : p.pre_o) + slot_of(q) * D + lane * E;
+                        if constexpr (E == 4) {
+                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
+                            y[k][0] = v.x;
+                            y[k][1] = v.y;
+                            y[k][2] = v.z;
+                            y[k][3] = v.w;
+                        } else {
+                            const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
+                            y[k][0] = v.x;
+                            y[k][1] = v.y;
+                        }
+                    }
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const float wk = __shfl_sync(0xffffffffu, w, k0 + k);
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            a[e] = fmaf(wk, y[k][e], a[e]);
                     }
                 }
             }
