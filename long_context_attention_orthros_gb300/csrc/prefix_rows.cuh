@@ -16,11 +16,12 @@ template <int G>
 __device__ __forceinline__ PrefixRow prefix_row(const PrefixAttnParams &p, long long row, int g, int D)
 {
     PrefixRow r = {nullptr, -1, g * G};
-    const long long bi = row / G;
-    if (bi >= static_cast<long long>(p.B) * p.T_out)
+    // in 32 bits (the launcher refuses more rows): a thread does this for dozens of rows
+    const uint32_t row32 = static_cast<uint32_t>(row), bi = row32 / G, h = row32 % G;
+    if (bi >= static_cast<uint32_t>(p.B) * static_cast<uint32_t>(p.T_out))
         return r;
-    const int b = static_cast<int>(bi / p.T_out), i = static_cast<int>(bi % p.T_out), h = static_cast<int>(row % G);
-    r.head = g * G + h;
+    const uint32_t b = p.T_out == 1 ? bi : bi / static_cast<uint32_t>(p.T_out), i = bi - b * p.T_out;
+    r.head = g * G + static_cast<int>(h);
     r.slot = (static_cast<long long>(b) * p.Hkv + g) * p.T_out * G + static_cast<long long>(i) * G + h;
     if (p.pos == nullptr || (p.pos[bi] >= 0 && p.pos[bi] < p.T_kv))
         r.q = p.qc + b * p.qc_bstride + (static_cast<long long>(i) * p.Hq + r.head) * D;

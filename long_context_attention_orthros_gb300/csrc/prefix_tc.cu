@@ -21,10 +21,10 @@
 // Roles (512 threads, one CTA an SM):
 //   warp 0        TMA producer of K/V blocks
 //   warp 1        allocates tensor memory; lane 0 issues every tcgen05.mma
-//   warps 2-3     convert each landed K block to fp16 (with warps 12-15)
-//   warps 4-7     softmax and partial of stream 0; a warp without a row only keeps step
+//   warps 2-3, 12-15  convert each landed K block to fp16
+//   warps 4-7     queries from global memory to fp16 tiles (with warps 8-11), then softmax and
+//                 partial of stream 0; a warp without a row only keeps step
 //   warps 8-11    the same for stream 1
-//   warps 12-15   queries from global memory to fp16 tiles, then K conversion
 // Tensor memory: S of stream t at 128 t; O at 256 + D t.  Every mbarrier wait is bounded; a timeout
 // records ORTHROS_DEVERR_TIMEOUT and all roles drain to the common exit.
 #include <cuda_fp16.h>
@@ -61,7 +61,7 @@ struct PtCfg {
     static_assert(SMEM <= 232448, "shared memory budget");
     static constexpr uint32_t TM_S = 0, TM_O = 256;
     static constexpr int CPR = D / 8;       // 16-byte chunks of a query row
-    static constexpr int RPP = 128 / CPR;   // rows one pass of 128 threads covers
+    static constexpr int RPP = 256 / CPR;   // rows one pass of the softmax warps' 256 threads covers
     static constexpr int CONV_THREADS = 192;
 };
 
@@ -100,7 +100,7 @@ __global__ void __launch_bounds__(512, 1)
             reinterpret_cast<uint64_t *>(smem + C::KFLAG_OFF)[s] = 0;
         }
         for (int t = 0; t < 2; ++t) {
-            mbar_init(&q_full[t], 4);
+            mbar_init(&q_full[t], 8);
             mbar_init(&s_full[t], 1);
             mbar_init(&p_full[t], 4);
             mbar_init(&o_done[t], 1);
@@ -203,65 +203,8 @@ __global__ void __launch_bounds__(512, 1)
                 record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
         }
     } else if (warp < 4 || warp >= 12) {
-        // ------------------------------------------------------------------ query prep + K converters
+        // ------------------------------------------------------------------ K converters
         bool ok = true, bad = false;
-        if (warp >= 12) {
-            const int tid = threadIdx.x - 384;  // 0 .. 127
-            const int cr = tid % C::CPR, r0 = tid / C::CPR;
-            constexpr int SETS = (C::RPP % G == 0) ? 1 : 2;  // heads a thread meets (G = 16 at D = 128: two)
-            static_assert((SETS * C::RPP) % G == 0, "a thread's heads repeat every SETS passes");
-            float al[SETS][8], be[SETS][8];
-#pragma unroll
-            for (int x = 0; x < SETS; ++x) {
-                const int h = g * G + (r0 + x * C::RPP) % G;
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    al[x][e] = __ldg(p.alpha_c + h * D + 8 * cr + e) * p.qscale;
-                    be[x][e] = __ldg(p.beta_c + h * D + 8 * cr + e) * p.qscale;
-                }
-            }
-            for (int t = 0; t < C::TILES; ++t) {
-                uint8_t *qb = smem + C::Q_OFF + t * C::Q_BYTES + (cr / 8) * C::Q_SLAB;
-#pragma unroll
-                for (int jr = 0; jr < 128 / C::RPP; ++jr) {
-                    const int r = r0 + jr * C::RPP;
-                    const PrefixRow row = prefix_row<G>(p, row_base + t * 128 + r, g, D);
-                    uint4 raw = make_uint4(0, 0, 0, 0);
-                    if (row.q != nullptr)
-                        raw = __ldg(reinterpret_cast<const uint4 *>(row.q + 8 * cr));
-                    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
-                    float f[8], amax = 0.f;
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const float2 y = ffma2(unpack_bf16x2(w[e]),
-                                               make_float2(al[jr % SETS][2 * e], al[jr % SETS][2 * e + 1]),
-                                               make_float2(be[jr % SETS][2 * e], be[jr % SETS][2 * e + 1]));
-                        f[2 * e] = row.q != nullptr ? y.x : 0.f;
-                        f[2 * e + 1] = row.q != nullptr ? y.y : 0.f;
-                        amax = fmax3(amax, fabsf(f[2 * e]), fabsf(f[2 * e + 1]));
-                    }
-#pragma unroll
-                    for (int off = 1; off < C::CPR; off <<= 1)
-                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-                    int sh = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
-                    sh = amax == 0.f ? 0 : (sh < -126 ? -126 : sh);
-                    const float sd = exp2i(-sh);
-                    uint32_t o4[4];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        const __half2 hv = __floats2half2_rn(f[2 * e] * sd, f[2 * e + 1] * sd);
-                        o4[e] = *reinterpret_cast<const uint32_t *>(&hv);
-                    }
-                    *reinterpret_cast<uint4 *>(qb + sw128_offset(r, cr % 8)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
-                    if (cr == 0)
-                        qexp[t * 128 + r] = static_cast<int8_t>(sh);
-                }
-                fence_proxy_async_smem();  // the MMA reads q through the async proxy
-                __syncwarp();
-                if (lane == 0)
-                    mbar_arrive(&q_full[t]);
-            }
-        }
         // K conversion: 8 consecutive lanes a key row, rows cid / 8 + 24 it of a block
         const int cid = warp < 4 ? threadIdx.x - 64 : threadIdx.x - 384 + 64;  // 0 .. 191
         const int cw = cid >> 5;
@@ -311,6 +254,71 @@ __global__ void __launch_bounds__(512, 1)
             record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
     } else {
         // ------------------------------------------------------------------ softmax + partials
+        // first the queries, from global memory to fp16 tiles, by all eight warps: a thread has 16 bytes of
+        // every RPP-th row, all of one head, and its rows' loads are in flight together
+        {
+            const int tid = threadIdx.x - 128;  // 0 .. 255
+            const int cr = tid % C::CPR, r0 = tid / C::CPR;
+            constexpr int ROWS = 128 / C::RPP;
+            static_assert(C::RPP % G == 0, "a thread's rows share a head");
+            const int h = g * G + r0 % G;
+            float al[8], be[8];
+#pragma unroll
+            for (int e = 0; e < 8; e += 4) {
+                const float4 y = __ldg(reinterpret_cast<const float4 *>(p.alpha_c + h * D + 8 * cr + e));
+                const float4 z = __ldg(reinterpret_cast<const float4 *>(p.beta_c + h * D + 8 * cr + e));
+                al[e] = y.x * p.qscale, al[e + 1] = y.y * p.qscale, al[e + 2] = y.z * p.qscale, al[e + 3] = y.w * p.qscale;
+                be[e] = z.x * p.qscale, be[e + 1] = z.y * p.qscale, be[e + 2] = z.z * p.qscale, be[e + 3] = z.w * p.qscale;
+            }
+#pragma unroll
+            for (int tl = 0; tl < C::TILES; ++tl) {
+                uint8_t *qb = smem + C::Q_OFF + tl * C::Q_BYTES + (cr / 8) * C::Q_SLAB;
+                uint4 raw[ROWS];
+                uint32_t have = 0;
+#pragma unroll
+                for (int x = 0; x < ROWS; ++x) {
+                    const PrefixRow row = prefix_row<G>(p, row_base + tl * 128 + r0 + x * C::RPP, g, D);
+                    raw[x] = make_uint4(0, 0, 0, 0);
+                    if (row.q != nullptr) {
+                        raw[x] = __ldg(reinterpret_cast<const uint4 *>(row.q + 8 * cr));
+                        have |= 1u << x;
+                    }
+                }
+#pragma unroll
+                for (int x = 0; x < ROWS; ++x) {
+                    const int r = r0 + x * C::RPP;
+                    const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+                    float f[8], amax = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float2 y = ffma2(unpack_bf16x2(w[e]), make_float2(al[2 * e], al[2 * e + 1]),
+                                               make_float2(be[2 * e], be[2 * e + 1]));
+                        f[2 * e] = (have >> x) & 1u ? y.x : 0.f;
+                        f[2 * e + 1] = (have >> x) & 1u ? y.y : 0.f;
+                        amax = fmax3(amax, fabsf(f[2 * e]), fabsf(f[2 * e + 1]));
+                    }
+#pragma unroll
+                    for (int off = 1; off < C::CPR; off <<= 1)
+                        amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+                    int sh = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
+                    sh = amax == 0.f ? 0 : (sh < -126 ? -126 : sh);
+                    const float sd = exp2i(-sh);
+                    uint32_t o4[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const __half2 hv = __floats2half2_rn(f[2 * e] * sd, f[2 * e + 1] * sd);
+                        o4[e] = *reinterpret_cast<const uint32_t *>(&hv);
+                    }
+                    *reinterpret_cast<uint4 *>(qb + sw128_offset(r, cr % 8)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+                    if (cr == 0)
+                        qexp[tl * 128 + r] = static_cast<int8_t>(sh);
+                }
+                fence_proxy_async_smem();  // the MMA reads q through the async proxy
+                __syncwarp();
+                if (lane == 0)
+                    mbar_arrive(&q_full[tl]);
+            }
+        }
         const int t = (warp - 4) >> 2;  // stream
         const int tile = ROWS2 ? t : 0, rw = warp & 3, r = rw * 32 + lane;
         const long long row_i = row_base + tile * 128 + r;
