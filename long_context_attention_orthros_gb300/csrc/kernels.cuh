@@ -137,14 +137,23 @@ struct PrefixAttnParams {
     const float *alpha_c, *beta_c;
     float *part_o;
     float2 *part_ml;
+    orthros_bf16 *oc;        // launch_prefix_direct: [B, T_out, Hq, d], batch stride oc_bstride
     int32_t *dev_err;
-    long long qc_bstride;
+    long long qc_bstride, oc_bstride;
     int B, T_out, T_kv, P, Hq, Hkv;
     int chunk;  // keys of a split, set by the launcher
     float qscale;
 };
-cudaError_t launch_prefix_tc(int D, bool rows2, const CUtensorMap &k, const CUtensorMap &v, const PrefixAttnParams &p,
-                             int splits, int tiles, cudaStream_t stream);
+struct PrefixMaps {
+    CUtensorMap k, v, ko, vo;  // the prefix's K and V; the sequences' own (launch_prefix_direct)
+};
+// mode: 0 one tile of 128 rows, 1 two tiles
+cudaError_t launch_prefix_tc(int D, int mode, const PrefixMaps &maps, const PrefixAttnParams &p, int splits, int tiles,
+                             cudaStream_t stream);
+// copies over the prefix and their own rows in one kernel, outputs at p.oc; tiles of a sequence, or 0
+// where partials serve better
+int prefix_direct_tiles(int B, int T_out, int Hq, int Hkv);
+cudaError_t launch_prefix_direct(int D, const PrefixMaps &maps, const PrefixAttnParams &p, cudaStream_t stream);
 int prefix_attn_parts(long long copies, int P, int Hq, int Hkv);
 cudaError_t launch_prefix_attn(int D, const CUtensorMap &k, const CUtensorMap &v, PrefixAttnParams p,
                                cudaStream_t stream);

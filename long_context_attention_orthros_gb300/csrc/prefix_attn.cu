@@ -240,7 +240,7 @@ cudaError_t launch_prefix_attn(int D, const CUtensorMap &k, const CUtensorMap &v
         return cudaErrorInvalidValue;
     p.chunk = pl.chunk;
     if (pl.tc)
-        return launch_prefix_tc(D, pl.tc == 2, k, v, p, pl.splits, pl.tiles, stream);
+        return launch_prefix_tc(D, pl.tc - 1, PrefixMaps{k, v, k, v}, p, pl.splits, pl.tiles, stream);
     const int G = p.Hq / p.Hkv;
 #define ORTHROS_PA_CASE(DD, GG) \
     if (D == DD && G == GG)     \

@@ -6,7 +6,9 @@
 // stream's MMAs run while the other's exponentials do:
 //   ROWS2: tiles of 128 rows each, A and B; every pair of 64-key blocks serves both (R > 128);
 //   KEYS2: one tile of 128 rows; the streams take pairs of key blocks in turn, each with its own
-//          maximum, sum and O (its own partial), and the ring is one pair deeper.
+//          maximum, sum and O (its own partial), and the ring is one pair deeper;
+//   DIRECT: as ROWS2 on two tiles of one sequence's rows, over the whole prefix and then the
+//          sequence's own rows up to each copy's position, and o' leaves rounded to bf16.
 // Per pair of blocks (128 keys) and stream:
 //   S = q K^T   one N = 128 product per 16 of d, fp16, fp32 accumulators in tensor memory.  A q row is
 //               scaled by a power of two to a largest value in [2^14, 2^15) before it is rounded (the
@@ -16,7 +18,7 @@
 //   softmax     a thread a row; the running maximum is raised only when it grows by more than 8
 //               (log2 units); P <= 256 as bf16 over S;
 //   O += P V    bf16, fp32 accumulators in tensor memory.
-// At the end O, the maximum and the sum leave as the stream's partial, unnormalised.
+// At the end (but for DIRECT) O, the maximum and the sum leave as the stream's partial, unnormalised.
 //
 // Roles (512 threads, one CTA an SM):
 //   warp 0        TMA producer of K/V blocks
@@ -36,8 +38,11 @@
 
 namespace orthros {
 
-template <int D, bool ROWS2>
+enum { PT_KEYS2 = 0, PT_ROWS2 = 1, PT_DIRECT = 2 };
+
+template <int D, int MODE>
 struct PtCfg {
+    static constexpr bool ROWS2 = MODE != PT_KEYS2;
     static constexpr int KB = 64;
     static constexpr int SLABS = D / 64;
     static constexpr int TILES = ROWS2 ? 2 : 1;
@@ -65,12 +70,12 @@ struct PtCfg {
     static constexpr int CONV_THREADS = 192;
 };
 
-template <int D, int G, bool ROWS2>
+template <int D, int G, int MODE>
 __global__ void __launch_bounds__(512, 1)
-    prefix_tc_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
-                     const PrefixAttnParams p)
+    prefix_tc_kernel(const __grid_constant__ PrefixMaps maps, const PrefixAttnParams p)
 {
-    using C = PtCfg<D, ROWS2>;
+    using C = PtCfg<D, MODE>;
+    constexpr bool ROWS2 = C::ROWS2, DIRECT = MODE == PT_DIRECT;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw);
     const uint32_t pad = ((raw_s + 1023u) & ~1023u) - raw_s;
@@ -90,8 +95,13 @@ __global__ void __launch_bounds__(512, 1)
 
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const int split = blockIdx.x, g = blockIdx.y;
-    const long long row_base = static_cast<long long>(blockIdx.z) * 128 * C::TILES;
+    // rows row_base .. of a KV head, up to row_end: of the whole batch, or (DIRECT) of one sequence
     const long long R = static_cast<long long>(p.B) * p.T_out * G;
+    const int seq_tiles = DIRECT ? gridDim.z / p.B : 1, b_own = DIRECT ? blockIdx.z / seq_tiles : 0;
+    const long long row_base =
+        DIRECT ? static_cast<long long>(b_own) * p.T_out * G + static_cast<long long>(blockIdx.z % seq_tiles) * 256
+               : static_cast<long long>(blockIdx.z) * 128 * C::TILES;
+    const long long row_end = DIRECT ? static_cast<long long>(b_own + 1) * p.T_out * G : R;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::SLOTS; ++s) {
             mbar_init(&full[s], 1);
@@ -117,17 +127,35 @@ __global__ void __launch_bounds__(512, 1)
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_holder;
-    const int js = split * p.chunk, je = min(js + p.chunk, p.P);
+    const int js = DIRECT ? 0 : split * p.chunk, je = DIRECT ? p.P : min(js + p.chunk, p.P);
     const int nkb = (je - js + C::KB - 1) / C::KB;  // at least 1: the plan has no empty split
-    const int npair = (nkb + 1) / 2;
+    const int pre_blocks = (nkb + 1) / 2 * 2;        // whole pairs
+    // DIRECT: the sequence's own keys up to the largest position among the rows follow
+    int kmax = -1;
+    if constexpr (DIRECT) {
+        __shared__ int kmax_s;
+        if (threadIdx.x == 0)
+            kmax_s = -1;
+        __syncthreads();
+        if (threadIdx.x < 256 && row_base + threadIdx.x < row_end) {
+            const int pos = p.pos[static_cast<uint32_t>(row_base + threadIdx.x) / G];
+            if (pos >= 0 && pos < p.T_kv)
+                atomicMax(&kmax_s, pos);
+            else if ((row_base + threadIdx.x) % G == 0)
+                record_error(p.dev_err, ORTHROS_DEVERR_POSITION);
+        }
+        __syncthreads();
+        kmax = kmax_s;
+    }
+    const int npair = pre_blocks / 2 + (DIRECT ? (kmax + 2 * C::KB) / (2 * C::KB) : 0);
     auto pairs_of = [&](int t) { return ROWS2 ? npair : (npair - t + 1) / 2; };  // of stream t
     auto pair_at = [&](int t, int u) { return ROWS2 ? u : 2 * u + t; };           // its u-th
 
     if (warp == 0) {
         // ------------------------------------------------------------------ producer
         if (lane == 0) {
-            tma_prefetch_desc(&kmap);
-            tma_prefetch_desc(&vmap);
+            tma_prefetch_desc(&maps.k);
+            tma_prefetch_desc(&maps.v);
             for (int j = 0; j < 2 * npair; ++j) {
                 const int s = j % C::SLOTS;
                 if (j >= C::SLOTS && !mbar_wait(&empty[s], static_cast<uint32_t>(((j / C::SLOTS) - 1) & 1))) {
@@ -138,8 +166,12 @@ __global__ void __launch_bounds__(512, 1)
                 mbar_arrive_expect_tx(&full[s], 2 * C::SLABS * C::KB * 128);
 #pragma unroll
                 for (int sl = 0; sl < C::SLABS; ++sl) {
-                    tma_load_4d(smem + C::K_OFF + at + sl * C::PAIR_SLAB, &kmap, &full[s], sl * 64, g, js + j * C::KB, 0);
-                    tma_load_4d(smem + C::V_OFF + at + sl * C::PAIR_SLAB, &vmap, &full[s], sl * 64, g, js + j * C::KB, 0);
+                    const bool own = DIRECT && j >= pre_blocks;
+                    const int j0 = own ? (j - pre_blocks) * C::KB : js + j * C::KB;
+                    tma_load_4d(smem + C::K_OFF + at + sl * C::PAIR_SLAB, own ? &maps.ko : &maps.k, &full[s], sl * 64, g,
+                                j0, own ? b_own : 0);
+                    tma_load_4d(smem + C::V_OFF + at + sl * C::PAIR_SLAB, own ? &maps.vo : &maps.v, &full[s], sl * 64, g,
+                                j0, own ? b_own : 0);
                 }
             }
         }
@@ -241,6 +273,20 @@ __global__ void __launch_bounds__(512, 1)
                 shift_key_rows<C::SLABS>(blk, C::PAIR_SLAB, 0, cid >> 3, C::CONV_THREADS / 8, nrows, cid & 7,
                                          kexp + s * C::KB, bad);
             }
+            if constexpr (DIRECT) {
+                // V rows behind the last position have no weight, but may hold anything
+                const int beyond = kmax + 1 - (j - pre_blocks) * C::KB;  // first such row of the block
+                if (j >= pre_blocks && beyond < C::KB) {
+                    for (int it = 0; it < nrows; ++it) {
+                        const int r = (cid >> 3) + 24 * it;
+                        if (r >= beyond)
+#pragma unroll
+                            for (int sl = 0; sl < C::SLABS; ++sl)
+                                *reinterpret_cast<uint4 *>(blk + (C::V_OFF - C::K_OFF) + sl * C::PAIR_SLAB + r * 128 +
+                                                           (cid & 7) * 16) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+            }
             if (lane == 0)
                 smem[C::KFLAG_OFF + s * 8 + cw] = wany ? 1 : 0;
             fence_proxy_async_smem();
@@ -277,7 +323,8 @@ __global__ void __launch_bounds__(512, 1)
                 uint32_t have = 0;
 #pragma unroll
                 for (int x = 0; x < ROWS; ++x) {
-                    const PrefixRow row = prefix_row<G>(p, row_base + tl * 128 + r0 + x * C::RPP, g, D);
+                    const long long ri = row_base + tl * 128 + r0 + x * C::RPP;
+                    const PrefixRow row = prefix_row<G>(p, ri < row_end ? ri : R, g, D);
                     raw[x] = make_uint4(0, 0, 0, 0);
                     if (row.q != nullptr) {
                         raw[x] = __ldg(reinterpret_cast<const uint4 *>(row.q + 8 * cr));
@@ -322,8 +369,10 @@ __global__ void __launch_bounds__(512, 1)
         const int t = (warp - 4) >> 2;  // stream
         const int tile = ROWS2 ? t : 0, rw = warp & 3, r = rw * 32 + lane;
         const long long row_i = row_base + tile * 128 + r;
-        const bool work = row_base + tile * 128 + rw * 32 < R;  // the warp has a row
-        const PrefixRow row = prefix_row<G>(p, row_i, g, D);
+        const bool work = row_base + tile * 128 + rw * 32 < row_end;  // the warp has a row
+        const PrefixRow row = prefix_row<G>(p, row_i < row_end ? row_i : R, g, D);
+        // the row's last own key; without a position none, and its results are not used
+        const int pos = DIRECT && row.q != nullptr ? p.pos[static_cast<uint32_t>(row_i) / G] : -1;
         const uint32_t s_lane = tbase + (static_cast<uint32_t>(rw * 32) << 16) + C::TM_S + 128 * t;
         const uint32_t o_col = tbase + (static_cast<uint32_t>(rw * 32) << 16) + C::TM_O + D * t;
         const float NEG_INF = -__int_as_float(0x7f800000);
@@ -343,7 +392,8 @@ __global__ void __launch_bounds__(512, 1)
                 for (int hh = 0; hh < 2 && ok; ++hh) {
                     const int j = 2 * pp + hh, ks = j % C::SLOTS;
                     const uint32_t s_col = s_lane + 64 * hh;
-                    const int nvalid = je - 1 - (js + j * C::KB);  // column c is a key iff c <= nvalid
+                    // column c is a key iff c <= nvalid
+                    const int nvalid = DIRECT && j >= pre_blocks ? pos - (j - pre_blocks) * C::KB : je - 1 - (js + j * C::KB);
                     uint32_t va[32], vb[32];
                     tmem_ld32(s_col, va);
                     tmem_ld32(s_col + 32, vb);
@@ -456,8 +506,12 @@ __global__ void __launch_bounds__(512, 1)
             const bool store = row.slot >= 0, valid = row.q != nullptr && nu > 0;
             const long long part = ROWS2 ? split : 2 * split + t;
             const long long slot = part * R * p.Hkv + row.slot;
-            if (store)
+            if (!DIRECT && store)
                 p.part_ml[slot] = valid ? make_float2(m, l) : make_float2(NEG_INF, 0.f);
+            const float inv = l > 0.f ? 1.f / l : 0.f;
+            const uint32_t i_own = DIRECT ? static_cast<uint32_t>(row_i - static_cast<long long>(b_own) * p.T_out * G) / G : 0;
+            orthros_bf16 *orow =
+                DIRECT ? p.oc + b_own * p.oc_bstride + (static_cast<long long>(i_own) * p.Hq + row.head) * D : nullptr;
             if (nu > 0 && !(ok = mbar_wait(&o_final[t], 0)))
                 record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
             if (ok) {
@@ -470,11 +524,23 @@ __global__ void __launch_bounds__(512, 1)
                         tmem_wait_ld();
                     }
                     if (store) {
+                        if constexpr (DIRECT) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            const uint4 a = valid ? make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]) : make_uint4(0, 0, 0, 0);
-                            const uint4 b = valid ? make_uint4(v[e + 4], v[e + 5], v[e + 6], v[e + 7]) : make_uint4(0, 0, 0, 0);
-                            st_global_v8(p.part_o + slot * D + c + e, a, b);
+                            for (int e = 0; e < 32; e += 8) {
+                                uint32_t w[4];
+#pragma unroll
+                                for (int x = 0; x < 4; ++x)
+                                    w[x] = valid ? pack_bf16x2(__uint_as_float(v[e + 2 * x]) * inv,
+                                                               __uint_as_float(v[e + 2 * x + 1]) * inv) : 0u;
+                                *reinterpret_cast<uint4 *>(orow + c + e) = make_uint4(w[0], w[1], w[2], w[3]);
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 32; e += 8) {
+                                const uint4 a = valid ? make_uint4(v[e], v[e + 1], v[e + 2], v[e + 3]) : make_uint4(0, 0, 0, 0);
+                                const uint4 b = valid ? make_uint4(v[e + 4], v[e + 5], v[e + 6], v[e + 7]) : make_uint4(0, 0, 0, 0);
+                                st_global_v8(p.part_o + slot * D + c + e, a, b);
+                            }
                         }
                     }
                 }
@@ -495,12 +561,12 @@ __global__ void __launch_bounds__(512, 1)
     }
 }
 
-template <int D, int G, bool ROWS2>
-static cudaError_t launch_ptc(const CUtensorMap &k, const CUtensorMap &v, const PrefixAttnParams &p, int splits, int tiles,
+template <int D, int G, int MODE>
+static cudaError_t launch_ptc(const PrefixMaps &maps, const PrefixAttnParams &p, int splits, int tiles,
                               cudaStream_t stream)
 {
-    using C = PtCfg<D, ROWS2>;
-    auto kern = prefix_tc_kernel<D, G, ROWS2>;
+    using C = PtCfg<D, MODE>;
+    auto kern = prefix_tc_kernel<D, G, MODE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess)
         return e;
@@ -514,18 +580,26 @@ static cudaError_t launch_ptc(const CUtensorMap &k, const CUtensorMap &v, const 
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, k, v, p);
+    e = cudaLaunchKernelEx(&cfg, kern, maps, p);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
-cudaError_t launch_prefix_tc(int D, bool rows2, const CUtensorMap &k, const CUtensorMap &v, const PrefixAttnParams &p,
-                             int splits, int tiles, cudaStream_t stream)
+template <int D, int G>
+static cudaError_t launch_ptc_mode(int mode, const PrefixMaps &maps, const PrefixAttnParams &p, int splits, int tiles,
+                                   cudaStream_t stream)
+{
+    return mode == PT_KEYS2   ? launch_ptc<D, G, PT_KEYS2>(maps, p, splits, tiles, stream)
+           : mode == PT_ROWS2 ? launch_ptc<D, G, PT_ROWS2>(maps, p, splits, tiles, stream)
+                              : launch_ptc<D, G, PT_DIRECT>(maps, p, 1, tiles, stream);
+}
+
+cudaError_t launch_prefix_tc(int D, int mode, const PrefixMaps &maps, const PrefixAttnParams &p, int splits, int tiles,
+                             cudaStream_t stream)
 {
     const int G = p.Hq / p.Hkv;
-#define ORTHROS_PTC_CASE(DD, GG)                                                         \
-    if (D == DD && G == GG)                                                              \
-        return rows2 ? launch_ptc<DD, GG, true>(k, v, p, splits, tiles, stream)          \
-                     : launch_ptc<DD, GG, false>(k, v, p, splits, tiles, stream);
+#define ORTHROS_PTC_CASE(DD, GG) \
+    if (D == DD && G == GG)      \
+        return launch_ptc_mode<DD, GG>(mode, maps, p, splits, tiles, stream);
     ORTHROS_PTC_CASE(128, 1)
     ORTHROS_PTC_CASE(128, 2)
     ORTHROS_PTC_CASE(128, 4)
@@ -538,6 +612,20 @@ cudaError_t launch_prefix_tc(int D, bool rows2, const CUtensorMap &k, const CUte
     ORTHROS_PTC_CASE(64, 16)
 #undef ORTHROS_PTC_CASE
     return cudaErrorInvalidValue;
+}
+
+// Many copies a sequence: tiles of 256 rows of one sequence each, prefix and own rows in one pass and
+// no partials.  Taken when padding the last tile costs at most a third and the tiles fill at least
+// half of the SMs (one CTA runs over all keys of its rows); otherwise splitting the prefix pays.
+int prefix_direct_tiles(int B, int T_out, int Hq, int Hkv)
+{
+    const long long rows = static_cast<long long>(T_out) * (Hq / Hkv), tiles = (rows + 255) / 256;
+    return tiles * 256 * 3 <= rows * 4 && B * tiles * Hkv >= 76 && B * tiles <= 65535 ? static_cast<int>(tiles) : 0;
+}
+
+cudaError_t launch_prefix_direct(int D, const PrefixMaps &maps, const PrefixAttnParams &p, cudaStream_t stream)
+{
+    return launch_prefix_tc(D, PT_DIRECT, maps, p, 1, p.B * prefix_direct_tiles(p.B, p.T_out, p.Hq, p.Hkv), stream);
 }
 
 }  // namespace orthros

@@ -2,7 +2,7 @@
 // prompt prefix: copy i of sequence b attends over the prefix rows 0 .. P-1 and its sequence's
 // own rows 0 .. pos.  The prefix kernel takes all rows of the batch over the prefix, the split-KV
 // kernels of xattn_fwd.cu the copies over their own rows, each writing partials; one combine
-// kernel joins both.
+// kernel joins both.  Many copies a sequence take prefix and own rows in one kernel instead.
 #include "kernels.cuh"
 
 namespace orthros {
@@ -16,7 +16,9 @@ struct XpLayout {
 
 XpLayout xp_layout(int B, int T_out, int P, int T_kv, int Hq, int Hkv, int D)
 {
-    XpLayout l;
+    XpLayout l = {0, 0, 0, 256};
+    if (prefix_direct_tiles(B, T_out, Hq, Hkv) > 0)
+        return l;
     l.pre = prefix_attn_parts(static_cast<long long>(B) * T_out, P, Hq, Hkv);
     l.own = xattn_parts(B, T_out, T_kv, Hq, Hkv);
     const size_t slots = (static_cast<size_t>(l.pre) + l.own) * B * T_out * Hq;
@@ -53,6 +55,11 @@ cudaError_t launch_xattn_prefix(int D, const CUtensorMap *m, XattnParams x, int 
     a.Hq = x.Hq;
     a.Hkv = x.Hkv;
     a.qscale = x.qscale;
+    if (prefix_direct_tiles(x.B, x.T_out, x.Hq, x.Hkv) > 0) {
+        a.oc = x.oc;
+        a.oc_bstride = x.oc_bstride;
+        return launch_prefix_direct(D, PrefixMaps{m[2], m[3], m[0], m[1]}, a, stream);
+    }
     cudaError_t e = launch_prefix_attn(D, m[2], m[3], a, stream);
     if (e != cudaSuccess)
         return e;

@@ -51,6 +51,11 @@ class Copies:
     (1, 300, 450, 310, 8, 2, 128),
     (1, 260, 100, 300, 2, 2, 64),        # G = 1, many copies
     (4, 1, 20000, 64, 8, 1, 128),        # a long prefix, one KV head
+    (2, 320, 333, 400, 32, 8, 128),      # many copies a sequence: prefix and own rows in one pass
+    (5, 60, 129, 61, 64, 8, 64),         # the same with G = 8, a padded tile
+    (5, 400, 70, 500, 8, 8, 64),         # G = 1
+    (7, 48, 1, 130, 64, 4, 128),         # G = 16
+    (10, 250, 64, 64, 16, 8, 128),       # G = 2
 ])
 def test_copies_match_oracle(B, T_out, P, T_kv, Hq, Hkv, d):
     c = Copies(B, T_out, P, T_kv, Hq, Hkv, d, 200 + P)
@@ -61,7 +66,7 @@ def test_copies_match_oracle(B, T_out, P, T_kv, Hq, Hkv, d):
     assert_parity(val(got), c.oracle(), "copies")
 
 
-@pytest.mark.parametrize("B,T_out,Hq,Hkv", [(2, 3, 8, 2), (16, 1, 32, 8), (2, 80, 8, 2)])
+@pytest.mark.parametrize("B,T_out,Hq,Hkv", [(2, 3, 8, 2), (16, 1, 32, 8), (2, 80, 8, 2), (10, 62, 32, 8)])
 def test_copies_out_of_range_are_zero_and_reported(B, T_out, Hq, Hkv):
     c = Copies(B, T_out, 300, 50, Hq, Hkv, 128, 21)
     ref = c.oracle()
@@ -72,6 +77,18 @@ def test_copies_out_of_range_are_zero_and_reported(B, T_out, Hq, Hkv):
     assert not got[0, 0].any() and not got[-1, -1].any()
     ref[0, 0], ref[-1, -1] = 0, 0
     assert_parity(got, ref, "the others")
+
+
+@pytest.mark.parametrize("B,T_out,Hq,Hkv,used", [(10, 64, 32, 8, 130), (10, 64, 32, 8, 64)])
+def test_rows_behind_the_last_position_do_not_matter(B, T_out, Hq, Hkv, used):
+    """Own rows that no copy of the batch has reached hold NaN."""
+    c = Copies(B, T_out, 200, 300, Hq, Hkv, 128, 24)
+    c.pos = np.minimum(c.pos, used - 1)
+    c.pos[:, 0] = used - 1
+    k, v = c.k.copy(), c.v.copy()
+    k[:, used:], v[:, used:] = 0x7FC0, 0x7FC0
+    got = orth.xattn_prefix_fwd(bf(c.qc), i32(c.pos), bf(c.kp), bf(c.vp), bf(k), bf(v), f32(c.ac), f32(c.bc), scale=c.scale)
+    assert_parity(val(got), c.oracle(), "copies")
 
 
 def test_copies_strided_and_repeatable():
@@ -107,12 +124,15 @@ def test_copies_strided_and_repeatable():
         np.testing.assert_array_equal(bits(out[:, :T_out]), ref)
 
 
-@pytest.mark.parametrize("rows", [1, 16, 40, 300])
+@pytest.mark.parametrize("rows", [1, 16, 40, 300, -1])
 def test_copies_with_large_keys(rows):
     """Keys four times as large at a few rows (logits that decide) and key rows beyond fp16's range against small
     queries, in the prefix and among the own rows."""
     B, P, T_kv, Hq, Hkv, d = rows, 500, 66, 4, 1, 128
-    c = Copies(B, 1, P, T_kv, Hq, Hkv, d, 23)
+    T_out = 1
+    if rows < 0:  # many copies a sequence
+        B, T_out, Hq, Hkv = 10, 64, 32, 8
+    c = Copies(B, T_out, P, T_kv, Hq, Hkv, d, 23)
     c.kp[100], c.k[:, 3] = c.kp[100] + (2 << 7), c.k[:, 3] + (2 << 7)  # exponent + 2
     c.kp[200, :, 5] = 0x4800  # 2^17 in one column
     c.k[:, 10, :, 5] = 0x4800
