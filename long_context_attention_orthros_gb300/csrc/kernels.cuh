@@ -143,6 +143,8 @@ struct PrefixAttnParams {
     int B, T_out, T_kv, P, Hq, Hkv;
     int chunk;  // keys of a split, set by the launcher
     float qscale;
+    int *clear;  // optional: n_clear ints that the kernel sets to zero before a dependent kernel reads them
+    int n_clear;
 };
 struct PrefixMaps {
     CUtensorMap k, v, ko, vo;  // the prefix's K and V; the sequences' own (launch_prefix_direct)
@@ -176,12 +178,18 @@ struct ServeParams {
     int B, Hq, Hkv, L_max, window;
     int P, n_part;            // prefix rows (0: 8-bit form) and splits
     float qscale;
+    long long q_bstride, o_bstride;  // elements between sequences of q_new, qc_new and of o, oc; set by the launchers
 };
 size_t serve_workspace_bytes(int B, int P, int L_max, int Hq, int Hkv, int D);
 // code: ORTHROS_KV_E4M3 / ORTHROS_KV_INT8, or -1 for bf16 caches behind a shared prefix; maps: the
 // cache's K and V, then the prefix's (boxes of 64 x 1 x 64; the 8-bit cache's d x 1 x 64)
 cudaError_t launch_serve(int D, int code, const CUtensorMap *maps, ServeParams p, void *workspace,
                          cudaStream_t stream);
+
+// one copy a sequence (T_out = 1) over a shared prefix and its own rows; maps as above, workspace of
+// serve_workspace_bytes(B, P, T_kv, ...), not initialised
+cudaError_t launch_serve_copies(int D, const CUtensorMap *maps, const XattnParams &p, int P, void *workspace,
+                                cudaStream_t stream);
 
 // output copies over a shared prefix and their own rows; maps: own K and V, the prefix's K and V
 size_t xattn_prefix_workspace_bytes(int B, int T_out, int P, int T_kv, int Hq, int Hkv, int D);

@@ -54,6 +54,9 @@ __global__ void __launch_bounds__(PaCfg<D>::THREADS)
     // what the kernels before wrote first, then a dependent grid may start beside this one
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (p.clear != nullptr && blockIdx.x + blockIdx.y + blockIdx.z == 0)
+        for (int i = threadIdx.x; i < p.n_clear; i += blockDim.x)
+            p.clear[i] = 0;
     __syncthreads();
     const int js = split * p.chunk, je = min(js + p.chunk, p.P);
     const int nblk = je > js ? (je - js + C::KB - 1) / C::KB : 0;

@@ -124,6 +124,9 @@ __global__ void __launch_bounds__(512, 1)
     // what the kernels before wrote first, then a dependent grid may start beside this one
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    if (p.clear != nullptr && blockIdx.x + blockIdx.y + blockIdx.z == 0)
+        for (int i = threadIdx.x; i < p.n_clear; i += blockDim.x)
+            p.clear[i] = 0;
     __syncthreads();
     tc_fence_after();
     const uint32_t tbase = *tmem_holder;

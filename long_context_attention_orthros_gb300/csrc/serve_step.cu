@@ -12,7 +12,7 @@
 // batch loads every SM alike.  A CTA's blocks arrive by TMA through a ring that runs on across
 // segment borders (one producer warp); a segment counts a few places more than its blocks, for
 // what its start and end cost.  Four warps take 16 keys of a block each (or 32 of
-// every other block), with the G query
+// every other block), with the query
 // rows of a KV head on the MMA's N side, and their results meet in shared memory.  A segment that
 // one CTA holds whole is written out at once; otherwise each CTA writes one partial (max, sum,
 // o), goes on, and when it has run out of blocks counts itself in: the last to finish a segment
@@ -25,7 +25,8 @@
 //
 // In the prefix form the copy's attention over the prefix itself runs in a kernel of its own
 // before this one, for all rows of the batch at once (prefix_attn.cu); this kernel is launched as
-// its programmatic dependent and waits for it only where it joins a copy's partials.
+// its programmatic dependent and waits for it only where it joins a copy's partials.  The same
+// kernel without window and append serves one copy a sequence behind a prefix (a prompt's end).
 #include <type_traits>
 
 #include "kernels.cuh"
@@ -44,9 +45,14 @@ struct Join {
 };
 constexpr int MAX_JOINS = 32;
 
+// what the kernel does beside the two 8-bit forms (ORTHROS_KV_E4M3, ORTHROS_KV_INT8)
+constexpr int SV_PREFIX = -1;  // a decode step behind a shared prefix
+constexpr int SV_COPIES = -2;  // one copy a sequence behind a shared prefix: no window, no append
+
 template <int D, int G, int CODE>
 struct SvCfg {
-    static constexpr bool Q8 = CODE >= 0;
+    static constexpr bool Q8 = CODE >= 0, STEP = CODE != SV_COPIES;
+    static constexpr int SEGS = STEP ? 2 : 1;  // segments of a (b, KV head)
     static constexpr int KB = 64;
     static constexpr int KV_BYTES = KB * D * (Q8 ? 1 : 2);
     static constexpr int SLAB = KB * 128;  // bf16: one 64-wide slab
@@ -90,34 +96,37 @@ struct SvCfg {
 // short segments gets fewer blocks.
 constexpr int SEG_COST = 4;
 
-// what a sequence's cache_len makes of it
+// what a sequence's length makes of it
 struct SeqPlan {
-    int p;         // the new token's own row
-    int full;      // nothing fits: zero outputs, no append
-    int nc, nb;    // blocks of the copy's and of the base token's segment
-    int npb;       // base blocks in the prefix (they come first)
-    int pb0, ob0;  // their first block, and the first own block
+    int p;         // the last own row: the new token's, or the copy's position
+    int full;      // no such row: zero outputs, no append
+    int nc, nb;    // blocks of the copy's segment and of the base token's
+    int npb;       // window blocks in the prefix; they come first
+    int pb0, ob0;  // their first block, and the first own block of the window
     int lo_p, lo;  // first prefix row and first own row of the window
 };
 
+template <class C>
 __device__ __forceinline__ SeqPlan seq_plan(const ServeParams &p, int len)
 {
     SeqPlan s;
     s.p = len;
     s.full = s.p < 0 || s.p >= p.L_max;
     s.npb = s.pb0 = s.ob0 = s.lo_p = s.lo = 0;
-    s.nc = s.nb = 1;
+    s.nc = 1;
+    s.nb = C::SEGS - 1;
     if (!s.full) {
-        const int lo = s.p - p.window + 1;  // window >= 1, p >= 0: no overflow
-        s.lo = lo > 0 ? lo : 0;
-        s.ob0 = s.lo / 64;
         s.nc = s.p / 64 + 1;
-        s.nb = s.nc - s.ob0;
-        if (p.P > 0 && lo < 0) {
-            s.lo_p = p.P + lo > 0 ? p.P + lo : 0;
-            s.pb0 = s.lo_p / 64;
-            s.npb = (p.P - 1) / 64 + 1 - s.pb0;
-            s.nb += s.npb;
+        if constexpr (C::STEP) {
+            const int lo = s.p - p.window + 1;  // window >= 1, p >= 0: no overflow
+            s.lo = lo > 0 ? lo : 0;
+            if (p.P > 0 && lo < 0) {
+                s.lo_p = p.P + lo > 0 ? p.P + lo : 0;
+                s.pb0 = s.lo_p / 64;
+                s.npb = (p.P - 1) / 64 + 1 - s.pb0;
+            }
+            s.ob0 = s.lo / 64;
+            s.nb = s.nc - s.ob0 + s.npb;
         }
     }
     return s;
@@ -129,10 +138,11 @@ struct Cursor {
     SeqPlan s;
     __device__ __forceinline__ int blocks() const { return base ? s.nb : s.nc; }
     __device__ __forceinline__ int places() const { return SEG_COST + blocks(); }
+    template <class C>
     __device__ __forceinline__ void next_segment(const ServeParams &p)
     {
         r = 0;
-        if (!base) {
+        if (C::SEGS == 2 && !base) {
             base = 1;
             return;
         }
@@ -140,15 +150,23 @@ struct Cursor {
         if (++g == p.Hkv) {
             g = 0;
             if (++b < p.B)
-                s = seq_plan(p, __ldcg(p.cache_len + b));
+                s = seq_plan<C>(p, __ldcg(p.cache_len + b));
         }
+    }
+    // block r of the segment: whether it lies in the prefix, and which 64 rows it holds there
+    template <class C>
+    __device__ __forceinline__ int block(int i, bool &pre) const
+    {
+        pre = C::STEP && base && i < s.npb;
+        return pre ? s.pb0 + i : (base ? s.ob0 + i - s.npb : i);
     }
 };
 
+template <class C>
 __device__ __forceinline__ long long seq_places(const ServeParams &p, int len)
 {
-    const SeqPlan s = seq_plan(p, len);
-    return static_cast<long long>(s.nc + s.nb + 2 * SEG_COST) * p.Hkv;
+    const SeqPlan s = seq_plan<C>(p, len);
+    return static_cast<long long>(s.nc + s.nb + C::SEGS * SEG_COST) * p.Hkv;
 }
 
 // Called by a whole warp: CTA c of at most n takes places it0 .. it1 - 1 of the list's W, and its
@@ -158,14 +176,15 @@ struct Share {
     Cursor cur;
 };
 
+template <class C>
 __device__ __forceinline__ Share plan_share(const ServeParams &p, long long c, long long n)
 {
     const int lane = threadIdx.x & 31;
     Share sh;
     int len = lane < p.B ? __ldcg(p.cache_len + lane) : 0;
-    long long w = lane < p.B ? seq_places(p, len) : 0, W = w;
+    long long w = lane < p.B ? seq_places<C>(p, len) : 0, W = w;
     for (int b = lane + 32; b < p.B; b += 32)
-        W += seq_places(p, __ldcg(p.cache_len + b));
+        W += seq_places<C>(p, __ldcg(p.cache_len + b));
 #pragma unroll
     for (int off = 16; off > 0; off >>= 1)
         W += __shfl_xor_sync(0xffffffffu, W, off);
@@ -180,7 +199,7 @@ __device__ __forceinline__ Share plan_share(const ServeParams &p, long long c, l
     for (int b0 = 0; b0 < p.B; b0 += 32) {
         if (b0 > 0) {
             len = b0 + lane < p.B ? __ldcg(p.cache_len + b0 + lane) : 0;
-            w = b0 + lane < p.B ? seq_places(p, len) : 0;
+            w = b0 + lane < p.B ? seq_places<C>(p, len) : 0;
         }
         long long inc = w;
 #pragma unroll
@@ -194,15 +213,15 @@ __device__ __forceinline__ Share plan_share(const ServeParams &p, long long c, l
             const int f = __ffs(here) - 1;
             it -= __shfl_sync(0xffffffffu, inc - w, f);
             sh.cur.b = b0 + f;
-            sh.cur.s = seq_plan(p, __shfl_sync(0xffffffffu, len, f));
+            sh.cur.s = seq_plan<C>(p, __shfl_sync(0xffffffffu, len, f));
             break;
         }
         it -= __shfl_sync(0xffffffffu, inc, 31);
     }
-    const int per = sh.cur.s.nc + sh.cur.s.nb + 2 * SEG_COST;
+    const int per = sh.cur.s.nc + sh.cur.s.nb + C::SEGS * SEG_COST;
     sh.cur.g = static_cast<int>(it / per);
     sh.cur.r = static_cast<int>(it % per);
-    sh.cur.base = sh.cur.r >= sh.cur.s.nc + SEG_COST;
+    sh.cur.base = C::SEGS == 2 && sh.cur.r >= sh.cur.s.nc + SEG_COST;
     sh.cur.r -= sh.cur.base ? sh.cur.s.nc + SEG_COST : 0;
     return sh;
 }
@@ -216,7 +235,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
     serve_step_kernel(const __grid_constant__ ServeMaps maps, const ServeParams p)
 {
     using C = SvCfg<D, G, CODE>;
-    constexpr bool Q8 = C::Q8;
+    constexpr bool Q8 = C::Q8, STEP = C::STEP;
     constexpr int NT = (G + 7) / 8;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw);
@@ -249,7 +268,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
     if constexpr (Q8)
         asm volatile("griddepcontrol.wait;" ::: "memory");
     const long long c = blockIdx.x;
-    const Share sh = plan_share(p, c, gridDim.x);
+    const Share sh = plan_share<C>(p, c, gridDim.x);
     const long long W = sh.W, n = sh.n, it0 = sh.it0, it1 = sh.it1;
     Cursor cur = sh.cur;
     __syncthreads();  // barriers are set up, and every warp has read cache_len
@@ -274,14 +293,15 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
                 }
                 uint8_t *h = smem + C::HDR_OFF + hb * C::HDR_BYTES;
                 const long long go = static_cast<long long>(cur.g) * G * D;
-                mbar_arrive_expect_tx(&hfull[hb], C::HDR_BYTES);
-                bulk_load(h, (cur.base ? p.q_new : p.qc_new) + static_cast<long long>(cur.b) * p.Hq * D + go, G * D * 2,
-                          &hfull[hb]);
+                mbar_arrive_expect_tx(&hfull[hb], STEP ? C::HDR_BYTES : C::HDR_NEW);
+                bulk_load(h, (cur.base ? p.q_new : p.qc_new) + cur.b * p.q_bstride + go, G * D * 2, &hfull[hb]);
                 bulk_load(h + G * D * 2, (cur.base ? p.alpha : p.alpha_c) + go, G * D * 4, &hfull[hb]);
                 bulk_load(h + G * D * 6, (cur.base ? p.beta : p.beta_c) + go, G * D * 4, &hfull[hb]);
-                const long long no = (static_cast<long long>(cur.b) * p.Hkv + cur.g) * D;
-                bulk_load(h + C::HDR_NEW, p.k_new + no, D * 2, &hfull[hb]);
-                bulk_load(h + C::HDR_NEW + D * 2, p.v_new + no, D * 2, &hfull[hb]);
+                if constexpr (STEP) {
+                    const long long no = (static_cast<long long>(cur.b) * p.Hkv + cur.g) * D;
+                    bulk_load(h + C::HDR_NEW, p.k_new + no, D * 2, &hfull[hb]);
+                    bulk_load(h + C::HDR_NEW + D * 2, p.v_new + no, D * 2, &hfull[hb]);
+                }
                 header = false;
                 ++segs;
             }
@@ -290,9 +310,8 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
                 record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
                 return;
             }
-            const int r = cur.r - SEG_COST;
-            const bool pre = cur.base && r < cur.s.npb;
-            const int blk = cur.base ? (pre ? cur.s.pb0 + r : cur.s.ob0 + r - cur.s.npb) : r;
+            bool pre;
+            const int blk = cur.block<C>(cur.r - SEG_COST, pre);
             const int j0 = blk * C::KB;
             uint8_t *dst = smem + s * 2 * C::KV_BYTES;
             if constexpr (Q8) {
@@ -316,7 +335,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
             }
             ++i;
             if (++cur.r == cur.places() && it + 1 < it1) {
-                cur.next_segment(p);
+                cur.next_segment<C>(p);
                 header = true;
             }
         }
@@ -332,9 +351,13 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
     long long i = 0;
     int segs = 0, njoin = 0;
     // Joins the segments on the list: each counts this CTA in (after its partials: the barrier orders
-    // them before the fence), and those that it was the last to finish are joined, a warp a row.
+    // them before the fence), and those that it was the last to finish are joined, half a warp a row.
     // At the end of the CTA's work only, so that no wait for memory stands between two segments.
     auto join_all = [&](bool final) {
+        // the prefix kernel's partials and, for SV_COPIES, the counters that it cleared; and the step
+        // has ended only when that kernel has
+        if constexpr (!Q8)
+            asm volatile("griddepcontrol.wait;" ::: "memory");
         named_barrier(1, C::CTHREADS);
         if (t < njoin) {
             Join &j = joins[t];
@@ -346,81 +369,91 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
             if (last)
                 *cnt = 0;
         }
-        if (final && t == C::CTHREADS - 1)  // every warp of this CTA has read cache_len for the last time
+        if (STEP && final && t == C::CTHREADS - 1)  // every warp of this CTA has read cache_len for the last time
             s_flag[0] = atomicAdd(p.cnt_all, 1) == static_cast<int>(gridDim.x) - 1;
-        if constexpr (!Q8) {
-            // the prefix kernel's partials; and the step has ended only when that kernel has
-            asm volatile("griddepcontrol.wait;" ::: "memory");
-        }
         named_barrier(1, C::CTHREADS);
         const long long BH = static_cast<long long>(p.B) * p.Hkv;
-        for (int x = warp; x < njoin * G; x += C::CWARPS) {
-            const Join j = joins[x / G];
-            const int row = x % G;
-            if (!j.last)
-                continue;
+        // half a warp a row: E columns a lane, 16 parts' weights in its lanes, 8 parts' loads in flight
+        constexpr int E = D / 16;
+        const int half = lane >> 4, hl = lane & 15, total = njoin * G;
+        for (int x0 = 2 * warp; x0 < total; x0 += 2 * C::CWARPS) {
+            const bool on = x0 + half < total;
+            const Join j = joins[on ? (x0 + half) / G : 0];
+            const int row = (x0 + half) % G;
+            const bool base = j.base;
             // parts: the CTAs' own, then (a copy behind a prefix) the prefix splits'
-            const int nq = j.parts + (!Q8 && !j.base ? p.n_part : 0);
+            const int nown = j.parts;
+            const int nq = on && j.last ? nown + (!Q8 && !base ? p.n_part : 0) : 0;
+            const int nmax = max(nq, __shfl_xor_sync(0xffffffffu, nq, 16));
+            if (nmax == 0)
+                continue;
             auto slot_of = [&](int q) -> long long {
-                return q < j.parts ? (j.parts == 1 ? 2LL * gridDim.x + j.bh : 2LL * (j.c0 + q) + (q == 0 ? 1 : 0)) * G + row
-                                   : ((q - j.parts) * BH + j.bh) * G + row;
+                return q < nown ? (j.parts == 1 ? 2LL * gridDim.x + j.bh
+                                                : 2LL * (j.c0 + q) + (q == 0 ? 1 : 0)) * G + row
+                                : ((q - nown) * BH + j.bh) * G + row;
             };
             auto ml_of = [&](int q) -> float2 {
-                return q >= nq ? make_float2(NEG_INF, 0.f) : __ldcg((q < j.parts ? p.part_ml : p.pre_ml) + slot_of(q));
+                return q >= nq ? make_float2(NEG_INF, 0.f) : __ldcg((q < nown ? p.part_ml : p.pre_ml) + slot_of(q));
             };
-            const float2 ml0 = ml_of(lane);
-            float M = ml0.x, L = 0.f;
-            for (int q = lane + 32; q < nq; q += 32)
+            float y[8][E];
+            auto load = [&](int q0) {  // past the end the last part again: its weight there is zero
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const int q = min(q0 + k, nq - 1);
+#pragma unroll
+                    for (int e = 0; e < E; e += 4) {
+                        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (nq > 0)
+                            v = __ldcg(reinterpret_cast<const float4 *>((q < nown ? p.part_o : p.pre_o) + slot_of(q) * D +
+                                                                        hl * E + e));
+                        y[k][e] = v.x;
+                        y[k][e + 1] = v.y;
+                        y[k][e + 2] = v.z;
+                        y[k][e + 3] = v.w;
+                    }
+                }
+            };
+            float2 ml = ml_of(hl);
+            load(0);
+            float M = ml.x, L = 0.f, w = 0.f;
+            for (int q = hl + 16; q < nq; q += 16)
                 M = fmaxf(M, ml_of(q).x);
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
+            for (int off = 8; off > 0; off >>= 1)
                 M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-            constexpr int E = D / 32;
             float a[E];
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 a[e] = 0.f;
-            for (int q0 = 0; q0 < nq; q0 += 32) {
-                const float2 ml = q0 == 0 ? ml0 : ml_of(q0 + lane);
-                const float w = ml.x == NEG_INF ? 0.f : fast_exp2(ml.x - M);
-                L += w * ml.y;
-                // eight parts' loads in flight; past the end the last part with a weight of zero
-                for (int k0 = 0; k0 < min(32, nq - q0); k0 += 8) {
-                    float y[8][E];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int q = min(q0 + k0 + k, nq - 1);
-                        const float *src = (q < j.parts ? p.part_o : p.pre_o) + slot_of(q) * D + lane * E;
-                        if constexpr (E == 4) {
-                            const float4 v = __ldcg(reinterpret_cast<const float4 *>(src));
-                            y[k][0] = v.x;
-                            y[k][1] = v.y;
-                            y[k][2] = v.z;
-                            y[k][3] = v.w;
-                        } else {
-                            const float2 v = __ldcg(reinterpret_cast<const float2 *>(src));
-                            y[k][0] = v.x;
-                            y[k][1] = v.y;
-                        }
-                    }
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const float wk = __shfl_sync(0xffffffffu, w, k0 + k);
-#pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            a[e] = fmaf(wk, y[k][e], a[e]);
-                    }
+            for (int q0 = 0; q0 < nmax; q0 += 8) {
+                if (q0 % 16 == 0) {
+                    if (q0 > 0)
+                        ml = ml_of(q0 + hl);
+                    w = ml.x == NEG_INF ? 0.f : fast_exp2(ml.x - M);
+                    L += w * ml.y;
                 }
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float wk = __shfl_sync(0xffffffffu, w, 16 * half + q0 % 16 + k);
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        a[e] = fmaf(wk, y[k][e], a[e]);
+                }
+                if (q0 + 8 < nmax)
+                    load(q0 + 8);
             }
 #pragma unroll
-            for (int off = 16; off > 0; off >>= 1)
+            for (int off = 8; off > 0; off >>= 1)
                 L += __shfl_xor_sync(0xffffffffu, L, off);
             const float inv = L > 0.f ? 1.f / L : 0.f;
-            orthros_bf16 *orow = (j.base ? p.o : p.oc) +
-                                 (static_cast<long long>(j.bh / p.Hkv) * p.Hq + (j.bh % p.Hkv) * G + row) * D + lane * E;
+            orthros_bf16 *orow = (base ? p.o : p.oc) + (j.bh / p.Hkv) * p.o_bstride +
+                                 ((j.bh % p.Hkv) * G + row) * D + hl * E;
+            if (nq > 0) {
 #pragma unroll
-            for (int e = 0; e < E; e += 2)
-                *reinterpret_cast<uint32_t *>(orow + e) = pack_bf16x2(a[e] * inv, a[e + 1] * inv);
+                for (int e = 0; e < E; e += 4)
+                    *reinterpret_cast<uint2 *>(orow + e) = make_uint2(pack_bf16x2(a[e] * inv, a[e + 1] * inv),
+                                                                      pack_bf16x2(a[e + 2] * inv, a[e + 3] * inv));
+            }
         }
         njoin = 0;
         named_barrier(1, C::CTHREADS);  // the list may be filled again
@@ -466,7 +499,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
         // the new rows as this lane takes them: lanes 0 .. 15 of K's, 16 .. 31 of V's, D / 16 values each
         const int kv = lane >> 4;
         uint32_t fresh_w[D / 32];
-        {
+        if constexpr (STEP) {
             const uint32_t *src = reinterpret_cast<const uint32_t *>(smem + C::HDR_OFF + (segs % C::HB) * C::HDR_BYTES +
                                                                      C::HDR_NEW) + lane * (D / 32);
 #pragma unroll
@@ -482,12 +515,10 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
             if (C::KT == 2 && (i & 1) != (warp >> 1))
                 continue;  // the other pair's block
             const int s = static_cast<int>(i % C::STAGES);
-            const int r = first + x;
-            const bool pre = cur.base && r < sp.npb;
-            const int blk = cur.base ? (pre ? sp.pb0 + r : sp.ob0 + r - sp.npb) : r;
+            bool pre;
+            const int blk = cur.block<C>(first + x, pre);
             // the block's rows that count: lo .. hi
-            const int lo = (cur.base ? (pre ? sp.lo_p : sp.lo) : 0) - blk * C::KB;
-            const int hi = (pre ? p.P - 1 : sp.p) - blk * C::KB;
+            const int lo = (cur.base ? (pre ? sp.lo_p : sp.lo) : 0) - blk * C::KB, hi = (pre ? p.P - 1 : sp.p) - blk * C::KB;
             if (ok && !mbar_wait(&full[s], static_cast<uint32_t>((i / C::STAGES) & 1)))
                 ok = false;
             constexpr int WK = 16 * C::KT;  // this warp's keys: rows r0 .. r0 + WK - 1 of the block
@@ -495,79 +526,88 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
             if (ok && !sp.full && r0 <= hi && r0 + WK - 1 >= lo) {
                 uint8_t *kb = smem + s * 2 * C::KV_BYTES, *vb = kb + C::KV_BYTES;
                 int8_t *ke = reinterpret_cast<int8_t *>(smem + C::EXP_OFF + s * 2 * C::KB), *ve = ke + C::KB;
-                const bool whole = lo <= r0 && r0 + WK - 1 < (pre ? hi + 1 : hi);  // row p itself is patched in
-                if (!whole) {
-                    // V rows that do not count become zeros (their weight is zero, but they may hold
-                    // anything), and the new row is put where it belongs
+                bool patched = false;
+                // V rows that do not count become zeros: their weight is zero, but they may hold anything
+                // (before the window, and behind the last row, which no token has reached)
+                auto zero_rows = [&](int from, int to) {
                     constexpr int CH = D * (Q8 ? 1 : 2) / 16;  // 16-byte chunks of a row
+                    from = max(from, r0);
+                    to = min(to, r0 + WK);
 #pragma unroll 1
-                    for (int e = lane; e < WK * CH; e += 32) {
-                        const int rr = r0 + e / CH, c16 = e % CH;
-                        if (rr >= lo && rr <= hi)
-                            continue;
-                        uint8_t *to;
+                    for (int e = lane; e < (to - from) * CH; e += 32) {
+                        const int rr = from + e / CH, c16 = e % CH;
+                        uint8_t *dst;
                         if constexpr (Q8) {
-                            to = vb + q8_offset<D>(rr, c16);
+                            dst = vb + q8_offset<D>(rr, c16);
                             if (c16 == 0)
                                 ve[rr] = -127;
                         } else {
-                            to = vb + (c16 / 8) * C::SLAB + sw128_offset(rr, c16 % 8);
+                            dst = vb + (c16 / 8) * C::SLAB + sw128_offset(rr, c16 % 8);
                         }
-                        *reinterpret_cast<uint4 *>(to) = make_uint4(0, 0, 0, 0);
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(0, 0, 0, 0);
                     }
-                    if (!pre && hi >= r0 && hi < r0 + WK) {
-                        const long long row = (static_cast<long long>(b) * p.L_max + sp.p) * p.Hkv + g;
-                        if constexpr (Q8) {
-                            constexpr int E = D / 16;
-                            float f[E], amax = 0.f;
+                    patched = true;
+                };
+                if (hi < r0 + WK - 1)
+                    zero_rows(hi + 1, r0 + WK);
+                if (lo > r0)
+                    zero_rows(r0, lo);
+                if (STEP && !pre && hi < r0 + WK) {  // the new row goes where it belongs
+                    const long long row = (static_cast<long long>(b) * p.L_max + sp.p) * p.Hkv + g;
+                    const bool append = !cur.base;
+                    if constexpr (Q8) {
+                        constexpr int E = D / 16;
+                        float f[E], amax = 0.f;
 #pragma unroll
-                            for (int e = 0; e < E; ++e) {
-                                const float2 two = unpack_bf16x2(fresh_w[e / 2]);
-                                f[e] = (e & 1) ? two.y : two.x;
-                                if (fabsf(f[e]) < __int_as_float(0x7f800000))
-                                    amax = fmaxf(amax, fabsf(f[e]));
-                                else
-                                    bad = true;
-                            }
+                        for (int e = 0; e < E; ++e) {
+                            const float2 two = unpack_bf16x2(fresh_w[e / 2]);
+                            f[e] = (e & 1) ? two.y : two.x;
+                            if (fabsf(f[e]) < __int_as_float(0x7f800000))
+                                amax = fmaxf(amax, fabsf(f[e]));
+                            else
+                                bad = true;
+                        }
 #pragma unroll
-                            for (int off = 8; off > 0; off >>= 1)
-                                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
-                            const int ex = q8_exponent<Q8 ? CODE : 0>(amax);
-                            const float sd = q8_pow2(-ex);
-                            uint32_t w[E / 4];
+                        for (int off = 8; off > 0; off >>= 1)
+                            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, off));
+                        const int ex = q8_exponent<Q8 ? CODE : 0>(amax);
+                        const float sd = q8_pow2(-ex);
+                        uint32_t w[E / 4];
 #pragma unroll
-                            for (int e = 0; e < E; e += 4)
-                                w[e / 4] = q8_codes2<Q8 ? CODE : 0>(f[e] * sd, f[e + 1] * sd) |
-                                           q8_codes2<Q8 ? CODE : 0>(f[e + 2] * sd, f[e + 3] * sd) << 16;
-                            const int d = E * (lane & 15);
-                            uint8_t *to = (kv ? vb : kb) + q8_offset<D>(hi, d / 16) + d % 16;
-                            uint8_t *cache = static_cast<uint8_t *>(kv ? p.v_cache : p.k_cache) + row * D + d;
+                        for (int e = 0; e < E; e += 4)
+                            w[e / 4] = q8_codes2<Q8 ? CODE : 0>(f[e] * sd, f[e + 1] * sd) |
+                                       q8_codes2<Q8 ? CODE : 0>(f[e + 2] * sd, f[e + 3] * sd) << 16;
+                        const int d = E * (lane & 15);
+                        uint8_t *to = (kv ? vb : kb) + q8_offset<D>(hi, d / 16) + d % 16;
+                        uint8_t *cache = static_cast<uint8_t *>(kv ? p.v_cache : p.k_cache) + row * D + d;
 #pragma unroll
-                            for (int e = 0; e < E / 4; ++e) {
-                                reinterpret_cast<uint32_t *>(to)[e] = w[e];
-                                if (!cur.base)
-                                    reinterpret_cast<uint32_t *>(cache)[e] = w[e];
-                            }
-                            if ((lane & 15) == 0) {
-                                (kv ? ve : ke)[hi] = static_cast<int8_t>(ex);
-                                if (!cur.base)
-                                    (kv ? p.v_exp : p.k_exp)[(static_cast<long long>(b) * p.Hkv + g) * p.L_max + sp.p] =
-                                        static_cast<int8_t>(ex);
-                            }
-                        } else {
-                            const int d = (D / 16) * (lane & 15);
-                            uint8_t *to = (kv ? vb : kb) + (d / 64) * C::SLAB + sw128_offset(hi, d % 64 / 8) + d % 8 * 2;
-                            orthros_bf16 *cache = static_cast<orthros_bf16 *>(kv ? p.v_cache : p.k_cache) + row * D + d;
+                        for (int e = 0; e < E / 4; ++e) {
+                            reinterpret_cast<uint32_t *>(to)[e] = w[e];
+                            if (append)
+                                reinterpret_cast<uint32_t *>(cache)[e] = w[e];
+                        }
+                        if ((lane & 15) == 0) {
+                            (kv ? ve : ke)[hi] = static_cast<int8_t>(ex);
+                            if (append)
+                                (kv ? p.v_exp : p.k_exp)[(static_cast<long long>(b) * p.Hkv + g) * p.L_max + sp.p] =
+                                    static_cast<int8_t>(ex);
+                        }
+                    } else {
+                        const int d = (D / 16) * (lane & 15);
+                        uint8_t *to = (kv ? vb : kb) + (d / 64) * C::SLAB + sw128_offset(hi, d % 64 / 8) + d % 8 * 2;
+                        orthros_bf16 *cache = static_cast<orthros_bf16 *>(kv ? p.v_cache : p.k_cache) + row * D + d;
 #pragma unroll
-                            for (int e = 0; e < D / 32; ++e) {
-                                reinterpret_cast<uint32_t *>(to)[e] = fresh_w[e];
-                                if (!cur.base)
-                                    reinterpret_cast<uint32_t *>(cache)[e] = fresh_w[e];
-                            }
+                        for (int e = 0; e < D / 32; ++e) {
+                            reinterpret_cast<uint32_t *>(to)[e] = fresh_w[e];
+                            if (append)
+                                reinterpret_cast<uint32_t *>(cache)[e] = fresh_w[e];
                         }
                     }
-                    __syncwarp();
+                    patched = true;
                 }
+                if (patched)
+                    __syncwarp();
+                const bool whole = lo <= r0 && r0 + WK - 1 <= hi;
                 if constexpr (Q8) {
                     st.template step<C::KT>(kb, vb, ke, ve, r0, whole, lo, hi);
                 } else {
@@ -578,7 +618,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
                         lim[nt][0] = lim[nt][1] = hi;
                     st.step(ks, C::SLAB, ks + C::KV_BYTES, C::SLAB, r0, r0, lim, whole, lo);
                 }
-                if (!whole)
+                if (patched)
                     fence_proxy_async_smem();  // before TMA writes over what was patched
             }
             __syncwarp();
@@ -622,7 +662,6 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
         // one slot for a segment that began before this CTA, one for one that runs out of it, and one
         // for each copy that only the prefix has to be joined with
         const long long slot = c0 == c1 ? 2LL * gridDim.x + static_cast<long long>(b) * p.Hkv + g : 2 * c + (c == c0 ? 1 : 0);
-        orthros_bf16 *out = (cur.base ? p.o : p.oc) + (static_cast<long long>(b) * p.Hq + g * G) * D;
         for (int e = t; e < G * (D / 4); e += C::CTHREADS) {
             const int row = e / (D / 4), d4 = 4 * (e % (D / 4));
             float M = NEG_INF, L = 0.f;
@@ -647,7 +686,8 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
             }
             if (alone) {
                 const float inv = L > 0.f ? 1.f / L : 0.f;
-                *reinterpret_cast<uint2 *>(out + row * D + d4) =
+                orthros_bf16 *out = (cur.base ? p.o : p.oc) + b * p.o_bstride + (g * G + row) * D + d4;
+                *reinterpret_cast<uint2 *>(out) =
                     make_uint2(pack_bf16x2(a.x * inv, a.y * inv), pack_bf16x2(a.z * inv, a.w * inv));
             } else {
                 *reinterpret_cast<float4 *>(p.part_o + (slot * G + row) * D + d4) = a;
@@ -656,7 +696,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
             }
         }
         if (sp.full && !cur.base && g == 0 && t == 0)
-            record_error(p.dev_err, ORTHROS_DEVERR_CACHE_FULL);
+            record_error(p.dev_err, STEP ? ORTHROS_DEVERR_CACHE_FULL : ORTHROS_DEVERR_POSITION);
         if (!alone) {
             if (t == 0)
                 joins[njoin] = {b * p.Hkv + g, cur.base, static_cast<int>(c0), static_cast<int>(c1 - c0) + 1, 0, 0};
@@ -666,7 +706,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
         it += places;
         cur.r += places;
         if (cur.r == seg_places && it < it1)
-            cur.next_segment(p);
+            cur.next_segment<C>(p);
     }
     if (bad)
         record_error(p.dev_err, ORTHROS_DEVERR_RANGE);
@@ -674,7 +714,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
         record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
     join_all(true);
     // the last CTA of the grid advances the lengths: every one has read them by now
-    if (s_flag[0]) {
+    if (STEP && s_flag[0]) {
         for (int b = t; b < p.B; b += C::CTHREADS) {
             const int len = __ldcg(p.cache_len + b);
             if (len >= 0 && len < p.L_max)
@@ -692,11 +732,11 @@ struct ServeLayout {
     size_t part_ml, cnt, pre_o, pre_ml, total;
 };
 
-// the grid: never more CTAs than the longest caches could give blocks
+// the grid: never more CTAs than the longest caches could give places
 static ServeLayout serve_layout(int B, int P, int L_max, int Hq, int Hkv, int D)
 {
     const size_t G = Hq / Hkv, BH = static_cast<size_t>(B) * Hkv;
-    const size_t most = 2 * BH * ((static_cast<size_t>(L_max) + 63) / 64 + (static_cast<size_t>(P) + 63) / 64 + 1);
+    const size_t most = 2 * BH * ((static_cast<size_t>(L_max) + 63) / 64 + (static_cast<size_t>(P) + 63) / 64 + SEG_COST);
     ServeLayout l;
     l.ctas = static_cast<int>(most < SERVE_CTAS ? most : SERVE_CTAS);
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
@@ -744,11 +784,14 @@ static cudaError_t launch_serve_t(int code, const ServeMaps &maps, const ServePa
         return launch_serve_tc<D, G, ORTHROS_KV_E4M3>(maps, p, ctas, stream);
     if (code == ORTHROS_KV_INT8)
         return launch_serve_tc<D, G, ORTHROS_KV_INT8>(maps, p, ctas, stream);
-    return launch_serve_tc<D, G, -1>(maps, p, ctas, stream);
+    if (code == SV_PREFIX)
+        return launch_serve_tc<D, G, SV_PREFIX>(maps, p, ctas, stream);
+    return launch_serve_tc<D, G, SV_COPIES>(maps, p, ctas, stream);
 }
 
-cudaError_t launch_serve(int D, int code, const CUtensorMap *m, ServeParams p, void *workspace, cudaStream_t stream)
+static cudaError_t launch_any(int D, int code, const CUtensorMap *m, ServeParams p, void *workspace, cudaStream_t stream)
 {
+    const bool step = code != SV_COPIES;
     const ServeLayout l = serve_layout(p.B, p.P, p.L_max, p.Hq, p.Hkv, D);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     p.part_o = reinterpret_cast<float *>(ws);
@@ -765,13 +808,17 @@ cudaError_t launch_serve(int D, int code, const CUtensorMap *m, ServeParams p, v
         a.part_o = p.pre_o;
         a.part_ml = p.pre_ml;
         a.dev_err = p.dev_err;
-        a.qc_bstride = static_cast<long long>(p.Hq) * D;
+        a.qc_bstride = p.q_bstride;
         a.B = p.B;
         a.T_out = 1;
         a.P = p.P;
         a.Hq = p.Hq;
         a.Hkv = p.Hkv;
         a.qscale = p.qscale;
+        if (!step) {  // its workspace comes as it is: the prefix kernel clears the counters
+            a.clear = p.cnt_bh;
+            a.n_clear = 2 * p.B * p.Hkv;
+        }
         const cudaError_t e = launch_prefix_attn(D, m[2], m[3], a, stream);
         if (e != cudaSuccess)
             return e;
@@ -794,6 +841,34 @@ cudaError_t launch_serve(int D, int code, const CUtensorMap *m, ServeParams p, v
     ORTHROS_SERVE_CASE(64, 16)
 #undef ORTHROS_SERVE_CASE
     return cudaErrorInvalidValue;
+}
+
+cudaError_t launch_serve(int D, int code, const CUtensorMap *maps, ServeParams p, void *workspace, cudaStream_t stream)
+{
+    p.q_bstride = p.o_bstride = static_cast<long long>(p.Hq) * D;
+    return launch_any(D, code, maps, p, workspace, stream);
+}
+
+cudaError_t launch_serve_copies(int D, const CUtensorMap *maps, const XattnParams &x, int P, void *workspace,
+                                cudaStream_t stream)
+{
+    ServeParams p{};
+    p.qc_new = x.qc;
+    p.cache_len = const_cast<int32_t *>(x.pos);  // read only in this form
+    p.alpha_c = x.alpha_c;
+    p.beta_c = x.beta_c;
+    p.oc = x.oc;
+    p.q_bstride = x.qc_bstride;
+    p.o_bstride = x.oc_bstride;
+    p.dev_err = x.dev_err;
+    p.B = x.B;
+    p.Hq = x.Hq;
+    p.Hkv = x.Hkv;
+    p.L_max = x.T_kv;
+    p.window = 1;
+    p.P = P;
+    p.qscale = x.qscale;
+    return launch_any(D, SV_COPIES, maps, p, workspace, stream);
 }
 
 }  // namespace orthros

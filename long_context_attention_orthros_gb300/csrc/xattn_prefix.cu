@@ -2,7 +2,8 @@
 // prompt prefix: copy i of sequence b attends over the prefix rows 0 .. P-1 and its sequence's
 // own rows 0 .. pos.  The prefix kernel takes all rows of the batch over the prefix, the split-KV
 // kernels of xattn_fwd.cu the copies over their own rows, each writing partials; one combine
-// kernel joins both.  Many copies a sequence take prefix and own rows in one kernel instead.
+// kernel joins both.  One copy a sequence goes through the decode step's kernel behind the prefix
+// kernel (serve_step.cu), which joins in the same launch.  Many copies a sequence take prefix and own rows in one kernel instead.
 #include "kernels.cuh"
 
 namespace orthros {
@@ -19,6 +20,10 @@ XpLayout xp_layout(int B, int T_out, int P, int T_kv, int Hq, int Hkv, int D)
     XpLayout l = {0, 0, 0, 256};
     if (prefix_direct_tiles(B, T_out, Hq, Hkv) > 0)
         return l;
+    if (T_out == 1) {
+        l.total = serve_workspace_bytes(B, P, T_kv, Hq, Hkv, D);
+        return l;
+    }
     l.pre = prefix_attn_parts(static_cast<long long>(B) * T_out, P, Hq, Hkv);
     l.own = xattn_parts(B, T_out, T_kv, Hq, Hkv);
     const size_t slots = (static_cast<size_t>(l.pre) + l.own) * B * T_out * Hq;
@@ -36,6 +41,8 @@ size_t xattn_prefix_workspace_bytes(int B, int T_out, int P, int T_kv, int Hq, i
 
 cudaError_t launch_xattn_prefix(int D, const CUtensorMap *m, XattnParams x, int P, void *workspace, cudaStream_t stream)
 {
+    if (x.T_out == 1 && prefix_direct_tiles(x.B, 1, x.Hq, x.Hkv) == 0)
+        return launch_serve_copies(D, m, x, P, workspace, stream);
     const XpLayout l = xp_layout(x.B, x.T_out, P, x.T_kv, x.Hq, x.Hkv, D);
     float *part_o = static_cast<float *>(workspace);
     float2 *part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + l.part_ml);

@@ -232,6 +232,21 @@ def test_decode_with_rows_of_very_different_size(code):
     assert int(s.err.item()) == 0
 
 
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 2), (2, 2)])
+def test_decode_window_does_not_meet_what_lies_before_it(Hq, Hkv):
+    """Rows before the base token's window hold NaN codes, up to the row next to it: the base output is the same."""
+    out = []
+    for nan in (False, True):
+        s = Q8Decode((500, 150), 1, Hq, Hkv, 64, 100, "e4m3", 17)
+        if nan:
+            for b, n in enumerate((500, 150)):
+                s.dev_cache[0].view(torch.int8)[b, :n - 99] = NAN_CODE
+                s.dev_cache[1].view(torch.int8)[b, :n - 99] = NAN_CODE
+        out.append(s.step(0))
+    np.testing.assert_array_equal(bits(out[0][0]), bits(out[1][0]))
+    assert torch.isfinite(out[0][1]).all() and torch.isnan(out[1][1]).all()
+
+
 def test_decode_full_cache_writes_nothing():
     s = Q8Decode((14, 31), 3, 8, 2, 64, 128, "e4m3", 12)  # L_max = 48
     s.cl.copy_(i32(np.array([14, 48])))

@@ -66,7 +66,7 @@ def test_copies_match_oracle(B, T_out, P, T_kv, Hq, Hkv, d):
     assert_parity(val(got), c.oracle(), "copies")
 
 
-@pytest.mark.parametrize("B,T_out,Hq,Hkv", [(2, 3, 8, 2), (16, 1, 32, 8), (2, 80, 8, 2), (10, 62, 32, 8)])
+@pytest.mark.parametrize("B,T_out,Hq,Hkv", [(2, 3, 8, 2), (16, 1, 32, 8), (2, 80, 8, 2), (10, 62, 32, 8), (2, 1, 16, 1)])
 def test_copies_out_of_range_are_zero_and_reported(B, T_out, Hq, Hkv):
     c = Copies(B, T_out, 300, 50, Hq, Hkv, 128, 21)
     ref = c.oracle()
@@ -79,7 +79,8 @@ def test_copies_out_of_range_are_zero_and_reported(B, T_out, Hq, Hkv):
     assert_parity(got, ref, "the others")
 
 
-@pytest.mark.parametrize("B,T_out,Hq,Hkv,used", [(10, 64, 32, 8, 130), (10, 64, 32, 8, 64)])
+@pytest.mark.parametrize("B,T_out,Hq,Hkv,used", [(10, 64, 32, 8, 130), (10, 64, 32, 8, 64), (3, 1, 8, 2, 100),
+                                                  (40, 1, 8, 1, 65), (1, 1, 2, 2, 1)])
 def test_rows_behind_the_last_position_do_not_matter(B, T_out, Hq, Hkv, used):
     """Own rows that no copy of the batch has reached hold NaN."""
     c = Copies(B, T_out, 200, 300, Hq, Hkv, 128, 24)
@@ -91,10 +92,11 @@ def test_rows_behind_the_last_position_do_not_matter(B, T_out, Hq, Hkv, used):
     assert_parity(val(got), c.oracle(), "copies")
 
 
-def test_copies_strided_and_repeatable():
+@pytest.mark.parametrize("B,T_out,Hq,Hkv", [(3, 2, 8, 2), (5, 1, 8, 2), (10, 64, 32, 8)])
+def test_copies_strided_and_repeatable(B, T_out, Hq, Hkv):
     """Batch strides above dense for queries, own rows and output; the bits do not depend on strides, stream or
     what the workspace held."""
-    B, T_out, P, T_kv, Hq, Hkv, d = 3, 2, 800, 70, 8, 2, 128
+    P, T_kv, d = 800, 70, 128
     c = Copies(B, T_out, P, T_kv, Hq, Hkv, d, 22)
     ref = bits(c.run())
 
@@ -199,6 +201,26 @@ def test_decode_steps_match_oracle(lens, steps, P, Hq, Hkv, d, window):
     np.testing.assert_array_equal(bits(s.dv), s.v[:, P:])
     np.testing.assert_array_equal(bits(s.dkp), s.kp)
     np.testing.assert_array_equal(s.cl.cpu().numpy() + P, s.total)
+
+
+@pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 2)])
+@pytest.mark.parametrize("lens,P,window", [((200, 77), 300, 100), ((20, 64), 130, 90)])
+def test_decode_window_does_not_meet_what_lies_before_it(Hq, Hkv, lens, P, window):
+    """Rows before the base token's window hold NaN, up to the row next to it: the base output does not change."""
+    s = PrefixDecode(lens, 1, P, Hq, Hkv, 128, window, 16)
+    o, _ = s.step(0)
+    t = PrefixDecode(lens, 1, P, Hq, Hkv, 128, window, 16)
+    first = [P + n - window + 1 for n in lens]  # the window's first row, counted through prefix and own rows
+    for b, f in enumerate(first):
+        t.dk[b, :max(0, f - P)] = float("nan")
+        t.dv[b, :max(0, f - P)] = float("nan")
+    t.dkp[:min(first)] = float("nan")
+    t.dvp[:min(first)] = float("nan")
+    o2, oc2 = t.step(0)
+    np.testing.assert_array_equal(bits(o), bits(o2))
+    assert torch.isnan(oc2).all()
+    ro, _ = s.oracle_step(0)
+    assert_parity(val(o2), ro, "base")
 
 
 @pytest.mark.parametrize("B", [2, 40])
