@@ -37,35 +37,50 @@ __device__ __forceinline__ float q8_pow2(int n)
     return __uint_as_float(n > -127 ? static_cast<uint32_t>(127 + n) << 23 : 0x400000u);
 }
 
-// codes of two values already scaled by 2^-e, in the low 16 bits (a in the lowest byte)
+// codes of two finite values already scaled by 2^-e, in the low 16 bits (a in the lowest byte)
 template <int CODE>
-__device__ __forceinline__ uint32_t q8_codes2(float a, float b)
+__device__ __forceinline__ uint32_t q8_codes2_finite(float a, float b)
 {
     if constexpr (CODE == ORTHROS_KV_E4M3) {
-        // the conversion saturates; what is not finite has to stay NaN
-        if (!(fabsf(a) < __int_as_float(0x7f800000)))
-            a = __int_as_float(0x7fffffff);
-        if (!(fabsf(b) < __int_as_float(0x7f800000)))
-            b = __int_as_float(0x7fffffff);
         uint16_t r;
         asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(r) : "f"(b), "f"(a));
         return r;
     } else {
-        const int x = __float2int_rn(fminf(fmaxf(a, -127.f), 127.f)), y = __float2int_rn(fminf(fmaxf(b, -127.f), 127.f));
-        return (static_cast<uint32_t>(a == a ? x : 0) & 0xffu) | ((static_cast<uint32_t>(b == b ? y : 0) & 0xffu) << 8);
+        return (static_cast<uint32_t>(__float2int_rn(a)) & 0xffu) | (static_cast<uint32_t>(__float2int_rn(b)) & 0xffu) << 8;
     }
 }
 
-// the value of one code, without its row's 2^e
+// the same for any two values: what is not finite becomes NaN (e4m3), the end of the range or 0 (int8)
 template <int CODE>
-__device__ __forceinline__ float q8_value(uint8_t c)
+__device__ __forceinline__ uint32_t q8_codes2(float a, float b)
 {
     if constexpr (CODE == ORTHROS_KV_E4M3) {
-        uint32_t h;
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<uint16_t>(c)));
-        return __half2float(__ushort_as_half(static_cast<uint16_t>(h)));
+        // the conversion saturates, so that infinities are made NaN first
+        if (!(fabsf(a) < __int_as_float(0x7f800000)))
+            a = __int_as_float(0x7fffffff);
+        if (!(fabsf(b) < __int_as_float(0x7f800000)))
+            b = __int_as_float(0x7fffffff);
+        return q8_codes2_finite<CODE>(a, b);
     } else {
-        return static_cast<float>(static_cast<int8_t>(c));
+        const uint32_t r = q8_codes2_finite<CODE>(fminf(fmaxf(a, -127.f), 127.f), fminf(fmaxf(b, -127.f), 127.f));
+        return (a == a ? r & 0xffu : 0u) | (b == b ? r & 0xff00u : 0u);
+    }
+}
+
+// the two low (hi = false) or high codes of a word as fp16
+template <int CODE>
+__device__ __forceinline__ uint32_t q8_half2(uint32_t w, bool hi)
+{
+    if constexpr (CODE == ORTHROS_KV_E4M3) {
+        uint32_t r;
+        const uint16_t two = static_cast<uint16_t>(hi ? w >> 16 : w & 0xffffu);
+        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(two));
+        return r;
+    } else {
+        // 0x6400 | u is 1024 + u: with u = code + 128, subtract 1152
+        const uint32_t u = __byte_perm(w ^ 0x80808080u, 0x64646464u, hi ? 0x4342 : 0x4140);
+        const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&u), __float2half2_rn(1152.f));
+        return *reinterpret_cast<const uint32_t *>(&r);
     }
 }
 

@@ -20,23 +20,6 @@
 
 namespace orthros {
 
-// the two low (hi = false) or high codes of a word as fp16
-template <int CODE>
-__device__ __forceinline__ uint32_t q8_half2(uint32_t w, bool hi)
-{
-    if constexpr (CODE == ORTHROS_KV_E4M3) {
-        uint32_t r;
-        const uint16_t two = static_cast<uint16_t>(hi ? w >> 16 : w & 0xffffu);
-        asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"(two));
-        return r;
-    } else {
-        // 0x6400 | u is 1024 + u: with u = code + 128, subtract 1152
-        const uint32_t u = __byte_perm(w ^ 0x80808080u, 0x64646464u, hi ? 0x4342 : 0x4140);
-        const __half2 r = __hsub2(*reinterpret_cast<const __half2 *>(&u), __float2half2_rn(1152.f));
-        return *reinterpret_cast<const uint32_t *>(&r);
-    }
-}
-
 // byte offset of 16-byte chunk c of row r in a tile of d-byte rows as TMA's 128-byte (d = 128) or
 // 64-byte (d = 64) swizzle lays it out
 template <int D>
