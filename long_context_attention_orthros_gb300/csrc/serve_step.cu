@@ -30,8 +30,8 @@
 #include <type_traits>
 
 #include "kernels.cuh"
+#include "warp_b16.cuh"
 #include "warp_q8.cuh"
-#include "xattn.cuh"
 
 namespace orthros {
 
@@ -56,9 +56,9 @@ struct SvCfg {
     static constexpr int KB = 64;
     static constexpr int KV_BYTES = KB * D * (Q8 ? 1 : 2);
     static constexpr int SLAB = KB * 128;  // bf16: one 64-wide slab
-    // A step of 16 keys is a chain of some 300 dependent instructions.  In the 8-bit form a warp
-    // takes 32 keys at once, two independent chains, and the warps take blocks by pairs.
-    static constexpr int KT = Q8 && G <= 8 ? 2 : 1;
+    // A step of 16 keys is a chain of some 300 dependent instructions.  A warp takes 32 keys at once,
+    // two independent chains, and the warps take blocks by pairs (G = 16 has no registers for it).
+    static constexpr int KT = G <= 8 ? 2 : 1;
     static constexpr int CWARPS = 4;
     static constexpr int GROUP = 4 / KT;  // warps that share a block
     static constexpr int SCR_ROWS = CWARPS * G;
@@ -467,34 +467,14 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
             it += places;
             continue;
         }
-        typename std::conditional<Q8, WarpQ8<D, NT, Q8 ? CODE : 0>, WarpKeys16<D, NT, false>>::type st;
+        typename std::conditional<Q8, WarpQ8<D, NT, Q8 ? CODE : 0>, WarpB16<D, NT>>::type st;
         {
             const int hb = segs % C::HB;
             if (ok && !mbar_wait(&hfull[hb], static_cast<uint32_t>((segs / C::HB) & 1)))
                 ok = false;
             const orthros_bf16 *q = reinterpret_cast<const orthros_bf16 *>(smem + C::HDR_OFF + hb * C::HDR_BYTES);
             const float *al = reinterpret_cast<const float *>(q + G * D), *be = al + G * D;
-            if constexpr (Q8) {
-                st.load_q(q, al, be, G, p.qscale);
-            } else {
-#pragma unroll
-                for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-                    for (int kt = 0; kt < D / 16; ++kt)
-#pragma unroll
-                        for (int hf = 0; hf < 2; ++hf) {
-                            const int row = 8 * nt + (lane >> 2), d = row * D + kt * 16 + 2 * (lane & 3) + 8 * hf;
-                            uint32_t hi = 0, lo = 0;
-                            if (row < G) {
-                                const float2 x = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(q + d));
-                                const float2 a = *reinterpret_cast<const float2 *>(al + d);
-                                const float2 c2 = *reinterpret_cast<const float2 *>(be + d);
-                                split_q_pair(fmaf(x.x, a.x, c2.x) * p.qscale, fmaf(x.y, a.y, c2.y) * p.qscale, hi, lo);
-                            }
-                            st.qb[nt][kt][hf] = hi;
-                            st.ql[nt][kt][hf] = lo;
-                        }
-            }
+            st.load_q(q, al, be, G, p.qscale);
         }
         // the new rows as this lane takes them: lanes 0 .. 15 of K's, 16 .. 31 of V's, D / 16 values each
         const int kv = lane >> 4;
@@ -612,11 +592,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
                     st.template step<C::KT>(kb, vb, ke, ve, r0, whole, lo, hi);
                 } else {
                     const uint32_t ks = sbase + s * 2 * C::KV_BYTES;
-                    int lim[NT][2];
-#pragma unroll
-                    for (int nt = 0; nt < NT; ++nt)
-                        lim[nt][0] = lim[nt][1] = hi;
-                    st.step(ks, C::SLAB, ks + C::KV_BYTES, C::SLAB, r0, r0, lim, whole, lo);
+                    st.template step<C::KT>(ks, ks + C::KV_BYTES, C::SLAB, r0, whole, lo, hi);
                 }
                 if (patched)
                     fence_proxy_async_smem();  // before TMA writes over what was patched

@@ -156,10 +156,10 @@ struct WarpKeys16 {
 
     // Keys j0 .. j0+15 at shared-memory rows krow0.. of a block staged as D/64 slabs
     // with the TMA 128-byte swizzle (K at kbase, slabs kslab bytes apart; V at vbase,
-    // vslab apart).  Key j counts for row (nt, i) iff lo <= j <= lim[nt][i]; pass whole =
+    // vslab apart).  Key j counts for row (nt, i) iff j <= lim[nt][i]; pass whole =
     // true when every key counts for every row this warp keeps.
     __device__ __forceinline__ void step(uint32_t kbase, int kslab, uint32_t vbase, int vslab, int krow0, int j0,
-                                         const int (&lim)[NT][2], bool whole, int lo = 0)
+                                         const int (&lim)[NT][2], bool whole)
     {
         const int lane = threadIdx.x & 31;
         const float NEG_INF = -__int_as_float(0x7f800000);
@@ -200,11 +200,9 @@ struct WarpKeys16 {
         for (int nt = 0; nt < NT; ++nt) {
             if (!whole) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int j = j0 + (lane >> 2) + ((e >> 1) << 3);
-                    if (j > lim[nt][e & 1] || j < lo)
+                for (int e = 0; e < 4; ++e)
+                    if (j0 + (lane >> 2) + ((e >> 1) << 3) > lim[nt][e & 1])
                         s[nt][e] = NEG_INF;
-                }
             }
             float cm0 = fmaxf(s[nt][0], s[nt][2]), cm1 = fmaxf(s[nt][1], s[nt][3]);
 #pragma unroll
