@@ -55,11 +55,14 @@ struct PtCfg {
     static constexpr int K_OFF = 0;
     static constexpr int V_OFF = PAIRS * PAIR_BYTES;
     static constexpr int Q_OFF = 2 * PAIRS * PAIR_BYTES;
-    static constexpr int KEXP_OFF = Q_OFF + TILES * Q_BYTES;   // int8 [SLOTS][KB]: key row shift
-    static constexpr int KFLAG_OFF = KEXP_OFF + SLOTS * KB;    // uint8 [SLOTS][8]
-    static constexpr int QSC_OFF = KFLAG_OFF + SLOTS * 8;      // int8 [TILES][128]: query row shift
+    // Marks of a block's conversion live two rounds of the ring: K is released when its S are complete,
+    // before the softmax has read them, and the block two rounds later is converted after it has.
+    static constexpr int MARKS = 2 * SLOTS;
+    static constexpr int KEXP_OFF = Q_OFF + TILES * Q_BYTES;   // int8 [MARKS][KB]: key row shift
+    static constexpr int KFLAG_OFF = KEXP_OFF + MARKS * KB;    // uint8 [MARKS][8]
+    static constexpr int QSC_OFF = KFLAG_OFF + MARKS * 8;      // int8 [TILES][128]: query row shift
     static constexpr int BAR_OFF = QSC_OFF + TILES * 128;
-    static constexpr int NBARS = 3 * SLOTS + 10;
+    static constexpr int NBARS = 2 * SLOTS + MARKS + 2 * PAIRS + 10;
     static constexpr int HOLD_OFF = BAR_OFF + NBARS * 8;
     static constexpr int USED = HOLD_OFF + 16 + 1024;
     static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;  // one CTA an SM: it takes all of tensor memory
@@ -81,10 +84,12 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t pad = ((raw_s + 1023u) & ~1023u) - raw_s;
     uint8_t *smem = smem_raw + pad;
     const uint32_t sbase = raw_s + pad;
-    uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);  // [SLOTS] K/V block landed
-    uint64_t *kconv = full + C::SLOTS;     // [SLOTS] K block converted
-    uint64_t *empty = kconv + C::SLOTS;    // [SLOTS] block released (MMA commit)
-    uint64_t *q_full = empty + C::SLOTS;   // [2] query tile prepared
+    uint64_t *kfull = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);  // [SLOTS] K block landed
+    uint64_t *kconv = kfull + C::SLOTS;    // [MARKS] K block converted
+    uint64_t *vfull = kconv + C::MARKS;    // [SLOTS] V block landed
+    uint64_t *kempty = vfull + C::SLOTS;   // [PAIRS] K of a pair released: its S are complete (MMA commit)
+    uint64_t *vempty = kempty + C::PAIRS;  // [PAIRS] V released: its P V are complete
+    uint64_t *q_full = vempty + C::PAIRS;  // [2] query tile prepared
     uint64_t *s_full = q_full + 2;         // [2] S of a pair complete
     uint64_t *p_full = s_full + 2;         // [2] P written
     uint64_t *o_done = p_full + 2;         // [2] O += P V of a pair complete
@@ -104,10 +109,16 @@ __global__ void __launch_bounds__(512, 1)
     const long long row_end = DIRECT ? static_cast<long long>(b_own + 1) * p.T_out * G : R;
     if (threadIdx.x == 0) {
         for (int s = 0; s < C::SLOTS; ++s) {
-            mbar_init(&full[s], 1);
+            mbar_init(&kfull[s], 1);
+            mbar_init(&vfull[s], 1);
+        }
+        for (int s = 0; s < C::MARKS; ++s) {
             mbar_init(&kconv[s], C::CONV_THREADS / 32);
-            mbar_init(&empty[s], 1);
             reinterpret_cast<uint64_t *>(smem + C::KFLAG_OFF)[s] = 0;
+        }
+        for (int s = 0; s < C::PAIRS; ++s) {
+            mbar_init(&kempty[s], 1);
+            mbar_init(&vempty[s], 1);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&q_full[t], 8);
@@ -159,22 +170,29 @@ __global__ void __launch_bounds__(512, 1)
         if (lane == 0) {
             tma_prefetch_desc(&maps.k);
             tma_prefetch_desc(&maps.v);
-            for (int j = 0; j < 2 * npair; ++j) {
-                const int s = j % C::SLOTS;
-                if (j >= C::SLOTS && !mbar_wait(&empty[s], static_cast<uint32_t>(((j / C::SLOTS) - 1) & 1))) {
-                    record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
-                    break;
-                }
-                const int at = (s / 2) * C::PAIR_BYTES + (s % 2) * C::KB * 128;
-                mbar_arrive_expect_tx(&full[s], 2 * C::SLABS * C::KB * 128);
+            // K of a pair, then its V: each is free again earlier than what comes after it
+            bool ok = true;
+            for (int pp = 0; pp < npair && ok; ++pp) {
+                const int ps = pp % C::PAIRS;
+                for (int kv = 0; kv < 2 && ok; ++kv) {
+                    if (pp >= C::PAIRS && !mbar_wait(kv ? &vempty[ps] : &kempty[ps],
+                                                     static_cast<uint32_t>((pp / C::PAIRS - 1) & 1))) {
+                        record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+                        ok = false;
+                        break;
+                    }
+                    for (int h = 0; h < 2; ++h) {
+                        const int j = 2 * pp + h;
+                        uint64_t *bar = (kv ? vfull : kfull) + 2 * ps + h;
+                        uint8_t *dst = smem + (kv ? C::V_OFF : C::K_OFF) + ps * C::PAIR_BYTES + h * C::KB * 128;
+                        const bool own = DIRECT && j >= pre_blocks;
+                        const CUtensorMap *map = own ? (kv ? &maps.vo : &maps.ko) : (kv ? &maps.v : &maps.k);
+                        const int j0 = own ? (j - pre_blocks) * C::KB : js + j * C::KB;
+                        mbar_arrive_expect_tx(bar, C::SLABS * C::KB * 128);
 #pragma unroll
-                for (int sl = 0; sl < C::SLABS; ++sl) {
-                    const bool own = DIRECT && j >= pre_blocks;
-                    const int j0 = own ? (j - pre_blocks) * C::KB : js + j * C::KB;
-                    tma_load_4d(smem + C::K_OFF + at + sl * C::PAIR_SLAB, own ? &maps.ko : &maps.k, &full[s], sl * 64, g,
-                                j0, own ? b_own : 0);
-                    tma_load_4d(smem + C::V_OFF + at + sl * C::PAIR_SLAB, own ? &maps.vo : &maps.v, &full[s], sl * 64, g,
-                                j0, own ? b_own : 0);
+                        for (int sl = 0; sl < C::SLABS; ++sl)
+                            tma_load_4d(dst + sl * C::PAIR_SLAB, map, bar, sl * 64, g, j0, own ? b_own : 0);
+                    }
                 }
             }
         }
@@ -188,9 +206,12 @@ __global__ void __launch_bounds__(512, 1)
                 const int pp = pair_at(t, u), s0 = (2 * pp) % C::SLOTS;
                 const uint32_t ph = static_cast<uint32_t>(((2 * pp) / C::SLOTS) & 1);
                 if (!ROWS2 || t == 0)  // the pair's blocks landed and converted
-                    for (int h = 0; h < 2; ++h)
-                        if (!(mbar_wait(&full[s0 + h], ph) && mbar_wait(&kconv[s0 + h], ph)))
+                    for (int h = 0; h < 2; ++h) {
+                        const int j = 2 * pp + h;
+                        if (!(mbar_wait(&kfull[s0 + h], ph) &&
+                              mbar_wait(&kconv[j % C::MARKS], static_cast<uint32_t>((j / C::MARKS) & 1))))
                             return false;
+                    }
                 // S overwrites the P that the stream's last P V reads
                 if (u >= 1 && !mbar_wait(&o_done[t], static_cast<uint32_t>((u - 1) & 1)))
                     return false;
@@ -204,13 +225,20 @@ __global__ void __launch_bounds__(512, 1)
                     umma_ss(tbase + C::TM_S + 128 * t, qdesc + off, kdesc + off, IDESC_QK, kk != 0);
                 }
                 umma_commit(&s_full[t]);
+                if (!ROWS2 || t == 1)  // everything that reads the pair's K has been issued
+                    umma_commit(&kempty[s0 / 2]);
                 return true;
             };
             auto issue_pv = [&](int t, int u) -> bool {
+                const int s0 = (2 * pair_at(t, u)) % C::SLOTS;
+                const uint32_t ph = static_cast<uint32_t>(((2 * pair_at(t, u)) / C::SLOTS) & 1);
+                if (!ROWS2 || t == 0)
+                    for (int h = 0; h < 2; ++h)
+                        if (!mbar_wait(&vfull[s0 + h], ph))
+                            return false;
                 if (!mbar_wait(&p_full[t], static_cast<uint32_t>(u & 1)))
                     return false;
                 tc_fence_after();
-                const int s0 = (2 * pair_at(t, u)) % C::SLOTS;
                 const uint64_t vdesc = umma_desc_sw128(sbase + C::V_OFF + (s0 / 2) * C::PAIR_BYTES, C::PAIR_SLAB, 1024);
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
@@ -219,10 +247,8 @@ __global__ void __launch_bounds__(512, 1)
                 umma_commit(&o_done[t]);
                 if (u == pairs_of(t) - 1)
                     umma_commit(&o_final[t]);
-                if (!ROWS2 || t == 1) {  // everything that reads the pair has been issued
-                    umma_commit(&empty[s0]);
-                    umma_commit(&empty[s0 + 1]);
-                }
+                if (!ROWS2 || t == 1)  // the same for its V
+                    umma_commit(&vempty[s0 / 2]);
                 return true;
             };
             for (int t = 0; t < 2; ++t)
@@ -247,7 +273,7 @@ __global__ void __launch_bounds__(512, 1)
         const int nrows = cid + (ITS - 1) * C::CONV_THREADS < C::KB * 8 ? ITS : ITS - 1;  // warp-uniform
         for (int j = 0; j < 2 * npair && ok; ++j) {
             const int s = j % C::SLOTS;
-            if (!(ok = mbar_wait(&full[s], static_cast<uint32_t>((j / C::SLOTS) & 1))))
+            if (!(ok = mbar_wait(&kfull[s], static_cast<uint32_t>((j / C::SLOTS) & 1))))
                 break;
             uint8_t *blk = smem + C::K_OFF + (s / 2) * C::PAIR_BYTES + (s % 2) * C::KB * 128;
             uint4 u[ITS][C::SLABS];
@@ -274,12 +300,14 @@ __global__ void __launch_bounds__(512, 1)
                     }
             } else {
                 shift_key_rows<C::SLABS>(blk, C::PAIR_SLAB, 0, cid >> 3, C::CONV_THREADS / 8, nrows, cid & 7,
-                                         kexp + s * C::KB, bad);
+                                         kexp + (j % C::MARKS) * C::KB, bad);
             }
             if constexpr (DIRECT) {
                 // V rows behind the last position have no weight, but may hold anything
                 const int beyond = kmax + 1 - (j - pre_blocks) * C::KB;  // first such row of the block
                 if (j >= pre_blocks && beyond < C::KB) {
+                    if (!(ok = mbar_wait(&vfull[s], static_cast<uint32_t>((j / C::SLOTS) & 1))))
+                        break;
                     for (int it = 0; it < nrows; ++it) {
                         const int r = (cid >> 3) + 24 * it;
                         if (r >= beyond)
@@ -291,11 +319,11 @@ __global__ void __launch_bounds__(512, 1)
                 }
             }
             if (lane == 0)
-                smem[C::KFLAG_OFF + s * 8 + cw] = wany ? 1 : 0;
+                smem[C::KFLAG_OFF + (j % C::MARKS) * 8 + cw] = wany ? 1 : 0;
             fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0)
-                mbar_arrive(&kconv[s]);
+                mbar_arrive(&kconv[j % C::MARKS]);
         }
         if (bad)
             record_error(p.dev_err, ORTHROS_DEVERR_RANGE);
@@ -393,7 +421,7 @@ __global__ void __launch_bounds__(512, 1)
                 float2 l2[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll 1
                 for (int hh = 0; hh < 2 && ok; ++hh) {
-                    const int j = 2 * pp + hh, ks = j % C::SLOTS;
+                    const int j = 2 * pp + hh, ks = j % C::MARKS;
                     const uint32_t s_col = s_lane + 64 * hh;
                     // column c is a key iff c <= nvalid
                     const int nvalid = DIRECT && j >= pre_blocks ? pos - (j - pre_blocks) * C::KB : je - 1 - (js + j * C::KB);
@@ -402,7 +430,7 @@ __global__ void __launch_bounds__(512, 1)
                     tmem_ld32(s_col + 32, vb);
                     // the block's conversion completed before its S was issued: this test succeeds and
                     // orders the flag read after the converters' writes
-                    const uint32_t kph = static_cast<uint32_t>((j / C::SLOTS) & 1);
+                    const uint32_t kph = static_cast<uint32_t>((j / C::MARKS) & 1);
                     const bool seen = mbar_test_wait(&kconv[ks], kph);
                     const uint64_t kf = *reinterpret_cast<const volatile uint64_t *>(smem + C::KFLAG_OFF + ks * 8);
                     tmem_wait_ld();
