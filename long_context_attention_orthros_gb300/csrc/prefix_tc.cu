@@ -350,22 +350,26 @@ __global__ void __launch_bounds__(512, 1)
 #pragma unroll
             for (int tl = 0; tl < C::TILES; ++tl) {
                 uint8_t *qb = smem + C::Q_OFF + tl * C::Q_BYTES + (cr / 8) * C::Q_SLAB;
-                uint4 raw[ROWS];
+                // the raw rows go straight to their places in the tile, all of a thread's in flight, and are
+                // turned into fp16 there (short code: the whole kernel is fetched anew at every launch)
                 uint32_t have = 0;
 #pragma unroll
                 for (int x = 0; x < ROWS; ++x) {
-                    const long long ri = row_base + tl * 128 + r0 + x * C::RPP;
+                    const int r = r0 + x * C::RPP;
+                    const long long ri = row_base + tl * 128 + r;
                     const PrefixRow row = prefix_row<G>(p, ri < row_end ? ri : R, g, D);
-                    raw[x] = make_uint4(0, 0, 0, 0);
                     if (row.q != nullptr) {
-                        raw[x] = __ldg(reinterpret_cast<const uint4 *>(row.q + 8 * cr));
+                        cp_async16(qb + sw128_offset(r, cr % 8), row.q + 8 * cr);
                         have |= 1u << x;
                     }
                 }
-#pragma unroll
+                cp_async_wait_all();
+#pragma unroll 2
                 for (int x = 0; x < ROWS; ++x) {
                     const int r = r0 + x * C::RPP;
-                    const uint32_t w[4] = {raw[x].x, raw[x].y, raw[x].z, raw[x].w};
+                    uint4 *slot = reinterpret_cast<uint4 *>(qb + sw128_offset(r, cr % 8));
+                    const uint4 raw = (have >> x) & 1u ? *slot : make_uint4(0, 0, 0, 0);
+                    const uint32_t w[4] = {raw.x, raw.y, raw.z, raw.w};
                     float f[8], amax = 0.f;
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
@@ -387,7 +391,7 @@ __global__ void __launch_bounds__(512, 1)
                         const __half2 hv = __floats2half2_rn(f[2 * e] * sd, f[2 * e + 1] * sd);
                         o4[e] = *reinterpret_cast<const uint32_t *>(&hv);
                     }
-                    *reinterpret_cast<uint4 *>(qb + sw128_offset(r, cr % 8)) = make_uint4(o4[0], o4[1], o4[2], o4[3]);
+                    *slot = make_uint4(o4[0], o4[1], o4[2], o4[3]);
                     if (cr == 0)
                         qexp[tl * 128 + r] = static_cast<int8_t>(sh);
                 }
