@@ -149,6 +149,8 @@ __device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t b
                  : "memory");
 }
 
+__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
+
 // 16 bytes from global to shared memory without a register on the way (both addresses 16-byte aligned)
 __device__ __forceinline__ void cp_async16(void *dst, const void *src)
 {

@@ -132,6 +132,25 @@ __global__ void __launch_bounds__(512, 1)
     if (warp == 1)
         tmem_alloc(tmem_holder, 512);
     tc_fence_before();
+    // the queries' and the scale-offset's lines on their way to L2 (no value is read yet)
+    if (threadIdx.x >= 128 && threadIdx.x < 256) {
+        for (int i = threadIdx.x - 128; i < G * D / 32; i += 128) {
+            prefetch_l2(p.alpha_c + g * G * D + 32 * i);
+            prefetch_l2(p.beta_c + g * G * D + 32 * i);
+        }
+    } else if (threadIdx.x >= 256 && !DIRECT) {
+        for (int i = threadIdx.x - 256; i < 128 * C::TILES; i += 256) {
+            const long long ri = row_base + i;
+            if (ri < R) {
+                const uint32_t bi = static_cast<uint32_t>(ri) / G, b = bi / static_cast<uint32_t>(p.T_out);
+                const orthros_bf16 *q = p.qc + b * p.qc_bstride +
+                                        (static_cast<long long>(bi - b * p.T_out) * p.Hq + g * G + static_cast<uint32_t>(ri) % G) * D;
+                prefetch_l2(q);
+                if (D == 128)
+                    prefetch_l2(q + 64);
+            }
+        }
+    }
     // what the kernels before wrote first, then a dependent grid may start beside this one
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
