@@ -493,22 +493,39 @@ def decode_step(q_new, qc_new, k_new, v_new, k_cache, v_cache, cache_len, alpha,
 _CODES = {torch.float8_e4m3fn: 0, torch.int8: 1}  # ORTHROS_KV_E4M3, ORTHROS_KV_INT8
 
 # The calls below are made once a token and layer, so what they cost on the host counts: a
-# tensor is checked with as few attribute reads as will do, and its address goes to ctypes as
-# a plain integer.
+# tensor is checked and its address taken in one go, with as few attribute reads as will do,
+# and addresses go to ctypes as plain integers.
 
 
-def _addr(t, dev: int):
-    """Device address of a tensor that has to live on device `dev` (or None)."""
-    if t is None:
-        return None
-    if t.get_device() != dev:
-        raise OrthrosError(f"tensor arguments must be CUDA tensors on the call's device (got {t.device})")
+def _refuse(t, name: str, what: str):
+    raise OrthrosError(f"{name} must be a {what} on the call's device (got {tuple(t.shape)}, {t.dtype}, {t.device})")
+
+
+def _dense(t, name: str, dtype, shape, dev: int) -> int:
+    """Address of a contiguous tensor of this type and shape on device `dev`."""
+    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous() or t.get_device() != dev:
+        _refuse(t, name, f"contiguous {dtype} CUDA tensor {tuple(shape)}")
     return t.data_ptr()
 
 
-def _expect(t, name: str, dtype, shape) -> None:
-    if t.dtype is not dtype or t.shape != shape or not t.is_contiguous():
-        raise OrthrosError(f"{name} must be a contiguous {dtype} CUDA tensor {shape}")
+def _rows(t, name: str, shape, dev: int):
+    """Address and batch stride of a bf16 tensor [B, T, H, d] whose [T, H, d] part is dense."""
+    if t.dtype is not torch.bfloat16 or t.shape != shape or t.get_device() != dev:
+        _refuse(t, name, f"bf16 CUDA tensor {tuple(shape)}")
+    return t.data_ptr(), 0 if t.is_contiguous() else _bf16_rows(t, name)
+
+
+def _optional(t, name: str, dtype, shape, dev: int):
+    return None if t is None else _dense(t, name, dtype, shape, dev)
+
+
+def _any_on(t, name: str, dev: int):
+    """Address of a workspace or an error word on device `dev` (or None)."""
+    if t is None:
+        return None
+    if t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, name, "contiguous CUDA tensor")
+    return t.data_ptr()
 
 
 def _invoke(name: str, dev: int, *args) -> None:
@@ -523,23 +540,16 @@ def _invoke(name: str, dev: int, *args) -> None:
         _check(st, name)
 
 
-def _device_of(t, name: str) -> int:
-    dev = t.get_device()
-    if dev < 0:
-        raise OrthrosError(f"{name} must be a CUDA tensor")
-    return dev
-
-
 def _cache_q8(k8, v8, k_exp, v_exp):
-    """Check the four tensors of an 8-bit cache; return (B, L_max, Hkv, d, code)."""
-    code = _CODES.get(k8.dtype)
-    if code is None or k8.dim() != 4 or not k8.is_contiguous():
-        raise OrthrosError("k8 must be a contiguous float8_e4m3fn or int8 CUDA tensor [B, L_max, Hkv, d]")
+    """Check the four tensors of an 8-bit cache; return ((B, L_max, Hkv, d, code), device, addresses)."""
+    code, dev = _CODES.get(k8.dtype), k8.get_device()
+    if code is None or k8.dim() != 4 or dev < 0:
+        _refuse(k8, "k8", "contiguous float8_e4m3fn or int8 CUDA tensor [B, L_max, Hkv, d]")
     B, L_max, Hkv, d = shape = k8.shape
-    _expect(v8, "v8", k8.dtype, shape)
-    _expect(k_exp, "k_exp", torch.int8, (B, Hkv, L_max))
-    _expect(v_exp, "v_exp", torch.int8, (B, Hkv, L_max))
-    return B, L_max, Hkv, d, code
+    exps = (B, Hkv, L_max)
+    a = (_dense(k8, "k8", k8.dtype, shape, dev), _dense(v8, "v8", k8.dtype, shape, dev),
+         _dense(k_exp, "k_exp", torch.int8, exps, dev), _dense(v_exp, "v_exp", torch.int8, exps, dev))
+    return (B, L_max, Hkv, d, code), dev, a
 
 
 def kv_cache_q8(B, L_max, Hkv, d, device, dtype=torch.float8_e4m3fn):
@@ -552,41 +562,37 @@ def kv_cache_q8(B, L_max, Hkv, d, device, dtype=torch.float8_e4m3fn):
     return codes[0], codes[1], exps[0], exps[1]
 
 
-def _kv_pair(k, v, B, Hkv, d) -> int:
-    """Check bf16 rows [B, T, Hkv, d] that go into, or come out of, a cache; return their batch stride."""
-    ks = _bf16_rows(k, "k")
-    if _bf16_rows(v, "v") != ks or v.shape != k.shape:
+def _kv_pair(k, v, B, Hkv, d, dev):
+    """Check K and V rows [B, T, Hkv, d]; return (T, batch stride, addresses)."""
+    shape = k.shape
+    if k.dim() != 4 or shape[0] != B or shape[2] != Hkv or shape[3] != d:
+        raise OrthrosError(f"k must be [B, T, Hkv, d] with B, Hkv, d = {B}, {Hkv}, {d}")
+    ka, ks = _rows(k, "k", shape, dev)
+    va, vs = _rows(v, "v", shape, dev)
+    if vs != ks:
         raise OrthrosError("k and v must have the same shape and strides")
-    if k.shape[0] != B or k.shape[2] != Hkv or k.shape[3] != d:
-        raise OrthrosError("k does not match the cache")
-    return ks
+    return shape[1], ks, (ka, va)
 
 
 def kv_quantize(k, v, k8, v8, k_exp, v_exp, start=None, rows=None, dev_err=None):
     """Write rows 0..rows[b]-1 (default all T) of k, v [B, T, Hkv, d] into the 8-bit cache at rows
     start[b].. (default 0): codes k8, v8 [B, L_max, Hkv, d] (float8_e4m3fn or int8) and exponents
     k_exp, v_exp int8 [B, Hkv, L_max]; a row stands for code * 2^exponent."""
-    B, L_max, Hkv, d, code = _cache_q8(k8, v8, k_exp, v_exp)
-    ks = _kv_pair(k, v, B, Hkv, d)
-    for t, nm in ((start, "start"), (rows, "rows")):
-        if t is not None:
-            _expect(t, nm, torch.int32, (B,))
-    dev = _device_of(k8, "k8")
-    a = [_addr(t, dev) for t in (k, v, start, rows, k8, v8, k_exp, v_exp, dev_err)]
-    _invoke("orthros_kv_quantize", dev, *a[:8], B, k.shape[1], Hkv, d, L_max, code, ks, a[8])
+    (B, L_max, Hkv, d, code), dev, cache = _cache_q8(k8, v8, k_exp, v_exp)
+    T, ks, kv = _kv_pair(k, v, B, Hkv, d, dev)
+    _invoke("orthros_kv_quantize", dev, *kv, _optional(start, "start", torch.int32, (B,), dev),
+            _optional(rows, "rows", torch.int32, (B,), dev), *cache, B, T, Hkv, d, L_max, code, ks,
+            _any_on(dev_err, "dev_err", dev))
 
 
 def kv_dequantize(k8, v8, k_exp, v_exp, k, v, start=None, rows=None, dev_err=None):
     """Read cache rows start[b].. (default 0) back as bf16 into rows 0..rows[b]-1 (default all T) of
     k, v [B, T, Hkv, d]; rows behind them are left as they are.  Returns (k, v)."""
-    B, L_max, Hkv, d, code = _cache_q8(k8, v8, k_exp, v_exp)
-    ks = _kv_pair(k, v, B, Hkv, d)
-    for t, nm in ((start, "start"), (rows, "rows")):
-        if t is not None:
-            _expect(t, nm, torch.int32, (B,))
-    dev = _device_of(k8, "k8")
-    a = [_addr(t, dev) for t in (k8, v8, k_exp, v_exp, start, rows, k, v, dev_err)]
-    _invoke("orthros_kv_dequantize", dev, *a[:8], B, k.shape[1], Hkv, d, L_max, code, ks, a[8])
+    (B, L_max, Hkv, d, code), dev, cache = _cache_q8(k8, v8, k_exp, v_exp)
+    T, ks, kv = _kv_pair(k, v, B, Hkv, d, dev)
+    _invoke("orthros_kv_dequantize", dev, *cache, _optional(start, "start", torch.int32, (B,), dev),
+            _optional(rows, "rows", torch.int32, (B,), dev), *kv, B, T, Hkv, d, L_max, code, ks,
+            _any_on(dev_err, "dev_err", dev))
     return k, v
 
 
@@ -599,26 +605,19 @@ def decode_q8_workspace(B, L_max, Hq, Hkv, d, device) -> torch.Tensor:
     return torch.zeros(max(decode_q8_workspace_size(B, L_max, Hq, Hkv, d), 256), dtype=torch.uint8, device=device)
 
 
-def _decode_args(q_new, qc_new, k_new, v_new, cache_len, vectors, o, oc, B, Hkv, d):
-    """Check what the decode steps share; return (o, oc, Hq)."""
+def _decode_args(q_new, qc_new, k_new, v_new, cache_len, alpha, beta, alpha_c, beta_c, o, oc, B, Hkv, d, dev):
+    """Check what the decode steps share; return (o, oc, Hq, addresses of the new token's tensors, of
+    cache_len, and of the vectors and outputs)."""
     Hq = q_new.shape[1]
-    rows, new, vec, bf16 = (B, Hq, d), (B, Hkv, d), (Hq, d), torch.bfloat16
-    _expect(q_new, "q_new", bf16, rows)
-    _expect(qc_new, "qc_new", bf16, rows)
-    _expect(k_new, "k_new", bf16, new)
-    _expect(v_new, "v_new", bf16, new)
-    _expect(cache_len, "cache_len", torch.int32, (B,))
-    for t, nm in zip(vectors, ("alpha", "beta", "alpha_c", "beta_c")):
-        _expect(t, nm, torch.float32, vec)
-    if o is None:
-        o = torch.empty_like(q_new)
-    else:
-        _expect(o, "o", bf16, rows)
-    if oc is None:
-        oc = torch.empty_like(q_new)
-    else:
-        _expect(oc, "oc", bf16, rows)
-    return o, oc, Hq
+    rows, new, vec, bf16, f32 = (B, Hq, d), (B, Hkv, d), (Hq, d), torch.bfloat16, torch.float32
+    token = (_dense(q_new, "q_new", bf16, rows, dev), _dense(qc_new, "qc_new", bf16, rows, dev),
+             _dense(k_new, "k_new", bf16, new, dev), _dense(v_new, "v_new", bf16, new, dev))
+    o = torch.empty_like(q_new) if o is None else o
+    oc = torch.empty_like(q_new) if oc is None else oc
+    rest = (_dense(alpha, "alpha", f32, vec, dev), _dense(beta, "beta", f32, vec, dev),
+            _dense(alpha_c, "alpha_c", f32, vec, dev), _dense(beta_c, "beta_c", f32, vec, dev),
+            _dense(o, "o", bf16, rows, dev), _dense(oc, "oc", bf16, rows, dev))
+    return o, oc, Hq, token, _dense(cache_len, "cache_len", torch.int32, (B,), dev), rest
 
 
 def decode_step_q8(q_new, qc_new, k_new, v_new, k8, v8, k_exp, v_exp, cache_len, alpha, beta, alpha_c, beta_c,
@@ -626,23 +625,21 @@ def decode_step_q8(q_new, qc_new, k_new, v_new, k8, v8, k_exp, v_exp, cache_len,
     """decode_step over an 8-bit cache (k8, v8 [B, L_max, Hkv, d] float8_e4m3fn or int8; k_exp, v_exp
     int8 [B, Hkv, L_max]): the new row is written as codes and both streams attend over the rows'
     values.  Returns (o, oc)."""
-    B, L_max, Hkv, d, code = _cache_q8(k8, v8, k_exp, v_exp)
-    dev = _device_of(k8, "k8")
-    o, oc, Hq = _decode_args(q_new, qc_new, k_new, v_new, cache_len, (alpha, beta, alpha_c, beta_c), o, oc, B, Hkv, d)
+    (B, L_max, Hkv, d, code), dev, cache = _cache_q8(k8, v8, k_exp, v_exp)
+    o, oc, Hq, token, lens, rest = _decode_args(q_new, qc_new, k_new, v_new, cache_len, alpha, beta, alpha_c, beta_c,
+                                                o, oc, B, Hkv, d, dev)
     if workspace is None:
         workspace = decode_q8_workspace(B, L_max, Hq, Hkv, d, k8.device)
-    a = [_addr(t, dev) for t in (q_new, qc_new, k_new, v_new, k8, v8, k_exp, v_exp, cache_len, alpha, beta, alpha_c,
-                                 beta_c, o, oc, workspace, dev_err)]
-    _invoke("orthros_decode_step_q8", dev, *a[:9], L_max, code, *a[9:15], B, Hq, Hkv, d, int(window),
-            _scale(scale, d), a[15], workspace.nbytes, a[16])
+    _invoke("orthros_decode_step_q8", dev, *token, *cache, lens, L_max, code, *rest, B, Hq, Hkv, d, int(window),
+            _scale(scale, d), _any_on(workspace, "workspace", dev), workspace.nbytes, _any_on(dev_err, "dev_err", dev))
     return o, oc
 
 
-def _prefix_rows(k_prefix, v_prefix, Hkv, d) -> int:
-    P = k_prefix.shape[0]
-    _expect(k_prefix, "k_prefix", torch.bfloat16, (P, Hkv, d))
-    _expect(v_prefix, "v_prefix", torch.bfloat16, (P, Hkv, d))
-    return P
+def _prefix_rows(k_prefix, v_prefix, Hkv, d, dev):
+    """Check the shared prefix [P, Hkv, d]; return (P, addresses)."""
+    shape = (k_prefix.shape[0], Hkv, d)
+    return shape[0], (_dense(k_prefix, "k_prefix", torch.bfloat16, shape, dev),
+                      _dense(v_prefix, "v_prefix", torch.bfloat16, shape, dev))
 
 
 def decode_prefix_workspace_size(B, P, L_max, Hq, Hkv, d) -> int:
@@ -661,17 +658,18 @@ def decode_step_prefix(q_new, qc_new, k_new, v_new, k_prefix, v_prefix, k_cache,
     b's rows are the prefix and then its own cache_len[b] rows of k_cache, v_cache
     [B, L_max, Hkv, d].  Returns (o, oc)."""
     B, L_max, Hkv, d = shape = k_cache.shape
-    _expect(k_cache, "k_cache", torch.bfloat16, shape)
-    _expect(v_cache, "v_cache", torch.bfloat16, shape)
-    P = _prefix_rows(k_prefix, v_prefix, Hkv, d)
-    dev = _device_of(k_cache, "k_cache")
-    o, oc, Hq = _decode_args(q_new, qc_new, k_new, v_new, cache_len, (alpha, beta, alpha_c, beta_c), o, oc, B, Hkv, d)
+    dev = k_cache.get_device()
+    if dev < 0:
+        _refuse(k_cache, "k_cache", "contiguous bf16 CUDA tensor [B, L_max, Hkv, d]")
+    cache = (_dense(k_cache, "k_cache", torch.bfloat16, shape, dev), _dense(v_cache, "v_cache", torch.bfloat16, shape, dev))
+    P, prefix = _prefix_rows(k_prefix, v_prefix, Hkv, d, dev)
+    o, oc, Hq, token, lens, rest = _decode_args(q_new, qc_new, k_new, v_new, cache_len, alpha, beta, alpha_c, beta_c,
+                                                o, oc, B, Hkv, d, dev)
     if workspace is None:
         workspace = decode_prefix_workspace(B, P, L_max, Hq, Hkv, d, k_cache.device)
-    a = [_addr(t, dev) for t in (q_new, qc_new, k_new, v_new, k_prefix, v_prefix, k_cache, v_cache, cache_len, alpha,
-                                 beta, alpha_c, beta_c, o, oc, workspace, dev_err)]
-    _invoke("orthros_decode_step_prefix", dev, *a[:6], P, *a[6:9], L_max, *a[9:15], B, Hq, Hkv, d, int(window),
-            _scale(scale, d), a[15], workspace.nbytes, a[16])
+    _invoke("orthros_decode_step_prefix", dev, *token, *prefix, P, *cache, lens, L_max, *rest, B, Hq, Hkv, d,
+            int(window), _scale(scale, d), _any_on(workspace, "workspace", dev), workspace.nbytes,
+            _any_on(dev_err, "dev_err", dev))
     return o, oc
 
 
@@ -685,24 +683,22 @@ def xattn_prefix_fwd(qc_raw, pos, k_prefix, v_prefix, k, v, alpha_c, beta_c, sca
     sequence b attends over the prefix and its sequence's own rows 0..pos[b, i] of k, v
     [B, T_kv, Hkv, d].  qc_raw [B, T_out, Hq, d]; pos int32 [B, T_out]."""
     B, T_kv, Hkv, d = k.shape
-    T_out, Hq = qc_raw.shape[1], qc_raw.shape[2]
-    ks = _kv_pair(k, v, B, Hkv, d)
-    if qc_raw.shape != (B, T_out, Hq, d):
-        raise OrthrosError("qc_raw shape does not match k")
-    qs = _bf16_rows(qc_raw, "qc_raw")
-    P = _prefix_rows(k_prefix, v_prefix, Hkv, d)
-    _expect(pos, "pos", torch.int32, (B, T_out))
-    _expect(alpha_c, "alpha_c", torch.float32, (Hq, d))
-    _expect(beta_c, "beta_c", torch.float32, (Hq, d))
-    dev = _device_of(k, "k")
+    dev = k.get_device()
+    if dev < 0:
+        _refuse(k, "k", "bf16 CUDA tensor [B, T_kv, Hkv, d]")
+    _, T_out, Hq, _ = qc_raw.shape
+    shape = (B, T_out, Hq, d)
+    _, ks, own = _kv_pair(k, v, B, Hkv, d, dev)
+    qa, qs = _rows(qc_raw, "qc_raw", shape, dev)
+    P, prefix = _prefix_rows(k_prefix, v_prefix, Hkv, d, dev)
     if out is None:
-        out = torch.empty((B, T_out, Hq, d), dtype=torch.bfloat16, device=k.device)
-    elif out.shape != (B, T_out, Hq, d):
-        raise OrthrosError("out shape does not match qc_raw")
+        out = torch.empty(shape, dtype=torch.bfloat16, device=k.device)
+    oa, os_ = _rows(out, "out", shape, dev)
     if workspace is None:
         workspace = torch.empty(max(xattn_prefix_workspace_size(B, T_out, P, T_kv, Hq, Hkv, d), 256),
                                 dtype=torch.uint8, device=k.device)
-    a = [_addr(t, dev) for t in (qc_raw, pos, k_prefix, v_prefix, k, v, alpha_c, beta_c, out, workspace, dev_err)]
-    _invoke("orthros_xattn_prefix_fwd", dev, *a[:4], P, *a[4:9], B, T_out, T_kv, Hq, Hkv, d, _scale(scale, d), qs, ks,
-            _bf16_rows(out, "out"), a[9], workspace.nbytes, a[10])
+    _invoke("orthros_xattn_prefix_fwd", dev, qa, _dense(pos, "pos", torch.int32, (B, T_out), dev), *prefix, P, *own,
+            _dense(alpha_c, "alpha_c", torch.float32, (Hq, d), dev),
+            _dense(beta_c, "beta_c", torch.float32, (Hq, d), dev), oa, B, T_out, T_kv, Hq, Hkv, d, _scale(scale, d),
+            qs, ks, os_, _any_on(workspace, "workspace", dev), workspace.nbytes, _any_on(dev_err, "dev_err", dev))
     return out
