@@ -112,6 +112,15 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity)
     return mbar_try_wait(bar, parity) || mbar_wait_slow(bar, parity);
 }
 
+// After a wait has given up: time enough (1 ms) for the copies and MMAs in flight to land before
+// their shared or tensor memory is given back.
+static __device__ __noinline__ void drain_in_flight()
+{
+    const uint64_t t0 = global_timer_ns();
+    while (global_timer_ns() - t0 < 1000000ull) {
+    }
+}
+
 // ------------------------------------------------------------------ TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map)

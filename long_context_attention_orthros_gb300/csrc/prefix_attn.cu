@@ -44,7 +44,9 @@ __global__ void __launch_bounds__(PaCfg<D>::THREADS)
     const int split = blockIdx.x, g = blockIdx.y % p.Hkv;
     const long long row0 = static_cast<long long>(blockIdx.y / p.Hkv) * 16 * RG;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    __shared__ volatile int s_abort;  // a wait has given up: the producer stops
     if (threadIdx.x == 0) {
+        s_abort = 0;
         for (int s = 0; s < C::STAGES; ++s) {
             mbar_init(&full[s], 1);
             mbar_init(&empty[s], C::CWARPS);
@@ -68,8 +70,9 @@ __global__ void __launch_bounds__(PaCfg<D>::THREADS)
         tma_prefetch_desc(&vmap);
         for (int i = 0; i < nblk; ++i) {
             const int s = i % C::STAGES;
-            if (i >= C::STAGES && !mbar_wait(&empty[s], static_cast<uint32_t>(((i / C::STAGES) - 1) & 1))) {
+            if ((i >= C::STAGES && !mbar_wait(&empty[s], static_cast<uint32_t>(((i / C::STAGES) - 1) & 1))) || s_abort) {
                 record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+                drain_in_flight();
                 return;
             }
             uint8_t *dst = smem + s * C::STAGE_BYTES;
@@ -104,7 +107,7 @@ __global__ void __launch_bounds__(PaCfg<D>::THREADS)
     for (int i = 0; i < nblk; ++i) {
         const int s = i % C::STAGES;
         if (ok && !mbar_wait(&full[s], static_cast<uint32_t>((i / C::STAGES) & 1)))
-            ok = false;
+            ok = false, s_abort = 1;
         const uint32_t kbase = sbase + s * C::STAGE_BYTES;
 #pragma unroll
         for (int c = kl; c < 4; c += KL) {
@@ -116,8 +119,11 @@ __global__ void __launch_bounds__(PaCfg<D>::THREADS)
         if (lane == 0)
             mbar_arrive(&empty[s]);
     }
-    if (!ok && lane == 0)
-        record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+    if (!ok) {
+        if (lane == 0)
+            record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+        drain_in_flight();
+    }
     st.finish_sums();
 
     // the KL warps of a group, scaled to their common max, summed through shared memory

@@ -107,7 +107,9 @@ __global__ void __launch_bounds__(512, 1)
         DIRECT ? static_cast<long long>(b_own) * p.T_out * G + static_cast<long long>(blockIdx.z % seq_tiles) * 256
                : static_cast<long long>(blockIdx.z) * 128 * C::TILES;
     const long long row_end = DIRECT ? static_cast<long long>(b_own + 1) * p.T_out * G : R;
+    __shared__ volatile int s_abort;  // a wait has given up: the producer stops
     if (threadIdx.x == 0) {
+        s_abort = 0;
         for (int s = 0; s < C::SLOTS; ++s) {
             mbar_init(&kfull[s], 1);
             mbar_init(&vfull[s], 1);
@@ -195,8 +197,11 @@ __global__ void __launch_bounds__(512, 1)
                 const int ps = pp % C::PAIRS;
                 for (int kv = 0; kv < 2 && ok; ++kv) {
                     if (pp >= C::PAIRS && !mbar_wait(kv ? &vempty[ps] : &kempty[ps],
-                                                     static_cast<uint32_t>((pp / C::PAIRS - 1) & 1))) {
+                                                     static_cast<uint32_t>((pp / C::PAIRS - 1) & 1)))
+                        ok = false;
+                    if (!ok || s_abort) {
                         record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+                        s_abort = 1;
                         ok = false;
                         break;
                     }
@@ -279,8 +284,10 @@ __global__ void __launch_bounds__(512, 1)
                     // ROWS2: S_A of the next pair goes out before P V of B; the pair B still reads stays
                     ok = issue_pv(t, u) && (u + 1 >= pairs_of(t) || issue_s(t, u + 1));
                 }
-            if (!ok)
+            if (!ok) {
+                s_abort = 1;
                 record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+            }
         }
     } else if (warp < 4 || warp >= 12) {
         // ------------------------------------------------------------------ K converters
@@ -346,8 +353,11 @@ __global__ void __launch_bounds__(512, 1)
         }
         if (bad)
             record_error(p.dev_err, ORTHROS_DEVERR_RANGE);
-        if (!ok && lane == 0)
-            record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+        if (!ok) {
+            s_abort = 1;
+            if (lane == 0)
+                record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+        }
     } else {
         // ------------------------------------------------------------------ softmax + partials
         // first the queries, from global memory to fp16 tiles, by all eight warps: a thread has 16 bytes of
@@ -602,13 +612,20 @@ __global__ void __launch_bounds__(512, 1)
         }
         if (range_bad)
             record_error(p.dev_err, ORTHROS_DEVERR_RANGE);
-        if (!ok && lane == 0)
-            record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+        if (!ok) {
+            s_abort = 1;
+            if (lane == 0)
+                record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+        }
     }
 
     // ---------------------------------------------------------------------- teardown
     tc_fence_before();
     __syncthreads();
+    if (s_abort) {
+        drain_in_flight();
+        __syncthreads();
+    }
     if (warp == 1) {
         tc_fence_after();
         tmem_dealloc(tbase, 512);

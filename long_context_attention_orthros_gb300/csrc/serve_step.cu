@@ -247,6 +247,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
     uint64_t *hfull = empty + C::STAGES, *hempty = hfull + C::HB;
     Join *joins = reinterpret_cast<Join *>(smem + C::JOIN_OFF);
     int *s_flag = reinterpret_cast<int *>(smem + C::FLAG_OFF);
+    volatile int *s_abort = s_flag + 1;  // a wait has given up: the producer stops
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     const float NEG_INF = -__int_as_float(0x7f800000);
 
@@ -259,6 +260,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
             mbar_init(&hfull[s], 1);
             mbar_init(&hempty[s], C::CWARPS);
         }
+        *s_abort = 0;
         fence_barrier_init();
     }
     // Programmatic dependent launch.  8-bit form: everything the step before wrote is waited for
@@ -287,8 +289,10 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
             }
             if (header) {  // the segment's queries
                 const int hb = segs % C::HB;
-                if (segs >= C::HB && !mbar_wait(&hempty[hb], static_cast<uint32_t>((segs / C::HB - 1) & 1))) {
+                if ((segs >= C::HB && !mbar_wait(&hempty[hb], static_cast<uint32_t>((segs / C::HB - 1) & 1))) ||
+                    *s_abort) {
                     record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+                    drain_in_flight();
                     return;
                 }
                 uint8_t *h = smem + C::HDR_OFF + hb * C::HDR_BYTES;
@@ -306,8 +310,9 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
                 ++segs;
             }
             const int s = static_cast<int>(i % C::STAGES);
-            if (i >= C::STAGES && !mbar_wait(&empty[s], static_cast<uint32_t>(((i / C::STAGES) - 1) & 1))) {
+            if ((i >= C::STAGES && !mbar_wait(&empty[s], static_cast<uint32_t>(((i / C::STAGES) - 1) & 1))) || *s_abort) {
                 record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+                drain_in_flight();
                 return;
             }
             bool pre;
@@ -471,7 +476,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
         {
             const int hb = segs % C::HB;
             if (ok && !mbar_wait(&hfull[hb], static_cast<uint32_t>((segs / C::HB) & 1)))
-                ok = false;
+                ok = false, *s_abort = 1;
             const orthros_bf16 *q = reinterpret_cast<const orthros_bf16 *>(smem + C::HDR_OFF + hb * C::HDR_BYTES);
             const float *al = reinterpret_cast<const float *>(q + G * D), *be = al + G * D;
             st.load_q(q, al, be, G, p.qscale);
@@ -500,7 +505,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
             // the block's rows that count: lo .. hi
             const int lo = (cur.base ? (pre ? sp.lo_p : sp.lo) : 0) - blk * C::KB, hi = (pre ? p.P - 1 : sp.p) - blk * C::KB;
             if (ok && !mbar_wait(&full[s], static_cast<uint32_t>((i / C::STAGES) & 1)))
-                ok = false;
+                ok = false, *s_abort = 1;
             constexpr int WK = 16 * C::KT;  // this warp's keys: rows r0 .. r0 + WK - 1 of the block
             const int r0 = (warp % C::GROUP) * WK;
             if (ok && !sp.full && r0 <= hi && r0 + WK - 1 >= lo) {
@@ -686,8 +691,11 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
     }
     if (bad)
         record_error(p.dev_err, ORTHROS_DEVERR_RANGE);
-    if (!ok && lane == 0)
-        record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+    if (!ok) {
+        if (lane == 0)
+            record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+        drain_in_flight();
+    }
     join_all(true);
     // the last CTA of the grid advances the lengths: every one has read them by now
     if (STEP && s_flag[0]) {
