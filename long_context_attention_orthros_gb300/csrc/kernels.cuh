@@ -154,7 +154,7 @@ cudaError_t launch_prefix_tc(int D, int mode, const PrefixMaps &maps, const Pref
                              cudaStream_t stream);
 // copies over the prefix and their own rows in one kernel, outputs at p.oc; tiles of a sequence, or 0
 // where partials serve better
-int prefix_direct_tiles(int B, int T_out, int Hq, int Hkv);
+int prefix_direct_tiles(int B, int T_out, int P, int T_kv, int Hq, int Hkv, int D);
 cudaError_t launch_prefix_direct(int D, const PrefixMaps &maps, const PrefixAttnParams &p, cudaStream_t stream);
 int prefix_attn_parts(long long copies, int P, int Hq, int Hkv);
 cudaError_t launch_prefix_attn(int D, const CUtensorMap &k, const CUtensorMap &v, PrefixAttnParams p,
@@ -177,6 +177,7 @@ struct ServeParams {
     int32_t *dev_err;
     int B, Hq, Hkv, L_max, window;
     int P, n_part;            // prefix rows (0: 8-bit form) and splits
+    int join_after;           // partials are joined by a kernel of its own; set by the launchers
     float qscale;
     long long q_bstride, o_bstride;  // elements between sequences of q_new, qc_new and of o, oc; set by the launchers
 };

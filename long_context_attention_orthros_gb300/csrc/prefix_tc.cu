@@ -685,18 +685,32 @@ cudaError_t launch_prefix_tc(int D, int mode, const PrefixMaps &maps, const Pref
     return cudaErrorInvalidValue;
 }
 
-// Many copies a sequence: tiles of 256 rows of one sequence each, prefix and own rows in one pass and
-// no partials.  Taken when padding the last tile costs at most a third and the tiles fill at least
-// half of the SMs (one CTA runs over all keys of its rows); otherwise splitting the prefix pays.
-int prefix_direct_tiles(int B, int T_out, int Hq, int Hkv)
+// Prefix and own rows in one pass (tiles of 256 rows of one sequence, one launch, no partials) or the
+// prefix split over all SMs, the own rows by warp MMAs and a join?  The first takes 2.1 us for every
+// 128 keys one CTA runs over (in as many waves as 152 SMs need) and 9 us around them; the second 20 us
+// for its three launches, 2 ns a row to join, the prefix's tiles shared out evenly and the own rows at
+// some 210 TFLOP/s.  Measured on a GB300 (split, direct, us): 3 x 37 copies over 617 + 1457 keys, G = 1:
+// 26, 40; 2 x 24 over 53852 + 548, G = 2: 60, 926; 10 x 52 over 920 + 2, G = 4: 76, 33; 5 x 313 over 1766 + 1695,
+// G = 2: 150, 81; 3 x 395 over 6 + 1, G = 4: 100, 30.  One copy a sequence has its own kernel.
+int prefix_direct_tiles(int B, int T_out, int P, int T_kv, int Hq, int Hkv, int D)
 {
     const long long rows = static_cast<long long>(T_out) * (Hq / Hkv), tiles = (rows + 255) / 256;
-    return tiles * 256 * 3 <= rows * 4 && B * tiles * Hkv >= 76 && B * tiles <= 65535 ? static_cast<int>(tiles) : 0;
+    if (T_out <= 1 || B * tiles > 65535)
+        return 0;
+    const double pairs = (P + 127) / 128 + (T_kv + 127) / 128;
+    const double waves = static_cast<double>((B * tiles * Hkv + 151) / 152);
+    const double direct = 9.0 + 2.1 * pairs * waves;
+    const double all = static_cast<double>(B) * T_out * Hq;
+    const double split = 20.0 + 0.002 * all +
+                         2.1 * static_cast<double>((B * rows + 255) / 256) * Hkv * ((P + 127) / 128) / 152.0 +
+                         all * T_kv * 4.0 * D / 210e6;
+    return direct <= split ? static_cast<int>(tiles) : 0;
 }
 
 cudaError_t launch_prefix_direct(int D, const PrefixMaps &maps, const PrefixAttnParams &p, cudaStream_t stream)
 {
-    return launch_prefix_tc(D, PT_DIRECT, maps, p, 1, p.B * prefix_direct_tiles(p.B, p.T_out, p.Hq, p.Hkv), stream);
+    return launch_prefix_tc(D, PT_DIRECT, maps, p, 1, p.B * static_cast<int>((static_cast<long long>(p.T_out) * (p.Hq / p.Hkv) + 255) / 256),
+                            stream);
 }
 
 }  // namespace orthros

@@ -678,7 +678,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
         }
         if (sp.full && !cur.base && g == 0 && t == 0)
             record_error(p.dev_err, STEP ? ORTHROS_DEVERR_CACHE_FULL : ORTHROS_DEVERR_POSITION);
-        if (!alone) {
+        if (!alone && !p.join_after) {
             if (t == 0)
                 joins[njoin] = {b * p.Hkv + g, cur.base, static_cast<int>(c0), static_cast<int>(c1 - c0) + 1, 0, 0};
             if (++njoin == MAX_JOINS)
@@ -696,6 +696,11 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
             record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
         drain_in_flight();
     }
+    if (p.join_after) {  // serve_join_kernel joins the partials and advances the lengths
+        if constexpr (!Q8)
+            asm volatile("griddepcontrol.wait;" ::: "memory");  // it waits for this grid, and the prefix kernel's too
+        return;
+    }
     join_all(true);
     // the last CTA of the grid advances the lengths: every one has read them by now
     if (STEP && s_flag[0]) {
@@ -706,6 +711,128 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
         }
         if (t == 0)
             *p.cnt_all = 0;
+    }
+}
+
+// Many parts of few segments (a long cache or prefix of one KV head over all SMs): one CTA a row, its
+// eight half-warps take every eighth part each.  The CTAs that held a segment are found by the same
+// arithmetic as in the step.  The last CTA advances the lengths.
+template <int D, int G, int CODE>
+__global__ void __launch_bounds__(128) serve_join_kernel(const ServeParams p, int ctas)
+{
+    using C = SvCfg<D, G, CODE>;
+    constexpr int E = D / 16;
+    __shared__ float red_s[4], o_s[8][D];
+    __shared__ int last_s;
+    const int t = threadIdx.x, warp = t >> 5, lane = t & 31, hw = t >> 4, hl = t & 15;
+    const int row = blockIdx.x % G, base = blockIdx.x / G % C::SEGS, bh = blockIdx.x / (G * C::SEGS);
+    const int b = bh / p.Hkv, g = bh % p.Hkv;
+    const float NEG_INF = -__int_as_float(0x7f800000);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    long long W = 0, before = 0;  // places of the list, and those before sequence b
+    for (int i = lane; i < p.B; i += 32) {
+        const long long w = seq_places<C>(p, __ldcg(p.cache_len + i));
+        W += w;
+        before += i < b ? w : 0;
+    }
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) {
+        W += __shfl_xor_sync(0xffffffffu, W, off);
+        before += __shfl_xor_sync(0xffffffffu, before, off);
+    }
+    const SeqPlan sp = seq_plan<C>(p, __ldcg(p.cache_len + b));
+    const long long n = ctas < W ? ctas : W;
+    const long long s0 = before + static_cast<long long>(sp.nc + sp.nb + C::SEGS * SEG_COST) * g + SEG_COST +
+                         (base ? sp.nc + SEG_COST : 0);
+    const long long s1 = s0 + (base ? sp.nb : sp.nc);
+    const long long c0 = ((s0 + 1) * n - 1) / W, c1 = (s1 * n - 1) / W;
+    // what one CTA held whole is written already, but for a copy that the prefix has to be joined with
+    const bool joins_prefix = !C::Q8 && !base && !sp.full;
+    if (c0 != c1 || joins_prefix) {
+        const int nown = static_cast<int>(c1 - c0) + 1, nq = nown + (joins_prefix ? p.n_part : 0);
+        const long long BH = static_cast<long long>(p.B) * p.Hkv;
+        auto slot_of = [&](int q) -> long long {
+            return q < nown ? (c0 == c1 ? 2LL * ctas + bh : 2LL * (c0 + q) + (q == 0 ? 1 : 0)) * G + row
+                            : ((q - nown) * BH + bh) * G + row;
+        };
+        auto ml_of = [&](int q) -> float2 { return __ldcg((q < nown ? p.part_ml : p.pre_ml) + slot_of(q)); };
+        float M = NEG_INF;
+        for (int q = t; q < nq; q += 128)
+            M = fmaxf(M, ml_of(q).x);
+#pragma unroll
+        for (int off = 16; off > 0; off >>= 1)
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        if (lane == 0)
+            red_s[warp] = M;
+        __syncthreads();
+        M = fmaxf(fmaxf(red_s[0], red_s[1]), fmaxf(red_s[2], red_s[3]));
+        float L = 0.f, a[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            a[e] = 0.f;
+        for (int q0 = hw; q0 < nq; q0 += 64) {
+            float2 ml[8];
+            float4 y[8][E / 4];
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                const int q = q0 + 8 * k;
+                ml[k] = make_float2(NEG_INF, 0.f);
+                if (q < nq) {
+                    ml[k] = ml_of(q);
+                    const float *src = (q < nown ? p.part_o : p.pre_o) + slot_of(q) * D + hl * E;
+#pragma unroll
+                    for (int e = 0; e < E / 4; ++e)
+                        y[k][e] = __ldcg(reinterpret_cast<const float4 *>(src) + e);
+                }
+            }
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+                if (ml[k].x == NEG_INF)
+                    continue;
+                const float w = fast_exp2(ml[k].x - M);
+                L += w * ml[k].y;
+#pragma unroll
+                for (int e = 0; e < E / 4; ++e) {
+                    a[4 * e] = fmaf(w, y[k][e].x, a[4 * e]);
+                    a[4 * e + 1] = fmaf(w, y[k][e].y, a[4 * e + 1]);
+                    a[4 * e + 2] = fmaf(w, y[k][e].z, a[4 * e + 2]);
+                    a[4 * e + 3] = fmaf(w, y[k][e].w, a[4 * e + 3]);
+                }
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            o_s[hw][hl * E + e] = a[e];
+        __syncthreads();  // red_s has been read, o_s is complete
+        L += __shfl_xor_sync(0xffffffffu, L, 16);  // all lanes of a half-warp hold its sum
+        if (lane == 0)
+            red_s[warp] = L;
+        __syncthreads();
+        L = (red_s[0] + red_s[1]) + (red_s[2] + red_s[3]);
+        const float inv = L > 0.f ? 1.f / L : 0.f;
+        if (t < D) {
+            float x = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8; ++i)
+                x += o_s[i][t];
+            (base ? p.o : p.oc)[b * p.o_bstride + (g * G + row) * D + t] = __bfloat16_as_ushort(__float2bfloat16_rn(x * inv));
+        }
+    }
+    if constexpr (C::STEP) {
+        __syncthreads();  // every warp has read cache_len
+        if (t == 0)
+            last_s = atomicAdd(p.cnt_all, 1) == static_cast<int>(gridDim.x) - 1;
+        __syncthreads();
+        if (last_s) {
+            for (int i = t; i < p.B; i += 128) {
+                const int len = __ldcg(p.cache_len + i);
+                if (len >= 0 && len < p.L_max)
+                    p.cache_len[i] = len + 1;
+            }
+            if (t == 0)
+                *p.cnt_all = 0;
+        }
     }
 }
 
@@ -739,14 +866,24 @@ size_t serve_workspace_bytes(int B, int P, int L_max, int Hq, int Hkv, int D)
     return serve_layout(B, P, L_max, Hq, Hkv, D).total;
 }
 
+// A join inside the step costs the CTA that does it 8.5 ns a part and row at d = 128 (one SM reads all of
+// them, 60 GB/s); a kernel of its own costs 3 us, whatever their number.  With one KV head of 16 query
+// heads and 4 sequences (76 parts a copy) the step took 57 us with the join inside.
+static bool join_after(const ServeParams &p, int ctas, int D)
+{
+    const long long parts = ctas / (static_cast<long long>(p.B) * p.Hkv) + p.n_part;
+    return parts * (p.Hq / p.Hkv) * D >= 45000;
+}
+
 template <int D, int G, int CODE>
-static cudaError_t launch_serve_tc(const ServeMaps &maps, const ServeParams &p, int ctas, cudaStream_t stream)
+static cudaError_t launch_serve_tc(const ServeMaps &maps, ServeParams p, int ctas, cudaStream_t stream)
 {
     using C = SvCfg<D, G, CODE>;
     auto kern = serve_step_kernel<D, G, CODE>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess)
         return e;
+    p.join_after = join_after(p, ctas, D);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(C::THREADS);
@@ -758,6 +895,12 @@ static cudaError_t launch_serve_tc(const ServeMaps &maps, const ServeParams &p, 
     cfg.attrs = attr;
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kern, maps, p);
+    if (e == cudaSuccess && p.join_after) {
+        cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hkv * C::SEGS * G);
+        cfg.blockDim = dim3(128);
+        cfg.dynamicSmemBytes = 0;
+        e = cudaLaunchKernelEx(&cfg, serve_join_kernel<D, G, CODE>, p, ctas);
+    }
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 

@@ -18,7 +18,7 @@ struct XpLayout {
 XpLayout xp_layout(int B, int T_out, int P, int T_kv, int Hq, int Hkv, int D)
 {
     XpLayout l = {0, 0, 0, 256};
-    if (prefix_direct_tiles(B, T_out, Hq, Hkv) > 0)
+    if (prefix_direct_tiles(B, T_out, P, T_kv, Hq, Hkv, D) > 0)
         return l;
     if (T_out == 1) {
         l.total = serve_workspace_bytes(B, P, T_kv, Hq, Hkv, D);
@@ -41,7 +41,7 @@ size_t xattn_prefix_workspace_bytes(int B, int T_out, int P, int T_kv, int Hq, i
 
 cudaError_t launch_xattn_prefix(int D, const CUtensorMap *m, XattnParams x, int P, void *workspace, cudaStream_t stream)
 {
-    if (x.T_out == 1 && prefix_direct_tiles(x.B, 1, x.Hq, x.Hkv) == 0)
+    if (x.T_out == 1)
         return launch_serve_copies(D, m, x, P, workspace, stream);
     const XpLayout l = xp_layout(x.B, x.T_out, P, x.T_kv, x.Hq, x.Hkv, D);
     float *part_o = static_cast<float *>(workspace);
@@ -62,7 +62,7 @@ cudaError_t launch_xattn_prefix(int D, const CUtensorMap *m, XattnParams x, int 
     a.Hq = x.Hq;
     a.Hkv = x.Hkv;
     a.qscale = x.qscale;
-    if (prefix_direct_tiles(x.B, x.T_out, x.Hq, x.Hkv) > 0) {
+    if (prefix_direct_tiles(x.B, x.T_out, P, x.T_kv, x.Hq, x.Hkv, D) > 0) {
         a.oc = x.oc;
         a.oc_bstride = x.oc_bstride;
         return launch_prefix_direct(D, PrefixMaps{m[2], m[3], m[0], m[1]}, a, stream);
