@@ -436,8 +436,9 @@ orthros_status orthros_attn_bwd(const orthros_bf16 *q_raw, const orthros_bf16 *k
  * 127 (int8), clamped to [-126, 127] (0 for a row of zeros), and codes x 2^-e rounded to
  * nearest even.  Scaling by a power of two is exact, so the codes do not depend on the
  * implementation, and a value read back is exact in bf16 (except below bf16's smallest, and
- * that a value whose code rounds up to 2^128 reads back as infinite).  A value that is not finite sets ORTHROS_DEVERR_RANGE where it is written: it does not count
- * for e, its e4m3 code is NaN, its int8 code the end of the range on its side (0 for a NaN).
+ * that a value whose code rounds up to 2^128 reads back as infinite).  A value that is not
+ * finite sets ORTHROS_DEVERR_RANGE where it is written: it does not count for e, its e4m3 code
+ * is NaN, its int8 code the end of the range on its side (0 for a NaN).
  */
 #define ORTHROS_KV_E4M3 0
 #define ORTHROS_KV_INT8 1
@@ -470,7 +471,8 @@ orthros_status orthros_kv_dequantize(const uint8_t *k8, const uint8_t *v8, const
 
 /*
  * Bytes of device workspace orthros_decode_step_q8 needs, zero-filled once before its first use
- * and left ready for the next step (not for two steps in flight).  Returns 0 for invalid sizes.
+ * and left ready for the next step, also one of other sizes that need no more, or of
+ * orthros_decode_step_prefix (not for two steps in flight).  Returns 0 for invalid sizes.
  */
 size_t orthros_decode_q8_workspace_size(int B, int L_max, int Hq, int Hkv, int d);
 
@@ -492,8 +494,8 @@ orthros_status orthros_decode_step_q8(const orthros_bf16 *q_new, const orthros_b
 
 /*
  * Bytes of device workspace orthros_decode_step_prefix needs, zero-filled once before its first
- * use and left ready for the next step (not for two steps in flight).  Returns 0 for invalid
- * sizes.
+ * use and left ready for the next step, as that of orthros_decode_step_q8.  Returns 0 for
+ * invalid sizes.
  */
 size_t orthros_decode_prefix_workspace_size(int B, int P, int L_max, int Hq, int Hkv, int d);
 
@@ -526,8 +528,9 @@ size_t orthros_xattn_prefix_workspace_size(int B, int T_out, int P, int T_kv, in
  * prefix and its sequence's own rows 0 .. pos[b, i] (k, v [B, T_kv, Hkv, d]; pos counts own rows,
  * each in [0, T_kv), so the copy's position is P + pos).  The prefix is read once for all copies
  * of the batch.  A copy whose position is out of range gets a zero output and sets
- * ORTHROS_DEVERR_POSITION.  workspace: orthros_xattn_prefix_workspace_size(...) bytes, 256-byte
- * aligned, contents need not be initialised.  Other arguments as orthros_xattn_fwd.
+ * ORTHROS_DEVERR_POSITION.  Own rows behind a sequence's largest position may hold anything.
+ * workspace: orthros_xattn_prefix_workspace_size(...) bytes, 256-byte aligned, contents need not
+ * be initialised.  Other arguments as orthros_xattn_fwd.
  */
 orthros_status orthros_xattn_prefix_fwd(const orthros_bf16 *qc_raw, const int32_t *pos,
                                         const orthros_bf16 *k_prefix, const orthros_bf16 *v_prefix,

@@ -519,12 +519,19 @@ def _optional(t, name: str, dtype, shape, dev: int):
     return None if t is None else _dense(t, name, dtype, shape, dev)
 
 
-def _any_on(t, name: str, dev: int):
-    """Address of a workspace or an error word on device `dev` (or None)."""
+def _space(t, dev: int) -> int:
+    """Address of a workspace on device `dev`."""
+    if t.get_device() != dev or not t.is_contiguous():
+        _refuse(t, "workspace", "contiguous CUDA tensor")
+    return t.data_ptr()
+
+
+def _word(t, dev: int):
+    """Address of an error word on device `dev` (or None)."""
     if t is None:
         return None
-    if t.get_device() != dev or not t.is_contiguous():
-        _refuse(t, name, "contiguous CUDA tensor")
+    if t.dtype is not torch.int32 or t.numel() < 1 or t.get_device() != dev:
+        _refuse(t, "dev_err", "int32 CUDA tensor")
     return t.data_ptr()
 
 
@@ -582,7 +589,7 @@ def kv_quantize(k, v, k8, v8, k_exp, v_exp, start=None, rows=None, dev_err=None)
     T, ks, kv = _kv_pair(k, v, B, Hkv, d, dev)
     _invoke("orthros_kv_quantize", dev, *kv, _optional(start, "start", torch.int32, (B,), dev),
             _optional(rows, "rows", torch.int32, (B,), dev), *cache, B, T, Hkv, d, L_max, code, ks,
-            _any_on(dev_err, "dev_err", dev))
+            _word(dev_err, dev))
 
 
 def kv_dequantize(k8, v8, k_exp, v_exp, k, v, start=None, rows=None, dev_err=None):
@@ -592,7 +599,7 @@ def kv_dequantize(k8, v8, k_exp, v_exp, k, v, start=None, rows=None, dev_err=Non
     T, ks, kv = _kv_pair(k, v, B, Hkv, d, dev)
     _invoke("orthros_kv_dequantize", dev, *cache, _optional(start, "start", torch.int32, (B,), dev),
             _optional(rows, "rows", torch.int32, (B,), dev), *kv, B, T, Hkv, d, L_max, code, ks,
-            _any_on(dev_err, "dev_err", dev))
+            _word(dev_err, dev))
     return k, v
 
 
@@ -631,7 +638,7 @@ def decode_step_q8(q_new, qc_new, k_new, v_new, k8, v8, k_exp, v_exp, cache_len,
     if workspace is None:
         workspace = decode_q8_workspace(B, L_max, Hq, Hkv, d, k8.device)
     _invoke("orthros_decode_step_q8", dev, *token, *cache, lens, L_max, code, *rest, B, Hq, Hkv, d, int(window),
-            _scale(scale, d), _any_on(workspace, "workspace", dev), workspace.nbytes, _any_on(dev_err, "dev_err", dev))
+            _scale(scale, d), _space(workspace, dev), workspace.nbytes, _word(dev_err, dev))
     return o, oc
 
 
@@ -668,8 +675,8 @@ def decode_step_prefix(q_new, qc_new, k_new, v_new, k_prefix, v_prefix, k_cache,
     if workspace is None:
         workspace = decode_prefix_workspace(B, P, L_max, Hq, Hkv, d, k_cache.device)
     _invoke("orthros_decode_step_prefix", dev, *token, *prefix, P, *cache, lens, L_max, *rest, B, Hq, Hkv, d,
-            int(window), _scale(scale, d), _any_on(workspace, "workspace", dev), workspace.nbytes,
-            _any_on(dev_err, "dev_err", dev))
+            int(window), _scale(scale, d), _space(workspace, dev), workspace.nbytes,
+            _word(dev_err, dev))
     return o, oc
 
 
@@ -700,5 +707,5 @@ def xattn_prefix_fwd(qc_raw, pos, k_prefix, v_prefix, k, v, alpha_c, beta_c, sca
     _invoke("orthros_xattn_prefix_fwd", dev, qa, _dense(pos, "pos", torch.int32, (B, T_out), dev), *prefix, P, *own,
             _dense(alpha_c, "alpha_c", torch.float32, (Hq, d), dev),
             _dense(beta_c, "beta_c", torch.float32, (Hq, d), dev), oa, B, T_out, T_kv, Hq, Hkv, d, _scale(scale, d),
-            qs, ks, os_, _any_on(workspace, "workspace", dev), workspace.nbytes, _any_on(dev_err, "dev_err", dev))
+            qs, ks, os_, _space(workspace, dev), workspace.nbytes, _word(dev_err, dev))
     return out

@@ -40,6 +40,9 @@ struct XattnParams {
     int32_t *dev_err;
     long long qc_bstride, oc_bstride;
     int B, T_out, T_kv, Hq, Hkv, G, R, row_tiles, splits, chunk, n_part, direct;
+    // own rows behind a prefix: V rows behind a CTA's last position may hold anything, and a partial whose
+    // sum is a NaN reaches the output
+    int behind_prefix;
     float qscale;
 };
 
@@ -170,7 +173,7 @@ struct ServeParams {
     orthros_bf16 *o, *oc;
     float *part_o;            // [2 * CTAs (+ B * Hkv behind a prefix)][G][D]
     float2 *part_ml;
-    int *cnt_bh;              // [B * Hkv][2]
+    int *cnt_seg;             // [CTAs]: parts of the segment that runs out of a CTA, counted in
     int *cnt_all;
     float *pre_o;             // the prefix kernel's partials (prefix form)
     float2 *pre_ml;

@@ -158,7 +158,7 @@ __global__ void __launch_bounds__(PaCfg<D>::THREADS)
 #pragma unroll
         for (int w = 0; w < KL; ++w) {
             const int x = (w0 + w) * 16 + r % 16;
-            if (ms[x] == NEG_INF)
+            if (ls[x] == 0.f)  // no key
                 continue;
             const float f = fast_exp2(ms[x] - M);
             L += f * ls[x];

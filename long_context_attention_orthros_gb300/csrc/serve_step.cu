@@ -366,12 +366,11 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
         named_barrier(1, C::CTHREADS);
         if (t < njoin) {
             Join &j = joins[t];
-            int *cnt = p.cnt_bh + 2LL * j.bh + j.base;
+            int *cnt = p.cnt_seg + j.c0;  // at most one segment runs out of a CTA
             __threadfence();
-            const int last = j.parts == 1 || atomicAdd(cnt, 1) == j.parts - 1;
+            j.last = j.parts == 1 || atomicAdd(cnt, 1) == j.parts - 1;
             __threadfence();
-            j.last = last;
-            if (last)
+            if (j.parts > 1 && j.last)
                 *cnt = 0;
         }
         if (STEP && final && t == C::CTHREADS - 1)  // every warp of this CTA has read cache_len for the last time
@@ -434,7 +433,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
                 if (q0 % 16 == 0) {
                     if (q0 > 0)
                         ml = ml_of(q0 + hl);
-                    w = ml.x == NEG_INF ? 0.f : fast_exp2(ml.x - M);
+                    w = ml.y == 0.f ? 0.f : fast_exp2(ml.x - M);  // a NaN reaches the output
                     L += w * ml.y;
                 }
 #pragma unroll
@@ -652,11 +651,11 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
             float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int w = 0; w < C::CWARPS; ++w) {
-                const float mw = ms[w * G + row];
-                if (mw == NEG_INF)
+                const float lw = ls[w * G + row];
+                if (lw == 0.f)  // no key (a NaN has a sum of NaN, and goes on)
                     continue;
-                float f = fast_exp2(mw - M);
-                L += f * ls[w * G + row];
+                float f = fast_exp2(ms[w * G + row] - M);
+                L += f * lw;
                 if constexpr (Q8)
                     f *= q8_pow2(max(es[w * G + row] - 6, -126));
                 const float4 y = *reinterpret_cast<const float4 *>(os + (w * G + row) * D + d4);
@@ -788,7 +787,7 @@ __global__ void __launch_bounds__(128) serve_join_kernel(const ServeParams p, in
             }
 #pragma unroll
             for (int k = 0; k < 8; ++k) {
-                if (ml[k].x == NEG_INF)
+                if (ml[k].y == 0.f)
                     continue;
                 const float w = fast_exp2(ml[k].x - M);
                 L += w * ml[k].y;
@@ -840,7 +839,7 @@ __global__ void __launch_bounds__(128) serve_join_kernel(const ServeParams p, in
 
 struct ServeLayout {
     int ctas;
-    size_t part_ml, cnt, pre_o, pre_ml, total;
+    size_t part_o, part_ml, pre_o, pre_ml, total;
 };
 
 // the grid: never more CTAs than the longest caches could give places
@@ -852,9 +851,9 @@ static ServeLayout serve_layout(int B, int P, int L_max, int Hq, int Hkv, int D)
     l.ctas = static_cast<int>(most < SERVE_CTAS ? most : SERVE_CTAS);
     auto up = [](size_t x) { return (x + 255) / 256 * 256; };
     const size_t slots = (2 * static_cast<size_t>(l.ctas) + (P > 0 ? BH : 0)) * G;
-    l.part_ml = up(slots * D * sizeof(float));
-    l.cnt = l.part_ml + up(slots * sizeof(float2));
-    l.pre_o = l.cnt + up((2 * BH + 1) * sizeof(int));
+    l.part_o = up((SERVE_CTAS + 1) * sizeof(int));  // the counters come first, for any sizes
+    l.part_ml = l.part_o + up(slots * D * sizeof(float));
+    l.pre_o = l.part_ml + up(slots * sizeof(float2));
     const size_t pre = P > 0 ? static_cast<size_t>(prefix_attn_parts(B, P, Hq, Hkv)) * BH * G : 0;
     l.pre_ml = l.pre_o + up(pre * D * sizeof(float));
     l.total = l.pre_ml + up(pre * sizeof(float2));
@@ -921,10 +920,10 @@ static cudaError_t launch_any(int D, int code, const CUtensorMap *m, ServeParams
     const bool step = code != SV_COPIES;
     const ServeLayout l = serve_layout(p.B, p.P, p.L_max, p.Hq, p.Hkv, D);
     uint8_t *ws = static_cast<uint8_t *>(workspace);
-    p.part_o = reinterpret_cast<float *>(ws);
+    p.cnt_seg = reinterpret_cast<int *>(ws);
+    p.cnt_all = p.cnt_seg + SERVE_CTAS;
+    p.part_o = reinterpret_cast<float *>(ws + l.part_o);
     p.part_ml = reinterpret_cast<float2 *>(ws + l.part_ml);
-    p.cnt_bh = reinterpret_cast<int *>(ws + l.cnt);
-    p.cnt_all = p.cnt_bh + 2 * static_cast<size_t>(p.B) * p.Hkv;
     p.pre_o = reinterpret_cast<float *>(ws + l.pre_o);
     p.pre_ml = reinterpret_cast<float2 *>(ws + l.pre_ml);
     if (p.P > 0) {
@@ -943,8 +942,8 @@ static cudaError_t launch_any(int D, int code, const CUtensorMap *m, ServeParams
         a.Hkv = p.Hkv;
         a.qscale = p.qscale;
         if (!step) {  // its workspace comes as it is: the prefix kernel clears the counters
-            a.clear = p.cnt_bh;
-            a.n_clear = 2 * p.B * p.Hkv;
+            a.clear = p.cnt_seg;
+            a.n_clear = SERVE_CTAS;
         }
         const cudaError_t e = launch_prefix_attn(D, m[2], m[3], a, stream);
         if (e != cudaSuccess)

@@ -43,6 +43,19 @@ struct XCfg {
     static constexpr int SMEM = MISC_OFF + 64 * 4 + 1024;
 };
 
+// A warp makes rows from .. to - 1 of a V block zero: keys behind the CTA's last position have weight zero,
+// but their rows may hold anything.  Several warps may do it to the same rows.
+template <int D>
+__device__ __noinline__ void zero_tail_rows(uint8_t *v, int slab, int from, int to)
+{
+    constexpr int CH = D / 8;  // 16-byte chunks of a row
+    for (int e = threadIdx.x & 31; e < (to - from) * CH; e += 32) {
+        const int row = from + e / CH, c = e % CH;
+        *reinterpret_cast<uint4 *>(v + (c / 8) * slab + sw128_offset(row, c % 8)) = make_uint4(0, 0, 0, 0);
+    }
+    __syncwarp();
+}
+
 template <int D, int WK>
 __global__ void __launch_bounds__(XCfg<D>::THREADS)
     xattn_partial_kernel(const __grid_constant__ CUtensorMap kmap,
@@ -164,6 +177,8 @@ __global__ void __launch_bounds__(XCfg<D>::THREADS)
             const int j0 = js + i * C::KB + c * 16;
             if (j0 > pmax)
                 continue;
+            if (p.behind_prefix && j0 + 15 > kmax)
+                zero_tail_rows<D>(smem + s * C::STAGE_BYTES + C::KV_BYTES, C::SLAB, c * 16 + kmax + 1 - j0, c * 16 + 16);
             st.step(kbase, C::SLAB, kbase + C::KV_BYTES, C::SLAB, c * 16, j0, limA, limB, j0 + 15 <= pmin);
         }
         __syncwarp();
@@ -326,6 +341,8 @@ __global__ void __launch_bounds__(XCfg<D>::THREADS)
         }
         const uint32_t kbase = sbase + s * C::STAGE_BYTES;
         const int j0 = js + i * C::KB + warp * 16;
+        if (p.behind_prefix && j0 <= pmax && j0 + 15 > kmax)
+            zero_tail_rows<D>(smem + s * C::STAGE_BYTES + C::KV_BYTES, C::SLAB, warp * 16 + kmax + 1 - j0, warp * 16 + 16);
         if (j0 <= pmax)
             st.step(kbase, C::SLAB, kbase + C::KV_BYTES, C::SLAB, warp * 16, j0, lim, j0 + 15 <= pmin);
         __syncwarp();
@@ -630,11 +647,13 @@ __global__ void __launch_bounds__(128) xattn_combine_kernel(const XattnParams p)
     __shared__ float red_o[4][D];
     auto ml_at = [&](int q) { return __ldcg(&p.part_ml[(static_cast<long long>(q) * BH + bh) * p.R + r]); };
 
+    auto counts = [&](float2 ml) { return ml.y > 0.f || (p.behind_prefix && ml.y != 0.f); };
+
     // the row's overall max M (log2 units) and sum L over the non-empty partials
     float M = NEG_INF;
     for (int q = threadIdx.x; q < p.n_part; q += 128) {
         const float2 ml = ml_at(q);
-        if (ml.y > 0.f)
+        if (counts(ml))
             M = fmaxf(M, ml.x);
     }
 #pragma unroll
@@ -648,7 +667,7 @@ __global__ void __launch_bounds__(128) xattn_combine_kernel(const XattnParams p)
     float L = 0.f;
     for (int q = threadIdx.x; q < p.n_part; q += 128) {
         const float2 ml = ml_at(q);
-        if (ml.y > 0.f)
+        if (counts(ml))
             L += ml.y * fast_exp2(ml.x - M);
     }
 #pragma unroll
@@ -669,12 +688,12 @@ __global__ void __launch_bounds__(128) xattn_combine_kernel(const XattnParams p)
     for (int q = warp; q < p.n_part; q += 4) {
         const long long slot = (static_cast<long long>(q) * BH + bh) * p.R + r;
         const float2 ml = __ldcg(&p.part_ml[slot]);
-        const float w = ml.y > 0.f ? fast_exp2(ml.x - M) : 0.f;
+        const float w = counts(ml) ? fast_exp2(ml.x - M) : 0.f;
         const float *po = p.part_o + slot * D + lane * E;
         if constexpr (E == 4) {
             const float4 v = __ldcg(reinterpret_cast<const float4 *>(po));
             // an empty partial may hold anything; its weight must not meet a NaN
-            if (ml.y > 0.f) {
+            if (counts(ml)) {
                 acc[0] += w * v.x;
                 acc[1] += w * v.y;
                 acc[2] += w * v.z;
@@ -682,7 +701,7 @@ __global__ void __launch_bounds__(128) xattn_combine_kernel(const XattnParams p)
             }
         } else {
             const float2 v = __ldcg(reinterpret_cast<const float2 *>(po));
-            if (ml.y > 0.f) {
+            if (counts(ml)) {
                 acc[0] += w * v.x;
                 acc[1] += w * v.y;
             }
@@ -816,6 +835,7 @@ cudaError_t launch_xattn_partials(int D, const CUtensorMap &k, const CUtensorMap
 {
     const XattnPlan pl = xattn_apply_plan(p);
     p.direct = 0;
+    p.behind_prefix = 1;
     p.lse = nullptr;
     if (pl.keys)
         return D == 128 ? launch_partial_keys<128>(k, v, p, stream) : launch_partial_keys<64>(k, v, p, stream);

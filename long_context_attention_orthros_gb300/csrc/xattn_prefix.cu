@@ -3,7 +3,8 @@
 // own rows 0 .. pos.  The prefix kernel takes all rows of the batch over the prefix, the split-KV
 // kernels of xattn_fwd.cu the copies over their own rows, each writing partials; one combine
 // kernel joins both.  One copy a sequence goes through the decode step's kernel behind the prefix
-// kernel (serve_step.cu), which joins in the same launch.  Many copies a sequence take prefix and own rows in one kernel instead.
+// kernel (serve_step.cu), which joins in the same launch.  Many copies a sequence take prefix and
+// own rows in one kernel instead.
 #include "kernels.cuh"
 
 namespace orthros {
@@ -78,6 +79,7 @@ cudaError_t launch_xattn_prefix(int D, const CUtensorMap *m, XattnParams x, int 
         return e;
     x.G = x.Hq / x.Hkv;
     x.R = x.T_out * x.G;
+    x.behind_prefix = 1;
     x.part_o = part_o;
     x.part_ml = part_ml;
     x.n_part = l.pre + l.own;

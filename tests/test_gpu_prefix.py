@@ -80,7 +80,8 @@ def test_copies_out_of_range_are_zero_and_reported(B, T_out, Hq, Hkv):
 
 
 @pytest.mark.parametrize("B,T_out,Hq,Hkv,used", [(10, 64, 32, 8, 130), (10, 64, 32, 8, 64), (3, 1, 8, 2, 100),
-                                                  (40, 1, 8, 1, 65), (1, 1, 2, 2, 1)])
+                                                  (40, 1, 8, 1, 65), (1, 1, 2, 2, 1), (2, 2, 8, 2, 101),
+                                                  (3, 3, 8, 2, 70), (2, 5, 16, 1, 290), (1, 30, 8, 2, 17)])
 def test_rows_behind_the_last_position_do_not_matter(B, T_out, Hq, Hkv, used):
     """Own rows that no copy of the batch has reached hold NaN."""
     c = Copies(B, T_out, 200, 300, Hq, Hkv, 128, 24)
@@ -90,6 +91,32 @@ def test_rows_behind_the_last_position_do_not_matter(B, T_out, Hq, Hkv, used):
     k[:, used:], v[:, used:] = 0x7FC0, 0x7FC0
     got = orth.xattn_prefix_fwd(bf(c.qc), i32(c.pos), bf(c.kp), bf(c.vp), bf(k), bf(v), f32(c.ac), f32(c.bc), scale=c.scale)
     assert_parity(val(got), c.oracle(), "copies")
+
+
+@pytest.mark.parametrize("B,T_out,P,Hq,Hkv", [(2, 1, 300, 8, 2), (3, 3, 300, 8, 2), (2, 2, 20000, 8, 2), (3, 3, 20000, 8, 2),
+                                              (40, 1, 300, 8, 2), (4, 1, 3000, 16, 1), (2, 80, 300, 8, 2), (10, 62, 300, 32, 8)])
+@pytest.mark.parametrize("where", ["prefix key", "prefix value", "own key", "own value", "query"])
+def test_nan_reaches_the_rows_that_see_it_and_no_other(where, B, T_out, P, Hq, Hkv):
+    """A NaN value row is 0 * NaN for the copies of its sequence that lie before it: those may be NaN too."""
+    c = Copies(B, T_out, P, 200, Hq, Hkv, 128, 25)
+    c.pos[-1, 0] = 150
+    ref = c.oracle()
+    sees = np.zeros((B, T_out, Hq), bool)
+    any_of = np.zeros((B, T_out, Hq), bool)
+    if where == "query":
+        c.qc[0, 0, 1, 7] = 0x7FC0
+        sees[0, 0, 1] = True
+    elif where.startswith("prefix"):
+        (c.kp if where == "prefix key" else c.vp)[150, 0, :] = 0x7FC0
+        sees[:, :, :Hq // Hkv] = True
+    else:
+        (c.k if where == "own key" else c.v)[-1, 5, 0, :] = 0x7FC0
+        sees[-1, c.pos[-1] >= 5, :Hq // Hkv] = True
+        any_of[-1, :, :Hq // Hkv] = where == "own value"
+    got = val(c.run())
+    assert np.isnan(got[sees]).all()
+    others = ~(sees | any_of)
+    assert_parity(got[others], ref[others], "the others")
 
 
 @pytest.mark.parametrize("B,T_out,Hq,Hkv", [(3, 2, 8, 2), (5, 1, 8, 2), (10, 64, 32, 8)])
@@ -201,6 +228,53 @@ def test_decode_steps_match_oracle(lens, steps, P, Hq, Hkv, d, window):
     np.testing.assert_array_equal(bits(s.dv), s.v[:, P:])
     np.testing.assert_array_equal(bits(s.dkp), s.kp)
     np.testing.assert_array_equal(s.cl.cpu().numpy() + P, s.total)
+
+
+def test_one_workspace_serves_batches_of_other_sizes():
+    """A workspace of the largest batch goes from step to step of other batches, and through two captured graphs
+    that run in turn; the bits are those of a workspace of one's own."""
+    shapes = [((700, 3, 64, 900), 500, 8, 2, 128), ((40,), 9000, 16, 1, 128), ((5, 1300), 70, 4, 4, 64)]
+    make = [lambda s=s, i=i: PrefixDecode(s[0], 1, s[1], s[2], s[3], s[4], 128, 60 + i) for i, s in enumerate(shapes)]
+    want = [[bits(x) for x in m().step(0)] for m in make]
+    big = max((m().ws.nbytes for m in make))
+    ws = torch.zeros(big, dtype=torch.uint8, device=dev())
+    runs = [m() for m in make]
+    for r in runs:
+        r.ws = ws
+    for i in (0, 2, 1, 0, 1, 2):
+        runs[i].cl.copy_(i32(runs[i].lens))
+        for got, ref in zip(runs[i].step(0), want[i]):
+            np.testing.assert_array_equal(bits(got), ref)
+    graphs, outs = [], []
+    for r in runs:
+        r.cl.copy_(i32(r.lens))
+        new = [bf(x) for x in (r.inp.q_new[0], r.inp.qc_new[0], r.inp.k_new[0], r.inp.v_new[0])]
+        torch.cuda.synchronize()
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            o = orth.decode_step_prefix(*new, r.dkp, r.dvp, r.dk, r.dv, r.cl, *r.vec, window=r.cfg.window,
+                                        scale=r.cfg.scale, workspace=ws, dev_err=r.err)
+        graphs.append((g, new)), outs.append(o)
+    for i in (1, 0, 2, 0, 1):
+        runs[i].cl.copy_(i32(runs[i].lens))
+        graphs[i][0].replay()
+        for got, ref in zip(outs[i], want[i]):
+            np.testing.assert_array_equal(bits(got), ref)
+    assert all(int(r.err.item()) == 0 for r in runs)
+
+
+def test_wrong_error_words_and_workspaces_are_refused():
+    s = PrefixDecode((3, 4), 1, 100, 8, 2, 64, 128, 61)
+    for bad in (torch.zeros(1, dtype=torch.uint8, device=dev()), torch.zeros(0, dtype=torch.int32, device=dev()),
+                torch.zeros(1, dtype=torch.int32)):
+        s.err = bad
+        with pytest.raises(orth.OrthrosError):
+            s.step(0)
+    s.err = None
+    for bad in (s.ws[:-256], s.ws.cpu(), s.ws[16:]):
+        s.ws = bad
+        with pytest.raises(orth.OrthrosError):
+            s.step(0)
 
 
 @pytest.mark.parametrize("Hq,Hkv", [(8, 2), (16, 2)])
