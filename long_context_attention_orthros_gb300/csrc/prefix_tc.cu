@@ -21,12 +21,17 @@
 // At the end (but for DIRECT) O, the maximum and the sum leave as the stream's partial, unnormalised.
 //
 // Roles (512 threads, one CTA an SM):
-//   warp 0        TMA producer of K/V blocks
-//   warp 1        allocates tensor memory; lane 0 issues every tcgen05.mma
-//   warps 2-3, 12-15  convert each landed K block to fp16
+//   warps 0, 3    TMA producers of K and of V
+//   warps 1, 2    lane 0 issues every tcgen05.mma of stream 0, of stream 1; warp 1 allocates tensor
+//                 memory.  One thread for both streams spends 2850 cycles a pair of blocks issuing and
+//                 1000 on waits that are over, more than the MMAs take
+//   warps 12-15   convert each landed K block to fp16
 //   warps 4-7     queries from global memory to fp16 tiles (with warps 8-11), then softmax and
 //                 partial of stream 0; a warp without a row only keeps step
-//   warps 8-11    the same for stream 1
+//   warps 8-11    the same for stream 1.  The streams' softmaxes take turns, warp by warp: left alone
+//                 they run side by side, at half the rate, and the MMAs of both wait for them
+// 4 x 256 copies of 32 heads over 16384 keys (d = 128): one issuer 328 us, two 393, two and turns 305; P V
+// in two halves, the first beside the second half's exponentials: 309 (not kept).
 // Tensor memory: S of stream t at 128 t; O at 256 + D t.  Every mbarrier wait is bounded; a timeout
 // records ORTHROS_DEVERR_TIMEOUT and all roles drain to the common exit.
 #include <cuda_fp16.h>
@@ -62,7 +67,8 @@ struct PtCfg {
     static constexpr int KFLAG_OFF = KEXP_OFF + MARKS * KB;    // uint8 [MARKS][8]
     static constexpr int QSC_OFF = KFLAG_OFF + MARKS * 8;      // int8 [TILES][128]: query row shift
     static constexpr int BAR_OFF = QSC_OFF + TILES * 128;
-    static constexpr int NBARS = 2 * SLOTS + MARKS + 2 * PAIRS + 10;
+    static constexpr int MPAIRS = 2 * PAIRS;  // an even number: a mark of a pair belongs to one stream for good
+    static constexpr int NBARS = SLOTS + MARKS + MPAIRS + 2 * PAIRS + 18;
     static constexpr int HOLD_OFF = BAR_OFF + NBARS * 8;
     static constexpr int USED = HOLD_OFF + 16 + 1024;
     static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;  // one CTA an SM: it takes all of tensor memory
@@ -70,7 +76,7 @@ struct PtCfg {
     static constexpr uint32_t TM_S = 0, TM_O = 256;
     static constexpr int CPR = D / 8;       // 16-byte chunks of a query row
     static constexpr int RPP = 256 / CPR;   // rows one pass of the softmax warps' 256 threads covers
-    static constexpr int CONV_THREADS = 192;
+    static constexpr int CONV_THREADS = 128;
 };
 
 template <int D, int G, int MODE>
@@ -86,14 +92,15 @@ __global__ void __launch_bounds__(512, 1)
     const uint32_t sbase = raw_s + pad;
     uint64_t *kfull = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);  // [SLOTS] K block landed
     uint64_t *kconv = kfull + C::SLOTS;    // [MARKS] K block converted
-    uint64_t *vfull = kconv + C::MARKS;    // [SLOTS] V block landed
-    uint64_t *kempty = vfull + C::SLOTS;   // [PAIRS] K of a pair released: its S are complete (MMA commit)
+    uint64_t *vfull = kconv + C::MARKS;    // [MPAIRS] V of a pair landed
+    uint64_t *kempty = vfull + C::MPAIRS;  // [PAIRS] K of a pair released: its S are complete (MMA commit)
     uint64_t *vempty = kempty + C::PAIRS;  // [PAIRS] V released: its P V are complete
     uint64_t *q_full = vempty + C::PAIRS;  // [2] query tile prepared
     uint64_t *s_full = q_full + 2;         // [2] S of a pair complete
     uint64_t *p_full = s_full + 2;         // [2] P written
     uint64_t *o_done = p_full + 2;         // [2] O += P V of a pair complete
     uint64_t *o_final = o_done + 2;        // [2] of the stream's last pair
+    uint64_t *turn = o_final + 2;          // [2][4] a softmax warp of the stream is done with a pair
     int8_t *kexp = reinterpret_cast<int8_t *>(smem + C::KEXP_OFF);
     int8_t *qexp = reinterpret_cast<int8_t *>(smem + C::QSC_OFF);
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::HOLD_OFF);
@@ -110,17 +117,17 @@ __global__ void __launch_bounds__(512, 1)
     __shared__ volatile int s_abort;  // a wait has given up: the producer stops
     if (threadIdx.x == 0) {
         s_abort = 0;
-        for (int s = 0; s < C::SLOTS; ++s) {
+        for (int s = 0; s < C::SLOTS; ++s)
             mbar_init(&kfull[s], 1);
+        for (int s = 0; s < C::MPAIRS; ++s)
             mbar_init(&vfull[s], 1);
-        }
         for (int s = 0; s < C::MARKS; ++s) {
             mbar_init(&kconv[s], C::CONV_THREADS / 32);
             reinterpret_cast<uint64_t *>(smem + C::KFLAG_OFF)[s] = 0;
         }
         for (int s = 0; s < C::PAIRS; ++s) {
-            mbar_init(&kempty[s], 1);
-            mbar_init(&vempty[s], 1);
+            mbar_init(&kempty[s], C::TILES);  // a commit of each stream that reads the pair
+            mbar_init(&vempty[s], C::TILES);
         }
         for (int t = 0; t < 2; ++t) {
             mbar_init(&q_full[t], 8);
@@ -129,6 +136,8 @@ __global__ void __launch_bounds__(512, 1)
             mbar_init(&o_done[t], 1);
             mbar_init(&o_final[t], 1);
         }
+        for (int i = 0; i < 8; ++i)
+            mbar_init(&turn[i], 1);
         fence_barrier_init();
     }
     if (warp == 1)
@@ -186,117 +195,101 @@ __global__ void __launch_bounds__(512, 1)
     auto pairs_of = [&](int t) { return ROWS2 ? npair : (npair - t + 1) / 2; };  // of stream t
     auto pair_at = [&](int t, int u) { return ROWS2 ? u : 2 * u + t; };           // its u-th
 
-    if (warp == 0) {
-        // ------------------------------------------------------------------ producer
+    if (warp == 0 || warp == 3) {
+        // ------------------------------------------------------------------ producers of K, of V
         if (lane == 0) {
-            tma_prefetch_desc(&maps.k);
-            tma_prefetch_desc(&maps.v);
-            // K of a pair, then its V: each is free again earlier than what comes after it
-            bool ok = true;
-            for (int pp = 0; pp < npair && ok; ++pp) {
+            const bool kv = warp == 3;
+            tma_prefetch_desc(kv ? &maps.v : &maps.k);
+            for (int pp = 0; pp < npair; ++pp) {
                 const int ps = pp % C::PAIRS;
-                for (int kv = 0; kv < 2 && ok; ++kv) {
-                    if (pp >= C::PAIRS && !mbar_wait(kv ? &vempty[ps] : &kempty[ps],
-                                                     static_cast<uint32_t>((pp / C::PAIRS - 1) & 1)))
-                        ok = false;
-                    if (!ok || s_abort) {
-                        record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
-                        s_abort = 1;
-                        ok = false;
-                        break;
-                    }
-                    for (int h = 0; h < 2; ++h) {
-                        const int j = 2 * pp + h;
-                        uint64_t *bar = (kv ? vfull : kfull) + 2 * ps + h;
-                        uint8_t *dst = smem + (kv ? C::V_OFF : C::K_OFF) + ps * C::PAIR_BYTES + h * C::KB * 128;
-                        const bool own = DIRECT && j >= pre_blocks;
-                        const CUtensorMap *map = own ? (kv ? &maps.vo : &maps.ko) : (kv ? &maps.v : &maps.k);
-                        const int j0 = own ? (j - pre_blocks) * C::KB : js + j * C::KB;
-                        mbar_arrive_expect_tx(bar, C::SLABS * C::KB * 128);
+                if ((pp >= C::PAIRS &&
+                     !mbar_wait(kv ? &vempty[ps] : &kempty[ps], static_cast<uint32_t>((pp / C::PAIRS - 1) & 1))) ||
+                    s_abort) {
+                    record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+                    s_abort = 1;
+                    break;
+                }
+                constexpr int BYTES = C::SLABS * C::KB * 128;
+                if (kv)
+                    mbar_arrive_expect_tx(&vfull[pp % C::MPAIRS], 2 * BYTES);
+                for (int h = 0; h < 2; ++h) {
+                    const int j = 2 * pp + h;
+                    uint64_t *bar = kv ? &vfull[pp % C::MPAIRS] : &kfull[2 * ps + h];
+                    uint8_t *dst = smem + (kv ? C::V_OFF : C::K_OFF) + ps * C::PAIR_BYTES + h * C::KB * 128;
+                    const bool own = DIRECT && j >= pre_blocks;
+                    const CUtensorMap *map = own ? (kv ? &maps.vo : &maps.ko) : (kv ? &maps.v : &maps.k);
+                    const int j0 = own ? (j - pre_blocks) * C::KB : js + j * C::KB;
+                    if (!kv)
+                        mbar_arrive_expect_tx(bar, BYTES);
 #pragma unroll
-                        for (int sl = 0; sl < C::SLABS; ++sl)
-                            tma_load_4d(dst + sl * C::PAIR_SLAB, map, bar, sl * 64, g, j0, own ? b_own : 0);
-                    }
+                    for (int sl = 0; sl < C::SLABS; ++sl)
+                        tma_load_4d(dst + sl * C::PAIR_SLAB, map, bar, sl * 64, g, j0, own ? b_own : 0);
                 }
             }
         }
-    } else if (warp == 1) {
-        // ------------------------------------------------------------------ MMA issuer
+    } else if (warp < 3) {
+        // ------------------------------------------------------------------ MMA issuer of stream t
         if (lane == 0) {
             constexpr uint32_t IDESC_QK = umma_idesc(128, 128, false, false);
             constexpr uint32_t IDESC_PV = umma_idesc(128, D, true, true);
-            bool ok = mbar_wait(&q_full[0], 0) && (!ROWS2 || mbar_wait(&q_full[1], 0));
-            auto issue_s = [&](int t, int u) -> bool {
-                const int pp = pair_at(t, u), s0 = (2 * pp) % C::SLOTS;
-                const uint32_t ph = static_cast<uint32_t>(((2 * pp) / C::SLOTS) & 1);
-                if (!ROWS2 || t == 0)  // the pair's blocks landed and converted
-                    for (int h = 0; h < 2; ++h) {
-                        const int j = 2 * pp + h;
-                        if (!(mbar_wait(&kfull[s0 + h], ph) &&
-                              mbar_wait(&kconv[j % C::MARKS], static_cast<uint32_t>((j / C::MARKS) & 1))))
-                            return false;
-                    }
+            const int t = warp - 1, nu = pairs_of(t);
+            const uint32_t s_tm = tbase + C::TM_S + 128 * t, o_tm = tbase + C::TM_O + D * t;
+            const uint64_t qdesc = umma_desc_sw128(sbase + C::Q_OFF + (ROWS2 ? t : 0) * C::Q_BYTES, 16, 1024);
+            const uint64_t kdesc0 = umma_desc_sw128(sbase + C::K_OFF, 16, 1024);
+            const uint64_t vdesc0 = umma_desc_sw128(sbase + C::V_OFF, C::PAIR_SLAB, 1024);
+            auto issue_s = [&](int u) -> bool {
+                const int pp = pair_at(t, u), ps = pp % C::PAIRS, j = 2 * pp + 1;
+                // converted (every converter warp is done with the pair's first block before its second);
                 // S overwrites the P that the stream's last P V reads
-                if (u >= 1 && !mbar_wait(&o_done[t], static_cast<uint32_t>((u - 1) & 1)))
+                if (!mbar_wait(&kconv[j % C::MARKS], static_cast<uint32_t>((j / C::MARKS) & 1)) ||
+                    (u >= 1 && !mbar_wait(&o_done[t], static_cast<uint32_t>((u - 1) & 1))))
                     return false;
                 tc_fence_after();
-                const uint64_t kdesc = umma_desc_sw128(sbase + C::K_OFF + (s0 / 2) * C::PAIR_BYTES, 16, 1024);
-                const uint64_t qdesc = umma_desc_sw128(sbase + C::Q_OFF + (ROWS2 ? t : 0) * C::Q_BYTES, 16, 1024);
+                const uint64_t kdesc = kdesc0 + static_cast<uint64_t>(ps * (C::PAIR_BYTES >> 4));
 #pragma unroll
                 for (int kk = 0; kk < D / 16; ++kk) {
                     const uint32_t off = static_cast<uint32_t>((kk >> 2) * C::PAIR_SLAB + (kk & 3) * 32) >> 4;
                     static_assert(C::PAIR_SLAB == C::Q_SLAB, "one offset serves both operands");
-                    umma_ss(tbase + C::TM_S + 128 * t, qdesc + off, kdesc + off, IDESC_QK, kk != 0);
+                    umma_ss(s_tm, qdesc + off, kdesc + off, IDESC_QK, kk != 0);
                 }
                 umma_commit(&s_full[t]);
-                if (!ROWS2 || t == 1)  // everything that reads the pair's K has been issued
-                    umma_commit(&kempty[s0 / 2]);
+                umma_commit(&kempty[ps]);  // this stream's part of the pair's K
                 return true;
             };
-            auto issue_pv = [&](int t, int u) -> bool {
-                const int s0 = (2 * pair_at(t, u)) % C::SLOTS;
-                const uint32_t ph = static_cast<uint32_t>(((2 * pair_at(t, u)) / C::SLOTS) & 1);
-                if (!ROWS2 || t == 0)
-                    for (int h = 0; h < 2; ++h)
-                        if (!mbar_wait(&vfull[s0 + h], ph))
-                            return false;
-                if (!mbar_wait(&p_full[t], static_cast<uint32_t>(u & 1)))
+            auto issue_pv = [&](int u) -> bool {
+                const int pp = pair_at(t, u), ps = pp % C::PAIRS;
+                if (!mbar_wait(&vfull[pp % C::MPAIRS], static_cast<uint32_t>((pp / C::MPAIRS) & 1)) ||
+                    !mbar_wait(&p_full[t], static_cast<uint32_t>(u & 1)))
                     return false;
                 tc_fence_after();
-                const uint64_t vdesc = umma_desc_sw128(sbase + C::V_OFF + (s0 / 2) * C::PAIR_BYTES, C::PAIR_SLAB, 1024);
+                const uint64_t vdesc = vdesc0 + static_cast<uint64_t>(ps * (C::PAIR_BYTES >> 4));
 #pragma unroll
                 for (int kk = 0; kk < 8; ++kk)
-                    umma_ts(tbase + C::TM_O + D * t, tbase + C::TM_S + 128 * t + 8 * kk,
-                            vdesc + static_cast<uint64_t>(kk * (2048 >> 4)), IDESC_PV, (u > 0 || kk > 0) ? 1u : 0u);
+                    umma_ts(o_tm, s_tm + 8 * kk, vdesc + static_cast<uint64_t>(kk * (2048 >> 4)), IDESC_PV,
+                            (u > 0 || kk > 0) ? 1u : 0u);
                 umma_commit(&o_done[t]);
-                if (u == pairs_of(t) - 1)
+                if (u == nu - 1)
                     umma_commit(&o_final[t]);
-                if (!ROWS2 || t == 1)  // the same for its V
-                    umma_commit(&vempty[s0 / 2]);
+                umma_commit(&vempty[ps]);  // the same for its V
                 return true;
             };
-            for (int t = 0; t < 2; ++t)
-                ok = ok && (pairs_of(t) == 0 || issue_s(t, 0));
-            for (int u = 0; u < pairs_of(0) && ok; ++u)
-                for (int t = 0; t < 2 && ok; ++t) {
-                    if (u >= pairs_of(t))
-                        continue;
-                    // ROWS2: S_A of the next pair goes out before P V of B; the pair B still reads stays
-                    ok = issue_pv(t, u) && (u + 1 >= pairs_of(t) || issue_s(t, u + 1));
-                }
+            bool ok = nu == 0 || (mbar_wait(&q_full[ROWS2 ? t : 0], 0) && issue_s(0));
+            for (int u = 0; u < nu && ok; ++u)
+                ok = issue_pv(u) && (u + 1 >= nu || issue_s(u + 1));
             if (!ok) {
                 s_abort = 1;
                 record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
             }
         }
-    } else if (warp < 4 || warp >= 12) {
+    } else if (warp >= 12) {
         // ------------------------------------------------------------------ K converters
         bool ok = true, bad = false;
-        // K conversion: 8 consecutive lanes a key row, rows cid / 8 + 24 it of a block
-        const int cid = warp < 4 ? threadIdx.x - 64 : threadIdx.x - 384 + 64;  // 0 .. 191
+        // K conversion: 8 consecutive lanes a key row, rows cid / 8 + STEP it of a block
+        constexpr int STEP = C::CONV_THREADS / 8;
+        const int cid = threadIdx.x - 384;
         const int cw = cid >> 5;
-        constexpr int ITS = (C::KB * 8 + C::CONV_THREADS - 1) / C::CONV_THREADS;
-        const int nrows = cid + (ITS - 1) * C::CONV_THREADS < C::KB * 8 ? ITS : ITS - 1;  // warp-uniform
+        constexpr int ITS = C::KB / STEP;
+        static_assert(C::KB % STEP == 0, "a thread's rows are all in the block");
         for (int j = 0; j < 2 * npair && ok; ++j) {
             const int s = j % C::SLOTS;
             if (!(ok = mbar_wait(&kfull[s], static_cast<uint32_t>((j / C::SLOTS) & 1))))
@@ -306,36 +299,32 @@ __global__ void __launch_bounds__(512, 1)
             bool big = false;
 #pragma unroll
             for (int it = 0; it < ITS; ++it)
-                if (it < nrows) {
 #pragma unroll
-                    for (int sl = 0; sl < C::SLABS; ++sl) {
-                        u[it][sl] = *reinterpret_cast<const uint4 *>(blk + sl * C::PAIR_SLAB + ((cid >> 3) + 24 * it) * 128 +
-                                                                     (cid & 7) * 16);
-                        big |= !(bf16x8_absmax(u[it][sl]) < 65520.f);
-                    }
+                for (int sl = 0; sl < C::SLABS; ++sl) {
+                    u[it][sl] = *reinterpret_cast<const uint4 *>(blk + sl * C::PAIR_SLAB + ((cid >> 3) + STEP * it) * 128 +
+                                                                 (cid & 7) * 16);
+                    big |= !(bf16x8_absmax(u[it][sl]) < 65520.f);
                 }
             const bool wany = __any_sync(0xffffffffu, big);
             if (!wany) {
 #pragma unroll
                 for (int it = 0; it < ITS; ++it)
-                    if (it < nrows) {
 #pragma unroll
-                        for (int sl = 0; sl < C::SLABS; ++sl)
-                            *reinterpret_cast<uint4 *>(blk + sl * C::PAIR_SLAB + ((cid >> 3) + 24 * it) * 128 +
-                                                       (cid & 7) * 16) = k_to_fp16(u[it][sl]);
-                    }
+                    for (int sl = 0; sl < C::SLABS; ++sl)
+                        *reinterpret_cast<uint4 *>(blk + sl * C::PAIR_SLAB + ((cid >> 3) + STEP * it) * 128 + (cid & 7) * 16) =
+                            k_to_fp16(u[it][sl]);
             } else {
-                shift_key_rows<C::SLABS>(blk, C::PAIR_SLAB, 0, cid >> 3, C::CONV_THREADS / 8, nrows, cid & 7,
+                shift_key_rows<C::SLABS>(blk, C::PAIR_SLAB, 0, cid >> 3, STEP, ITS, cid & 7,
                                          kexp + (j % C::MARKS) * C::KB, bad);
             }
             if constexpr (DIRECT) {
                 // V rows behind the last position have no weight, but may hold anything
                 const int beyond = kmax + 1 - (j - pre_blocks) * C::KB;  // first such row of the block
                 if (j >= pre_blocks && beyond < C::KB) {
-                    if (!(ok = mbar_wait(&vfull[s], static_cast<uint32_t>((j / C::SLOTS) & 1))))
+                    if (!(ok = mbar_wait(&vfull[j / 2 % C::MPAIRS], static_cast<uint32_t>((j / 2 / C::MPAIRS) & 1))))
                         break;
-                    for (int it = 0; it < nrows; ++it) {
-                        const int r = (cid >> 3) + 24 * it;
+                    for (int it = 0; it < ITS; ++it) {
+                        const int r = (cid >> 3) + STEP * it;
                         if (r >= beyond)
 #pragma unroll
                             for (int sl = 0; sl < C::SLABS; ++sl)
@@ -447,7 +436,8 @@ __global__ void __launch_bounds__(512, 1)
         float m = NEG_INF, l = 0.f;
         for (int u = 0; u < nu && ok; ++u) {
             const int pp = pair_at(t, u);
-            if (!(ok = mbar_wait(&s_full[t], static_cast<uint32_t>(u & 1))))
+            if (!(ok = mbar_wait(&s_full[t], static_cast<uint32_t>(u & 1)) &&
+                       (t + u == 0 || mbar_wait(&turn[4 * (1 - t) + rw], static_cast<uint32_t>((t == 0 ? u - 1 : u) & 1)))))
                 break;
             tc_fence_after();
             if (work) {
@@ -476,8 +466,8 @@ __global__ void __launch_bounds__(512, 1)
                         for (int cw = 0; cw < C::CONV_THREADS / 32; ++cw)
                             kw |= (((kf2 >> (8 * cw)) & 0xffu) ? 1u : 0u) << cw;
                         if (kw != 0) {  // logits of shifted key rows times 2^e (rare), in tensor memory
-                            unshift_chunk32(s_col, kexp + ks * C::KB, 0, kw, 24, 4, range_bad);
-                            unshift_chunk32(s_col + 32, kexp + ks * C::KB, 32, kw, 24, 4, range_bad);
+                            unshift_chunk32(s_col, kexp + ks * C::KB, 0, kw, C::CONV_THREADS / 8, 4, range_bad);
+                            unshift_chunk32(s_col + 32, kexp + ks * C::KB, 32, kw, C::CONV_THREADS / 8, 4, range_bad);
                             tmem_ld32(s_col, va);
                             tmem_ld32(s_col + 32, vb);
                             tmem_wait_ld();
@@ -562,8 +552,10 @@ __global__ void __launch_bounds__(512, 1)
             }
             tc_fence_before();
             __syncwarp();
-            if (lane == 0)
+            if (lane == 0) {
                 mbar_arrive(&p_full[t]);
+                mbar_arrive(&turn[4 * t + rw]);
+            }
         }
         // ---- the stream's partial: a thread a row
         if (ok && work) {
