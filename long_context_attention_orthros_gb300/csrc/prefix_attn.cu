@@ -4,9 +4,13 @@
 // split of the prefix's keys, in the layout the combine kernel and the decode step join with
 // the sequences' own rows:  slot (split, b, KV head, copy * G + head).
 //
-// Grid (split, KV head x row tile).  A CTA streams its keys through a TMA ring (64-key blocks, one
-// producer warp); four warps run the online softmax on warp MMAs, RG groups of 16 rows with
-// 4 / RG warps sharing a group's keys and merging in shared memory.
+// This kernel serves up to 16 rows a KV head (beyond that its warp MMAs fall behind memory and
+// prefix_tc.cu takes over): bound by the prefix's bytes.  4 sequences over 511 + 70 rows (8/2 heads,
+// d = 64), this kernel and the step behind it: 9.6 us, two dependent launches' latency.
+//
+// Grid (split, KV head).  A CTA streams its keys through a TMA ring (64-key blocks, one producer
+// warp); four warps run the online softmax of the 16 rows on warp MMAs, each on a quarter of the
+// keys, and merge in shared memory.
 #include "kernels.cuh"
 #include "prefix_rows.cuh"
 #include "xattn.cuh"
@@ -27,13 +31,12 @@ struct PaCfg {
     static_assert(STAGES * STAGE_BYTES >= CWARPS * 16 * (D + 2) * 4, "the warps' merge reuses the ring");
 };
 
-template <int D, int G, int RG>
+template <int D, int G>
 __global__ void __launch_bounds__(PaCfg<D>::THREADS)
     prefix_attn_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                        const PrefixAttnParams p)
 {
     using C = PaCfg<D>;
-    constexpr int KL = C::CWARPS / RG;  // warps that share a group's keys
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw);
     const uint32_t pad = ((raw_s + 1023u) & ~1023u) - raw_s;
@@ -41,8 +44,7 @@ __global__ void __launch_bounds__(PaCfg<D>::THREADS)
     const uint32_t sbase = raw_s + pad;
     uint64_t *full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);
     uint64_t *empty = full + C::STAGES;
-    const int split = blockIdx.x, g = blockIdx.y % p.Hkv;
-    const long long row0 = static_cast<long long>(blockIdx.y / p.Hkv) * 16 * RG;
+    const int split = blockIdx.x, g = blockIdx.y;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
     __shared__ volatile int s_abort;  // a wait has given up: the producer stops
     if (threadIdx.x == 0) {
@@ -56,7 +58,7 @@ __global__ void __launch_bounds__(PaCfg<D>::THREADS)
     // what the kernels before wrote first, then a dependent grid may start beside this one
     asm volatile("griddepcontrol.wait;" ::: "memory");
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    if (p.clear != nullptr && blockIdx.x + blockIdx.y + blockIdx.z == 0)
+    if (p.clear != nullptr && blockIdx.x + blockIdx.y == 0)
         for (int i = threadIdx.x; i < p.n_clear; i += blockDim.x)
             p.clear[i] = 0;
     __syncthreads();
@@ -86,9 +88,8 @@ __global__ void __launch_bounds__(PaCfg<D>::THREADS)
         return;
     }
 
-    const int rg = warp / KL, kl = warp % KL;
     const int gr = lane >> 2, qd = (lane & 3) * 2;
-    const PrefixRow rows[2] = {prefix_row<G>(p, row0 + rg * 16 + gr, g, D), prefix_row<G>(p, row0 + rg * 16 + gr + 8, g, D)};
+    const PrefixRow rows[2] = {prefix_row<G>(p, gr, g, D), prefix_row<G>(p, gr + 8, g, D)};
     WarpRows16<D> st;
 #pragma unroll
     for (int kt = 0; kt < D / 16; ++kt)
@@ -109,12 +110,9 @@ __global__ void __launch_bounds__(PaCfg<D>::THREADS)
         if (ok && !mbar_wait(&full[s], static_cast<uint32_t>((i / C::STAGES) & 1)))
             ok = false, s_abort = 1;
         const uint32_t kbase = sbase + s * C::STAGE_BYTES;
-#pragma unroll
-        for (int c = kl; c < 4; c += KL) {
-            const int j0 = js + i * C::KB + c * 16;
-            if (ok && j0 < je)
-                st.step(kbase, C::SLAB, kbase + C::KV_BYTES, C::SLAB, c * 16, j0, je - 1, je - 1, j0 + 15 < je);
-        }
+        const int j0 = js + i * C::KB + warp * 16;
+        if (ok && j0 < je)
+            st.step(kbase, C::SLAB, kbase + C::KV_BYTES, C::SLAB, warp * 16, j0, je - 1, je - 1, j0 + 15 < je);
         __syncwarp();
         if (lane == 0)
             mbar_arrive(&empty[s]);
@@ -126,7 +124,7 @@ __global__ void __launch_bounds__(PaCfg<D>::THREADS)
     }
     st.finish_sums();
 
-    // the KL warps of a group, scaled to their common max, summed through shared memory
+    // the four warps, scaled to their common max, summed through shared memory
     float *os = reinterpret_cast<float *>(smem);  // [CWARPS][16][D]; the ring is free once all are here
     float *ms = os + C::CWARPS * 16 * D, *ls = ms + C::CWARPS * 16;
     named_barrier(1, C::CWARPS * 32);
@@ -144,20 +142,19 @@ __global__ void __launch_bounds__(PaCfg<D>::THREADS)
     named_barrier(1, C::CWARPS * 32);
     const float NEG_INF = -__int_as_float(0x7f800000);
     const long long BHR = static_cast<long long>(p.B) * p.Hkv * p.T_out * G;
-    for (int e = threadIdx.x; e < 16 * RG * (D / 4); e += C::CWARPS * 32) {
+    for (int e = threadIdx.x; e < 16 * (D / 4); e += C::CWARPS * 32) {
         const int r = e / (D / 4), d4 = 4 * (e % (D / 4));
-        const PrefixRow row = prefix_row<G>(p, row0 + r, g, D);
+        const PrefixRow row = prefix_row<G>(p, r, g, D);
         if (row.slot < 0)
             continue;
-        const int w0 = (r / 16) * KL;
         float M = NEG_INF, L = 0.f;
 #pragma unroll
-        for (int w = 0; w < KL; ++w)
-            M = fmaxf(M, ms[(w0 + w) * 16 + r % 16]);
+        for (int w = 0; w < C::CWARPS; ++w)
+            M = fmaxf(M, ms[w * 16 + r]);
         float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
-        for (int w = 0; w < KL; ++w) {
-            const int x = (w0 + w) * 16 + r % 16;
+        for (int w = 0; w < C::CWARPS; ++w) {
+            const int x = w * 16 + r;
             if (ls[x] == 0.f)  // no key
                 continue;
             const float f = fast_exp2(ms[x] - M);
@@ -183,18 +180,20 @@ __global__ void __launch_bounds__(PaCfg<D>::THREADS)
 
 struct PaPlan {
     int tc;     // 0: warp MMAs; 1: tensor memory, one tile of rows; 2: two tiles
-    int rg, tiles, splits, chunk, parts;
+    int tiles, splits, chunk, parts;
 };
 
 // warp MMAs: two CTAs on each of 152 SMs in one wave, at least 256 keys a split; tensor memory: one
-// CTA an SM, at least 512 keys a split
+// CTA an SM, at least 512 keys a split.  Up to 16 rows warp MMAs keep up with memory and start sooner.
+// A decode step with them, with tensor memory, us (16 rows a KV head, G = 4): 511 prefix rows of 2 heads,
+// d = 64: 9.7, 13.8; of 8 heads, d = 128: 16.1, 20.5; 16384 rows 30.1, 32.2; 131072 rows 97.3, 96.4.
+// With 32 rows over 131072 the step took 151 us on warp MMAs, 101 on tensor memory.
 static PaPlan pa_plan(long long copies, int P, int Hq, int Hkv)
 {
     PaPlan pl;
     const long long R = copies * (Hq / Hkv);
     pl.tc = R <= 16 ? 0 : (R <= 128 ? 1 : 2);
-    pl.rg = R <= 16 ? 1 : (R <= 32 ? 2 : 4);
-    const int rows = pl.tc ? 128 * pl.tc : 16 * pl.rg, ctas = pl.tc ? 152 : 304, keys = pl.tc ? 512 : 256;
+    const int rows = pl.tc ? 128 * pl.tc : 16, ctas = pl.tc ? 152 : 304, keys = pl.tc ? 512 : 256;
     const long long tiles = (R + rows - 1) / rows;
     pl.tiles = static_cast<int>(tiles);
     long long splits = ctas / (tiles * Hkv);
@@ -211,16 +210,16 @@ static PaPlan pa_plan(long long copies, int P, int Hq, int Hkv)
 
 int prefix_attn_parts(long long copies, int P, int Hq, int Hkv) { return pa_plan(copies, P, Hq, Hkv).parts; }
 
-template <int D, int G, int RG>
+template <int D, int G>
 static cudaError_t launch_pa(const CUtensorMap &k, const CUtensorMap &v, const PrefixAttnParams &p, const PaPlan &pl,
                              cudaStream_t stream)
 {
-    auto kern = prefix_attn_kernel<D, G, RG>;
+    auto kern = prefix_attn_kernel<D, G>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, PaCfg<D>::SMEM);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3(pl.splits, static_cast<unsigned>(pl.tiles) * p.Hkv);
+    cfg.gridDim = dim3(pl.splits, p.Hkv);
     cfg.blockDim = dim3(PaCfg<D>::THREADS);
     cfg.dynamicSmemBytes = PaCfg<D>::SMEM;
     cfg.stream = stream;
@@ -231,14 +230,6 @@ static cudaError_t launch_pa(const CUtensorMap &k, const CUtensorMap &v, const P
     cfg.numAttrs = 1;
     e = cudaLaunchKernelEx(&cfg, kern, k, v, p);
     return e == cudaSuccess ? cudaGetLastError() : e;
-}
-
-template <int D, int G>
-static cudaError_t launch_pa_t(const CUtensorMap &k, const CUtensorMap &v, const PrefixAttnParams &p, const PaPlan &pl,
-                               cudaStream_t stream)
-{
-    return pl.rg == 1 ? launch_pa<D, G, 1>(k, v, p, pl, stream)
-                      : pl.rg == 2 ? launch_pa<D, G, 2>(k, v, p, pl, stream) : launch_pa<D, G, 4>(k, v, p, pl, stream);
 }
 
 cudaError_t launch_prefix_attn(int D, const CUtensorMap &k, const CUtensorMap &v, PrefixAttnParams p,
@@ -253,7 +244,7 @@ cudaError_t launch_prefix_attn(int D, const CUtensorMap &k, const CUtensorMap &v
     const int G = p.Hq / p.Hkv;
 #define ORTHROS_PA_CASE(DD, GG) \
     if (D == DD && G == GG)     \
-        return launch_pa_t<DD, GG>(k, v, p, pl, stream);
+        return launch_pa<DD, GG>(k, v, p, pl, stream);
     ORTHROS_PA_CASE(128, 1)
     ORTHROS_PA_CASE(128, 2)
     ORTHROS_PA_CASE(128, 4)

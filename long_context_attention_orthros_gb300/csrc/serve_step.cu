@@ -5,6 +5,11 @@
 //   oc = Eq. (5) for its output copy over every row (prefix, own rows, the new one),
 //   cache_len[b] = p + 1.
 //
+// Bound by the cache's bytes (2 (d + 1) a row and head as codes, 4 d in bf16) where there are many, by the
+// start, the segments' borders and the join where there are few.  Measured (32/8 heads, d = 128): codes,
+// 2 x 131072 rows 88 us (6.1 TB/s: 91% of a plain copy's rate), 8 ragged caches of up to 16384 rows 39 us
+// (59%), 1 x 300 rows 8.9 us.
+//
 // The work of a step is a list of segments, two for each (b, KV head): the copy's own rows
 // 0 .. p, and the base token's window (which in the prefix form may begin in the prefix).  Each
 // is a run of 64-key blocks; laid end to end they form one list of W blocks, and CTA c of n takes
