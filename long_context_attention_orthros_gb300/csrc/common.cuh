@@ -112,15 +112,6 @@ __device__ __forceinline__ bool mbar_wait(uint64_t *bar, uint32_t parity)
     return mbar_try_wait(bar, parity) || mbar_wait_slow(bar, parity);
 }
 
-// After a wait has given up: time enough (1 ms) for the copies and MMAs in flight to land before
-// their shared or tensor memory is given back.
-static __device__ __noinline__ void drain_in_flight()
-{
-    const uint64_t t0 = global_timer_ns();
-    while (global_timer_ns() - t0 < 1000000ull) {
-    }
-}
-
 // ------------------------------------------------------------------ TMA
 
 __device__ __forceinline__ void tma_prefetch_desc(const CUtensorMap *map)
@@ -148,25 +139,6 @@ __device__ __forceinline__ void tma_store_4d(const CUtensorMap *map, const void 
         "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(src))
         : "memory");
 }
-
-// untiled bulk copy: addresses and bytes are multiples of 16
-__device__ __forceinline__ void bulk_load(void *dst, const void *src, uint32_t bytes, uint64_t *bar)
-{
-    asm volatile("cp.async.bulk.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1], %2, [%3];" ::"r"(
-                     smem_u32(dst)),
-                 "l"(src), "r"(bytes), "r"(smem_u32(bar))
-                 : "memory");
-}
-
-__device__ __forceinline__ void prefetch_l2(const void *p) { asm volatile("prefetch.global.L2 [%0];" ::"l"(p)); }
-
-// 16 bytes from global to shared memory without a register on the way (both addresses 16-byte aligned)
-__device__ __forceinline__ void cp_async16(void *dst, const void *src)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(smem_u32(dst)), "l"(src) : "memory");
-}
-
-__device__ __forceinline__ void cp_async_wait_all() { asm volatile("cp.async.wait_all;" ::: "memory"); }
 
 __device__ __forceinline__ void bulk_commit() { asm volatile("cp.async.bulk.commit_group;" ::: "memory"); }
 

@@ -40,9 +40,6 @@ struct XattnParams {
     int32_t *dev_err;
     long long qc_bstride, oc_bstride;
     int B, T_out, T_kv, Hq, Hkv, G, R, row_tiles, splits, chunk, n_part, direct;
-    // own rows behind a prefix: V rows behind a CTA's last position may hold anything, and a partial whose
-    // sum is a NaN reaches the output
-    int behind_prefix;
     float qscale;
 };
 
@@ -119,95 +116,10 @@ bool swa_tc_supported(int D, int G, int window);
 cudaError_t launch_swa_tc(int D, int G, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                           const CUtensorMap &o, const SwaParams &p, int num_sms, cudaStream_t stream);
 
-// prompt rows written into, or read back from, the 8-bit cache
-struct KvQ8Params {
-    orthros_bf16 *k, *v;        // [B, T, Hkv, d], batch stride kv_bstride (inputs of the write)
-    uint8_t *k8, *v8;           // codes [B, L_max, Hkv, d]
-    int8_t *k_exp, *v_exp;      // exponents [B, Hkv, L_max]
-    const int32_t *start, *rows;  // [B] or NULL (0 and T)
-    long long kv_bstride;
-    int32_t *dev_err;
-    int B, T, Hkv, L_max;
-};
-cudaError_t launch_kv_quantize(int D, int code, const KvQ8Params &p, cudaStream_t stream);
-cudaError_t launch_kv_dequantize(int D, int code, const KvQ8Params &p, cudaStream_t stream);
-
-// attention of all rows of a batch over one shared prefix [P, Hkv, d]: partials in slots
-// (split, b, KV head, copy * G + head).  k, v maps with boxes of 64 x 1 x 64.
-struct PrefixAttnParams {
-    const orthros_bf16 *qc;  // [B, T_out, Hq, d], batch stride qc_bstride
-    const int32_t *pos;      // [B, T_out] own positions (a copy outside [0, T_kv) takes no key), or NULL
-    const float *alpha_c, *beta_c;
-    float *part_o;
-    float2 *part_ml;
-    orthros_bf16 *oc;        // launch_prefix_direct: [B, T_out, Hq, d], batch stride oc_bstride
-    int32_t *dev_err;
-    long long qc_bstride, oc_bstride;
-    int B, T_out, T_kv, P, Hq, Hkv;
-    int chunk;  // keys of a split, set by the launcher
-    float qscale;
-    int *clear;  // optional: n_clear ints that the kernel sets to zero before a dependent kernel reads them
-    int n_clear;
-};
-struct PrefixMaps {
-    CUtensorMap k, v, ko, vo;  // the prefix's K and V; the sequences' own (launch_prefix_direct)
-};
-// mode: 0 one tile of 128 rows, 1 two tiles
-cudaError_t launch_prefix_tc(int D, int mode, const PrefixMaps &maps, const PrefixAttnParams &p, int splits, int tiles,
-                             cudaStream_t stream);
-// copies over the prefix and their own rows in one kernel, outputs at p.oc; tiles of a sequence, or 0
-// where partials serve better
-int prefix_direct_tiles(int B, int T_out, int P, int T_kv, int Hq, int Hkv, int D);
-cudaError_t launch_prefix_direct(int D, const PrefixMaps &maps, const PrefixAttnParams &p, cudaStream_t stream);
-int prefix_attn_parts(long long copies, int P, int Hq, int Hkv);
-cudaError_t launch_prefix_attn(int D, const CUtensorMap &k, const CUtensorMap &v, PrefixAttnParams p,
-                               cudaStream_t stream);
-
-// one decode step over the 8-bit cache, or over a shared prefix and each sequence's own bf16 cache
-struct ServeParams {
-    const orthros_bf16 *q_new, *qc_new, *k_new, *v_new;
-    void *k_cache, *v_cache;  // bf16, or codes, [B, L_max, Hkv, d]
-    int8_t *k_exp, *v_exp;    // [B, Hkv, L_max] (8-bit form)
-    int32_t *cache_len;
-    const float *alpha, *beta, *alpha_c, *beta_c;
-    orthros_bf16 *o, *oc;
-    float *part_o;            // [2 * CTAs (+ B * Hkv behind a prefix)][G][D]
-    float2 *part_ml;
-    int *cnt_seg;             // [CTAs]: parts of the segment that runs out of a CTA, counted in
-    int *cnt_all;
-    float *pre_o;             // the prefix kernel's partials (prefix form)
-    float2 *pre_ml;
-    int32_t *dev_err;
-    int B, Hq, Hkv, L_max, window;
-    int P, n_part;            // prefix rows (0: 8-bit form) and splits
-    int join_after;           // partials are joined by a kernel of its own; set by the launchers
-    float qscale;
-    long long q_bstride, o_bstride;  // elements between sequences of q_new, qc_new and of o, oc; set by the launchers
-};
-size_t serve_workspace_bytes(int B, int P, int L_max, int Hq, int Hkv, int D);
-// code: ORTHROS_KV_E4M3 / ORTHROS_KV_INT8, or -1 for bf16 caches behind a shared prefix; maps: the
-// cache's K and V, then the prefix's (boxes of 64 x 1 x 64; the 8-bit cache's d x 1 x 64)
-cudaError_t launch_serve(int D, int code, const CUtensorMap *maps, ServeParams p, void *workspace,
-                         cudaStream_t stream);
-
-// one copy a sequence (T_out = 1) over a shared prefix and its own rows; maps as above, workspace of
-// serve_workspace_bytes(B, P, T_kv, ...), not initialised
-cudaError_t launch_serve_copies(int D, const CUtensorMap *maps, const XattnParams &p, int P, void *workspace,
-                                cudaStream_t stream);
-
-// output copies over a shared prefix and their own rows; maps: own K and V, the prefix's K and V
-size_t xattn_prefix_workspace_bytes(int B, int T_out, int P, int T_kv, int Hq, int Hkv, int D);
-cudaError_t launch_xattn_prefix(int D, const CUtensorMap *maps, XattnParams p, int P, void *workspace,
-                                cudaStream_t stream);
-
 size_t xattn_workspace_bytes(int B, int T_out, int T_kv, int Hq, int Hkv, int D);
 // ctas > 0: at most 8 copy rows per (batch, KV head) run on exactly `ctas` CTAs of one SM each
 cudaError_t launch_xattn(int D, const CUtensorMap &k, const CUtensorMap &v, XattnParams p, void *workspace,
                          cudaStream_t stream, int ctas = 0);
-// the split-KV kernels alone: every row's xattn_parts() partials at p.part_o / p.part_ml
-int xattn_parts(int B, int T_out, int T_kv, int Hq, int Hkv);
-cudaError_t launch_xattn_partials(int D, const CUtensorMap &k, const CUtensorMap &v, XattnParams p,
-                                  cudaStream_t stream);
 // merge split partials [n_part][B*Hkv][R][D] into the copy outputs
 cudaError_t launch_xattn_combine(int D, const XattnParams &p, cudaStream_t stream);
 // many copies per (batch, KV head) (T_out * G >= 256): tcgen05 flash kernel over key blocks of

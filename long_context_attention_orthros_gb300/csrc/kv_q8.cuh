@@ -12,8 +12,7 @@
 
 #include <cuda_fp16.h>
 
-#include "common.cuh"
-#include "kernels.cuh"
+#include "serve.cuh"
 
 namespace orthros {
 

@@ -6,7 +6,7 @@
 #include <cmath>
 #include <mutex>
 
-#include "kernels.cuh"
+#include "serve.cuh"
 
 namespace {
 

@@ -11,8 +11,8 @@
 // Grid (split, KV head).  A CTA streams its keys through a TMA ring (64-key blocks, one producer
 // warp); four warps run the online softmax of the 16 rows on warp MMAs, each on a quarter of the
 // keys, and merge in shared memory.
-#include "kernels.cuh"
 #include "prefix_rows.cuh"
+#include "serve.cuh"
 #include "xattn.cuh"
 
 namespace orthros {

@@ -2,7 +2,7 @@
 // partials go: row = copy * G + head within one KV head, copies counted through the batch.
 #pragma once
 
-#include "kernels.cuh"
+#include "serve.cuh"
 
 namespace orthros {
 

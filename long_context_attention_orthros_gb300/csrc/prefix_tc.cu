@@ -40,9 +40,8 @@
 // records ORTHROS_DEVERR_TIMEOUT and all roles drain to the common exit.
 #include <cuda_fp16.h>
 
-#include "common.cuh"
-#include "kernels.cuh"
 #include "prefix_rows.cuh"
+#include "serve.cuh"
 #include "tc.cuh"
 
 namespace orthros {

@@ -34,7 +34,7 @@
 // kernel without window and append serves one copy a sequence behind a prefix (a prompt's end).
 #include <type_traits>
 
-#include "kernels.cuh"
+#include "serve.cuh"
 #include "warp_b16.cuh"
 #include "warp_q8.cuh"
 

@@ -24,7 +24,7 @@
 // Partials are unnormalised (max, sum, o[d]) per row; a second kernel merges the
 // partials of a row with a warp-shuffle log-sum-exp reduction.  When a row has a
 // single partial the first kernel writes the output directly.
-#include "kernels.cuh"
+#include "serve.cuh"
 #include "xattn.cuh"
 
 namespace orthros {
@@ -56,7 +56,8 @@ __device__ __noinline__ void zero_tail_rows(uint8_t *v, int slab, int from, int 
     __syncwarp();
 }
 
-template <int D, int WK>
+// BEHIND: the rows behind a shared prefix (launch_xattn_partials).
+template <int D, int WK, bool BEHIND>
 __global__ void __launch_bounds__(XCfg<D>::THREADS)
     xattn_partial_kernel(const __grid_constant__ CUtensorMap kmap,
                          const __grid_constant__ CUtensorMap vmap, const XattnParams p)
@@ -177,7 +178,7 @@ __global__ void __launch_bounds__(XCfg<D>::THREADS)
             const int j0 = js + i * C::KB + c * 16;
             if (j0 > pmax)
                 continue;
-            if (p.behind_prefix && j0 + 15 > kmax)
+            if (BEHIND && j0 + 15 > kmax)
                 zero_tail_rows<D>(smem + s * C::STAGE_BYTES + C::KV_BYTES, C::SLAB, c * 16 + kmax + 1 - j0, c * 16 + 16);
             st.step(kbase, C::SLAB, kbase + C::KV_BYTES, C::SLAB, c * 16, j0, limA, limB, j0 + 15 <= pmin);
         }
@@ -229,7 +230,7 @@ __global__ void __launch_bounds__(XCfg<D>::THREADS)
 // every 64-key block, and the four warps' (max, sum, o) are merged in shared memory (the ring is
 // free once every block has been consumed) into one partial per CTA, or the output when the CTA
 // is the row's only split.
-template <int D>
+template <int D, bool BEHIND>
 __global__ void __launch_bounds__(XCfg<D>::THREADS)
     xattn_partial_keys_kernel(const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap,
                               const XattnParams p)
@@ -341,7 +342,7 @@ __global__ void __launch_bounds__(XCfg<D>::THREADS)
         }
         const uint32_t kbase = sbase + s * C::STAGE_BYTES;
         const int j0 = js + i * C::KB + warp * 16;
-        if (p.behind_prefix && j0 <= pmax && j0 + 15 > kmax)
+        if (BEHIND && j0 <= pmax && j0 + 15 > kmax)
             zero_tail_rows<D>(smem + s * C::STAGE_BYTES + C::KV_BYTES, C::SLAB, warp * 16 + kmax + 1 - j0, warp * 16 + 16);
         if (j0 <= pmax)
             st.step(kbase, C::SLAB, kbase + C::KV_BYTES, C::SLAB, warp * 16, j0, lim, j0 + 15 <= pmin);
@@ -629,7 +630,7 @@ __global__ void __launch_bounds__(XpCfg<D>::THREADS, 1)
 }
 
 // One warp per output row: merge the row's partial (max, sum, o) triples.
-template <int D>
+template <int D, bool BEHIND>
 __global__ void __launch_bounds__(128) xattn_combine_kernel(const XattnParams p)
 {
     // one block per output row (b, copy i, head h); its four warps split the partials
@@ -647,7 +648,7 @@ __global__ void __launch_bounds__(128) xattn_combine_kernel(const XattnParams p)
     __shared__ float red_o[4][D];
     auto ml_at = [&](int q) { return __ldcg(&p.part_ml[(static_cast<long long>(q) * BH + bh) * p.R + r]); };
 
-    auto counts = [&](float2 ml) { return ml.y > 0.f || (p.behind_prefix && ml.y != 0.f); };
+    auto counts = [&](float2 ml) { return ml.y > 0.f || (BEHIND && ml.y != 0.f); };
 
     // the row's overall max M (log2 units) and sum L over the non-empty partials
     float M = NEG_INF;
@@ -774,11 +775,11 @@ size_t xattn_workspace_bytes(int B, int T_out, int T_kv, int Hq, int Hkv, int D)
     return o_bytes + (rows * sizeof(float2) + 255) / 256 * 256;
 }
 
-template <int D, int WK>
+template <int D, int WK, bool BEHIND = false>
 static cudaError_t launch_partial(const CUtensorMap &k, const CUtensorMap &v, const XattnParams &p,
                                   cudaStream_t stream)
 {
-    auto kern = xattn_partial_kernel<D, WK>;
+    auto kern = xattn_partial_kernel<D, WK, BEHIND>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, XCfg<D>::SMEM);
     if (e != cudaSuccess)
         return e;
@@ -799,11 +800,11 @@ static cudaError_t launch_partial_keys_persist(const CUtensorMap &k, const CUten
     return cudaGetLastError();
 }
 
-template <int D>
+template <int D, bool BEHIND = false>
 static cudaError_t launch_partial_keys(const CUtensorMap &k, const CUtensorMap &v, const XattnParams &p,
                                        cudaStream_t stream)
 {
-    auto kern = xattn_partial_keys_kernel<D>;
+    auto kern = xattn_partial_keys_kernel<D, BEHIND>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, XCfg<D>::SMEM);
     if (e != cudaSuccess)
         return e;
@@ -835,13 +836,12 @@ cudaError_t launch_xattn_partials(int D, const CUtensorMap &k, const CUtensorMap
 {
     const XattnPlan pl = xattn_apply_plan(p);
     p.direct = 0;
-    p.behind_prefix = 1;
     p.lse = nullptr;
     if (pl.keys)
-        return D == 128 ? launch_partial_keys<128>(k, v, p, stream) : launch_partial_keys<64>(k, v, p, stream);
+        return D == 128 ? launch_partial_keys<128, true>(k, v, p, stream) : launch_partial_keys<64, true>(k, v, p, stream);
     if (D == 128)
-        return pl.WK == 4 ? launch_partial<128, 4>(k, v, p, stream) : launch_partial<128, 1>(k, v, p, stream);
-    return pl.WK == 4 ? launch_partial<64, 4>(k, v, p, stream) : launch_partial<64, 1>(k, v, p, stream);
+        return pl.WK == 4 ? launch_partial<128, 4, true>(k, v, p, stream) : launch_partial<128, 1, true>(k, v, p, stream);
+    return pl.WK == 4 ? launch_partial<64, 4, true>(k, v, p, stream) : launch_partial<64, 1, true>(k, v, p, stream);
 }
 
 cudaError_t launch_xattn(int D, const CUtensorMap &k, const CUtensorMap &v, XattnParams p,
@@ -869,16 +869,27 @@ cudaError_t launch_xattn(int D, const CUtensorMap &k, const CUtensorMap &v, Xatt
     return launch_xattn_combine(D, p, stream);
 }
 
-cudaError_t launch_xattn_combine(int D, const XattnParams &p, cudaStream_t stream)
+template <bool BEHIND>
+static cudaError_t launch_combine(int D, const XattnParams &p, cudaStream_t stream)
 {
     const unsigned blocks = static_cast<unsigned>(static_cast<long long>(p.B) * p.T_out * p.Hq);
     if (blocks == 0)
         return cudaSuccess;
     if (D == 128)
-        xattn_combine_kernel<128><<<blocks, 128, 0, stream>>>(p);
+        xattn_combine_kernel<128, BEHIND><<<blocks, 128, 0, stream>>>(p);
     else
-        xattn_combine_kernel<64><<<blocks, 128, 0, stream>>>(p);
+        xattn_combine_kernel<64, BEHIND><<<blocks, 128, 0, stream>>>(p);
     return cudaGetLastError();
+}
+
+cudaError_t launch_xattn_combine(int D, const XattnParams &p, cudaStream_t stream)
+{
+    return launch_combine<false>(D, p, stream);
+}
+
+cudaError_t launch_xattn_combine_prefix(int D, const XattnParams &p, cudaStream_t stream)
+{
+    return launch_combine<true>(D, p, stream);
 }
 
 }  // namespace orthros

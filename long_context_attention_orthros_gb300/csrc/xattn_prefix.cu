@@ -5,7 +5,7 @@
 // kernel joins both.  One copy a sequence goes through the decode step's kernel behind the prefix
 // kernel (serve_step.cu), which joins in the same launch.  Many copies a sequence take prefix and
 // own rows in one kernel instead.
-#include "kernels.cuh"
+#include "serve.cuh"
 
 namespace orthros {
 
@@ -79,11 +79,10 @@ cudaError_t launch_xattn_prefix(int D, const CUtensorMap *m, XattnParams x, int 
         return e;
     x.G = x.Hq / x.Hkv;
     x.R = x.T_out * x.G;
-    x.behind_prefix = 1;
     x.part_o = part_o;
     x.part_ml = part_ml;
     x.n_part = l.pre + l.own;
-    return launch_xattn_combine(D, x, stream);
+    return launch_xattn_combine_prefix(D, x, stream);
 }
 
 }  // namespace orthros
