@@ -97,6 +97,7 @@ struct ServeParams {
     int B, Hq, Hkv, L_max, window;
     int P, n_part;            // prefix rows (0: 8-bit form) and splits
     int join_after;           // partials are joined by a kernel of its own; set by the launchers
+    int join_two;             // a row's partials are joined by two half-warps (by sizes: the order of sums is fixed)
     float qscale;
     long long q_bstride, o_bstride;  // elements between sequences of q_new, qc_new and of o, oc; set by the launchers
 };

@@ -382,17 +382,21 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
             s_flag[0] = atomicAdd(p.cnt_all, 1) == static_cast<int>(gridDim.x) - 1;
         named_barrier(1, C::CTHREADS);
         const long long BH = static_cast<long long>(p.B) * p.Hkv;
-        // half a warp a row: E columns a lane, 16 parts' weights in its lanes, 8 parts' loads in flight
+        // half a warp a row (or two halves, each every other part): E columns a lane, 16 parts' weights in
+        // its lanes, 8 parts' loads in flight
         constexpr int E = D / 16;
-        const int half = lane >> 4, hl = lane & 15, total = njoin * G;
-        for (int x0 = 2 * warp; x0 < total; x0 += 2 * C::CWARPS) {
-            const bool on = x0 + half < total;
-            const Join j = joins[on ? (x0 + half) / G : 0];
-            const int row = (x0 + half) % G;
+        const int half = lane >> 4, hl = lane & 15, total = njoin * G, two = p.join_two;
+        for (int x0 = warp << (1 - two); x0 < total; x0 += C::CWARPS << (1 - two)) {
+            const int x = two ? x0 : x0 + half;
+            const bool on = x < total;
+            const Join j = joins[on ? x / G : 0];
+            const int row = x % G;
             const bool base = j.base;
             // parts: the CTAs' own, then (a copy behind a prefix) the prefix splits'
             const int nown = j.parts;
-            const int nq = on && j.last ? nown + (!Q8 && !base ? p.n_part : 0) : 0;
+            const int nall = on && j.last ? nown + (!Q8 && !base ? p.n_part : 0) : 0;
+            const int nq = two ? (nall + 1 - half) / 2 : nall;  // this half's; its q-th is the row's part_of(q)
+            auto part_of = [&](int q) { return two ? 2 * q + half : q; };
             const int nmax = max(nq, __shfl_xor_sync(0xffffffffu, nq, 16));
             if (nmax == 0)
                 continue;
@@ -402,13 +406,16 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
                                 : ((q - nown) * BH + j.bh) * G + row;
             };
             auto ml_of = [&](int q) -> float2 {
-                return q >= nq ? make_float2(NEG_INF, 0.f) : __ldcg((q < nown ? p.part_ml : p.pre_ml) + slot_of(q));
+                if (q >= nq)
+                    return make_float2(NEG_INF, 0.f);
+                q = part_of(q);
+                return __ldcg((q < nown ? p.part_ml : p.pre_ml) + slot_of(q));
             };
             float y[8][E];
             auto load = [&](int q0) {  // past the end the last part again: its weight there is zero
 #pragma unroll
                 for (int k = 0; k < 8; ++k) {
-                    const int q = min(q0 + k, nq - 1);
+                    const int q = part_of(min(q0 + k, nq - 1));
 #pragma unroll
                     for (int e = 0; e < E; e += 4) {
                         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -430,6 +437,8 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
 #pragma unroll
             for (int off = 8; off > 0; off >>= 1)
                 M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+            if (two)
+                M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, 16));
             float a[E];
 #pragma unroll
             for (int e = 0; e < E; ++e)
@@ -454,10 +463,16 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
 #pragma unroll
             for (int off = 8; off > 0; off >>= 1)
                 L += __shfl_xor_sync(0xffffffffu, L, off);
+            if (two) {
+                L += __shfl_xor_sync(0xffffffffu, L, 16);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    a[e] += __shfl_xor_sync(0xffffffffu, a[e], 16);
+            }
             const float inv = L > 0.f ? 1.f / L : 0.f;
             orthros_bf16 *orow = (base ? p.o : p.oc) + (j.bh / p.Hkv) * p.o_bstride +
                                  ((j.bh % p.Hkv) * G + row) * D + hl * E;
-            if (nq > 0) {
+            if (nq > 0 && !(two && half)) {
 #pragma unroll
                 for (int e = 0; e < E; e += 4)
                     *reinterpret_cast<uint2 *>(orow + e) = make_uint2(pack_bf16x2(a[e] * inv, a[e + 1] * inv),
@@ -873,11 +888,7 @@ size_t serve_workspace_bytes(int B, int P, int L_max, int Hq, int Hkv, int D)
 // A join inside the step costs the CTA that does it 8.5 ns a part and row at d = 128 (one SM reads all of
 // them, 60 GB/s); a kernel of its own costs 3 us, whatever their number.  With one KV head of 16 query
 // heads and 4 sequences (76 parts a copy) the step took 57 us with the join inside.
-static bool join_after(const ServeParams &p, int ctas, int D)
-{
-    const long long parts = ctas / (static_cast<long long>(p.B) * p.Hkv) + p.n_part;
-    return parts * (p.Hq / p.Hkv) * D >= 45000;
-}
+static bool join_after(const ServeParams &p, long long parts, int D) { return parts * (p.Hq / p.Hkv) * D >= 45000; }
 
 template <int D, int G, int CODE>
 static cudaError_t launch_serve_tc(const ServeMaps &maps, ServeParams p, int ctas, cudaStream_t stream)
@@ -887,7 +898,12 @@ static cudaError_t launch_serve_tc(const ServeMaps &maps, ServeParams p, int cta
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess)
         return e;
-    p.join_after = join_after(p, ctas, D);
+    const long long parts = ctas / (static_cast<long long>(p.B) * p.Hkv) + p.n_part;  // about, of a long segment
+    p.join_after = join_after(p, parts, D);
+    // Two half-warps a row where rows are few and their partials many.  Steps with one and with two, us on one
+    // GB300: 4 sequences behind 16384 rows (2 heads, d = 64) 19.6, 15.2; 4 behind 131072 (8 heads, d = 128) 99.4, 97.0;
+    // codes, 2 x 131072 rows 91.2, 89.9; but 64 behind 16384 (7 rows a CTA) 64.2, 65.4.
+    p.join_two = parts > 8 && static_cast<long long>(p.B) * p.Hq <= 4LL * ctas;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(ctas);
     cfg.blockDim = dim3(C::THREADS);
