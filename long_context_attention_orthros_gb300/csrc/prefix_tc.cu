@@ -21,7 +21,7 @@
 // At the end (but for DIRECT) O, the maximum and the sum leave as the stream's partial, unnormalised.
 //
 // Bound by HBM where the rows are few (8 sequences over 131072 rows, 32/8 heads, d = 128: 85 us, 6.3 TB/s,
-// and 16 for its start and the own rows), by a stream's chain of S, softmax and P V where they fill
+// and 14 for its start and the own rows), by a stream's chain of S, softmax and P V where they fill
 // the tile (4 x 256 copies: 305 us, 930 TFLOP/s).
 //
 // Roles (512 threads, one CTA an SM):
