@@ -229,6 +229,15 @@ __global__ void __launch_bounds__(512, 1)
                         tma_load_4d(dst + sl * C::PAIR_SLAB, map, bar, sl * 64, g, j0, own ? b_own : 0);
                 }
             }
+            // Every MMA that reads the last pairs, and its commit, has landed before shared and tensor memory
+            // are given back: of a stream whose tile has no row nothing else waits for the last P V.
+            for (int pp = max(npair - C::PAIRS, 0); pp < npair && !s_abort; ++pp) {
+                const int ps = pp % C::PAIRS;
+                if (!mbar_wait(kv ? &vempty[ps] : &kempty[ps], static_cast<uint32_t>((pp / C::PAIRS) & 1))) {
+                    record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+                    s_abort = 1;
+                }
+            }
         }
     } else if (warp < 3) {
         // ------------------------------------------------------------------ MMA issuer of stream t
@@ -279,6 +288,9 @@ __global__ void __launch_bounds__(512, 1)
             bool ok = nu == 0 || (mbar_wait(&q_full[ROWS2 ? t : 0], 0) && issue_s(0));
             for (int u = 0; u < nu && ok; ++u)
                 ok = issue_pv(u) && (u + 1 >= nu || issue_s(u + 1));
+            // the last commits to o_done and o_final too (see the producers' end)
+            if (ok && nu > 0)
+                ok = mbar_wait(&o_done[t], static_cast<uint32_t>((nu - 1) & 1)) && mbar_wait(&o_final[t], 0);
             if (!ok) {
                 s_abort = 1;
                 record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
