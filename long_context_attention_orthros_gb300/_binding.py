@@ -135,6 +135,9 @@ def _bf16_rows(t: torch.Tensor, name: str) -> int:
     if ((d > 1 and t.stride(3) != 1) or (H > 1 and t.stride(2) != d)
             or (T > 1 and t.stride(1) != H * d)):
         raise OrthrosError(f"{name}: the [T, H, d] part must be dense (d contiguous)")
+    # an expanded batch: the library takes a batch stride of 0 for the dense one
+    if B > 1 and t.stride(0) == 0 and T * H * d > 0:
+        raise OrthrosError(f"{name}: the sequences of a batch must not be one another's memory (expanded tensor)")
     return t.stride(0) if B > 1 else T * H * d
 
 
