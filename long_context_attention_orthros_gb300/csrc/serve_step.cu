@@ -676,9 +676,11 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
                     continue;
                 float f = fast_exp2(ms[w * G + row] - M);
                 L += f * lw;
-                if constexpr (Q8)
-                    f *= q8_pow2(max(es[w * G + row] - 6, -126));
-                const float4 y = *reinterpret_cast<const float4 *>(os + (w * G + row) * D + d4);
+                float4 y = *reinterpret_cast<const float4 *>(os + (w * G + row) * D + d4);
+                if constexpr (Q8) {  // o holds 2^(6 - E); in two factors, as E - 6 can lie below fp32's exponents
+                    f *= q8_pow2(max(es[w * G + row], -126));
+                    y = make_float4(y.x * 0.015625f, y.y * 0.015625f, y.z * 0.015625f, y.w * 0.015625f);
+                }
                 a.x += f * y.x;
                 a.y += f * y.y;
                 a.z += f * y.z;
