@@ -67,7 +67,7 @@ struct SvCfg {
     static constexpr int CWARPS = 4;
     static constexpr int GROUP = 4 / KT;  // warps that share a block
     static constexpr int SCR_ROWS = CWARPS * G;
-    static constexpr int SCR_BYTES = SCR_ROWS * (D + 3) * 4;  // the warps' o, max, sum, exponent
+    static constexpr int SCR_BYTES = SCR_ROWS * (D + 3) * 4;  // the warps' o, max, sum, scale of o
     static constexpr int LIMIT = 113 * 1024 - 2048;            // two CTAs share an SM
     // a segment's queries, its alpha and beta and the new K and V row come through a buffer of their
     // own, free again once the segment has begun
@@ -356,7 +356,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
     const int t = threadIdx.x;
     float *os = reinterpret_cast<float *>(smem + C::SCR_OFF);  // [CWARPS][G][D]
     float *ms = os + C::CWARPS * G * D, *ls = ms + C::CWARPS * G;
-    int *es = reinterpret_cast<int *>(ls + C::CWARPS * G);
+    float *vs = ls + C::CWARPS * G;  // codes: the scale of the warps' o
     bool ok = true, bad = false;
     long long i = 0;
     int segs = 0, njoin = 0;
@@ -640,7 +640,7 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
                     ms[warp * G + row] = st.m[nt][r2];
                     ls[warp * G + row] = st.l[nt][r2];
                     if constexpr (Q8)
-                        es[warp * G + row] = st.E;
+                        vs[warp * G + row] = st.mv[nt][r2];
                 }
                 float *po = os + (warp * G + row) * D;
 #pragma unroll
@@ -677,9 +677,9 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
                 float f = fast_exp2(ms[w * G + row] - M);
                 L += f * lw;
                 float4 y = *reinterpret_cast<const float4 *>(os + (w * G + row) * D + d4);
-                if constexpr (Q8) {  // o holds 2^(6 - E); in two factors, as E - 6 can lie below fp32's exponents
-                    f *= q8_pow2(max(es[w * G + row], -126));
-                    y = make_float4(y.x * 0.015625f, y.y * 0.015625f, y.z * 0.015625f, y.w * 0.015625f);
+                if constexpr (Q8) {  // o stands for o 2^(mv - 6); in two factors, as 2^(mv - 6 - M) can pass fp32's range
+                    f = fast_exp2(0.5f * (vs[w * G + row] - 6.f - M));
+                    y = make_float4(f * y.x, f * y.y, f * y.z, f * y.w);
                 }
                 a.x += f * y.x;
                 a.y += f * y.y;

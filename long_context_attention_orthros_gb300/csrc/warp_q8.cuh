@@ -10,10 +10,14 @@
 //      of two keys are paired by a byte permute before they are converted.
 // Scales are powers of two.  A query row is scaled to a largest value in [2^14, 2^15), so its
 // size does not matter to fp16; the logit is (q . code) 2^(row shift) 2^(key exponent), in fp32.
-// The running maximum is raised only when a logit passes it by more than 8 (log2 units), so the
-// rows' maxima are reduced across lanes rarely and P <= 2^8; P enters the second product as
-// P 2^(ve - E + 6), E the largest V exponent the warp has met, at most 2^14 in fp16, and rounds
-// to a multiple of 2^-24 at worst: 2^-38 of that largest (row sums stay in fp32, unrounded).
+// Two running maxima a row, in log2 units: m of the logits x, for the sum of weights, and mv of
+// x + ve (ve the key's V exponent), for the second product, whose factors are P = 2^(x + ve - mv + 6)
+// in fp16: what a key brings to the output, its weight and its V row's size together, decides what
+// its P keeps, so neither a large V row of no weight nor small V rows throughout cost bits.  Both are
+// raised only when they are passed by more than 8, so that reductions across lanes are rare and
+// P <= 2^14; P rounds to a multiple of 2^-24 at worst, 2^-30 of what the weightiest key of the row
+// brings (row sums stay in fp32, unrounded).  A V row of zeros has the exponent 0 but brings nothing:
+// where it would raise mv it is passed over.
 #pragma once
 
 #include "kv_q8.cuh"
@@ -34,7 +38,7 @@ struct WarpQ8 {
     float qf[NT][2];             // 2^shift of rows 8 nt + 2 (lane % 4) + {0, 1}
     float o[NT][D / 16][4];      // O^T: d = (d / 8) (lane / 4) + 2 mt + (e >> 1), row 2 (lane % 4) + (e & 1)
     float m[NT][2], l[NT][2];
-    int E;
+    float mv[NT][2];             // o stands for o 2^(mv - 6)
 
     __device__ __forceinline__ void reset()
     {
@@ -44,10 +48,9 @@ struct WarpQ8 {
 #pragma unroll
             for (int mt = 0; mt < D / 16; ++mt)
                 o[nt][mt][0] = o[nt][mt][1] = o[nt][mt][2] = o[nt][mt][3] = 0.f;
-            m[nt][0] = m[nt][1] = NEG_INF;
+            m[nt][0] = m[nt][1] = mv[nt][0] = mv[nt][1] = NEG_INF;
             l[nt][0] = l[nt][1] = 0.f;
         }
-        E = -256;
     }
 
     // query rows of x [n][D] with the scale-offset (all three in shared memory); rows from n on are zeros
@@ -99,7 +102,7 @@ struct WarpQ8 {
 
     // Keys at rows r0 .. r0 + 16 KT - 1 of the staged block (K codes at kb, V codes at vb, both
     // exponents in shared memory).  Unless whole, only rows lo .. hi of the block count; V rows
-    // that do not count must hold finite codes and an exponent no larger than the others'.
+    // that do not count must hold finite codes.
     template <int KT>
     __device__ __forceinline__ void step(const uint8_t *kb, const uint8_t *vb, const int8_t *ke, const int8_t *ve, int r0,
                                          bool whole, int lo, int hi)
@@ -107,8 +110,7 @@ struct WarpQ8 {
         const int lane = threadIdx.x & 31, gq = lane >> 2, t = lane & 3;
         const float NEG_INF = -__int_as_float(0x7f800000);
         uint4 ka[KT][D / 64], kc[KT][D / 64];
-        float kf[KT][2];
-        int v[KT][2], vmax = -256;
+        float kf[KT][2], ve2[KT][2];
 #pragma unroll
         for (int j = 0; j < KT; ++j) {
 #pragma unroll
@@ -119,8 +121,7 @@ struct WarpQ8 {
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 kf[j][i] = q8_pow2(ke[r0 + 16 * j + gq + 8 * i]);
-                v[j][i] = ve[r0 + 16 * j + gq + 8 * i];
-                vmax = max(vmax, v[j][i]);
+                ve2[j][i] = static_cast<float>(ve[r0 + 16 * j + gq + 8 * i]);
             }
         }
         float s[KT][NT][4], s2[KT][NT][4];
@@ -158,30 +159,47 @@ struct WarpQ8 {
                         if (x < lo || x > hi)
                             s[j][nt][e] = NEG_INF;
                     }
-                    raise |= s[j][nt][e] > m[nt][e & 1] + 8.f;
+                    raise |= s[j][nt][e] > m[nt][e & 1] + 8.f || s[j][nt][e] + ve2[j][e >> 1] > mv[nt][e & 1] + 8.f;
                 }
-        raise |= vmax > E;
-        // rare: a row's maximum, or the largest V exponent met so far, goes up
+        // rare: one of a row's maxima goes up
         if (__any_sync(0xffffffffu, raise)) {
-            const int emax = max(E, __reduce_max_sync(0xffffffffu, vmax));
-            const float oscale = fast_exp2(static_cast<float>(E - emax));
-            E = emax;
+            constexpr uint32_t SIZE = CODE == ORTHROS_KV_E4M3 ? 0x7f7f7f7fu : 0xffffffffu;  // e4m3 has a zero of either sign
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                float c[2] = {oscale, oscale};
+            for (int j = 0; j < KT; ++j)
 #pragma unroll
                 for (int i = 0; i < 2; ++i) {
-                    float mx = NEG_INF;
+                    uint32_t any = 0;  // of a quarter of the V row, then of all of it
 #pragma unroll
-                    for (int j = 0; j < KT; ++j)
+                    for (int c = 0; c < D / 64; ++c) {
+                        const uint4 u = *reinterpret_cast<const uint4 *>(vb + q8_offset<D>(r0 + 16 * j + gq + 8 * i, t + 4 * c));
+                        any |= (u.x | u.y | u.z | u.w) & SIZE;
+                    }
+                    any |= __shfl_xor_sync(0xffffffffu, any, 1);
+                    any |= __shfl_xor_sync(0xffffffffu, any, 2);
+                    if (any == 0)
+                        ve2[j][i] = NEG_INF;
+                }
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) {
+                float c[2];
+#pragma unroll
+                for (int i = 0; i < 2; ++i) {
+                    float mx = NEG_INF, mw = NEG_INF;
+#pragma unroll
+                    for (int j = 0; j < KT; ++j) {
                         mx = fmaxf(mx, fmaxf(s[j][nt][i], s[j][nt][2 + i]));
+                        mw = fmaxf(mw, fmaxf(s[j][nt][i] + ve2[j][0], s[j][nt][2 + i] + ve2[j][1]));
+                    }
 #pragma unroll
-                    for (int off = 4; off < 32; off <<= 1)
+                    for (int off = 4; off < 32; off <<= 1) {
                         mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-                    const float n = fmaxf(m[nt][i], mx), f = n == NEG_INF ? 1.f : fast_exp2(m[nt][i] - n);
+                        mw = fmaxf(mw, __shfl_xor_sync(0xffffffffu, mw, off));
+                    }
+                    const float n = fmaxf(m[nt][i], mx), nv = fmaxf(mv[nt][i], mw);
+                    l[nt][i] *= n == NEG_INF ? 1.f : fast_exp2(m[nt][i] - n);
+                    c[i] = nv == NEG_INF ? 1.f : fast_exp2(mv[nt][i] - nv);
                     m[nt][i] = n;
-                    l[nt][i] *= f;
-                    c[i] *= f;
+                    mv[nt][i] = nv;
                 }
 #pragma unroll
                 for (int mt = 0; mt < D / 16; ++mt) {
@@ -194,21 +212,23 @@ struct WarpQ8 {
         }
         uint32_t pb[KT][NT][2];
 #pragma unroll
-        for (int j = 0; j < KT; ++j) {
-            const float vf[2] = {q8_pow2(max(v[j][0] - E + 6, -126)), q8_pow2(max(v[j][1] - E + 6, -126))};
+        for (int j = 0; j < KT; ++j)
 #pragma unroll
             for (int nt = 0; nt < NT; ++nt) {
-                const float u0 = m[nt][0] == NEG_INF ? 0.f : m[nt][0], u1 = m[nt][1] == NEG_INF ? 0.f : m[nt][1];
-                const float p0 = fast_exp2(s[j][nt][0] - u0), p1 = fast_exp2(s[j][nt][1] - u1);
-                const float p2 = fast_exp2(s[j][nt][2] - u0), p3 = fast_exp2(s[j][nt][3] - u1);
-                l[nt][0] += p0 + p2;
-                l[nt][1] += p1 + p3;
-                const __half2 h0 = __floats2half2_rn(p0 * vf[0], p1 * vf[0]);
-                const __half2 h1 = __floats2half2_rn(p2 * vf[1], p3 * vf[1]);
+                float p[4], pv[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float mm = m[nt][e & 1], mw = mv[nt][e & 1];
+                    p[e] = fast_exp2(s[j][nt][e] - (mm == NEG_INF ? 0.f : mm));
+                    pv[e] = fast_exp2(s[j][nt][e] + (ve2[j][e >> 1] - (mw == NEG_INF ? 0.f : mw - 6.f)));
+                }
+                l[nt][0] += p[0] + p[2];
+                l[nt][1] += p[1] + p[3];
+                const __half2 h0 = __floats2half2_rn(pv[0], pv[1]);
+                const __half2 h1 = __floats2half2_rn(pv[2], pv[3]);
                 pb[j][nt][0] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&h0));
                 pb[j][nt][1] = movmatrix_trans(*reinterpret_cast<const uint32_t *>(&h1));
             }
-        }
         // V: four keys of every 16, D / 8 bytes each
 #pragma unroll
         for (int j = 0; j < KT; ++j) {

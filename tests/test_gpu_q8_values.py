@@ -69,3 +69,74 @@ def test_values_near_the_smallest(lens, Hq, Hkv, d, code):
     t.v, t.s.inp.v_new[0] = scaled(t.v, n), scaled(t.s.inp.v_new[0], n)
     assert quantize(t.v, code)[1].min() < -120
     t.check()
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("shift", [-10, -17, -24, -60])
+@pytest.mark.parametrize("lens,Hq,Hkv,d", SHAPES)
+def test_rows_of_zeros_among_small_values(lens, Hq, Hkv, d, shift, code):
+    """A row of zeros (its exponent is 0, above all others) takes weight but no other row's bits, wherever it lies:
+    first, in a block's middle, in the window, as the new token."""
+    t = Step(lens, Hq, Hkv, d, code, 72)
+    t.v, t.s.inp.v_new[0] = scaled(t.v, shift), scaled(t.s.inp.v_new[0], shift)
+    for b, m in enumerate(lens):
+        t.v[b, [0, 40, m - 60, m - 1]] = 0
+        t.v[b, m // 2] = 0x8000  # zeros of the other sign
+    t.check("rows")
+    t = Step(lens, Hq, Hkv, d, code, 73)
+    t.v, t.s.inp.v_new[0] = scaled(t.v, shift), 0
+    t.check("new row")
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("lens,Hq,Hkv,d", SHAPES)
+def test_every_value_is_zero(lens, Hq, Hkv, d, code):
+    t = Step(lens, Hq, Hkv, d, code, 74)
+    t.v[:], t.s.inp.v_new[0] = 0, 0
+    s = t.s
+    for j, rows in enumerate((t.k, t.v)):
+        for b, m in enumerate(lens):
+            s.codes[j][b, :m], s.exps[j][b, :m] = quantize(rows[b, :m], code)
+    s.dev_cache = [codes(c, code) for c in s.codes] + [exps(e) for e in s.exps]
+    o, oc = s.step(0)
+    assert not o.any() and not oc.any() and int(s.err.item()) == 0
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("shift", [-17, -60, -100])
+@pytest.mark.parametrize("lens,Hq,Hkv,d", SHAPES)
+def test_large_values_without_weight(lens, Hq, Hkv, d, shift, code):
+    """V rows of ordinary size whose keys every query avoids (weights under 2^-80), among rows smaller by 2^shift."""
+    t = Step(lens, Hq, Hkv, d, code, 75)
+    n = t.s.inp
+    far = 64 if shift > -80 else 128  # nats below the others
+    for al, be in ((n.alpha, n.beta), (n.alpha_c, n.beta_c)):
+        al[:, 0], be[:, 0] = 0, far / 8 / t.s.cfg.scale  # column 0 of every scaled query is far / 8
+    small = scaled(t.v, shift)
+    t.k[..., 0] = 0
+    n.k_new[0][..., 0] = 0
+    n.v_new[0] = scaled(n.v_new[0], shift)
+    for b, m in enumerate(lens):
+        for r in (3, m // 2, m - 30):
+            small[b, r] = t.v[b, r]
+            t.k[b, r], t.k[b, r, :, 0] = 0, 0xC100  # -8
+    t.v = small
+    t.check()
+
+
+@pytest.mark.parametrize("code", ["e4m3", "int8"])
+@pytest.mark.parametrize("lens,Hq,Hkv,d", SHAPES)
+def test_large_values_of_little_weight(lens, Hq, Hkv, d, code):
+    """V rows whose sizes span 2^-50 .. 2^50, their weights the other way round: all count in the output alike."""
+    t = Step(lens, Hq, Hkv, d, code, 76)
+    n = t.s.inp
+    for al, be in ((n.alpha, n.beta), (n.alpha_c, n.beta_c)):
+        al[:, 0], be[:, 0] = 0, 4 / t.s.cfg.scale  # column 0 of every scaled query is 4
+    t.k[..., 0], n.k_new[0][..., 0] = 0, 0
+    rng = np.random.default_rng(77)
+    for b, m in enumerate(lens):
+        for r in range(m):
+            size = int(rng.integers(-50, 51))
+            t.v[b, r] = scaled(t.v[b, r], size)
+            t.k[b, r, :, 0] = np.float32(-size * np.log(2) / 4).view(np.uint32) >> 16
+    t.check()
