@@ -310,6 +310,15 @@ __global__ void __launch_bounds__(512, 1)
             if (!(ok = mbar_wait(&kfull[s], static_cast<uint32_t>((j / C::SLOTS) & 1))))
                 break;
             uint8_t *blk = smem + C::K_OFF + (s / 2) * C::PAIR_BYTES + (s % 2) * C::KB * 128;
+            // DIRECT: own rows from this one on lie behind every copy's position: they have no weight, but may
+            // hold anything, and become zeros before they are looked at
+            const int beyond = DIRECT && j >= pre_blocks ? kmax + 1 - (j - pre_blocks) * C::KB : C::KB;
+            if (DIRECT && beyond < C::KB)
+                for (int r = cid >> 3; r < C::KB; r += STEP)
+                    if (r >= beyond)
+#pragma unroll
+                        for (int sl = 0; sl < C::SLABS; ++sl)
+                            *reinterpret_cast<uint4 *>(blk + sl * C::PAIR_SLAB + r * 128 + (cid & 7) * 16) = make_uint4(0, 0, 0, 0);
             uint4 u[ITS][C::SLABS];
             bool big = false;
 #pragma unroll
@@ -333,9 +342,7 @@ __global__ void __launch_bounds__(512, 1)
                                          kexp + (j % C::MARKS) * C::KB, bad);
             }
             if constexpr (DIRECT) {
-                // V rows behind the last position have no weight, but may hold anything
-                const int beyond = kmax + 1 - (j - pre_blocks) * C::KB;  // first such row of the block
-                if (j >= pre_blocks && beyond < C::KB) {
+                if (beyond < C::KB) {  // the same for V
                     if (!(ok = mbar_wait(&vfull[j / 2 % C::MPAIRS], static_cast<uint32_t>((j / 2 / C::MPAIRS) & 1))))
                         break;
                     for (int it = 0; it < ITS; ++it) {
@@ -481,8 +488,8 @@ __global__ void __launch_bounds__(512, 1)
                         for (int cw = 0; cw < C::CONV_THREADS / 32; ++cw)
                             kw |= (((kf2 >> (8 * cw)) & 0xffu) ? 1u : 0u) << cw;
                         if (kw != 0) {  // logits of shifted key rows times 2^e (rare), in tensor memory
-                            unshift_chunk32(s_col, kexp + ks * C::KB, 0, kw, C::CONV_THREADS / 8, 4, range_bad);
-                            unshift_chunk32(s_col + 32, kexp + ks * C::KB, 32, kw, C::CONV_THREADS / 8, 4, range_bad);
+                            unshift_chunk32(s_col, kexp + ks * C::KB, 0, kw, C::CONV_THREADS / 8, 4, range_bad, nvalid);
+                            unshift_chunk32(s_col + 32, kexp + ks * C::KB, 32, kw, C::CONV_THREADS / 8, 4, range_bad, nvalid - 32);
                             tmem_ld32(s_col, va);
                             tmem_ld32(s_col + 32, vb);
                             tmem_wait_ld();
