@@ -101,7 +101,7 @@ __global__ void __launch_bounds__(512, 1)
     uint64_t *q_full = vempty + C::PAIRS;  // [2] query tile prepared
     uint64_t *s_full = q_full + 2;         // [2] S of a pair complete
     uint64_t *p_full = s_full + 2;         // [2] P written
-    uint64_t *o_done = p_full + 2;         // [2] O += P V of a pair complete
+    uint64_t *o_done = p_full + 2;         // [2] O += P V of a pair complete, but the last
     uint64_t *o_final = o_done + 2;        // [2] of the stream's last pair
     uint64_t *turn = o_final + 2;          // [2][4] a softmax warp of the stream is done with a pair
     int8_t *kexp = reinterpret_cast<int8_t *>(smem + C::KEXP_OFF);
@@ -229,15 +229,6 @@ __global__ void __launch_bounds__(512, 1)
                         tma_load_4d(dst + sl * C::PAIR_SLAB, map, bar, sl * 64, g, j0, own ? b_own : 0);
                 }
             }
-            // Every MMA that reads the last pairs, and its commit, has landed before shared and tensor memory
-            // are given back: of a stream whose tile has no row nothing else waits for the last P V.
-            for (int pp = max(npair - C::PAIRS, 0); pp < npair && !s_abort; ++pp) {
-                const int ps = pp % C::PAIRS;
-                if (!mbar_wait(kv ? &vempty[ps] : &kempty[ps], static_cast<uint32_t>((pp / C::PAIRS) & 1))) {
-                    record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
-                    s_abort = 1;
-                }
-            }
         }
     } else if (warp < 3) {
         // ------------------------------------------------------------------ MMA issuer of stream t
@@ -265,7 +256,8 @@ __global__ void __launch_bounds__(512, 1)
                     umma_ss(s_tm, qdesc + off, kdesc + off, IDESC_QK, kk != 0);
                 }
                 umma_commit(&s_full[t]);
-                umma_commit(&kempty[ps]);  // this stream's part of the pair's K
+                if (pp + C::PAIRS < npair)     // the producer waits for it
+                    umma_commit(&kempty[ps]);  // this stream's part of the pair's K
                 return true;
             };
             auto issue_pv = [&](int u) -> bool {
@@ -279,18 +271,18 @@ __global__ void __launch_bounds__(512, 1)
                 for (int kk = 0; kk < 8; ++kk)
                     umma_ts(o_tm, s_tm + 8 * kk, vdesc + static_cast<uint64_t>(kk * (2048 >> 4)), IDESC_PV,
                             (u > 0 || kk > 0) ? 1u : 0u);
-                umma_commit(&o_done[t]);
-                if (u == nu - 1)
-                    umma_commit(&o_final[t]);
-                umma_commit(&vempty[ps]);  // the same for its V
+                umma_commit(u == nu - 1 ? &o_final[t] : &o_done[t]);
+                if (pp + C::PAIRS < npair)
+                    umma_commit(&vempty[ps]);  // the same for its V
                 return true;
             };
             bool ok = nu == 0 || (mbar_wait(&q_full[ROWS2 ? t : 0], 0) && issue_s(0));
             for (int u = 0; u < nu && ok; ++u)
                 ok = issue_pv(u) && (u + 1 >= nu || issue_s(u + 1));
-            // the last commits to o_done and o_final too (see the producers' end)
+            // A stream whose tile has no row: nothing else waits for its last P V before shared and tensor
+            // memory are given back.  All other commits have been waited for.
             if (ok && nu > 0)
-                ok = mbar_wait(&o_done[t], static_cast<uint32_t>((nu - 1) & 1)) && mbar_wait(&o_final[t], 0);
+                ok = mbar_wait(&o_final[t], 0);
             if (!ok) {
                 s_abort = 1;
                 record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
