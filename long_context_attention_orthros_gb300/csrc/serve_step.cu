@@ -676,15 +676,20 @@ __global__ void __launch_bounds__(SvCfg<D, G, CODE>::THREADS, 2)
                     continue;
                 float f = fast_exp2(ms[w * G + row] - M);
                 L += f * lw;
-                float4 y = *reinterpret_cast<const float4 *>(os + (w * G + row) * D + d4);
                 if constexpr (Q8) {  // o stands for o 2^(mv - 6); in two factors, as 2^(mv - 6 - M) can pass fp32's range
                     f = fast_exp2(0.5f * (vs[w * G + row] - 6.f - M));
-                    y = make_float4(f * y.x, f * y.y, f * y.z, f * y.w);
+                    const float4 y = *reinterpret_cast<const float4 *>(os + (w * G + row) * D + d4);
+                    a.x += f * (f * y.x);
+                    a.y += f * (f * y.y);
+                    a.z += f * (f * y.z);
+                    a.w += f * (f * y.w);
+                } else {
+                    const float4 y = *reinterpret_cast<const float4 *>(os + (w * G + row) * D + d4);
+                    a.x += f * y.x;
+                    a.y += f * y.y;
+                    a.z += f * y.z;
+                    a.w += f * y.w;
                 }
-                a.x += f * y.x;
-                a.y += f * y.y;
-                a.z += f * y.z;
-                a.w += f * y.w;
             }
             if (alone) {
                 const float inv = L > 0.f ? 1.f / L : 0.f;
