@@ -507,6 +507,9 @@ size_t orthros_decode_prefix_workspace_size(int B, int P, int L_max, int Hq, int
  * to own row cache_len[b] (position P + cache_len[b]), its copy attends over the prefix and every
  * own row, and the base token's window reaches back into the prefix where the own rows do not
  * fill it.  The prefix is read once for the whole batch.  P + L_max must stay below 2^31.
+ * More than 16 query rows a KV head take q . k over the prefix in fp16, a query row and a key row
+ * each with a power of two of its own where fp16 needs one (keys from 2^-9 to 65504 need none),
+ * so that keys of any size count; an infinite key of the prefix then sets ORTHROS_DEVERR_RANGE.
  * Other arguments, results and errors as orthros_decode_step.
  */
 orthros_status orthros_decode_step_prefix(const orthros_bf16 *q_new, const orthros_bf16 *qc_new,
@@ -529,6 +532,8 @@ size_t orthros_xattn_prefix_workspace_size(int B, int T_out, int P, int T_kv, in
  * each in [0, T_kv), so the copy's position is P + pos).  The prefix is read once for all copies
  * of the batch.  A copy whose position is out of range gets a zero output and sets
  * ORTHROS_DEVERR_POSITION.  Own rows behind a sequence's largest position may hold anything.
+ * Query rows and keys in fp16 as in orthros_decode_step_prefix; where many copies a sequence take
+ * prefix and own rows in one pass, an infinite key among the own rows that count is reported too.
  * workspace: orthros_xattn_prefix_workspace_size(...) bytes, 256-byte aligned, contents need not
  * be initialised.  Other arguments as orthros_xattn_fwd.
  */

@@ -13,8 +13,8 @@
 //   S = q K^T   one N = 128 product per 16 of d, fp16, fp32 accumulators in tensor memory.  A q row is
 //               scaled by a power of two to a largest value in [2^14, 2^15) before it is rounded (the
 //               factor comes back in the exponent's FMA); K is converted from bf16 in shared memory,
-//               a key row whose largest |k| reaches 65520 by an exact 2^-e first and its logits
-//               multiplied back by 2^e;
+//               a key row whose largest |k| reaches 65520, or lies below 2^-9, by an exact 2^-e
+//               first and its logits multiplied back by 2^e;
 //   softmax     a thread a row; the running maximum is raised only when it grows by more than 8
 //               (log2 units); P <= 256 as bf16 over S;
 //   O += P V    bf16, fp32 accumulators in tensor memory.
@@ -312,16 +312,31 @@ __global__ void __launch_bounds__(512, 1)
                         for (int sl = 0; sl < C::SLABS; ++sl)
                             *reinterpret_cast<uint4 *>(blk + sl * C::PAIR_SLAB + r * 128 + (cid & 7) * 16) = make_uint4(0, 0, 0, 0);
             uint4 u[ITS][C::SLABS];
-            bool big = false;
+            float most = 0.f, least = kSmallKey;  // of this lane's part of each row its largest |k|: the extremes
+            float row_max[ITS];
 #pragma unroll
-            for (int it = 0; it < ITS; ++it)
+            for (int it = 0; it < ITS; ++it) {
+                row_max[it] = 0.f;
 #pragma unroll
                 for (int sl = 0; sl < C::SLABS; ++sl) {
                     u[it][sl] = *reinterpret_cast<const uint4 *>(blk + sl * C::PAIR_SLAB + ((cid >> 3) + STEP * it) * 128 +
                                                                  (cid & 7) * 16);
-                    big |= !(bf16x8_absmax(u[it][sl]) < 65520.f);
+                    row_max[it] = fmaxf(row_max[it], bf16x8_absmax(u[it][sl]));
                 }
-            const bool wany = __any_sync(0xffffffffu, big);
+                most = fmaxf(most, row_max[it]);
+                least = fminf(least, row_max[it]);
+            }
+            bool wany = __any_sync(0xffffffffu, !(most < 65520.f) || least < kSmallKey);
+            if (wany && !__any_sync(0xffffffffu, !(most < 65520.f))) {  // is a whole row (8 lanes) small, and not zero?
+                wany = false;
+#pragma unroll
+                for (int it = 0; it < ITS; ++it) {
+                    const uint32_t row = 0xffu << (lane & 24);
+                    const uint32_t below = __ballot_sync(0xffffffffu, row_max[it] < kSmallKey) & row;
+                    const uint32_t some = __ballot_sync(0xffffffffu, row_max[it] > 0.f) & row;
+                    wany |= __any_sync(0xffffffffu, below == row && some != 0);
+                }
+            }
             if (!wany) {
 #pragma unroll
                 for (int it = 0; it < ITS; ++it)
@@ -330,8 +345,8 @@ __global__ void __launch_bounds__(512, 1)
                         *reinterpret_cast<uint4 *>(blk + sl * C::PAIR_SLAB + ((cid >> 3) + STEP * it) * 128 + (cid & 7) * 16) =
                             k_to_fp16(u[it][sl]);
             } else {
-                shift_key_rows<C::SLABS>(blk, C::PAIR_SLAB, 0, cid >> 3, STEP, ITS, cid & 7,
-                                         kexp + (j % C::MARKS) * C::KB, bad);
+                shift_key_rows<C::SLABS, true>(blk, C::PAIR_SLAB, 0, cid >> 3, STEP, ITS, cid & 7,
+                                               kexp + (j % C::MARKS) * C::KB, bad);
             }
             if constexpr (DIRECT) {
                 if (beyond < C::KB) {  // the same for V

@@ -137,7 +137,10 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&v)[16
 // |k| < 65520 (fp16's range; bf16 values below fp16's normal range keep their value to within
 // 2^-25).  A key row whose largest |k| reaches 65520 is scaled by an exact power of two 2^-e
 // that puts its largest element in [2^14, 2^15), and its logits are multiplied back by 2^e in
-// fp32, so every finite bf16 key is taken.
+// fp32, so every finite bf16 key is taken.  Small keys: bf16's 8 significant bits are exact in fp16
+// down to 2^-17, so a row whose largest |k| is at least 2^-9 keeps every value within 2^8 of it, the
+// others to within 2^-16 of it.  Smaller rows are scaled up in the same way by the kernels that ask
+// for it (SMALL); in the others they keep their values to within 2^-25 only.
 
 // 2^n for an integer n in [-126, 127], exactly
 __device__ __forceinline__ float exp2i(int n) { return __uint_as_float(static_cast<uint32_t>(127 + n) << 23); }
@@ -155,10 +158,18 @@ __device__ __forceinline__ float bf16x8_absmax(uint4 u)
     return m;
 }
 
+constexpr float kSmallKey = 0.001953125f;  // 2^-9
+
 // shift e of a key row whose largest |k| is amax: 0 below 65520, else amax * 2^-e lies in
-// [2^14, 2^15); an infinite key sets bad (its logits cannot be finite) and keeps e = 0
+// [2^14, 2^15); an infinite key sets bad (its logits cannot be finite) and keeps e = 0.  SMALL: a row
+// below 2^-9 that is not zero is shifted likewise (by -126 at most)
+template <bool SMALL = false>
 __device__ __forceinline__ int fp16_key_shift(float amax, bool &bad)
 {
+    if (SMALL && amax < kSmallKey && amax > 0.f) {
+        const int e = static_cast<int>(__float_as_uint(amax) >> 23) - 127 - 14;
+        return e < -126 ? -126 : e;
+    }
     if (amax < 65520.f)
         return 0;
     const int ex = static_cast<int>((__float_as_uint(amax) >> 23) & 0xffu);
@@ -196,12 +207,12 @@ __device__ __forceinline__ uint4 k_to_fp16_scaled(uint4 u, float sd)
 }
 
 // The rare path of a key-block conversion done by one warp, 8 lanes per key row, when one of
-// its rows holds a value at or beyond 65520: this lane holds chunk c8 of every slab of rows
+// its rows holds a value at or beyond 65520 (or, SMALL, is small): this lane holds chunk c8 of every slab of rows
 // rsub + rstep * r (r < nrows), all still bf16.  Each row's largest |k| over its 8 lanes decides
 // its shift e; the row is written as fp16 of k * 2^-e (at blk + sl * slab_bytes, and again
 // `mirror` bytes further when mirror != 0) and e is stored at kexp[row].  Called by the whole
 // warp.
-template <int SLABS>
+template <int SLABS, bool SMALL = false>
 __device__ __noinline__ void shift_key_rows(uint8_t *blk, int slab_bytes, int mirror, int rsub, int rstep, int nrows,
                                             int c8, int8_t *kexp, bool &bad)
 {
@@ -218,7 +229,7 @@ __device__ __noinline__ void shift_key_rows(uint8_t *blk, int slab_bytes, int mi
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
         amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 4));
-        const int ex = fp16_key_shift(amax, bad);
+        const int ex = fp16_key_shift<SMALL>(amax, bad);
         if (c8 == 0)
             kexp[row] = static_cast<int8_t>(ex);
         const float sd = exp2i(-ex);
@@ -236,7 +247,7 @@ __device__ __noinline__ void shift_key_rows(uint8_t *blk, int slab_bytes, int mi
 // The rare path of the softmax warps: the logits of 32 consecutive keys (one 32-column chunk of
 // this warp's 32 tensor-memory lanes at taddr; key rows row0 .. row0 + 31 of their block) times
 // 2^e_j, read back and stored in place.  Row r's shift is ke[r] when bit ((r % period) / per) of
-// wmask is set (the converter warp owning the row found it beyond fp16), else 0.  A logit that is
+// wmask is set (the converter warp owning the row has shifted some of its rows), else 0.  A logit that is
 // no longer finite sets bad, unless its column lies behind the last that counts (it is masked later).
 // Called by the whole warp; the caller reloads the chunk afterwards.
 static __device__ __noinline__ void unshift_chunk32(uint32_t taddr, const int8_t *ke, int row0, uint32_t wmask, int period,
