@@ -22,7 +22,7 @@
 //
 // Bound by HBM where the rows are few (8 sequences over 131072 rows, 32/8 heads, d = 128: 85 us, 6.3 TB/s,
 // and 14 for its start and the own rows), by a stream's chain of S, softmax and P V where they fill
-// the tile (4 x 256 copies: 305 us, 930 TFLOP/s).
+// the tile (4 x 256 copies: 308 us, 920 TFLOP/s; 305 without the look for small key rows).
 //
 // Roles (512 threads, one CTA an SM):
 //   warps 0, 3    TMA producers of K and of V

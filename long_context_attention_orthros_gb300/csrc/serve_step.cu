@@ -7,8 +7,8 @@
 //
 // Bound by the cache's bytes (2 (d + 1) a row and head as codes, 4 d in bf16) where there are many, by the
 // start, the segments' borders and the join where there are few.  Measured (32/8 heads, d = 128): codes,
-// 2 x 131072 rows 88 us (6.1 TB/s: 91% of a plain copy's rate), 8 ragged caches of up to 16384 rows 39 us
-// (59%), 1 x 300 rows 8.9 us.
+// 2 x 131072 rows 90 us (6.0 TB/s: 90% of a plain copy's rate), 8 ragged caches of up to 16384 rows 40 us
+// (57%), 1 x 300 rows (8/2 heads, d = 64) 9.1 us.
 //
 // The work of a step is a list of segments, two for each (b, KV head): the copy's own rows
 // 0 .. p, and the base token's window (which in the prefix form may begin in the prefix).  Each
@@ -40,7 +40,7 @@
 
 namespace orthros {
 
-constexpr int SERVE_CTAS = 304;  // two on each of 152 SMs
+constexpr int SERVE_CTAS = 304;  // two on each of 152 SMs (G = 16, d = 128 behind a prefix: one, two rounds)
 
 // a segment whose partials have to be joined, kept until the CTA has run out of blocks
 struct Join {
@@ -68,7 +68,7 @@ struct SvCfg {
     static constexpr int GROUP = 4 / KT;  // warps that share a block
     static constexpr int SCR_ROWS = CWARPS * G;
     static constexpr int SCR_BYTES = SCR_ROWS * (D + 3) * 4;  // the warps' o, max, sum, scale of o
-    static constexpr int LIMIT = 113 * 1024 - 2048;            // two CTAs share an SM
+    static constexpr int LIMIT = 113 * 1024 - 2048;            // two CTAs share an SM (see STAGES)
     // a segment's queries, its alpha and beta and the new K and V row come through a buffer of their
     // own, free again once the segment has begun
     static constexpr int HB = 1;
@@ -80,6 +80,7 @@ struct SvCfg {
     // At most four stages: with more bytes in flight the SMs that are nearer to memory get ahead of
     // the others, and equal shares end as late as the last one.  A step over 2 x 131072 rows (D = 128,
     // e4m3): 6 stages 100 us, 4 stages 89 us, the median CTA at 78 us in both.
+    // bf16 at G = 16, D = 128 has room for one stage beside the warps' results; it takes two (122 KB), and one CTA an SM.
     static constexpr int MOST = 4;
     static constexpr int STAGES = FIT < 2 ? 2 : (FIT > MOST ? MOST : FIT / KT * KT);
     static_assert(STAGES % KT == 0, "a slot belongs to one group of warps");
