@@ -131,6 +131,24 @@ orthros_status orthros_swa_fwd_lse(const orthros_bf16 *q_raw, const orthros_bf16
                                    int64_t o_bstride, int32_t *dev_err, void *stream);
 
 /*
+ * Base-stream attention with sinks (the paper has no counterpart): the first `sinks` keys of a
+ * sequence stay visible to every row behind them, beside the window:
+ *   row t attends over keys j <= t with j > t - window or j < sinks
+ * 0 <= sinks <= 32 (0: as orthros_swa_fwd).  lse (optional, NULL: none) gets each row's log-sum-exp
+ * over those keys, fp32 [B, T, Hq], for orthros_swa_sink_bwd.  Only output rows row_begin ..
+ * row_end-1 are computed (0 and T for all; rules and reads as orthros_swa_fwd_rows, and key rows
+ * 0 .. sinks-1 have to be in place).  Values of K and V are finite; one that is not reaches, beside
+ * the rows that see it, only rows up to window + 128 away.  Other arguments, arithmetic and errors as
+ * orthros_swa_fwd.
+ */
+orthros_status orthros_swa_sink_fwd(const orthros_bf16 *q_raw, const orthros_bf16 *k,
+                                    const orthros_bf16 *v, const float *alpha, const float *beta,
+                                    orthros_bf16 *o, float *lse, int B, int T, int Hq, int Hkv, int d,
+                                    int window, int sinks, float scale, int64_t q_bstride,
+                                    int64_t kv_bstride, int64_t o_bstride, int row_begin, int row_end,
+                                    int32_t *dev_err, void *stream);
+
+/*
  * Bytes of device workspace orthros_xattn_fwd needs for these sizes
  * (split-KV partial results).  Many copies per KV head (T_out * Hq/Hkv >= 256)
  * run on a kernel that keeps no partials, and few copies whose rows all fit one
@@ -343,6 +361,28 @@ orthros_status orthros_swa_bwd(const orthros_bf16 *q_raw, const orthros_bf16 *k,
                                int Hq, int Hkv, int d, int window, float scale, void *workspace,
                                size_t ws_bytes, int32_t *dev_err, void *stream);
 
+/* Bytes of device workspace orthros_swa_sink_bwd needs.  Returns 0 for invalid sizes. */
+size_t orthros_swa_sink_bwd_workspace_size(int B, int T, int Hq, int Hkv, int d);
+
+/*
+ * Gradient of orthros_swa_sink_fwd: that of orthros_swa_bwd with each row's sum over the keys that
+ * it sees, the sinks among them, given the forward's output o and log-sum-exp lse (needed; over window
+ * and sinks).  The fp32 outputs are computed to match: K, V, Q_raw and dO enter the products as they
+ * are, q, dS and P as a bf16 high part plus residual (some 2^-17 of them, where orthros_swa_bwd's one
+ * fp16 or bf16 gives 2^-12 or 2^-9), sums and exponents are fp32; no value is out of range.  alpha may
+ * hold zeros.  dalpha and dbeta are summed with atomics (their last bits depend on the order).
+ * B * Hq <= 65535.  workspace: orthros_swa_sink_bwd_workspace_size(...) bytes, 16-byte aligned, contents
+ * need not be initialised.  The copies' gradient is added by orthros_xattn_bwd with accumulate.  Other
+ * arguments as orthros_swa_bwd.
+ */
+orthros_status orthros_swa_sink_bwd(const orthros_bf16 *q_raw, const orthros_bf16 *k,
+                                    const orthros_bf16 *v, const float *alpha, const float *beta,
+                                    const orthros_bf16 *o, const orthros_bf16 *dO, const float *lse,
+                                    float *dq_raw, float *dk, float *dv, float *dalpha, float *dbeta,
+                                    int B, int T, int Hq, int Hkv, int d, int window, int sinks,
+                                    float scale, void *workspace, size_t ws_bytes, int32_t *dev_err,
+                                    void *stream);
+
 /*
  * Bytes of device workspace orthros_xattn_bwd needs (two fp32 values per copy
  * row, fp16 copies of K and of the copies' scale-offset q, and per-split row
@@ -545,6 +585,58 @@ orthros_status orthros_xattn_prefix_fwd(const orthros_bf16 *qc_raw, const int32_
                                         int64_t qc_bstride, int64_t kv_bstride, int64_t oc_bstride,
                                         void *workspace, size_t ws_bytes, int32_t *dev_err,
                                         void *stream);
+
+/*
+ * Bytes of device workspace orthros_decode_tree needs (contents need not be initialised).  Returns 0
+ * for invalid sizes.
+ */
+size_t orthros_decode_tree_workspace_size(int B, int N, int L_max, int Hq, int Hkv, int d);
+
+/*
+ * Both streams of a tree of up to N <= 64 drafted tokens over a KV cache (the paper has no
+ * counterpart), for their check in one pass; nothing is appended.  Node i of sequence b hangs below node
+ * parent[b, i], 0 <= parent < i, or below the last cached row (-1), and stands at position
+ * cache_len[b] + depth (0 for the latter).  Its path is its ancestors and itself.  For every node:
+ *   oc[b, i] = Eq. (5) for qc_new[b, i] over cache rows 0 .. cache_len[b]-1 and the path's rows of
+ *              k_new, v_new;
+ *   o[b, i]  = Eq. (4) for q_new[b, i] over those of them that lie at positions > its own - window or
+ *              < sinks (0 <= sinks <= 32).
+ * One node (N = 1, parent -1) is the decode step of a layer with sinks, without the append.
+ *   q_new, qc_new, o, oc [B, N, Hq, d] bf16; k_new, v_new [B, N, Hkv, d] bf16, dense
+ *   parent [B, N] int32; nodes [B] int32 or NULL (N): nodes of each sequence's tree, 0 .. N; output
+ *   rows behind them are left as they are, inputs behind them may hold anything
+ *   k_cache, v_cache [B, L_max, Hkv, d] bf16; cache_len [B], each in [0, L_max]; rows at or beyond it
+ *   may hold anything
+ * A node below a parent that is not -1 or an earlier node, and every node of a sequence with nodes
+ * out of range, gets zeros and sets ORTHROS_DEVERR_POSITION; a sequence with cache_len out of range
+ * gets zeros and sets ORTHROS_DEVERR_CACHE_FULL.  A V row that is not finite reaches every node of its
+ * tree's rows of a KV head that are computed together, whether they see it or not; rows that no node
+ * sees do not count.  workspace: orthros_decode_tree_workspace_size(...) bytes, 256-byte aligned.
+ */
+orthros_status orthros_decode_tree(const orthros_bf16 *q_new, const orthros_bf16 *qc_new,
+                                   const orthros_bf16 *k_new, const orthros_bf16 *v_new,
+                                   const int32_t *parent, const int32_t *nodes,
+                                   const orthros_bf16 *k_cache, const orthros_bf16 *v_cache,
+                                   const int32_t *cache_len, int L_max, const float *alpha,
+                                   const float *beta, const float *alpha_c, const float *beta_c,
+                                   orthros_bf16 *o, orthros_bf16 *oc, int B, int N, int Hq, int Hkv,
+                                   int d, int window, int sinks, float scale, void *workspace,
+                                   size_t ws_bytes, int32_t *dev_err, void *stream);
+
+/*
+ * Appends what the check accepted: the rows of k_new, v_new on the path to node[b] (in its order) go
+ * to cache rows cache_len[b] .., and cache_len[b] grows by their number; node[b] = -1 accepts none.
+ *   node [B] int32; path [B, N] int32 output: the path's nodes in order, -1 behind the last
+ *   other arguments as orthros_decode_tree
+ * A sequence whose node is outside [-1, N) or hangs below a bad parent is left as it is and sets
+ * ORTHROS_DEVERR_POSITION; one whose rows do not fit, or whose cache_len is out of range, likewise with
+ * ORTHROS_DEVERR_CACHE_FULL (its path is all -1).
+ */
+orthros_status orthros_decode_tree_accept(const orthros_bf16 *k_new, const orthros_bf16 *v_new,
+                                          const int32_t *parent, const int32_t *node,
+                                          orthros_bf16 *k_cache, orthros_bf16 *v_cache,
+                                          int32_t *cache_len, int L_max, int32_t *path, int B, int N,
+                                          int Hkv, int d, int32_t *dev_err, void *stream);
 
 #ifdef __cplusplus
 }

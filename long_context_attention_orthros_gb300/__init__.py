@@ -17,6 +17,10 @@ CUDA kernels.  PyTorch provides device memory and the current stream.
 * :func:`kv_quantize`, :func:`kv_dequantize` -- prompt rows written into an 8-bit KV cache
   (:func:`kv_cache_q8`) and read back as bf16
 * :func:`decode_step_q8` -- the decode step over an 8-bit cache
+* :func:`swa_sink_fwd`, :func:`swa_sink_bwd` -- the base stream with attention sinks (a few first
+  tokens that stay visible behind the window) and its gradient
+* :func:`decode_tree`, :func:`decode_tree_accept` -- both streams of a tree of drafted tokens over
+  a cache (with sinks, or not), and the accepted path's rows appended to it
 * :func:`xattn_prefix_fwd`, :func:`decode_step_prefix` -- the copies' attention and the decode
   step for a batch that shares a prompt prefix
 
@@ -35,6 +39,9 @@ from ._binding import (  # noqa: F401
     decode_step,
     decode_step_prefix,
     decode_step_q8,
+    decode_tree,
+    decode_tree_accept,
+    decode_tree_workspace_size,
     decode_workspace_size,
     kv_cache_q8,
     kv_dequantize,
@@ -48,6 +55,9 @@ from ._binding import (  # noqa: F401
     swa_fwd,
     swa_fwd_lse,
     swa_fwd_rows,
+    swa_sink_bwd,
+    swa_sink_bwd_workspace_size,
+    swa_sink_fwd,
     xattn_bwd,
     xattn_bwd_workspace_size,
     xattn_fwd,

@@ -102,6 +102,18 @@ def lib() -> ctypes.CDLL:
             L.orthros_xattn_prefix_workspace_size.argtypes = [I] * 7
             L.orthros_xattn_prefix_fwd.restype = I
             L.orthros_xattn_prefix_fwd.argtypes = [P] * 4 + [I] + [P] * 5 + [I] * 6 + [F, L64, L64, L64, P, SZ, P, P]
+            L.orthros_swa_sink_fwd.restype = I
+            L.orthros_swa_sink_fwd.argtypes = [P] * 7 + [I] * 7 + [F, L64, L64, L64, I, I, P, P]
+            L.orthros_swa_sink_bwd_workspace_size.restype = SZ
+            L.orthros_swa_sink_bwd_workspace_size.argtypes = [I] * 5
+            L.orthros_swa_sink_bwd.restype = I
+            L.orthros_swa_sink_bwd.argtypes = [P] * 13 + [I] * 7 + [F, P, SZ, P, P]
+            L.orthros_decode_tree_workspace_size.restype = SZ
+            L.orthros_decode_tree_workspace_size.argtypes = [I] * 6
+            L.orthros_decode_tree.restype = I
+            L.orthros_decode_tree.argtypes = [P] * 9 + [I] + [P] * 6 + [I] * 7 + [F, P, SZ, P, P]
+            L.orthros_decode_tree_accept.restype = I
+            L.orthros_decode_tree_accept.argtypes = [P] * 7 + [I, P] + [I] * 4 + [P, P]
             _lib = L
     return _lib
 
@@ -712,3 +724,117 @@ def xattn_prefix_fwd(qc_raw, pos, k_prefix, v_prefix, k, v, alpha_c, beta_c, sca
             _dense(beta_c, "beta_c", torch.float32, (Hq, d), dev), oa, B, T_out, T_kv, Hq, Hkv, d, _scale(scale, d),
             qs, ks, os_, _space(workspace, dev), workspace.nbytes, _word(dev_err, dev))
     return out
+
+
+def swa_sink_fwd(q_raw, k, v, alpha, beta, sinks: int, window: int = 128, scale=None, out=None, lse=None,
+                 row_begin: int = 0, row_end=None, dev_err=None):
+    """swa_fwd with attention sinks: row t attends over keys j <= t with j > t - window or j < sinks
+    (0 <= sinks <= 32).  Only rows row_begin..row_end-1 (default all T) are computed, by swa_fwd_rows'
+    rules.  With lse (fp32 [B, T, Hq], or True for a fresh one) each row's log-sum-exp is written too,
+    for swa_sink_bwd, and (out, lse) is returned."""
+    B, T, Hkv, d = k.shape
+    dev = k.get_device()
+    if dev < 0:
+        _refuse(k, "k", "bf16 CUDA tensor [B, T, Hkv, d]")
+    _, ks, kv = _kv_pair(k, v, B, Hkv, d, dev)
+    if q_raw.dim() != 4 or q_raw.shape[0] != B or q_raw.shape[1] < T or q_raw.shape[3] != d:
+        raise OrthrosError("q_raw shape does not match k")
+    Hq = q_raw.shape[2]
+    qa, qs = _rows(q_raw, "q_raw", q_raw.shape, dev)
+    if qs == 0:  # dense, but it may hold appended copies
+        qs = _bf16_rows(q_raw, "q_raw")
+    shape = (B, T, Hq, d)
+    if out is None:
+        out = torch.empty(shape, dtype=torch.bfloat16, device=k.device)
+    oa, os_ = _rows(out, "out", shape, dev)
+    if lse is True:
+        lse = torch.empty((B, T, Hq), dtype=torch.float32, device=k.device)
+    _invoke("orthros_swa_sink_fwd", dev, qa, *kv, _dense(alpha, "alpha", torch.float32, (Hq, d), dev),
+            _dense(beta, "beta", torch.float32, (Hq, d), dev), oa,
+            _optional(lse, "lse", torch.float32, (B, T, Hq), dev), B, T, Hq, Hkv, d, int(window), int(sinks),
+            _scale(scale, d), qs, ks, os_, int(row_begin), T if row_end is None else int(row_end), _word(dev_err, dev))
+    return out if lse is None else (out, lse)
+
+
+def swa_sink_bwd_workspace_size(B, T, Hq, Hkv, d) -> int:
+    return int(lib().orthros_swa_sink_bwd_workspace_size(B, T, Hq, Hkv, d))
+
+
+def swa_sink_bwd(q_raw, k, v, alpha, beta, o, dO, lse, sinks: int, window: int = 128, scale=None, workspace=None,
+                 dev_err=None):
+    """Gradient of swa_sink_fwd: returns fp32 (dq_raw, dk, dv, dalpha, dbeta) for the output gradient dO, given the
+    forward's inputs, output o and log-sum-exp lse (fp32 [B, T, Hq]).  q_raw, o, dO [B, T, Hq, d] and k, v
+    [B, T, Hkv, d], all dense bf16; alpha, beta [Hq, d] fp32.  xattn_bwd adds the copies' share to dk, dv."""
+    B, T, Hkv, d = kv = k.shape
+    dev = k.get_device()
+    if dev < 0:
+        _refuse(k, "k", "contiguous bf16 CUDA tensor [B, T, Hkv, d]")
+    Hq = q_raw.shape[2]
+    rows, vec, bf16, f32 = (B, T, Hq, d), (Hq, d), torch.bfloat16, torch.float32
+    args = (_dense(q_raw, "q_raw", bf16, rows, dev), _dense(k, "k", bf16, kv, dev), _dense(v, "v", bf16, kv, dev),
+            _dense(alpha, "alpha", f32, vec, dev), _dense(beta, "beta", f32, vec, dev), _dense(o, "o", bf16, rows, dev),
+            _dense(dO, "dO", bf16, rows, dev), _dense(lse, "lse", f32, (B, T, Hq), dev))
+    out = [torch.empty(shape, dtype=f32, device=k.device) for shape in (rows, kv, kv, vec, vec)]
+    if workspace is None:
+        workspace = torch.empty(max(swa_sink_bwd_workspace_size(B, T, Hq, Hkv, d), 256), dtype=torch.uint8,
+                                device=k.device)
+    _invoke("orthros_swa_sink_bwd", dev, *args, *[t.data_ptr() for t in out], B, T, Hq, Hkv, d, int(window), int(sinks),
+            _scale(scale, d), _space(workspace, dev), workspace.nbytes, _word(dev_err, dev))
+    return tuple(out)
+
+
+def decode_tree_workspace_size(B, N, L_max, Hq, Hkv, d) -> int:
+    return int(lib().orthros_decode_tree_workspace_size(B, N, L_max, Hq, Hkv, d))
+
+
+def decode_tree(q_new, qc_new, k_new, v_new, parent, k_cache, v_cache, cache_len, alpha, beta, alpha_c, beta_c,
+                window: int = 128, sinks: int = 0, nodes=None, scale=None, o=None, oc=None, workspace=None,
+                dev_err=None):
+    """Both streams of a tree of N <= 64 drafted tokens over a cache; nothing is appended (decode_tree_accept).
+    Node i of sequence b hangs below node parent[b, i] < i, or below the last cached row (-1).  Its copy
+    qc_new[b, i] attends over cache rows 0..cache_len[b]-1 and the rows of its path (ancestors and itself) in
+    k_new, v_new; its base token q_new[b, i] over those of them in its window or among the first `sinks`
+    positions.  q_new, qc_new [B, N, Hq, d]; k_new, v_new [B, N, Hkv, d]; parent int32 [B, N]; k_cache, v_cache
+    [B, L_max, Hkv, d]; cache_len int32 [B]; nodes int32 [B]: nodes of each tree (default N; rows of o, oc behind
+    them are left as they are).  Returns (o, oc)."""
+    B, L_max, Hkv, d = shape = k_cache.shape
+    dev = k_cache.get_device()
+    if dev < 0 or q_new.dim() != 4:
+        _refuse(q_new if dev >= 0 else k_cache, "q_new and k_cache", "contiguous bf16 CUDA tensor of four dimensions")
+    _, N, Hq, _ = q_new.shape
+    rows, new, vec, bf16, f32, i32 = (B, N, Hq, d), (B, N, Hkv, d), (Hq, d), torch.bfloat16, torch.float32, torch.int32
+    o = torch.empty_like(q_new) if o is None else o
+    oc = torch.empty_like(q_new) if oc is None else oc
+    if workspace is None:
+        workspace = torch.empty(max(decode_tree_workspace_size(B, N, L_max, Hq, Hkv, d), 256), dtype=torch.uint8,
+                                device=k_cache.device)
+    _invoke("orthros_decode_tree", dev, _dense(q_new, "q_new", bf16, rows, dev), _dense(qc_new, "qc_new", bf16, rows, dev),
+            _dense(k_new, "k_new", bf16, new, dev), _dense(v_new, "v_new", bf16, new, dev),
+            _dense(parent, "parent", i32, (B, N), dev), _optional(nodes, "nodes", i32, (B,), dev),
+            _dense(k_cache, "k_cache", bf16, shape, dev), _dense(v_cache, "v_cache", bf16, shape, dev),
+            _dense(cache_len, "cache_len", i32, (B,), dev), L_max, _dense(alpha, "alpha", f32, vec, dev),
+            _dense(beta, "beta", f32, vec, dev), _dense(alpha_c, "alpha_c", f32, vec, dev),
+            _dense(beta_c, "beta_c", f32, vec, dev), _dense(o, "o", bf16, rows, dev), _dense(oc, "oc", bf16, rows, dev),
+            B, N, Hq, Hkv, d, int(window), int(sinks), _scale(scale, d), _space(workspace, dev), workspace.nbytes,
+            _word(dev_err, dev))
+    return o, oc
+
+
+def decode_tree_accept(k_new, v_new, parent, node, k_cache, v_cache, cache_len, path=None, dev_err=None):
+    """Append what the check of a drafted tree accepted: the rows of k_new, v_new [B, N, Hkv, d] on the path to
+    node[b] (int32 [B]; -1: none) go to cache rows cache_len[b].., and cache_len[b] grows by their number.
+    Returns path, int32 [B, N]: the path's nodes in order, -1 behind the last."""
+    B, L_max, Hkv, d = shape = k_cache.shape
+    dev = k_cache.get_device()
+    if dev < 0 or k_new.dim() != 4:
+        _refuse(k_new if dev >= 0 else k_cache, "k_new and k_cache", "contiguous bf16 CUDA tensor of four dimensions")
+    N = k_new.shape[1]
+    new, bf16, i32 = (B, N, Hkv, d), torch.bfloat16, torch.int32
+    if path is None:
+        path = torch.empty((B, N), dtype=i32, device=k_cache.device)
+    _invoke("orthros_decode_tree_accept", dev, _dense(k_new, "k_new", bf16, new, dev),
+            _dense(v_new, "v_new", bf16, new, dev), _dense(parent, "parent", i32, (B, N), dev),
+            _dense(node, "node", i32, (B,), dev), _dense(k_cache, "k_cache", bf16, shape, dev),
+            _dense(v_cache, "v_cache", bf16, shape, dev), _dense(cache_len, "cache_len", i32, (B,), dev), L_max,
+            _dense(path, "path", i32, (B, N), dev), B, N, Hkv, d, _word(dev_err, dev))
+    return path

@@ -36,6 +36,7 @@
 
 #include <cuda_fp16.h>
 
+#include "bwd_util.cuh"
 #include "common.cuh"
 #include "kernels.cuh"
 #include "tc.cuh"
@@ -45,35 +46,8 @@ namespace orthros {
 
 namespace {
 
-constexpr float kLog2eF = 1.4426950408889634f;
 constexpr int BWD_ROWS = 64;  // query rows of a warp-MMA dq CTA
 constexpr int BWD_KEYS = 64;  // keys per streamed block of the warp-MMA dq kernel
-
-// [rows][D] bf16 tile in shared memory as D/64 slabs of rows x 128 bytes, 128-byte swizzle
-__device__ __forceinline__ uint32_t tile_off(int row, int col, int slab_bytes)
-{
-    return static_cast<uint32_t>((col / 64) * slab_bytes) + sw128_offset(row, (col % 64) / 8);
-}
-
-// 16-byte asynchronous copy global -> shared; valid = false writes zeros (nothing is read)
-__device__ __forceinline__ void cp_async16(uint32_t dst, const void *src, bool valid)
-{
-    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(valid ? 16 : 0)
-                 : "memory");
-}
-
-__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-
-template <int N>
-__device__ __forceinline__ void cp_async_wait()
-{
-    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
-}
-
-__device__ __forceinline__ uint8_t *align1024(uint8_t *p)
-{
-    return p + ((1024u - (smem_u32(p) & 1023u)) & 1023u);
-}
 
 // position of unit u of sequence b, or -1 when it has none in [0, T_kv)
 template <bool COPY>
@@ -573,15 +547,6 @@ __device__ __forceinline__ void mbar_arrive_cnt(uint64_t *bar, uint32_t count)
 {
     asm volatile("mbarrier.arrive.release.cta.shared::cta.b64 _, [%0], %1;" ::"r"(smem_u32(bar)), "r"(count)
                  : "memory");
-}
-
-// wait on an mbarrier as a whole warp (lane 0 polls); false after the time limit
-__device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
-{
-    bool ok = true;
-    if ((threadIdx.x & 31) == 0)
-        ok = mbar_wait(bar, parity);
-    return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 
 // the next round (of `units` units) at or after r that holds a unit seeing keys >= kt0

@@ -26,7 +26,9 @@ struct SwaParams {
     int reuse;             // 1: keep K/V blocks resident across consecutive tiles (set by launcher)
     float *lse;            // optional [B, T, Hq]: natural log of each row's sum of exp(scale q . k)
     int B;
+    int sinks;             // keys 0 .. sinks-1 stay visible behind the window (0 .. SWA_MAX_SINKS)
 };
+constexpr int SWA_MAX_SINKS = 32;
 
 struct XattnParams {
     const orthros_bf16 *qc;
@@ -105,6 +107,27 @@ size_t attn_bwd_split_bytes(int B, int Hkv);
 // [10], [11] the fp16 K and V with boxes of 64 x 1 x 32 (the base stream's band dQ)
 constexpr int ATTN_BWD_MAPS = 13;
 cudaError_t launch_attn_bwd(int D, int G, const AttnBwdParams &p, const CUtensorMap *maps, cudaStream_t stream);
+// gradient of the base stream with sinks, all launches (prepared queries, dq, dk and dv, the sinks' share)
+struct SinkBwdParams {
+    const orthros_bf16 *q, *k, *v, *o, *dO;  // q raw, the forward output o, its gradient dO, all dense
+    const float *alpha, *beta, *lse_in;      // lse_in: natural log [B, T, Hq]
+    float *dq, *dk, *dv, *dalpha, *dbeta;
+    // workspace: q = x alpha + beta as a bf16 high part and residual, [B, T, Hq, d] each; log2-sum-exp and
+    // dO . o, [B, T, Hq] each; the sinks' partial sums
+    uint16_t *q_hi, *q_lo;
+    float *lse, *Drow, *part;
+    int32_t *dev_err;
+    int B, T, Hq, Hkv, window, sinks;
+    float scale;
+};
+struct SinkBwdMaps {
+    CUtensorMap q_hi, q_lo, dO;  // boxes of 64 x G heads x 64/G tokens
+    CUtensorMap k, v;            // boxes of 64 x 1 x 128
+};
+size_t sink_bwd_workspace_bytes(int B, int T, int Hq, int D);
+void sink_bwd_workspace(SinkBwdParams &p, int D, void *workspace);
+cudaError_t launch_sink_bwd(int D, const SinkBwdMaps &maps, const SinkBwdParams &p, cudaStream_t stream);
+cudaError_t launch_sink_dkv(int D, const SinkBwdMaps &maps, const SinkBwdParams &p, cudaStream_t stream);
 // a layer's gradient, both streams: p the base stream, pc the copies (pc.k16 = p.k16; maps and
 // mapsc as above for each stream, mapsc's fp16-K maps over p.k16); dK / dV written once
 cudaError_t launch_attn_bwd_layer(int D, int G, const AttnBwdParams &p, const AttnBwdParams &pc,

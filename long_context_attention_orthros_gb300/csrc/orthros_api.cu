@@ -7,6 +7,7 @@
 #include <mutex>
 
 #include "serve.cuh"
+#include "tree.cuh"
 
 namespace {
 
@@ -207,7 +208,7 @@ orthros_status swa_fwd_impl(const orthros_bf16 *q_raw, const orthros_bf16 *k, co
                             const float *alpha, const float *beta, orthros_bf16 *o, float *lse, int B, int T, int Hq,
                             int Hkv, int d, int window, float scale, int64_t q_bstride, int64_t kv_bstride,
                             int64_t o_bstride, int row_begin, int row_end, int32_t *dev_err, void *stream,
-                            int sm_reserve = 0)
+                            int sm_reserve = 0, int sinks = 0)
 {
     CUtensorMap maps[4];
     SwaParams p;
@@ -216,6 +217,7 @@ orthros_status swa_fwd_impl(const orthros_bf16 *q_raw, const orthros_bf16 *k, co
                                         kv_bstride, o_bstride, row_begin, row_end, dev_err, maps, p, &empty);
     if (st != ORTHROS_OK || empty)
         return st;
+    p.sinks = sinks;
     const int sms = num_sms() - sm_reserve;  // the persistent kernel's CTAs
     if (sms <= 0)
         return ORTHROS_ERR_CUDA;
@@ -255,6 +257,21 @@ orthros_status orthros_swa_fwd(const orthros_bf16 *q_raw, const orthros_bf16 *k,
 {
     return orthros_swa_fwd_rows(q_raw, k, v, alpha, beta, o, B, T, Hq, Hkv, d, window, scale, q_bstride, kv_bstride,
                                 o_bstride, 0, T < 1 ? 0 : T, dev_err, stream);
+}
+
+orthros_status orthros_swa_sink_fwd(const orthros_bf16 *q_raw, const orthros_bf16 *k, const orthros_bf16 *v,
+                                    const float *alpha, const float *beta, orthros_bf16 *o, float *lse, int B, int T,
+                                    int Hq, int Hkv, int d, int window, int sinks, float scale, int64_t q_bstride,
+                                    int64_t kv_bstride, int64_t o_bstride, int row_begin, int row_end,
+                                    int32_t *dev_err, void *stream)
+{
+    if (sinks < 0 || (lse != nullptr && !aligned16(lse)))
+        return ORTHROS_ERR_INVALID_ARG;
+    if (sinks > orthros::SWA_MAX_SINKS)
+        return ORTHROS_ERR_UNSUPPORTED;
+    // a window over the whole sequence leaves nothing to the sinks
+    return swa_fwd_impl(q_raw, k, v, alpha, beta, o, lse, B, T, Hq, Hkv, d, window, scale, q_bstride, kv_bstride,
+                        o_bstride, row_begin, row_end, dev_err, stream, 0, window < T ? sinks : 0);
 }
 
 size_t orthros_xattn_workspace_size(int B, int T_out, int T_kv, int Hq, int Hkv, int d)
@@ -568,6 +585,64 @@ orthros_status orthros_swa_bwd(const orthros_bf16 *q_raw, const orthros_bf16 *k,
     if (!bwd_maps(maps, q_raw, dO, k, v, p.k16, p.q16, d, Hq, Hkv, T, T, B, dq_raw))
         return ORTHROS_ERR_CUDA;
     const cudaError_t e = orthros::launch_attn_bwd(d, Hq / Hkv, p, maps, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
+}
+
+size_t orthros_swa_sink_bwd_workspace_size(int B, int T, int Hq, int Hkv, int d)
+{
+    if (B < 1 || T < 1 || (d != 64 && d != 128) || !heads_ok(Hq, Hkv) || static_cast<long long>(B) * Hq > 65535)
+        return 0;
+    return orthros::sink_bwd_workspace_bytes(B, T, Hq, d);
+}
+
+orthros_status orthros_swa_sink_bwd(const orthros_bf16 *q_raw, const orthros_bf16 *k, const orthros_bf16 *v,
+                                    const float *alpha, const float *beta, const orthros_bf16 *o,
+                                    const orthros_bf16 *dO, const float *lse, float *dq_raw, float *dk, float *dv,
+                                    float *dalpha, float *dbeta, int B, int T, int Hq, int Hkv, int d, int window,
+                                    int sinks, float scale, void *workspace, size_t ws_bytes, int32_t *dev_err,
+                                    void *stream)
+{
+    if (!aligned16(q_raw) || !aligned16(k) || !aligned16(v) || !aligned16(alpha) || !aligned16(beta) ||
+        !aligned16(o) || !aligned16(dO) || !aligned16(lse) || !aligned16(dq_raw) || !aligned16(dk) || !aligned16(dv) ||
+        !aligned16(dalpha) || !aligned16(dbeta) || B < 1 || T < 1 || window < 1 || sinks < 0 || !std::isfinite(scale))
+        return ORTHROS_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || !heads_ok(Hq, Hkv) || sinks > orthros::SWA_MAX_SINKS)
+        return ORTHROS_ERR_UNSUPPORTED;
+    if (static_cast<long long>(B) * Hq > 65535)
+        return ORTHROS_ERR_INVALID_ARG;
+    if (!aligned16(workspace) || ws_bytes < orthros::sink_bwd_workspace_bytes(B, T, Hq, d))
+        return ORTHROS_ERR_WORKSPACE;
+    orthros::SinkBwdParams p{};
+    p.q = q_raw;
+    p.k = k;
+    p.v = v;
+    p.o = o;
+    p.dO = dO;
+    p.alpha = alpha;
+    p.beta = beta;
+    p.lse_in = lse;
+    p.dq = dq_raw;
+    p.dk = dk;
+    p.dv = dv;
+    p.dalpha = dalpha;
+    p.dbeta = dbeta;
+    p.dev_err = dev_err;
+    p.B = B;
+    p.T = T;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.window = window;
+    p.sinks = sinks;
+    p.scale = scale;
+    orthros::sink_bwd_workspace(p, d, workspace);
+    orthros::SinkBwdMaps m;
+    const int G = Hq / Hkv;
+    const long long qs = static_cast<long long>(T) * Hq * d, ks = static_cast<long long>(T) * Hkv * d;
+    if (!make_map(&m.q_hi, p.q_hi, d, Hq, T, B, qs, G, 64 / G) || !make_map(&m.q_lo, p.q_lo, d, Hq, T, B, qs, G, 64 / G) ||
+        !make_map(&m.dO, dO, d, Hq, T, B, qs, G, 64 / G) || !make_map(&m.k, k, d, Hkv, T, B, ks, 1, 128) ||
+        !make_map(&m.v, v, d, Hkv, T, B, ks, 1, 128))
+        return ORTHROS_ERR_CUDA;
+    const cudaError_t e = orthros::launch_sink_bwd(d, m, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
 }
 
@@ -998,6 +1073,105 @@ orthros_status orthros_xattn_prefix_fwd(const orthros_bf16 *qc_raw, const int32_
         !make_map(&m[2], k_prefix, d, Hkv, P, 1, ps, 1, 64) || !make_map(&m[3], v_prefix, d, Hkv, P, 1, ps, 1, 64))
         return ORTHROS_ERR_CUDA;
     const cudaError_t e = orthros::launch_xattn_prefix(d, m, p, P, workspace, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
+}
+
+}  // extern "C"
+
+namespace {
+
+bool tree_sizes_ok(int B, int N, int L_max, int Hkv)
+{
+    return B >= 1 && N >= 1 && L_max >= 1 && L_max < 0x7fffffff - orthros::TREE_MAX_NODES &&
+           static_cast<long long>(B) * Hkv <= 65535;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t orthros_decode_tree_workspace_size(int B, int N, int L_max, int Hq, int Hkv, int d)
+{
+    if ((d != 64 && d != 128) || !heads_ok(Hq, Hkv) || !tree_sizes_ok(B, N, L_max, Hkv) || N > orthros::TREE_MAX_NODES)
+        return 0;
+    return orthros::tree_workspace_bytes(B, N, L_max, Hq, Hkv, d);
+}
+
+orthros_status orthros_decode_tree(const orthros_bf16 *q_new, const orthros_bf16 *qc_new, const orthros_bf16 *k_new,
+                                   const orthros_bf16 *v_new, const int32_t *parent, const int32_t *nodes,
+                                   const orthros_bf16 *k_cache, const orthros_bf16 *v_cache,
+                                   const int32_t *cache_len, int L_max, const float *alpha, const float *beta,
+                                   const float *alpha_c, const float *beta_c, orthros_bf16 *o, orthros_bf16 *oc,
+                                   int B, int N, int Hq, int Hkv, int d, int window, int sinks, float scale,
+                                   void *workspace, size_t ws_bytes, int32_t *dev_err, void *stream)
+{
+    if (!aligned16(q_new) || !aligned16(qc_new) || !aligned16(k_new) || !aligned16(v_new) || !parent ||
+        !aligned16(k_cache) || !aligned16(v_cache) || !cache_len || !aligned16(alpha) || !aligned16(beta) ||
+        !aligned16(alpha_c) || !aligned16(beta_c) || !aligned16(o) || !aligned16(oc) || window < 1 || sinks < 0 ||
+        !std::isfinite(scale))
+        return ORTHROS_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || !heads_ok(Hq, Hkv) || N > orthros::TREE_MAX_NODES || sinks > orthros::TREE_MAX_SINKS)
+        return ORTHROS_ERR_UNSUPPORTED;
+    if (!tree_sizes_ok(B, N, L_max, Hkv))
+        return ORTHROS_ERR_INVALID_ARG;
+    const size_t need = orthros::tree_workspace_bytes(B, N, L_max, Hq, Hkv, d);
+    if (!workspace || ws_bytes < need || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
+        return ORTHROS_ERR_WORKSPACE;
+    orthros::TreeParams p{};
+    p.q_new = q_new;
+    p.qc_new = qc_new;
+    p.parent = parent;
+    p.nodes = nodes;
+    p.cache_len = cache_len;
+    p.alpha = alpha;
+    p.beta = beta;
+    p.alpha_c = alpha_c;
+    p.beta_c = beta_c;
+    p.o = o;
+    p.oc = oc;
+    p.dev_err = dev_err;
+    p.B = B;
+    p.N = N;
+    p.Hq = Hq;
+    p.Hkv = Hkv;
+    p.L_max = L_max;
+    p.window = window;
+    p.sinks = sinks;
+    p.qscale = scale * kLog2e;
+    orthros::TreeMaps m;
+    const long long cs = static_cast<long long>(L_max) * Hkv * d, ns = static_cast<long long>(N) * Hkv * d;
+    if (!make_map(&m.k, k_cache, d, Hkv, L_max, B, cs, 1, 64) || !make_map(&m.v, v_cache, d, Hkv, L_max, B, cs, 1, 64) ||
+        !make_map(&m.kt, k_new, d, Hkv, N, B, ns, 1, 64) || !make_map(&m.vt, v_new, d, Hkv, N, B, ns, 1, 64))
+        return ORTHROS_ERR_CUDA;
+    const cudaError_t e = orthros::launch_tree(d, m, p, workspace, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
+}
+
+orthros_status orthros_decode_tree_accept(const orthros_bf16 *k_new, const orthros_bf16 *v_new, const int32_t *parent,
+                                          const int32_t *node, orthros_bf16 *k_cache, orthros_bf16 *v_cache,
+                                          int32_t *cache_len, int L_max, int32_t *path, int B, int N, int Hkv, int d,
+                                          int32_t *dev_err, void *stream)
+{
+    if (!aligned16(k_new) || !aligned16(v_new) || !parent || !node || !aligned16(k_cache) || !aligned16(v_cache) ||
+        !cache_len || !path || Hkv < 1 || !tree_sizes_ok(B, N, L_max, Hkv))
+        return ORTHROS_ERR_INVALID_ARG;
+    if ((d != 64 && d != 128) || N > orthros::TREE_MAX_NODES)
+        return ORTHROS_ERR_UNSUPPORTED;
+    orthros::TreeAcceptParams p{};
+    p.k_new = k_new;
+    p.v_new = v_new;
+    p.parent = parent;
+    p.node = node;
+    p.k_cache = k_cache;
+    p.v_cache = v_cache;
+    p.cache_len = cache_len;
+    p.path = path;
+    p.dev_err = dev_err;
+    p.B = B;
+    p.N = N;
+    p.L_max = L_max;
+    p.row = Hkv * d;
+    const cudaError_t e = orthros::launch_tree_accept(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
 }
 

@@ -1,0 +1,329 @@
+// sink_dkv.cu -- dk, dv of the base stream's window (row t, keys t - window < j <= t) in fp32, for the gradient with
+// sinks (sink_bwd.cu), on the 5th-generation tensor cores.  Without sinks in the window's part it is the gradient of
+// Eq. (4): the log-sum-exp and D = dO . o of the joint softmax are given.
+//
+// A CTA owns 128 keys of one (sequence, KV head): the MMA's M side, K and V resident in shared memory.  The query rows
+// that can see them stream through a ring in rounds of 64 (64/G tokens x G heads): q's bf16 high part and residual
+// and dO.  Per round
+//   S^T = K q^T (both parts), dP^T = V dO^T                      fp32 in tensor memory, two buffers each
+//   P^T = exp2(S^T c - lse), dS^T = P^T (dP^T - D)               as a bf16 high part and residual each, over S^T, dP^T
+//   dV += P^T dO (two products), dK += dS^T q (three: the residuals' product is below fp32's rounding here)
+// Two warpgroups take 32 rows (columns) of the round each, so that a round's exponentials end while the next
+// round's S^T, dP^T run.
+// Bound by the MMAs: 44 a round of 16 x (64 or 128) x 128, some 2050 cycles at d = 128.
+// Roles (384 threads, one CTA an SM): warp 0 TMA producer; warp 1 tensor memory and MMA issue; warps 2-3 the rows'
+// log-sum-exp, D and token; warps 4-7, 8-11 P^T, dS^T (lane = key) of columns 0-31, 32-63, and at the end dK, dV.
+// Tensor memory: S^T at 64 u, dP^T at 128 + 64 u (buffer u), dK at 256, dV at 256 + D.  Every wait is bounded.
+#include "bwd_util.cuh"
+#include "kernels.cuh"
+#include "serve.cuh"
+#include "tc.cuh"
+#include "xattn.cuh"
+
+namespace orthros {
+
+namespace {
+
+template <int D>
+struct SdCfg {
+    static constexpr int KEYS = 128, RB = 64;
+    static constexpr int SLABS = D / 64;
+    static constexpr int STG = 3;
+    static constexpr int KSLAB = KEYS * 128;  // one 64-wide slab of the K (or V) tile
+    static constexpr int RSLAB = RB * 128;    // one 64-wide slab of a row tile
+    static constexpr int TILE = SLABS * RSLAB;
+    static constexpr int K_OFF = 0;
+    static constexpr int V_OFF = K_OFF + SLABS * KSLAB;
+    static constexpr int ST_OFF = V_OFF + SLABS * KSLAB;  // [STG]: q high part, q residual, dO
+    static constexpr int ST_BYTES = 3 * TILE;
+    static constexpr int META_OFF = ST_OFF + STG * ST_BYTES;  // [STG][3][RB]: lse, D, token
+    static constexpr int BAR_OFF = META_OFF + STG * 3 * RB * 4;
+    static constexpr int NBARS = 1 + 3 * STG + 3 * 2 + 1;
+    static constexpr int HOLD_OFF = BAR_OFF + NBARS * 8;
+    static constexpr int USED = HOLD_OFF + 16 + 1024;
+    static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;  // one CTA an SM: it takes all of tensor memory
+    static_assert(SMEM <= 232448, "shared memory budget");
+    static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DK = 256, TM_DV = 256 + D;
+    static constexpr int THREADS = 384;
+};
+
+template <int D, int G>
+__global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_constant__ SinkBwdMaps maps, const SinkBwdParams p)
+{
+    using C = SdCfg<D>;
+    constexpr int TOK = C::RB / G;  // tokens of a round
+    extern __shared__ uint8_t smem_raw[];
+    uint8_t *smem = align1024(smem_raw);
+    const uint32_t sbase = smem_u32(smem);
+    uint64_t *kv_full = reinterpret_cast<uint64_t *>(smem + C::BAR_OFF);  // K, V landed
+    uint64_t *st_full = kv_full + 1;              // [STG] row tiles landed
+    uint64_t *meta_full = st_full + C::STG;       // [STG] the rows' numbers staged
+    uint64_t *st_empty = meta_full + C::STG;      // [STG] round's MMAs done with the stage
+    uint64_t *s_full = st_empty + C::STG;         // [2] S^T, dP^T of a round complete
+    uint64_t *p_full = s_full + 2;                // [2] P^T, dS^T written
+    uint64_t *pv_done = s_full + 4;               // [2] dV, dK of a round complete
+    uint64_t *acc_final = s_full + 6;             // of the last round
+    uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::HOLD_OFF);
+    float *meta = reinterpret_cast<float *>(smem + C::META_OFF);
+
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int kt0 = blockIdx.x * C::KEYS, bh = blockIdx.y, b = bh / p.Hkv, g = bh % p.Hkv;
+    // rounds r: tokens r TOK ..; from the first that sees the tile to the last
+    const int r0 = kt0 / TOK;
+    const long long end = static_cast<long long>(kt0) + C::KEYS - 1 + p.window;  // tokens below this one
+    const int r1 = static_cast<int>(((end < p.T ? end : p.T) + TOK - 1) / TOK);
+    const int rounds = r1 - r0;  // at least 1
+
+    __shared__ volatile int s_abort;  // a wait has given up
+    if (threadIdx.x == 0) {
+        s_abort = 0;
+        mbar_init(kv_full, 1);
+        for (int s = 0; s < C::STG; ++s) {
+            mbar_init(&st_full[s], 1);
+            mbar_init(&meta_full[s], 2);
+            mbar_init(&st_empty[s], 1);
+        }
+        for (int u = 0; u < 2; ++u) {
+            mbar_init(&s_full[u], 1);
+            mbar_init(&p_full[u], 8);
+            mbar_init(&pv_done[u], 1);
+        }
+        mbar_init(acc_final, 1);
+        fence_barrier_init();
+    }
+    if (warp == 1)
+        tmem_alloc(tmem_holder, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tbase = *tmem_holder;
+    bool ok = true;
+
+    if (warp == 0) {
+        // ------------------------------------------------------------------ producer
+        if (lane == 0) {
+            mbar_arrive_expect_tx(kv_full, 2 * C::SLABS * C::KSLAB);
+#pragma unroll
+            for (int sl = 0; sl < C::SLABS; ++sl) {
+                tma_load_4d(smem + C::K_OFF + sl * C::KSLAB, &maps.k, kv_full, sl * 64, g, kt0, b);
+                tma_load_4d(smem + C::V_OFF + sl * C::KSLAB, &maps.v, kv_full, sl * 64, g, kt0, b);
+            }
+            for (int i = 0; i < rounds; ++i) {
+                const int s = i % C::STG, t0 = (r0 + i) * TOK;
+                if ((i >= C::STG && !mbar_wait(&st_empty[s], static_cast<uint32_t>((i / C::STG - 1) & 1))) || s_abort) {
+                    ok = false;
+                    break;
+                }
+                uint8_t *st = smem + C::ST_OFF + s * C::ST_BYTES;
+                mbar_arrive_expect_tx(&st_full[s], C::ST_BYTES);
+#pragma unroll
+                for (int sl = 0; sl < C::SLABS; ++sl) {
+                    tma_load_4d(st + sl * C::RSLAB, &maps.q_hi, &st_full[s], sl * 64, g * G, t0, b);
+                    tma_load_4d(st + C::TILE + sl * C::RSLAB, &maps.q_lo, &st_full[s], sl * 64, g * G, t0, b);
+                    tma_load_4d(st + 2 * C::TILE + sl * C::RSLAB, &maps.dO, &st_full[s], sl * 64, g * G, t0, b);
+                }
+            }
+        }
+    } else if (warp == 1) {
+        // ------------------------------------------------------------------ MMA issuer
+        if (lane == 0) {
+            constexpr uint32_t IDESC_S = umma_idesc(128, C::RB, true, false);
+            constexpr uint32_t IDESC_D = umma_idesc(128, D, true, true);
+            const uint64_t kdesc = umma_desc_sw128(sbase + C::K_OFF, 16, 1024);
+            const uint64_t vdesc = umma_desc_sw128(sbase + C::V_OFF, 16, 1024);
+            // dV += P^T dO and dK += dS^T q of round j; 16 rows of P^T (dS^T) are 8 columns of its half's high
+            // parts, or of the residuals 16 columns further
+            auto accumulate = [&](int j) -> bool {
+                const int u = j & 1, s = j % C::STG;
+                if (!mbar_wait(&p_full[u], static_cast<uint32_t>((j >> 1) & 1)))
+                    return false;
+                tc_fence_after();
+                const uint32_t st = sbase + C::ST_OFF + s * C::ST_BYTES;
+                const uint64_t hdesc = umma_desc_sw128(st, C::RSLAB, 1024);
+                const uint64_t ldesc = umma_desc_sw128(st + C::TILE, C::RSLAB, 1024);
+                const uint64_t odesc = umma_desc_sw128(st + 2 * C::TILE, C::RSLAB, 1024);
+#pragma unroll
+                for (int kk = 0; kk < C::RB / 16; ++kk) {
+                    const uint32_t acc = (j > 0 || kk > 0) ? 1u : 0u;
+                    const uint64_t at = static_cast<uint64_t>(kk * (2048 >> 4));
+                    const uint32_t ph = tbase + C::TM_S + 64 * u + 32 * (kk >> 1) + 8 * (kk & 1);
+                    const uint32_t sh = ph + (C::TM_DP - C::TM_S);
+                    umma_ts(tbase + C::TM_DV, ph, odesc + at, IDESC_D, acc);
+                    umma_ts(tbase + C::TM_DV, ph + 16, odesc + at, IDESC_D, 1);
+                    umma_ts(tbase + C::TM_DK, sh, hdesc + at, IDESC_D, acc);
+                    umma_ts(tbase + C::TM_DK, sh + 16, hdesc + at, IDESC_D, 1);
+                    umma_ts(tbase + C::TM_DK, sh, ldesc + at, IDESC_D, 1);
+                }
+                // no commit that nothing waits for: round j + 2 waits for pv_done
+                if (j == rounds - 1)
+                    umma_commit(acc_final);
+                else if (j + 2 < rounds)
+                    umma_commit(&pv_done[u]);
+                if (j + C::STG < rounds)  // the producer waits for it
+                    umma_commit(&st_empty[s]);
+                return true;
+            };
+            ok = mbar_wait(kv_full, 0);
+            for (int i = 0; ok && i < rounds; ++i) {
+                const int s = i % C::STG, u = i & 1;
+                // S^T / dP^T buffer u is free once dV, dK of round i - 2 have read P^T, dS^T from it
+                if (!(ok = mbar_wait(&st_full[s], static_cast<uint32_t>((i / C::STG) & 1)) &&
+                           (i < 2 || mbar_wait(&pv_done[u], static_cast<uint32_t>(((i - 2) >> 1) & 1)))))
+                    break;
+                tc_fence_after();
+                const uint32_t st = sbase + C::ST_OFF + s * C::ST_BYTES;
+                const uint64_t hdesc = umma_desc_sw128(st, 16, 1024), ldesc = umma_desc_sw128(st + C::TILE, 16, 1024);
+                const uint64_t odesc = umma_desc_sw128(st + 2 * C::TILE, 16, 1024);
+#pragma unroll
+                for (int kk = 0; kk < D / 16; ++kk) {
+                    const uint32_t ko = static_cast<uint32_t>((kk >> 2) * C::KSLAB + (kk & 3) * 32) >> 4;
+                    const uint32_t ro = static_cast<uint32_t>((kk >> 2) * C::RSLAB + (kk & 3) * 32) >> 4;
+                    umma_ss(tbase + C::TM_S + 64 * u, kdesc + ko, hdesc + ro, IDESC_S, kk != 0);
+                    umma_ss(tbase + C::TM_S + 64 * u, kdesc + ko, ldesc + ro, IDESC_S, 1);
+                    umma_ss(tbase + C::TM_DP + 64 * u, vdesc + ko, odesc + ro, IDESC_S, kk != 0);
+                }
+                umma_commit(&s_full[u]);
+                if (i >= 1)
+                    ok = accumulate(i - 1);
+            }
+            ok = ok && accumulate(rounds - 1) && mbar_wait(acc_final, 0);
+        }
+    } else if (warp < 4) {
+        // ------------------------------------------------------------------ the rows' numbers
+        const int ct = threadIdx.x - 64;  // 0..63: one row of the round each
+        for (int i = 0; ok && i < rounds; ++i) {
+            const int s = i % C::STG, t = (r0 + i) * TOK + ct / G;
+            float m_lse = 0.f, m_d = 0.f;
+            if (t < p.T) {
+                const long long ri = (static_cast<long long>(b) * p.T + t) * p.Hq + g * G + ct % G;
+                m_lse = p.lse[ri];
+                m_d = p.Drow[ri];
+            }
+            // the place is free once the stage of this round has landed: its producer waited for the MMAs of round
+            // i - STG, which waited for that round's softmax
+            if (!(ok = warp_wait(&st_full[s], static_cast<uint32_t>((i / C::STG) & 1))))
+                break;
+            float *m = meta + s * 3 * C::RB;
+            m[ct] = m_lse;
+            m[C::RB + ct] = m_d;
+            m[2 * C::RB + ct] = __int_as_float(t < p.T ? t : -1);
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&meta_full[s]);
+        }
+    } else {
+        // ------------------------------------------------------------------ P^T, dS^T, then dK, dV
+        const int rw = warp & 3, half = (warp - 4) >> 2;
+        const int key = kt0 + rw * 32 + lane;
+        const uint32_t tl = tbase + (static_cast<uint32_t>(rw * 32) << 16);
+        const float c2 = p.scale * kLog2eF;
+        for (int i = 0; i < rounds; ++i) {
+            const int s = i % C::STG, u = i & 1;
+            if (!(ok = warp_wait(&s_full[u], static_cast<uint32_t>((i >> 1) & 1)) &&
+                       warp_wait(&meta_full[s], static_cast<uint32_t>((i / C::STG) & 1))))
+                break;
+            tc_fence_after();
+            const float *m = meta + s * 3 * C::RB + 32 * half;
+            const uint32_t s_at = tl + C::TM_S + 64 * u + 32 * half, d_at = tl + C::TM_DP + 64 * u + 32 * half;
+            uint32_t sv[32], dv[32];
+            tmem_ld32(s_at, sv);
+            tmem_ld32(d_at, dv);
+            tmem_wait_ld();
+            uint32_t ph[16], pl[16], sh[16], sl[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                float pr[2], ds[2];
+#pragma unroll
+                for (int q = 0; q < 2; ++q) {
+                    const int c = 2 * e + q, t = __float_as_int(m[2 * C::RB + c]);
+                    const bool seen = key <= t && key > t - p.window;  // t = -1: none
+                    const float x = fast_exp2(__uint_as_float(sv[c]) * c2 - m[c]);
+                    pr[q] = seen ? x : 0.f;
+                    ds[q] = seen ? x * (__uint_as_float(dv[c]) - m[C::RB + c]) : 0.f;
+                }
+                split_q_pair(pr[0], pr[1], ph[e], pl[e]);
+                split_q_pair(ds[0], ds[1], sh[e], sl[e]);
+            }
+            tmem_st16(s_at, ph);
+            tmem_st16(s_at + 16, pl);
+            tmem_st16(d_at, sh);
+            tmem_st16(d_at + 16, sl);
+            tmem_wait_st();
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0)
+                mbar_arrive(&p_full[u]);
+        }
+        // dK (scaled) by the first group, dV by the second
+        if (ok && (ok = warp_wait(acc_final, 0))) {
+            tc_fence_after();
+            const float f = half ? 1.f : p.scale;
+            float *dst = (half ? p.dv : p.dk) + ((static_cast<long long>(b) * p.T + key) * p.Hkv + g) * D;
+#pragma unroll 1
+            for (int c = 0; c < D; c += 32) {
+                uint32_t w[32];
+                tmem_ld32(tl + (half ? C::TM_DV : C::TM_DK) + c, w);
+                tmem_wait_ld();
+                if (key < p.T) {
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4)
+                        *reinterpret_cast<uint4 *>(dst + c + e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+                }
+            }
+        }
+    }
+    if (!ok) {
+        s_abort = 1;
+        if (lane == 0)
+            record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (s_abort) {
+        drain_in_flight();
+        __syncthreads();
+    }
+    if (warp == 1) {
+        tc_fence_after();
+        tmem_dealloc(tbase, 512);
+    }
+}
+
+template <int D, int G>
+cudaError_t launch_dkv(const SinkBwdMaps &maps, const SinkBwdParams &p, cudaStream_t stream)
+{
+    using C = SdCfg<D>;
+    auto kern = sink_dkv_tc_kernel<D, G>;
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    if (e != cudaSuccess)
+        return e;
+    kern<<<dim3((p.T + C::KEYS - 1) / C::KEYS, p.B * p.Hkv), C::THREADS, C::SMEM, stream>>>(maps, p);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+cudaError_t launch_sink_dkv(int D, const SinkBwdMaps &maps, const SinkBwdParams &p, cudaStream_t stream)
+{
+    const int G = p.Hq / p.Hkv;
+#define ORTHROS_DKV_CASE(DD, GG) \
+    if (D == DD && G == GG)      \
+        return launch_dkv<DD, GG>(maps, p, stream);
+    ORTHROS_DKV_CASE(128, 1)
+    ORTHROS_DKV_CASE(128, 2)
+    ORTHROS_DKV_CASE(128, 4)
+    ORTHROS_DKV_CASE(128, 8)
+    ORTHROS_DKV_CASE(128, 16)
+    ORTHROS_DKV_CASE(64, 1)
+    ORTHROS_DKV_CASE(64, 2)
+    ORTHROS_DKV_CASE(64, 4)
+    ORTHROS_DKV_CASE(64, 8)
+    ORTHROS_DKV_CASE(64, 16)
+#undef ORTHROS_DKV_CASE
+    return cudaErrorInvalidValue;
+}
+
+}  // namespace orthros

@@ -58,6 +58,13 @@ struct WarpB16 {
     template <int KT>
     __device__ __forceinline__ void step(uint32_t kbase, uint32_t vbase, int slab, int r0, bool whole, int lo, int hi)
     {
+        step_where<KT>(kbase, vbase, slab, r0, whole, [=](int x, int, int) { return x >= lo && x <= hi; });
+    }
+
+    // The same; unless whole, key x counts for this lane's query row 8 nt + 2 (lane % 4) + i iff counts(x, nt, i).
+    template <int KT, class F>
+    __device__ __forceinline__ void step_where(uint32_t kbase, uint32_t vbase, int slab, int r0, bool whole, F counts)
+    {
         const int lane = threadIdx.x & 31, gq = lane >> 2;
         const float NEG_INF = -__int_as_float(0x7f800000);
         const int ka_row = r0 + (lane & 7) + (((lane >> 3) & 1) << 3), ka_hi = lane >> 4;
@@ -93,7 +100,7 @@ struct WarpB16 {
                     s[j][nt][e] += s2[j][nt][e];
                     if (!whole) {
                         const int x = r0 + 16 * j + gq + 8 * (e >> 1);
-                        if (x < lo || x > hi)
+                        if (!counts(x, nt, e & 1))
                             s[j][nt][e] = NEG_INF;
                     }
                     raise |= s[j][nt][e] > m[nt][e & 1] + 8.f;
