@@ -139,6 +139,11 @@ bool swa_tc_supported(int D, int G, int window);
 cudaError_t launch_swa_tc(int D, int G, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                           const CUtensorMap &o, const SwaParams &p, int num_sms, cudaStream_t stream);
 
+// the same with p.sinks > 0
+bool swa_sink_tc_supported(int D, int G, int window);
+cudaError_t launch_swa_sink_tc(int D, int G, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                               const SwaParams &p, int num_sms, cudaStream_t stream);
+
 size_t xattn_workspace_bytes(int B, int T_out, int T_kv, int Hq, int Hkv, int D);
 // ctas > 0: at most 8 copy rows per (batch, KV head) run on exactly `ctas` CTAs of one SM each
 cudaError_t launch_xattn(int D, const CUtensorMap &k, const CUtensorMap &v, XattnParams p, void *workspace,

@@ -64,6 +64,7 @@ __global__ void __launch_bounds__(256) sink_rows_kernel(const SinkBwdParams p)
 
 constexpr int DQ_ROWS = 64;  // query rows of a CTA: 64 / G tokens x G heads
 constexpr int DQ_KEYS = 64;  // keys of a streamed block
+constexpr int DQ_RUN = 32;   // blocks that dq is summed over in the MMA's accumulators (256 steps: some 4e-6)
 
 template <int D, int G>
 __global__ void __launch_bounds__(128) sink_dq_kernel(const SinkBwdParams p)
@@ -203,6 +204,20 @@ __global__ void __launch_bounds__(128) sink_dq_kernel(const SinkBwdParams p)
             }
         }
         __syncthreads();  // the slot is refilled by the next iteration's prefetch
+        // the MMA's accumulators are truncated at every step: a long run of keys is summed up in memory
+        if (i % DQ_RUN == DQ_RUN - 1 && i < nblk - 1) {
+#pragma unroll
+            for (int half = 0; half < 2; ++half)
+                if (half ? vB : vA) {
+                    float *to = p.dq + (half ? rB : rA) * D + qd;
+#pragma unroll
+                    for (int e = 0; e < D / 8; ++e) {
+                        float2 y = i < DQ_RUN ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2 *>(to + 8 * e);
+                        *reinterpret_cast<float2 *>(to + 8 * e) = make_float2(y.x + st.o[e][2 * half], y.y + st.o[e][2 * half + 1]);
+                    }
+                }
+            st.reset();
+        }
     }
     // dq = scale dQ; dq_raw = dq alpha; dalpha += x dq, dbeta += dq
 #pragma unroll
@@ -214,7 +229,8 @@ __global__ void __launch_bounds__(128) sink_dq_kernel(const SinkBwdParams p)
 #pragma unroll
         for (int i = 0; i < D / 8; ++i) {
             const int dcol = i * 8 + qd;
-            const float dq0 = st.o[i][2 * half] * p.scale, dq1 = st.o[i][2 * half + 1] * p.scale;
+            float2 y = nblk > DQ_RUN ? *reinterpret_cast<const float2 *>(p.dq + off + dcol) : make_float2(0.f, 0.f);
+            const float dq0 = (y.x + st.o[i][2 * half]) * p.scale, dq1 = (y.y + st.o[i][2 * half + 1]) * p.scale;
             const float2 al = __ldg(reinterpret_cast<const float2 *>(p.alpha + h * D + dcol));
             *reinterpret_cast<float2 *>(p.dq + off + dcol) = make_float2(dq0 * al.x, dq1 * al.y);
             const float2 x = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(p.q + off + dcol));
@@ -390,11 +406,12 @@ __global__ void __launch_bounds__(2 * D) sink_join_kernel(const SinkBwdParams p,
 
 // ------------------------------------------------------------------ host side
 
-// four waves of two CTAs on each of 152 SMs, 64 tokens a CTA at least
+// four waves of two CTAs on each of 152 SMs, from 64 tokens a CTA to 4096 (64 a warp's step: the accumulators are
+// truncated at each)
 int sink_chunks(int B, int T, int Hq)
 {
-    const int most = (T + 63) / 64, want = 1216 / (B * Hq) < 1 ? 1 : 1216 / (B * Hq);
-    return want < most ? want : most;
+    const int most = (T + 63) / 64, least = (T + 4095) / 4096, want = 1216 / (B * Hq);
+    return want < least ? least : (want < most ? want : most);
 }
 
 template <int D, int G>

@@ -8,6 +8,8 @@
 //   S^T = K q^T (both parts), dP^T = V dO^T                      fp32 in tensor memory, two buffers each
 //   P^T = exp2(S^T c - lse), dS^T = P^T (dP^T - D)               as a bf16 high part and residual each, over S^T, dP^T
 //   dV += P^T dO (two products), dK += dS^T q (three: the residuals' product is below fp32's rounding here)
+// The MMA's fp32 accumulators are truncated at every step, not rounded: dk of 4800 rows a key (1284 steps) came out
+// 1.9e-5 off.  So every 24 rounds (1536 rows, 288 steps) dV and dK are added to memory and begin anew.
 // Two warpgroups take 32 rows (columns) of the round each, so that a round's exponentials end while the next
 // round's S^T, dP^T run.
 // Bound by the MMAs: 44 a round of 16 x (64 or 128) x 128, some 2050 cycles at d = 128.
@@ -29,6 +31,7 @@ struct SdCfg {
     static constexpr int KEYS = 128, RB = 64;
     static constexpr int SLABS = D / 64;
     static constexpr int STG = 3;
+    static constexpr int RUN = 24;            // rounds that dK, dV are summed over in tensor memory
     static constexpr int KSLAB = KEYS * 128;  // one 64-wide slab of the K (or V) tile
     static constexpr int RSLAB = RB * 128;    // one 64-wide slab of a row tile
     static constexpr int TILE = SLABS * RSLAB;
@@ -38,7 +41,7 @@ struct SdCfg {
     static constexpr int ST_BYTES = 3 * TILE;
     static constexpr int META_OFF = ST_OFF + STG * ST_BYTES;  // [STG][3][RB]: lse, D, token
     static constexpr int BAR_OFF = META_OFF + STG * 3 * RB * 4;
-    static constexpr int NBARS = 1 + 3 * STG + 3 * 2 + 1;
+    static constexpr int NBARS = 1 + 3 * STG + 3 * 2 + 2;
     static constexpr int HOLD_OFF = BAR_OFF + NBARS * 8;
     static constexpr int USED = HOLD_OFF + 16 + 1024;
     static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;  // one CTA an SM: it takes all of tensor memory
@@ -62,7 +65,8 @@ __global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_consta
     uint64_t *s_full = st_empty + C::STG;         // [2] S^T, dP^T of a round complete
     uint64_t *p_full = s_full + 2;                // [2] P^T, dS^T written
     uint64_t *pv_done = s_full + 4;               // [2] dV, dK of a round complete
-    uint64_t *acc_final = s_full + 6;             // of the last round
+    uint64_t *acc_final = s_full + 6;             // of a run's last round
+    uint64_t *acc_free = s_full + 7;              // a run's dK, dV read out of tensor memory
     uint32_t *tmem_holder = reinterpret_cast<uint32_t *>(smem + C::HOLD_OFF);
     float *meta = reinterpret_cast<float *>(smem + C::META_OFF);
 
@@ -89,6 +93,7 @@ __global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_consta
             mbar_init(&pv_done[u], 1);
         }
         mbar_init(acc_final, 1);
+        mbar_init(acc_free, 8);
         fence_barrier_init();
     }
     if (warp == 1)
@@ -135,7 +140,8 @@ __global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_consta
             // parts, or of the residuals 16 columns further
             auto accumulate = [&](int j) -> bool {
                 const int u = j & 1, s = j % C::STG;
-                if (!mbar_wait(&p_full[u], static_cast<uint32_t>((j >> 1) & 1)))
+                if (!mbar_wait(&p_full[u], static_cast<uint32_t>((j >> 1) & 1)) ||
+                    (j > 0 && j % C::RUN == 0 && !mbar_wait(acc_free, static_cast<uint32_t>((j / C::RUN - 1) & 1))))
                     return false;
                 tc_fence_after();
                 const uint32_t st = sbase + C::ST_OFF + s * C::ST_BYTES;
@@ -144,7 +150,7 @@ __global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_consta
                 const uint64_t odesc = umma_desc_sw128(st + 2 * C::TILE, C::RSLAB, 1024);
 #pragma unroll
                 for (int kk = 0; kk < C::RB / 16; ++kk) {
-                    const uint32_t acc = (j > 0 || kk > 0) ? 1u : 0u;
+                    const uint32_t acc = (j % C::RUN > 0 || kk > 0) ? 1u : 0u;
                     const uint64_t at = static_cast<uint64_t>(kk * (2048 >> 4));
                     const uint32_t ph = tbase + C::TM_S + 64 * u + 32 * (kk >> 1) + 8 * (kk & 1);
                     const uint32_t sh = ph + (C::TM_DP - C::TM_S);
@@ -155,9 +161,9 @@ __global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_consta
                     umma_ts(tbase + C::TM_DK, sh, ldesc + at, IDESC_D, 1);
                 }
                 // no commit that nothing waits for: round j + 2 waits for pv_done
-                if (j == rounds - 1)
+                if (j == rounds - 1 || j % C::RUN == C::RUN - 1)
                     umma_commit(acc_final);
-                else if (j + 2 < rounds)
+                if (j + 2 < rounds)
                     umma_commit(&pv_done[u]);
                 if (j + C::STG < rounds)  // the producer waits for it
                     umma_commit(&st_empty[s]);
@@ -186,7 +192,7 @@ __global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_consta
                 if (i >= 1)
                     ok = accumulate(i - 1);
             }
-            ok = ok && accumulate(rounds - 1) && mbar_wait(acc_final, 0);
+            ok = ok && accumulate(rounds - 1) && mbar_wait(acc_final, static_cast<uint32_t>(((rounds - 1) / C::RUN) & 1));
         }
     } else if (warp < 4) {
         // ------------------------------------------------------------------ the rows' numbers
@@ -253,9 +259,11 @@ __global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_consta
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&p_full[u]);
-        }
-        // dK (scaled) by the first group, dV by the second
-        if (ok && (ok = warp_wait(acc_final, 0))) {
+            if (i < rounds - 1 && i % C::RUN < C::RUN - 1)
+                continue;
+            // a run's end: dK (scaled) by the first group, dV by the second
+            if (!(ok = warp_wait(acc_final, static_cast<uint32_t>((i / C::RUN) & 1))))
+                break;
             tc_fence_after();
             const float f = half ? 1.f : p.scale;
             float *dst = (half ? p.dv : p.dk) + ((static_cast<long long>(b) * p.T + key) * p.Hkv + g) * D;
@@ -266,13 +274,22 @@ __global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_consta
                 tmem_wait_ld();
                 if (key < p.T) {
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        w[e] = __float_as_uint(__uint_as_float(w[e]) * f);
-#pragma unroll
-                    for (int e = 0; e < 32; e += 4)
-                        *reinterpret_cast<uint4 *>(dst + c + e) = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+                    for (int e = 0; e < 32; e += 4) {
+                        float4 y = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (i >= C::RUN)
+                            y = *reinterpret_cast<const float4 *>(dst + c + e);
+                        y.x = fmaf(__uint_as_float(w[e]), f, y.x);
+                        y.y = fmaf(__uint_as_float(w[e + 1]), f, y.y);
+                        y.z = fmaf(__uint_as_float(w[e + 2]), f, y.z);
+                        y.w = fmaf(__uint_as_float(w[e + 3]), f, y.w);
+                        *reinterpret_cast<float4 *>(dst + c + e) = y;
+                    }
                 }
             }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0 && i < rounds - 1)
+                mbar_arrive(acc_free);
         }
     }
     if (!ok) {

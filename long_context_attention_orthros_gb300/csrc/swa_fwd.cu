@@ -455,6 +455,8 @@ cudaError_t launch_swa(int D, int G, const CUtensorMap &q, const CUtensorMap &k,
     // tensor-memory kernel whenever a tile's whole band fits its ring and tensor memory
     if (p.sinks == 0 && swa_tc_supported(D, G, p.window))
         return launch_swa_tc(D, G, q, k, v, o, p, num_sms, stream);
+    if (p.sinks > 0 && swa_sink_tc_supported(D, G, p.window))
+        return launch_swa_sink_tc(D, G, q, k, v, p, num_sms, stream);
 #define ORTHROS_SWA_CASE(DD, GG) \
     if (D == DD && G == GG)      \
         return launch_swa_t<DD, GG>(q, k, v, o, p, num_sms, stream);
