@@ -37,6 +37,11 @@ struct TreeMaps {
 size_t tree_workspace_bytes(int B, int N, int L_max, int Hq, int Hkv, int D);
 cudaError_t launch_tree(int D, const TreeMaps &maps, TreeParams p, void *workspace, cudaStream_t stream);
 
+// the tensor-memory kernel; tr: rows of a tile, 128 or 256
+constexpr int TREE_TC_CTAS = 152;  // one on each of 152 SMs
+constexpr int TREE_TC_COST = 5;    // what a segment costs it beside its blocks
+cudaError_t launch_tree_tc(int D, int tr, const TreeMaps &maps, const TreeParams &p, int ctas, cudaStream_t stream);
+
 struct TreeAcceptParams {
     const orthros_bf16 *k_new, *v_new;  // [B, N, Hkv, d]
     const int32_t *parent, *node;       // [B, N], [B]

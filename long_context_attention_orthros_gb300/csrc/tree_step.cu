@@ -295,7 +295,7 @@ template <int D, int TR, int COST>
 __global__ void __launch_bounds__(128) tree_join_kernel(const TreeParams p, int ctas)
 {
     constexpr int E = D / 16;
-    const int t = threadIdx.x, lane = t & 31, hl = t & 15, half = lane >> 4;
+    const int t = threadIdx.x, lane = t & 31, hl = t & 15;
     const int G = p.Hq / p.Hkv, most = (p.N * G + TR - 1) / TR;  // tiles of a full tree
     int x = blockIdx.x;
     const int piece = x % (TR / 8);
@@ -384,7 +384,6 @@ __global__ void __launch_bounds__(128) tree_join_kernel(const TreeParams p, int 
             *reinterpret_cast<uint2 *>(out + e) = make_uint2(pack_bf16x2(a[e] * inv, a[e + 1] * inv),
                                                              pack_bf16x2(a[e + 2] * inv, a[e + 3] * inv));
     }
-    (void)half;
 }
 
 // ------------------------------------------------------------------ host side
@@ -394,15 +393,17 @@ struct TreePlan {
     size_t part_ml, total;
 };
 
+// Warp MMAs keep up with memory for up to 16 query rows a KV head, and start sooner; more go to tensor memory, in
+// tiles of 128 rows or, where one does not hold them, two at a time.
 static TreePlan tree_plan(int B, int N, int L_max, int Hq, int Hkv, int D)
 {
     TreePlan pl;
     const long long R = static_cast<long long>(N) * (Hq / Hkv);
-    pl.tr = R <= 8 ? 8 : 16;
+    pl.tr = R <= 8 ? 8 : (R <= 16 ? 16 : (R <= 128 ? 128 : 256));
     // never more CTAs than the longest caches could give places
     const long long tiles = (R + pl.tr - 1) / pl.tr;
-    const long long most = 2 * tiles * B * Hkv * (TREE_COST + 2 + (L_max + 63LL) / 64);
-    pl.ctas = static_cast<int>(most < TREE_CTAS ? most : TREE_CTAS);
+    const long long most = 2 * tiles * B * Hkv * (TREE_COST + 2 + (L_max + 63LL) / 64), ctas = pl.tr <= 16 ? TREE_CTAS : TREE_TC_CTAS;
+    pl.ctas = static_cast<int>(most < ctas ? most : ctas);
     const size_t slots = 2 * static_cast<size_t>(pl.ctas) * pl.tr;
     pl.part_ml = (slots * D * sizeof(float) + 255) / 256 * 256;
     pl.total = pl.part_ml + (slots * sizeof(float2) + 255) / 256 * 256;
@@ -419,7 +420,7 @@ static cudaError_t launch_tree_step(const TreeMaps &maps, const TreeParams &p, i
 {
     using C = TsCfg<D, NT>;
     auto kern = tree_step_kernel<D, NT>;
-    cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
+    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess)
         return e;
     cudaLaunchConfig_t cfg = {};
@@ -432,14 +433,31 @@ static cudaError_t launch_tree_step(const TreeMaps &maps, const TreeParams &p, i
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = attr;
     cfg.numAttrs = 1;
-    e = cudaLaunchKernelEx(&cfg, kern, maps, p);
+    return cudaLaunchKernelEx(&cfg, kern, maps, p);
+}
+
+template <int D, int TR>
+static cudaError_t launch_tree_t(const TreeMaps &maps, const TreeParams &p, int ctas, cudaStream_t stream)
+{
+    constexpr int COST = TR <= 16 ? TREE_COST : TREE_TC_COST;
+    cudaError_t e;
+    if constexpr (TR <= 16)
+        e = launch_tree_step<D, TR / 8>(maps, p, ctas, stream);
+    else
+        e = launch_tree_tc(D, TR, maps, p, ctas, stream);
     if (e != cudaSuccess)
         return e;
-    const int tiles = (p.N * (p.Hq / p.Hkv) + C::TR - 1) / C::TR;
-    cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hkv * 2 * tiles * (C::TR / 8));
+    const int tiles = (p.N * (p.Hq / p.Hkv) + TR - 1) / TR;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(static_cast<unsigned>(p.B) * p.Hkv * 2 * tiles * (TR / 8));
     cfg.blockDim = dim3(128);
-    cfg.dynamicSmemBytes = 0;
-    e = cudaLaunchKernelEx(&cfg, tree_join_kernel<D, C::TR, TREE_COST>, p, ctas);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr[1];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, tree_join_kernel<D, TR, COST>, p, ctas);
     return e == cudaSuccess ? cudaGetLastError() : e;
 }
 
@@ -448,12 +466,18 @@ cudaError_t launch_tree(int D, const TreeMaps &maps, TreeParams p, void *workspa
     const TreePlan pl = tree_plan(p.B, p.N, p.L_max, p.Hq, p.Hkv, D);
     p.part_o = static_cast<float *>(workspace);
     p.part_ml = reinterpret_cast<float2 *>(static_cast<uint8_t *>(workspace) + pl.part_ml);
-    if (D == 128)
-        return pl.tr == 8 ? launch_tree_step<128, 1>(maps, p, pl.ctas, stream)
-                          : launch_tree_step<128, 2>(maps, p, pl.ctas, stream);
-    if (D == 64)
-        return pl.tr == 8 ? launch_tree_step<64, 1>(maps, p, pl.ctas, stream)
-                          : launch_tree_step<64, 2>(maps, p, pl.ctas, stream);
+#define ORTHROS_TREE_CASE(DD, RR) \
+    if (D == DD && pl.tr == RR)   \
+        return launch_tree_t<DD, RR>(maps, p, pl.ctas, stream);
+    ORTHROS_TREE_CASE(128, 8)
+    ORTHROS_TREE_CASE(128, 16)
+    ORTHROS_TREE_CASE(128, 128)
+    ORTHROS_TREE_CASE(128, 256)
+    ORTHROS_TREE_CASE(64, 8)
+    ORTHROS_TREE_CASE(64, 16)
+    ORTHROS_TREE_CASE(64, 128)
+    ORTHROS_TREE_CASE(64, 256)
+#undef ORTHROS_TREE_CASE
     return cudaErrorInvalidValue;
 }
 
@@ -466,7 +490,7 @@ constexpr int ACCEPT_CTAS = 8;
 
 __global__ void __cluster_dims__(ACCEPT_CTAS, 1, 1) __launch_bounds__(256) tree_accept_kernel(const TreeAcceptParams p)
 {
-    const int b = blockIdx.y, rank = blockIdx.x, lane = threadIdx.x & 31;
+    const int b = blockIdx.y, rank = blockIdx.x;
     const int node = __ldg(p.node + b), len = __ldcg(p.cache_len + b);
     const bool inside = node >= 0 && node < p.N;
     // every warp finds the path by itself
@@ -502,7 +526,6 @@ __global__ void __cluster_dims__(ACCEPT_CTAS, 1, 1) __launch_bounds__(256) tree_
             *reinterpret_cast<uint4 *>((v ? p.v_cache : p.k_cache) + to + e) = y;
         }
     }
-    (void)lane;
     asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
     if (rank == 0 && threadIdx.x == 0 && count > 0)
         p.cache_len[b] = len + count;
