@@ -7,7 +7,7 @@
 // q, dS and P enter as a bf16 high part plus residual (their product's relative error some 2^-17, where one
 // bf16 would give 2^-9); sums, exponents and D are fp32.  Launches:
 //   sink_rows_kernel    q's two parts, D and the log-sum-exp in log2 units, one pass over x, o, dO
-//   sink_dq_kernel      dq of 64 rows over their band and the sinks, warp MMAs; dalpha, dbeta by atomics
+//   sink_dq_tc_kernel   dq over a row's window and the sinks; dalpha, dbeta by atomics (sink_dq.cu)
 //   sink_dkv_tc_kernel  dk, dv of the window's part (sink_dkv.cu)
 //   sink_keys_kernel    the sinks' share of the rows behind their window: every row adds to the same few keys, so
 //                       the tokens are split over CTAs, whose partial sums sink_join_kernel adds to dk, dv in order
@@ -57,193 +57,6 @@ __global__ void __launch_bounds__(256) sink_rows_kernel(const SinkBwdParams p)
     if (row < rows && sub == 0) {
         p.Drow[row] = acc;
         p.lse[row] = p.lse_in[row] * kLog2eF;
-    }
-}
-
-// ------------------------------------------------------------------ dq
-
-constexpr int DQ_ROWS = 64;  // query rows of a CTA: 64 / G tokens x G heads
-constexpr int DQ_KEYS = 64;  // keys of a streamed block
-constexpr int DQ_RUN = 32;   // blocks that dq is summed over in the MMA's accumulators (256 steps: some 4e-6)
-
-template <int D, int G>
-__global__ void __launch_bounds__(128) sink_dq_kernel(const SinkBwdParams p)
-{
-    constexpr int TOK = DQ_ROWS / G;
-    constexpr int SLAB = DQ_KEYS * 128;   // one 64-column slab of a 64-key block
-    constexpr int BLK = (D / 64) * SLAB;  // one K (or V) block
-    const int u0 = blockIdx.x * TOK, bh = blockIdx.y;
-    const int b = bh / p.Hkv, g = bh % p.Hkv;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-    extern __shared__ uint8_t smem_raw[];
-    uint8_t *smem = align1024(smem_raw);
-    float *red = reinterpret_cast<float *>(smem + 4 * BLK);  // [2][G][D]: dalpha, dbeta
-    const uint32_t sbase = smem_u32(smem);
-
-    // this warp's 16 rows: r = 16 warp + 0..15 -> token u0 + r / G, head g G + r % G
-    const int gr = lane >> 2, qd = (lane & 3) * 2;
-    const int rowA = 16 * warp + gr, rowB = rowA + 8;
-    const int tA = u0 + rowA / G, tB = u0 + rowB / G;
-    const int hA = g * G + rowA % G, hB = g * G + rowB % G;
-    const bool vA = tA < p.T, vB = tB < p.T;
-    const int loA = tA - p.window + 1, loB = tB - p.window + 1;
-    const int t_lo = u0 + 16 * warp / G, t_hi = min(p.T - 1, u0 + (16 * warp + 15) / G);  // the warp's tokens
-    const int wlo = max(0, t_lo - p.window + 1), whi = t_lo < p.T ? t_hi : -1;
-    for (int i = threadIdx.x; i < 2 * G * D; i += 128)
-        red[i] = 0.f;
-    const int cb0 = max(0, u0 - p.window + 1) / DQ_KEYS, cb1 = min(p.T - 1, u0 + TOK - 1) / DQ_KEYS + 1;
-    const int far = p.sinks > 0 && cb0 > 0 ? 1 : 0;  // the sinks' block comes first
-    const int nblk = cb1 - cb0 + far;
-
-    const long long q_bs = static_cast<long long>(p.T) * p.Hq * D;
-    const float c2 = p.scale * kLog2eF;  // logits in log2 units
-    WarpRows16<D> st;                    // q fragments and the dQ accumulators
-    uint32_t ga[D / 16][4];              // dO fragments (A operand)
-#pragma unroll
-    for (int kt2 = 0; kt2 < D / 16; ++kt2)
-#pragma unroll
-        for (int r = 0; r < 4; ++r) {
-            const bool isB = r & 1;
-            const int t = isB ? tB : tA, h = isB ? hB : hA;
-            const int dcol = kt2 * 16 + qd + ((r & 2) ? 8 : 0);
-            uint32_t hi = 0, lo = 0, gw = 0;
-            if (isB ? vB : vA) {
-                const long long off = b * q_bs + (static_cast<long long>(t) * p.Hq + h) * D + dcol;
-                hi = *reinterpret_cast<const uint32_t *>(p.q_hi + off);
-                lo = *reinterpret_cast<const uint32_t *>(p.q_lo + off);
-                gw = *reinterpret_cast<const uint32_t *>(p.dO + off);
-            }
-            st.qa[kt2][r] = hi;
-            st.ql[kt2][r] = lo;
-            ga[kt2][r] = gw;
-        }
-    st.reset();
-    const int kld_row = (lane & 7) + ((lane >> 4) << 3), kld_hi = (lane >> 3) & 1;
-    const int vld_row = (lane & 7) + (((lane >> 3) & 1) << 3), vld_hi = lane >> 4;
-
-    const long long kv_rs = static_cast<long long>(p.Hkv) * D;
-    const orthros_bf16 *kb = p.k + static_cast<long long>(b) * p.T * kv_rs + static_cast<long long>(g) * D;
-    const orthros_bf16 *vb = p.v + static_cast<long long>(b) * p.T * kv_rs + static_cast<long long>(g) * D;
-    // stream the i-th block into ring slot i % 2; behind the sinks their block has zeros
-    auto stage = [&](int i) {
-        const bool sink = i < far;
-        const int key0 = sink ? 0 : (cb0 + i - far) * DQ_KEYS, end = sink ? p.sinks : p.T;
-        for (int e = threadIdx.x; e < DQ_KEYS * (D / 8); e += 128) {
-            const int r = e / (D / 8), c = (e % (D / 8)) * 8;
-            const bool ok = key0 + r < end;
-            const long long off = static_cast<long long>(ok ? key0 + r : 0) * kv_rs + c;
-            const uint32_t o = sbase + (i & 1) * 2 * BLK + tile_off(r, c, SLAB);
-            cp_async16(o, kb + off, ok);
-            cp_async16(o + BLK, vb + off, ok);
-        }
-        cp_async_commit();
-    };
-
-    const long long rA = (static_cast<long long>(b) * p.T + tA) * p.Hq + hA;
-    const long long rB = (static_cast<long long>(b) * p.T + tB) * p.Hq + hB;
-    const float lseA = vA ? p.lse[rA] : 0.f, lseB = vB ? p.lse[rB] : 0.f;
-    const float DA = vA ? p.Drow[rA] : 0.f, DB = vB ? p.Drow[rB] : 0.f;
-    stage(0);
-#pragma unroll 1
-    for (int i = 0; i < nblk; ++i) {
-        const bool sink = i < far;
-        if (i + 1 < nblk) {
-            stage(i + 1);
-            cp_async_wait<1>();
-        } else {
-            cp_async_wait<0>();
-        }
-        __syncthreads();
-        const uint32_t kbase = sbase + (i & 1) * 2 * BLK, vbase = kbase + BLK;
-#pragma unroll 1
-        for (int jc = 0; jc < DQ_KEYS; jc += 16) {
-            const int kc = (sink ? 0 : (cb0 + i - far) * DQ_KEYS) + jc;
-            if (kc > whi || (kc + 15 < wlo && kc >= p.sinks))
-                continue;  // warp-uniform: no key of this chunk is seen by the warp's rows
-            float s[2][4], dp[2][4];
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    s[n][e] = dp[n][e] = 0.f;
-#pragma unroll
-            for (int kt2 = 0; kt2 < D / 16; ++kt2) {
-                uint32_t b0, b1, b2, b3;
-                ldsm_x4(kbase + tile_off(jc + kld_row, kt2 * 16 + kld_hi * 8, SLAB), b0, b1, b2, b3);
-                mma_16816(s[0], st.qa[kt2], b0, b1);
-                mma_16816(s[1], st.qa[kt2], b2, b3);
-                mma_16816(s[0], st.ql[kt2], b0, b1);
-                mma_16816(s[1], st.ql[kt2], b2, b3);
-                ldsm_x4(vbase + tile_off(jc + kld_row, kt2 * 16 + kld_hi * 8, SLAB), b0, b1, b2, b3);
-                mma_16816(dp[0], ga[kt2], b0, b1);
-                mma_16816(dp[1], ga[kt2], b2, b3);
-            }
-            float ds[2][4];
-#pragma unroll
-            for (int n = 0; n < 2; ++n)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const bool isB = e & 2;
-                    const int key = kc + n * 8 + qd + (e & 1), t = isB ? tB : tA;
-                    const bool seen = key <= t && (key >= (isB ? loB : loA) || key < p.sinks) && (isB ? vB : vA);
-                    ds[n][e] = seen ? fast_exp2(s[n][e] * c2 - (isB ? lseB : lseA)) * (dp[n][e] - (isB ? DB : DA)) : 0.f;
-                }
-            uint32_t dh[4], dl[4];
-            split_q_pair(ds[0][0], ds[0][1], dh[0], dl[0]);
-            split_q_pair(ds[0][2], ds[0][3], dh[1], dl[1]);
-            split_q_pair(ds[1][0], ds[1][1], dh[2], dl[2]);
-            split_q_pair(ds[1][2], ds[1][3], dh[3], dl[3]);
-#pragma unroll
-            for (int dp2 = 0; dp2 < D / 16; ++dp2) {
-                uint32_t v0, v1, v2, v3;
-                ldsm_x4_trans(kbase + tile_off(jc + vld_row, dp2 * 16 + vld_hi * 8, SLAB), v0, v1, v2, v3);
-                mma_16816(st.o[2 * dp2], dh, v0, v1);
-                mma_16816(st.o[2 * dp2 + 1], dh, v2, v3);
-                mma_16816(st.o[2 * dp2], dl, v0, v1);
-                mma_16816(st.o[2 * dp2 + 1], dl, v2, v3);
-            }
-        }
-        __syncthreads();  // the slot is refilled by the next iteration's prefetch
-        // the MMA's accumulators are truncated at every step: a long run of keys is summed up in memory
-        if (i % DQ_RUN == DQ_RUN - 1 && i < nblk - 1) {
-#pragma unroll
-            for (int half = 0; half < 2; ++half)
-                if (half ? vB : vA) {
-                    float *to = p.dq + (half ? rB : rA) * D + qd;
-#pragma unroll
-                    for (int e = 0; e < D / 8; ++e) {
-                        float2 y = i < DQ_RUN ? make_float2(0.f, 0.f) : *reinterpret_cast<const float2 *>(to + 8 * e);
-                        *reinterpret_cast<float2 *>(to + 8 * e) = make_float2(y.x + st.o[e][2 * half], y.y + st.o[e][2 * half + 1]);
-                    }
-                }
-            st.reset();
-        }
-    }
-    // dq = scale dQ; dq_raw = dq alpha; dalpha += x dq, dbeta += dq
-#pragma unroll
-    for (int half = 0; half < 2; ++half) {
-        if (!(half ? vB : vA))
-            continue;
-        const int t = half ? tB : tA, h = half ? hB : hA, hh = h - g * G;
-        const long long off = b * q_bs + (static_cast<long long>(t) * p.Hq + h) * D;
-#pragma unroll
-        for (int i = 0; i < D / 8; ++i) {
-            const int dcol = i * 8 + qd;
-            float2 y = nblk > DQ_RUN ? *reinterpret_cast<const float2 *>(p.dq + off + dcol) : make_float2(0.f, 0.f);
-            const float dq0 = (y.x + st.o[i][2 * half]) * p.scale, dq1 = (y.y + st.o[i][2 * half + 1]) * p.scale;
-            const float2 al = __ldg(reinterpret_cast<const float2 *>(p.alpha + h * D + dcol));
-            *reinterpret_cast<float2 *>(p.dq + off + dcol) = make_float2(dq0 * al.x, dq1 * al.y);
-            const float2 x = unpack_bf16x2(*reinterpret_cast<const uint32_t *>(p.q + off + dcol));
-            atomicAdd(&red[hh * D + dcol], x.x * dq0);
-            atomicAdd(&red[hh * D + dcol + 1], x.y * dq1);
-            atomicAdd(&red[G * D + hh * D + dcol], dq0);
-            atomicAdd(&red[G * D + hh * D + dcol + 1], dq1);
-        }
-    }
-    __syncthreads();
-    for (int i = threadIdx.x; i < G * D; i += 128) {
-        atomicAdd(p.dalpha + g * G * D + i, red[i]);
-        atomicAdd(p.dbeta + g * G * D + i, red[G * D + i]);
     }
 }
 
@@ -414,36 +227,15 @@ int sink_chunks(int B, int T, int Hq)
     return want < least ? least : (want < most ? want : most);
 }
 
-template <int D, int G>
-cudaError_t launch_dq(const SinkBwdParams &p, cudaStream_t stream)
-{
-    const int smem = 4 * (D / 64) * DQ_KEYS * 128 + 2 * G * D * 4 + 1024;
-    auto kern = sink_dq_kernel<D, G>;
-    const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
-    if (e != cudaSuccess)
-        return e;
-    constexpr int TOK = DQ_ROWS / G;
-    kern<<<dim3((p.T + TOK - 1) / TOK, p.B * p.Hkv), 128, smem, stream>>>(p);
-    return cudaGetLastError();
-}
-
 template <int D>
-cudaError_t launch_t(const SinkBwdMaps &maps, const SinkBwdParams &p, cudaStream_t stream)
+cudaError_t launch_t(const SinkDqMaps &qmaps, const SinkBwdMaps &maps, const SinkBwdParams &p, cudaStream_t stream)
 {
     const long long lanes = static_cast<long long>(p.B) * p.T * p.Hq * (D / 8);
     sink_rows_kernel<D><<<static_cast<unsigned>((lanes + 255) / 256), 256, 0, stream>>>(p);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    switch (p.Hq / p.Hkv) {
-    case 1: e = launch_dq<D, 1>(p, stream); break;
-    case 2: e = launch_dq<D, 2>(p, stream); break;
-    case 4: e = launch_dq<D, 4>(p, stream); break;
-    case 8: e = launch_dq<D, 8>(p, stream); break;
-    case 16: e = launch_dq<D, 16>(p, stream); break;
-    default: e = cudaErrorInvalidValue;
-    }
-    if (e != cudaSuccess || (e = launch_sink_dkv(D, maps, p, stream)) != cudaSuccess)
+    if ((e = launch_sink_dq(D, qmaps, p, stream)) != cudaSuccess || (e = launch_sink_dkv(D, maps, p, stream)) != cudaSuccess)
         return e;
     const int count = p.sinks < p.T - p.window ? p.sinks : p.T - p.window;  // sinks that some row sees behind its window
     if (count <= 0)
@@ -476,9 +268,10 @@ void sink_bwd_workspace(SinkBwdParams &p, int D, void *workspace)
     p.part = reinterpret_cast<float *>(ws + up256(4 * rows));
 }
 
-cudaError_t launch_sink_bwd(int D, const SinkBwdMaps &maps, const SinkBwdParams &p, cudaStream_t stream)
+cudaError_t launch_sink_bwd(int D, const SinkDqMaps &qmaps, const SinkBwdMaps &maps, const SinkBwdParams &p,
+                            cudaStream_t stream)
 {
-    return D == 128 ? launch_t<128>(maps, p, stream) : launch_t<64>(maps, p, stream);
+    return D == 128 ? launch_t<128>(qmaps, maps, p, stream) : launch_t<64>(qmaps, maps, p, stream);
 }
 
 }  // namespace orthros
