@@ -137,8 +137,8 @@ orthros_status orthros_swa_fwd_lse(const orthros_bf16 *q_raw, const orthros_bf16
  * 0 <= sinks <= 32 (0: as orthros_swa_fwd).  lse (optional, NULL: none) gets each row's log-sum-exp
  * over those keys, fp32 [B, T, Hq], for orthros_swa_sink_bwd.  Only output rows row_begin ..
  * row_end-1 are computed (0 and T for all; rules and reads as orthros_swa_fwd_rows, and key rows
- * 0 .. sinks-1 have to be in place).  Values of K and V are finite; one that is not reaches, beside
- * the rows that see it, only rows up to window + 128 away.  Other arguments, arithmetic and errors as
+ * 0 .. sinks-1 have to be in place).  Values of V are finite; one that is not reaches, beside the rows
+ * that see it, only rows up to window + 256 away.  Other arguments, arithmetic and errors as
  * orthros_swa_fwd.
  */
 orthros_status orthros_swa_sink_fwd(const orthros_bf16 *q_raw, const orthros_bf16 *k,

@@ -44,5 +44,13 @@ __device__ __forceinline__ bool warp_wait(uint64_t *bar, uint32_t parity)
     return __shfl_sync(0xffffffffu, ok ? 1 : 0, 0) != 0;
 }
 
+// two fp32 values as a bf16 high part and a bf16 residual each
+__device__ __forceinline__ void split_pair2(float2 x, uint32_t &hi, uint32_t &lo)
+{
+    hi = pack_bf16x2(x.x, x.y);
+    const float2 r = ffma2(unpack_bf16x2(hi), make_float2(-1.f, -1.f), x);
+    lo = pack_bf16x2(r.x, r.y);
+}
+
 }  // namespace
 }  // namespace orthros

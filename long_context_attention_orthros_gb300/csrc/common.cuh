@@ -10,6 +10,12 @@
 
 #include "../../include/orthros.h"
 
+// Rare paths are out of line, but where the including file says otherwise: a kernel whose warps change their register
+// count (setmaxnreg) can make no calls.
+#ifndef ORTHROS_RARE
+#define ORTHROS_RARE inline __noinline__
+#endif
+
 namespace orthros {
 
 constexpr uint64_t kWaitLimitNs = 2000000000ull;  // bounded spin: 2 s
@@ -95,7 +101,7 @@ __device__ __forceinline__ bool mbar_try_wait_sleep(uint64_t *bar, uint32_t pari
 }
 
 // The waiting loop of mbar_wait, out of line so that every call site stays small.
-static __device__ __noinline__ bool mbar_wait_slow(uint64_t *bar, uint32_t parity)
+static __device__ ORTHROS_RARE bool mbar_wait_slow(uint64_t *bar, uint32_t parity)
 {
     const uint64_t t0 = global_timer_ns();
     while (true) {

@@ -126,7 +126,14 @@ struct SinkBwdMaps {
 };
 size_t sink_bwd_workspace_bytes(int B, int T, int Hq, int D);
 void sink_bwd_workspace(SinkBwdParams &p, int D, void *workspace);
-cudaError_t launch_sink_bwd(int D, const SinkBwdMaps &maps, const SinkBwdParams &p, cudaStream_t stream);
+struct SinkDqMaps {
+    CUtensorMap q_hi, q_lo, dO;  // boxes of 64 x G heads x 128/G tokens
+    CUtensorMap k, v;            // boxes of 64 x 1 x 64
+    CUtensorMap ks, vs;          // the sinks alone (zeros behind them): boxes of 64 x 1 x 32
+};
+cudaError_t launch_sink_bwd(int D, const SinkDqMaps &qmaps, const SinkBwdMaps &maps, const SinkBwdParams &p,
+                            cudaStream_t stream);
+cudaError_t launch_sink_dq(int D, const SinkDqMaps &maps, const SinkBwdParams &p, cudaStream_t stream);
 cudaError_t launch_sink_dkv(int D, const SinkBwdMaps &maps, const SinkBwdParams &p, cudaStream_t stream);
 // a layer's gradient, both streams: p the base stream, pc the copies (pc.k16 = p.k16; maps and
 // mapsc as above for each stream, mapsc's fp16-K maps over p.k16); dK / dV written once
@@ -139,6 +146,23 @@ bool swa_tc_supported(int D, int G, int window);
 cudaError_t launch_swa_tc(int D, int G, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                           const CUtensorMap &o, const SwaParams &p, int num_sms, cudaStream_t stream);
 
+// base stream with sinks, any window and grouping, over blocks of 64 keys (swa_wide.cu)
+struct SwaWideParams {
+    const orthros_bf16 *q;
+    const float *alpha, *beta;
+    orthros_bf16 *o;
+    float *lse;  // optional [B, T, Hq]
+    int32_t *dev_err;
+    long long q_bstride, o_bstride;
+    int B, T, Hq, Hkv, window, sinks, row_begin, row_end;
+    float qscale;
+    int per_stream;    // pieces of a (sequence, KV head); set by the launcher
+    long long pieces;
+};
+struct SwaWideMaps {
+    CUtensorMap k, v;  // boxes of 64 x 1 x 64
+};
+cudaError_t launch_swa_wide(int D, const SwaWideMaps &maps, const SwaWideParams &p, cudaStream_t stream);
 // the same with p.sinks > 0
 bool swa_sink_tc_supported(int D, int G, int window);
 cudaError_t launch_swa_sink_tc(int D, int G, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,

@@ -218,6 +218,32 @@ orthros_status swa_fwd_impl(const orthros_bf16 *q_raw, const orthros_bf16 *k, co
     if (st != ORTHROS_OK || empty)
         return st;
     p.sinks = sinks;
+    if (sinks > 0 && !orthros::swa_sink_tc_supported(d, Hq / Hkv, window)) {
+        orthros::SwaWideParams w{};
+        w.q = q_raw;
+        w.alpha = alpha;
+        w.beta = beta;
+        w.o = o;
+        w.lse = lse;
+        w.dev_err = dev_err;
+        w.q_bstride = q_bstride ? q_bstride : static_cast<long long>(T) * Hq * d;
+        w.o_bstride = p.o_bstride;
+        w.B = B;
+        w.T = T;
+        w.Hq = Hq;
+        w.Hkv = Hkv;
+        w.window = window;
+        w.sinks = sinks;
+        w.row_begin = row_begin;
+        w.row_end = row_end;
+        w.qscale = p.qscale;
+        orthros::SwaWideMaps wm;
+        const long long ks = kv_bstride ? kv_bstride : static_cast<long long>(T) * Hkv * d;
+        if (!make_map(&wm.k, k, d, Hkv, T, B, ks, 1, 64) || !make_map(&wm.v, v, d, Hkv, T, B, ks, 1, 64))
+            return ORTHROS_ERR_CUDA;
+        const cudaError_t e = orthros::launch_swa_wide(d, wm, w, static_cast<cudaStream_t>(stream));
+        return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
+    }
     const int sms = num_sms() - sm_reserve;  // the persistent kernel's CTAs
     if (sms <= 0)
         return ORTHROS_ERR_CUDA;
@@ -642,7 +668,14 @@ orthros_status orthros_swa_sink_bwd(const orthros_bf16 *q_raw, const orthros_bf1
         !make_map(&m.dO, dO, d, Hq, T, B, qs, G, 64 / G) || !make_map(&m.k, k, d, Hkv, T, B, ks, 1, 128) ||
         !make_map(&m.v, v, d, Hkv, T, B, ks, 1, 128))
         return ORTHROS_ERR_CUDA;
-    const cudaError_t e = orthros::launch_sink_bwd(d, m, p, static_cast<cudaStream_t>(stream));
+    orthros::SinkDqMaps mq;
+    const int first = sinks < 1 ? 1 : (sinks < T ? sinks : T);  // without sinks these two maps are not used
+    if (!make_map(&mq.q_hi, p.q_hi, d, Hq, T, B, qs, G, 128 / G) || !make_map(&mq.q_lo, p.q_lo, d, Hq, T, B, qs, G, 128 / G) ||
+        !make_map(&mq.dO, dO, d, Hq, T, B, qs, G, 128 / G) || !make_map(&mq.k, k, d, Hkv, T, B, ks, 1, 64) ||
+        !make_map(&mq.v, v, d, Hkv, T, B, ks, 1, 64) || !make_map(&mq.ks, k, d, Hkv, first, B, ks, 1, 32) ||
+        !make_map(&mq.vs, v, d, Hkv, first, B, ks, 1, 32))
+        return ORTHROS_ERR_CUDA;
+    const cudaError_t e = orthros::launch_sink_bwd(d, mq, m, p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
 }
 

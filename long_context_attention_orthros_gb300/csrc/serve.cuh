@@ -9,7 +9,7 @@ namespace orthros {
 
 // After a wait has given up: time enough (1 ms) for the copies and MMAs in flight to land before
 // their shared or tensor memory is given back.
-inline __device__ __noinline__ void drain_in_flight()
+__device__ ORTHROS_RARE void drain_in_flight()
 {
     const uint64_t t0 = global_timer_ns();
     while (global_timer_ns() - t0 < 1000000ull) {

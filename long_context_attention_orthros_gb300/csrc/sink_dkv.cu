@@ -39,8 +39,9 @@ struct SdCfg {
     static constexpr int V_OFF = K_OFF + SLABS * KSLAB;
     static constexpr int ST_OFF = V_OFF + SLABS * KSLAB;  // [STG]: q high part, q residual, dO
     static constexpr int ST_BYTES = 3 * TILE;
-    static constexpr int META_OFF = ST_OFF + STG * ST_BYTES;  // [STG][3][RB]: lse, D, token
-    static constexpr int BAR_OFF = META_OFF + STG * 3 * RB * 4;
+    static constexpr int META_OFF = ST_OFF + STG * ST_BYTES;  // [STG][2][RB]: -lse, -D
+    static constexpr int BAR_OFF = META_OFF + STG * 2 * RB * 4;
+    static_assert(META_OFF % 16 == 0, "read 16 bytes at a time");
     static constexpr int NBARS = 1 + 3 * STG + 3 * 2 + 2;
     static constexpr int HOLD_OFF = BAR_OFF + NBARS * 8;
     static constexpr int USED = HOLD_OFF + 16 + 1024;
@@ -199,20 +200,19 @@ __global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_consta
         const int ct = threadIdx.x - 64;  // 0..63: one row of the round each
         for (int i = 0; ok && i < rounds; ++i) {
             const int s = i % C::STG, t = (r0 + i) * TOK + ct / G;
-            float m_lse = 0.f, m_d = 0.f;
+            float m_lse = -__int_as_float(0x7f800000), m_d = 0.f;  // behind the last token: weights of zero
             if (t < p.T) {
                 const long long ri = (static_cast<long long>(b) * p.T + t) * p.Hq + g * G + ct % G;
-                m_lse = p.lse[ri];
-                m_d = p.Drow[ri];
+                m_lse = -p.lse[ri];
+                m_d = -p.Drow[ri];
             }
             // the place is free once the stage of this round has landed: its producer waited for the MMAs of round
             // i - STG, which waited for that round's softmax
             if (!(ok = warp_wait(&st_full[s], static_cast<uint32_t>((i / C::STG) & 1))))
                 break;
-            float *m = meta + s * 3 * C::RB;
+            float *m = meta + s * 2 * C::RB;
             m[ct] = m_lse;
             m[C::RB + ct] = m_d;
-            m[2 * C::RB + ct] = __int_as_float(t < p.T ? t : -1);
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&meta_full[s]);
@@ -222,38 +222,59 @@ __global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_consta
         const int rw = warp & 3, half = (warp - 4) >> 2;
         const int key = kt0 + rw * 32 + lane;
         const uint32_t tl = tbase + (static_cast<uint32_t>(rw * 32) << 16);
-        const float c2 = p.scale * kLog2eF;
+        const float2 c22 = make_float2(p.scale * kLog2eF, p.scale * kLog2eF);
         for (int i = 0; i < rounds; ++i) {
             const int s = i % C::STG, u = i & 1;
             if (!(ok = warp_wait(&s_full[u], static_cast<uint32_t>((i >> 1) & 1)) &&
                        warp_wait(&meta_full[s], static_cast<uint32_t>((i / C::STG) & 1))))
                 break;
             tc_fence_after();
-            const float *m = meta + s * 3 * C::RB + 32 * half;
+            const float *m = meta + s * 2 * C::RB + 32 * half;
             const uint32_t s_at = tl + C::TM_S + 64 * u + 32 * half, d_at = tl + C::TM_DP + 64 * u + 32 * half;
-            uint32_t sv[32], dv[32];
-            tmem_ld32(s_at, sv);
-            tmem_ld32(d_at, dv);
-            tmem_wait_ld();
-            uint32_t ph[16], pl[16], sh[16], sl[16];
+            // what the warp's 32 keys are to the 32 rows: seen by all of them, by none, or by some
+            const int t0 = (r0 + i) * TOK + 32 * half / G, t1 = (r0 + i) * TOK + (32 * half + 31) / G;
+            const int k0 = kt0 + rw * 32;
+            if (t1 < k0 || k0 + 31 <= t0 - p.window) {
+                const uint32_t zero[32] = {};
+                tmem_st32(s_at, zero);
+                tmem_st32(d_at, zero);
+            } else {
+                const bool whole = k0 + 31 <= t0 && k0 > t1 - p.window;
+                uint32_t sv[32], dv[32];
+                tmem_ld32(s_at, sv);
+                tmem_ld32(d_at, dv);
+                tmem_wait_ld();
 #pragma unroll
-            for (int e = 0; e < 16; ++e) {
-                float pr[2], ds[2];
+                for (int x = 0; x < 2; ++x) {
+                    uint32_t ph[8], pl[8], sh[8], sl[8];
 #pragma unroll
-                for (int q = 0; q < 2; ++q) {
-                    const int c = 2 * e + q, t = __float_as_int(m[2 * C::RB + c]);
-                    const bool seen = key <= t && key > t - p.window;  // t = -1: none
-                    const float x = fast_exp2(__uint_as_float(sv[c]) * c2 - m[c]);
-                    pr[q] = seen ? x : 0.f;
-                    ds[q] = seen ? x * (__uint_as_float(dv[c]) - m[C::RB + c]) : 0.f;
+                    for (int e4 = 0; e4 < 4; ++e4) {
+                        const float4 nl = *reinterpret_cast<const float4 *>(m + 16 * x + 4 * e4);
+                        const float4 nd = *reinterpret_cast<const float4 *>(m + C::RB + 16 * x + 4 * e4);
+#pragma unroll
+                        for (int y = 0; y < 2; ++y) {
+                            const int c = 16 * x + 4 * e4 + 2 * y, e = 2 * e4 + y;
+                            float2 pr = ffma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), c22,
+                                              y ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y));
+                            pr = make_float2(fast_exp2(pr.x), fast_exp2(pr.y));
+                            float2 ds = fmul2(pr, fadd2(make_float2(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1])),
+                                                        y ? make_float2(nd.z, nd.w) : make_float2(nd.x, nd.y)));
+                            if (!whole) {
+                                const int ta = (r0 + i) * TOK + (32 * half + c) / G, tb = (r0 + i) * TOK + (32 * half + c + 1) / G;
+                                const bool sa = key <= ta && key > ta - p.window, sb = key <= tb && key > tb - p.window;
+                                pr = make_float2(sa ? pr.x : 0.f, sb ? pr.y : 0.f);
+                                ds = make_float2(sa ? ds.x : 0.f, sb ? ds.y : 0.f);
+                            }
+                            split_pair2(pr, ph[e], pl[e]);
+                            split_pair2(ds, sh[e], sl[e]);
+                        }
+                    }
+                    tmem_st8(s_at + 8 * x, ph);
+                    tmem_st8(s_at + 16 + 8 * x, pl);
+                    tmem_st8(d_at + 8 * x, sh);
+                    tmem_st8(d_at + 16 + 8 * x, sl);
                 }
-                split_q_pair(pr[0], pr[1], ph[e], pl[e]);
-                split_q_pair(ds[0], ds[1], sh[e], sl[e]);
             }
-            tmem_st16(s_at, ph);
-            tmem_st16(s_at + 16, pl);
-            tmem_st16(d_at, sh);
-            tmem_st16(d_at + 16, sl);
             tmem_wait_st();
             tc_fence_before();
             __syncwarp();

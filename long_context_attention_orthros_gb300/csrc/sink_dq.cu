@@ -13,8 +13,9 @@
 // memory and begins anew.
 // Bound by memory and MMAs alike: 96 KB of rows in and 64 KB of fp32 out a tile (d = 128), 40 MMAs a round.
 // Roles (512 threads): warps 0, 2 TMA producers of rows, of keys; warp 1 tensor memory and MMA issue; warps 4-7, 8-11 dS of
-// a round's columns 0-31, 32-63 (lane = row); warps 12-15 dq_raw and the sums over a tile's rows, through a
-// transposing buffer of 32 columns (a thread sums one column of one head).  Every wait is bounded.
+// a round's columns 0-31, 32-63 (lane = row); warps 12-15 dq_raw and the sums over a tile's rows: 16 columns at a
+// time x dq and dq go through a transposing buffer, where a thread sums one column of one head over its rows (loads
+// of x in that order, 2 bytes a lane, took 10 us a tile).  Every wait is bounded.
 #include "bwd_util.cuh"
 #include "kernels.cuh"
 #include "serve.cuh"
@@ -37,8 +38,8 @@ struct SqCfg {
     static constexpr int KTILE = SLABS * KSLAB;
     static constexpr int Q_OFF = 0;  // q high part, q residual, dO
     static constexpr int ST_OFF = 3 * QTILE;  // [STG]: K, V
-    static constexpr int TP_OFF = ST_OFF + STG * 2 * KTILE;  // float [128][33]
-    static constexpr int BAR_OFF = TP_OFF + ROWS * 33 * 4;
+    static constexpr int TP_OFF = ST_OFF + STG * 2 * KTILE;  // float [2][128][17]: x dq and dq of 16 columns
+    static constexpr int BAR_OFF = TP_OFF + 2 * ROWS * 17 * 4;
     static constexpr int NBARS = 2 + 2 * STG + 3 * 2 + 2 * 2;
     static constexpr int HOLD_OFF = BAR_OFF + NBARS * 8;
     static constexpr int USED = HOLD_OFF + 16 + 1024;
@@ -249,20 +250,21 @@ __global__ void __launch_bounds__(512, 1) sink_dq_tc_kernel(const __grid_constan
         // ------------------------------------------------------------------ dS (lane = row)
         const int rw = warp & 3, half = (warp - 4) >> 2, row = rw * 32 + lane;
         const uint32_t tl_at = tbase + (static_cast<uint32_t>(rw * 32) << 16);
-        const float c2 = p.scale * kLog2eF;
+        const float2 c22 = make_float2(p.scale * kLog2eF, p.scale * kLog2eF);
         long long i = 0;
         for (long long tau = t_begin; ok && tau < t_end; ++tau) {
             const SqTile tl = sq_tile<D, G>(p, tau, per_stream);
             const int b = tl.bh / p.Hkv, g = tl.bh % p.Hkv;
             const int t = tl.u0 + row / G;
-            float lse = 0.f, Drow = 0.f;
+            float lse = __int_as_float(0x7f800000), Drow = 0.f;  // behind the last token: weights of zero
             if (t < p.T) {
                 const long long ri = (static_cast<long long>(b) * p.T + t) * p.Hq + g * G + row % G;
                 lse = p.lse[ri];
                 Drow = p.Drow[ri];
             }
-            const int klo = t < p.T ? t - p.window : 0x7fffffff;  // keys klo + 1 .. t, and the sinks
-            const int ksink = t < p.T ? p.sinks : 0, khi = t < p.T ? t : -1;
+            const int klo = t - p.window, ksink = p.sinks, khi = t;  // keys klo + 1 .. t, and the sinks
+            const int t_lo = tl.u0 + rw * 32 / G, t_hi = tl.u0 + (rw * 32 + 31) / G;  // the warp's tokens
+            const float2 nlse2 = make_float2(-lse, -lse), nd2 = make_float2(-Drow, -Drow);
             for (int r = 0; r < tl.rounds; ++r, ++i) {
                 const int u = static_cast<int>(i & 1);
                 const bool sink = r < tl.far;
@@ -272,29 +274,38 @@ __global__ void __launch_bounds__(512, 1) sink_dq_tc_kernel(const __grid_constan
                     tc_fence_after();
                     const int key0 = (sink ? 0 : (tl.lo + r - tl.far) * C::KB) + 32 * half;
                     const uint32_t s_at = tl_at + C::TM_S + 64 * u + 32 * half, d_at = tl_at + C::TM_DP + 64 * u + 32 * half;
-                    uint32_t sv[2][16], dv[2][16];
-                    tmem_ld16(s_at, sv[0]);
-                    tmem_ld16(d_at, dv[0]);
-                    tmem_ld16(s_at + 16, sv[1]);
-                    tmem_ld16(d_at + 16, dv[1]);
-                    tmem_wait_ld();
+                    // what the warp's rows see of the 32 keys: all of them, none, or some
+                    const bool whole = key0 + 31 <= t_lo && (key0 > t_hi - p.window || key0 + 31 < p.sinks);
+                    const bool none = key0 > t_hi || (key0 + 31 <= t_lo - p.window && key0 >= p.sinks);
+                    if (none) {
+                        const uint32_t zero[16] = {};
+                        tmem_st16(d_at, zero);
+                        tmem_st16(d_at + 16, zero);
+                    } else {
+                        uint32_t sv[2][16], dv[2][16];
+                        tmem_ld16(s_at, sv[0]);
+                        tmem_ld16(d_at, dv[0]);
+                        tmem_ld16(s_at + 16, sv[1]);
+                        tmem_ld16(d_at + 16, dv[1]);
+                        tmem_wait_ld();
 #pragma unroll
-                    for (int x = 0; x < 2; ++x) {
-                        uint32_t hi[8], lo[8];
+                        for (int x = 0; x < 2; ++x) {
+                            uint32_t hi[8], lo[8];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float ds[2];
-#pragma unroll
-                            for (int q = 0; q < 2; ++q) {
-                                const int c = 2 * e + q, key = key0 + 16 * x + c;
-                                const bool seen = key <= khi && (key > klo || key < ksink);
-                                const float pr = fast_exp2(__uint_as_float(sv[x][c]) * c2 - lse);
-                                ds[q] = seen ? pr * (__uint_as_float(dv[x][c]) - Drow) : 0.f;
+                            for (int e = 0; e < 8; ++e) {
+                                const int c = 2 * e, key = key0 + 16 * x + c;
+                                float2 y = ffma2(make_float2(__uint_as_float(sv[x][c]), __uint_as_float(sv[x][c + 1])), c22, nlse2);
+                                y = make_float2(fast_exp2(y.x), fast_exp2(y.y));
+                                y = fmul2(y, fadd2(make_float2(__uint_as_float(dv[x][c]), __uint_as_float(dv[x][c + 1])), nd2));
+                                if (!whole) {
+                                    y.x = key <= khi && (key > klo || key < ksink) ? y.x : 0.f;
+                                    y.y = key < khi && (key >= klo || key + 1 < ksink) ? y.y : 0.f;
+                                }
+                                split_pair2(y, hi[e], lo[e]);
                             }
-                            split_q_pair(ds[0], ds[1], hi[e], lo[e]);
+                            tmem_st8(d_at + 8 * x, hi);
+                            tmem_st8(d_at + 16 + 8 * x, lo);
                         }
-                        tmem_st8(d_at + 8 * x, hi);
-                        tmem_st8(d_at + 16 + 8 * x, lo);
                     }
                     tmem_wait_st();
                     tc_fence_before();
@@ -309,22 +320,22 @@ __global__ void __launch_bounds__(512, 1) sink_dq_tc_kernel(const __grid_constan
         const int rw = warp & 3, row = rw * 32 + lane, tid = threadIdx.x - 384;
         float *tp = reinterpret_cast<float *>(smem + C::TP_OFF);
         const bool v8 = (reinterpret_cast<uintptr_t>(p.dq) & 31) == 0;
-        // A thread sums column tid % 32 of each 32 over rows of one head: of PER heads with the group of 32 threads
-        // (G >= 4), or with 4 / G groups a head (G < 4), every 4 / G-th token each
-        constexpr int PER = G >= 4 ? G / 4 : 1, SPLIT = G >= 4 ? 1 : 4 / G;
-        float sa[D / 32][PER], sb[D / 32][PER];
+        // A thread sums column tid % 16 of each 16 over rows of one head: one of 8 groups of threads, 8 / G of them a
+        // head, every 8 / G-th token each (G <= 8), or two heads a group
+        constexpr int PER = G == 16 ? 2 : 1, SPLIT = G >= 8 ? 1 : 8 / G;
+        float sa[D / 16][PER], sb[D / 16][PER];
 #pragma unroll
-        for (int c = 0; c < D / 32; ++c)
+        for (int c = 0; c < D / 16; ++c)
 #pragma unroll
             for (int e = 0; e < PER; ++e)
                 sa[c][e] = sb[c][e] = 0.f;
-        const int grp = tid >> 5, h0 = G >= 4 ? grp * PER : grp % G, first = G >= 4 ? 0 : grp / G;
+        const int grp = tid >> 4, col = tid & 15, h0 = G == 16 ? 2 * grp : grp % G, first = G == 16 ? 0 : grp / G;
         auto flush = [&](int g) {
 #pragma unroll
-            for (int c = 0; c < D / 32; ++c)
+            for (int c = 0; c < D / 16; ++c)
 #pragma unroll
                 for (int e = 0; e < PER; ++e) {
-                    const int at = (g * G + h0 + e) * D + 32 * c + (tid & 31);
+                    const int at = (g * G + h0 + e) * D + 16 * c + col;
                     atomicAdd(p.dalpha + at, sa[c][e]);
                     atomicAdd(p.dbeta + at, sb[c][e]);
                     sa[c][e] = sb[c][e] = 0.f;
@@ -340,31 +351,39 @@ __global__ void __launch_bounds__(512, 1) sink_dq_tc_kernel(const __grid_constan
                 cur_g = g;
             }
             const int t = tl.u0 + row / G, h = g * G + row % G;
-            float *dst = p.dq + ((static_cast<long long>(b) * p.T + t) * p.Hq + h) * D;
-            const long long x0 = (static_cast<long long>(b) * p.T + tl.u0) * p.Hq + g * G;
+            const bool live = t < p.T;
+            const long long at0 = ((static_cast<long long>(b) * p.T + (live ? t : 0)) * p.Hq + h) * D;
+            float *dst = p.dq + at0;
+            const uint4 *xrow = reinterpret_cast<const uint4 *>(p.q + at0);
             for (int r0 = 0; r0 < tl.rounds; r0 += C::RUN, ++run) {
                 const bool last = r0 + C::RUN >= tl.rounds;
                 const int buf = run & 1;
+                uint4 xa = __ldg(xrow), xb = __ldg(xrow + 1);  // 16 values of x, a step ahead
                 const bool got = warp_wait(&dq_full[buf], static_cast<uint32_t>((run >> 1) & 1));
                 if (!(ok = bar_red_and(1, 128, got)))
                     break;
                 tc_fence_after();
                 const uint32_t at = tbase + (static_cast<uint32_t>(rw * 32) << 16) + C::TM_DQ + D * buf;
 #pragma unroll
-                for (int c = 0; c < D / 32; ++c) {
-                    uint32_t w[32];
-                    tmem_ld32(at + 32 * c, w);
+                for (int c = 0; c < D / 16; ++c) {
+                    uint32_t w[16];
+                    tmem_ld16(at + 16 * c, w);
+                    const uint32_t xw[8] = {xa.x, xa.y, xa.z, xa.w, xb.x, xb.y, xb.z, xb.w};
+                    if (c + 1 < D / 16) {
+                        xa = __ldg(xrow + 2 * c + 2);
+                        xb = __ldg(xrow + 2 * c + 3);
+                    }
                     tmem_wait_ld();
-                    if (c == D / 32 - 1) {
+                    if (c == D / 16 - 1) {
                         tc_fence_before();
                         __syncwarp();
                         if (lane == 0)
                             mbar_arrive(&dq_free[buf]);
                     }
-                    if (r0 > 0 && t < p.T)
+                    if (r0 > 0 && live)
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 y = *reinterpret_cast<const float4 *>(dst + 32 * c + e);
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 y = *reinterpret_cast<const float4 *>(dst + 16 * c + e);
                             w[e] = __float_as_uint(__uint_as_float(w[e]) + y.x);
                             w[e + 1] = __float_as_uint(__uint_as_float(w[e + 1]) + y.y);
                             w[e + 2] = __float_as_uint(__uint_as_float(w[e + 2]) + y.z);
@@ -372,30 +391,29 @@ __global__ void __launch_bounds__(512, 1) sink_dq_tc_kernel(const __grid_constan
                         }
                     if (last) {
 #pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const float y = t < p.T ? __uint_as_float(w[e]) * p.scale : 0.f;
-                            tp[row * 33 + e] = y;
-                            w[e] = __float_as_uint(y);
-                        }
+                        for (int e = 0; e < 16; e += 4) {
+                            const float4 a = __ldg(reinterpret_cast<const float4 *>(p.alpha + h * D + 16 * c + e));
+                            const float2 x0 = unpack_bf16x2(xw[e / 2]), x1 = unpack_bf16x2(xw[e / 2 + 1]);
+                            const float xv[4] = {x0.x, x0.y, x1.x, x1.y}, av[4] = {a.x, a.y, a.z, a.w};
 #pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 a = __ldg(reinterpret_cast<const float4 *>(p.alpha + h * D + 32 * c + e));
-                            w[e] = __float_as_uint(__uint_as_float(w[e]) * a.x);
-                            w[e + 1] = __float_as_uint(__uint_as_float(w[e + 1]) * a.y);
-                            w[e + 2] = __float_as_uint(__uint_as_float(w[e + 2]) * a.z);
-                            w[e + 3] = __float_as_uint(__uint_as_float(w[e + 3]) * a.w);
+                            for (int q = 0; q < 4; ++q) {
+                                const float y = live ? __uint_as_float(w[e + q]) * p.scale : 0.f;
+                                tp[row * 17 + e + q] = live ? xv[q] * y : 0.f;
+                                tp[(C::ROWS + row) * 17 + e + q] = y;
+                                w[e + q] = __float_as_uint(y * av[q]);
+                            }
                         }
                     }
-                    if (t < p.T) {
+                    if (live) {
 #pragma unroll
-                        for (int e = 0; e < 32; e += 8) {
-                            const uint4 a = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
+                        for (int e = 0; e < 16; e += 8) {
+                            const uint4 y = make_uint4(w[e], w[e + 1], w[e + 2], w[e + 3]);
                             const uint4 z = make_uint4(w[e + 4], w[e + 5], w[e + 6], w[e + 7]);
                             if (v8) {
-                                st_global_v8(dst + 32 * c + e, a, z);
+                                st_global_v8(dst + 16 * c + e, y, z);
                             } else {
-                                *reinterpret_cast<uint4 *>(dst + 32 * c + e) = a;
-                                *reinterpret_cast<uint4 *>(dst + 32 * c + e + 4) = z;
+                                *reinterpret_cast<uint4 *>(dst + 16 * c + e) = y;
+                                *reinterpret_cast<uint4 *>(dst + 16 * c + e + 4) = z;
                             }
                         }
                     }
@@ -404,14 +422,11 @@ __global__ void __launch_bounds__(512, 1) sink_dq_tc_kernel(const __grid_constan
 #pragma unroll
                         for (int e = 0; e < PER; ++e) {
                             float ya = 0.f, yb = 0.f;
-#pragma unroll 8
-                            for (int k = first; k < TOK; k += SPLIT) {
-                                const float y = tp[(k * G + h0 + e) * 33 + (tid & 31)];
-                                uint32_t x = 0;
-                                if (tl.u0 + k < p.T)
-                                    x = p.q[(x0 + static_cast<long long>(k) * p.Hq + h0 + e) * D + 32 * c + (tid & 31)];
-                                ya = fmaf(__uint_as_float(x << 16), y, ya);
-                                yb += y;
+#pragma unroll
+                            for (int k = 0; k < TOK / SPLIT; ++k) {
+                                const int r = (first + k * SPLIT) * G + h0 + e;
+                                ya += tp[r * 17 + col];
+                                yb += tp[(C::ROWS + r) * 17 + col];
                             }
                             sa[c][e] += ya;
                             sb[c][e] += yb;

@@ -23,9 +23,6 @@
 //
 //   When the window is so wide that a tile's band does not fit in the ring,
 //   blocks are streamed once per tile instead (same code, no reuse).
-//
-//   SINK: keys 0 .. sinks-1 (at most one block) stay visible to every later row.  A tile
-//   whose band begins behind block 0 streams that block before its band.
 #include "common.cuh"
 #include "kernels.cuh"
 #include "xattn.cuh"
@@ -68,7 +65,7 @@ __device__ __forceinline__ int swa_kb_hi(int n, int TOK, int T, int KB)
     return t / KB;
 }
 
-template <int D, int G, bool SINK>
+template <int D, int G>
 __global__ void __launch_bounds__(SwaCfg<D, G>::THREADS, 1)
     swa_fwd_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                    const __grid_constant__ CUtensorMap vmap, const __grid_constant__ CUtensorMap omap,
@@ -156,8 +153,6 @@ __global__ void __launch_bounds__(SwaCfg<D, G>::THREADS, 1)
                 ok = load_q(b, g, n);
                 const int hi = swa_kb_hi(n, C::TOK, p.T, C::KB);
                 int kb = p.reuse ? next_kb : swa_kb_lo(n, C::TOK, p.window, C::KB);
-                if (SINK && kb > 0 && ok)
-                    ok = load_block(b, g, 0);
                 for (; kb <= hi && ok; ++kb)
                     ok = load_block(b, g, kb);
                 next_kb = kb;
@@ -247,11 +242,8 @@ __global__ void __launch_bounds__(SwaCfg<D, G>::THREADS, 1)
 
             const int kb_lo = swa_kb_lo(n, C::TOK, p.window, C::KB);
             const int kb_hi = swa_kb_hi(n, C::TOK, p.T, C::KB);
-            const int far = SINK && kb_lo > 0 ? 1 : 0;  // the sinks' block comes first
-            for (int kbi = kb_lo - far; kbi <= kb_hi; ++kbi) {
-                const bool sink_blk = SINK && kbi < kb_lo;
-                const int kb = sink_blk ? 0 : kbi;
-                const long long idx = p.reuse ? seg_base + (kb - seg_kb0) : load_idx + (kbi - kb_lo + far);
+            for (int kb = kb_lo; kb <= kb_hi; ++kb) {
+                const long long idx = p.reuse ? seg_base + (kb - seg_kb0) : load_idx + (kb - kb_lo);
                 const int s = static_cast<int>(idx % C::STAGES);
                 if (!mbar_wait(&full[s], static_cast<uint32_t>((idx / C::STAGES) & 1))) {
                     ok = false;
@@ -262,7 +254,7 @@ __global__ void __launch_bounds__(SwaCfg<D, G>::THREADS, 1)
 #pragma unroll
                 for (int c = 0; c < 2; ++c) {
                     const int j0 = kb * C::KB + c * 16;
-                    if (j0 > tmax || (j0 + 15 < tmin - p.window + 1 && !(SINK && j0 < p.sinks)))
+                    if (j0 > tmax || j0 + 15 < tmin - p.window + 1)
                         continue;  // chunk outside every row's window (warp-uniform)
                     float sacc[2][4];
 #pragma unroll
@@ -287,7 +279,7 @@ __global__ void __launch_bounds__(SwaCfg<D, G>::THREADS, 1)
                             for (int e = 0; e < 4; ++e) {
                                 const int j = j0 + i * 8 + qd + (e & 1);
                                 const int t = (e & 2) ? tB : tA;
-                                if (!(j <= t && (j > t - p.window || (SINK && j < p.sinks)) && j >= 0))
+                                if (!(j <= t && j > t - p.window && j >= 0))
                                     sacc[i][e] = NEG_INF;
                             }
                     }
@@ -327,25 +319,12 @@ __global__ void __launch_bounds__(SwaCfg<D, G>::THREADS, 1)
                     pa[1] = pack_bf16x2(pr[0][2], pr[0][3]);
                     pa[2] = pack_bf16x2(pr[1][0], pr[1][1]);
                     pa[3] = pack_bf16x2(pr[1][2], pr[1][3]);
-                    // V rows of the sinks' block that are no sinks (they may be any values far from these rows):
-                    // zeros; this lane holds rows c * 16 + qd, qd + 1 (v0, v2) and 8 further (v1, v3)
-                    uint32_t keep[2] = {0xffffffffu, 0xffffffffu};
-                    if (SINK && sink_blk)
-#pragma unroll
-                        for (int i = 0; i < 2; ++i) {
-                            const int j = j0 + 8 * i + qd;
-                            keep[i] = j + 1 < p.sinks ? 0xffffffffu : (j < p.sinks ? 0x0000ffffu : 0u);
-                        }
 #pragma unroll
                     for (int dp = 0; dp < D / 16; ++dp) {
                         uint32_t v0, v1, v2, v3;
                         const uint32_t a = vbase + (dp * 16 / 64) * C::KV_SLAB +
                                            sw128_offset(c * 16 + ld_row, ((dp * 16) % 64) / 8 + ld_hi);
                         ldsm_x4_trans(a, v0, v1, v2, v3);
-                        if (SINK) {
-                            v0 &= keep[0], v2 &= keep[0];
-                            v1 &= keep[1], v3 &= keep[1];
-                        }
                         mma_16816(o[2 * dp], pa, v0, v1);
                         mma_16816(o[2 * dp + 1], pa, v2, v3);
                     }
@@ -367,7 +346,7 @@ __global__ void __launch_bounds__(SwaCfg<D, G>::THREADS, 1)
                     for (int kb = kb_lo; kb <= rel_hi; ++kb)
                         mbar_arrive(&empty[static_cast<int>((seg_base + (kb - seg_kb0)) % C::STAGES)]);
             } else {
-                load_idx += kb_hi - kb_lo + 1 + far;
+                load_idx += kb_hi - kb_lo + 1;
             }
 
             // ---- epilogue: normalise, stage as bf16 (128-byte swizzle), TMA store
@@ -429,7 +408,7 @@ static cudaError_t launch_swa_t(const CUtensorMap &q, const CUtensorMap &k, cons
                                 cudaStream_t stream)
 {
     using C = SwaCfg<D, G>;
-    auto kern = p.sinks > 0 ? swa_fwd_kernel<D, G, true> : swa_fwd_kernel<D, G, false>;
+    auto kern = swa_fwd_kernel<D, G>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess)
         return e;
@@ -450,13 +429,13 @@ cudaError_t launch_swa(int D, int G, const CUtensorMap &q, const CUtensorMap &k,
     p.tiles_per_stream = (p.row_end + TOK - 1) / TOK - p.n_base;
     // widest band of key blocks any tile can need (worst-case alignment)
     const long long band = (static_cast<long long>(p.window) - 1 + TOK + KB - 1) / KB + 1;
-    p.reuse = band <= STAGES && p.sinks == 0 ? 1 : 0;
+    p.reuse = band <= STAGES ? 1 : 0;
     p.total_tiles *= p.tiles_per_stream;
     // tensor-memory kernel whenever a tile's whole band fits its ring and tensor memory
-    if (p.sinks == 0 && swa_tc_supported(D, G, p.window))
+    if (p.sinks > 0)
+        return launch_swa_sink_tc(D, G, q, k, v, p, num_sms, stream);  // where swa_sink_tc_supported
+    if (swa_tc_supported(D, G, p.window))
         return launch_swa_tc(D, G, q, k, v, o, p, num_sms, stream);
-    if (p.sinks > 0 && swa_sink_tc_supported(D, G, p.window))
-        return launch_swa_sink_tc(D, G, q, k, v, p, num_sms, stream);
 #define ORTHROS_SWA_CASE(DD, GG) \
     if (D == DD && G == GG)      \
         return launch_swa_t<DD, GG>(q, k, v, o, p, num_sms, stream);

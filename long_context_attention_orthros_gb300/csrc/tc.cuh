@@ -213,7 +213,7 @@ __device__ __forceinline__ uint4 k_to_fp16_scaled(uint4 u, float sd)
 // `mirror` bytes further when mirror != 0) and e is stored at kexp[row].  Called by the whole
 // warp.
 template <int SLABS, bool SMALL = false>
-__device__ __noinline__ void shift_key_rows(uint8_t *blk, int slab_bytes, int mirror, int rsub, int rstep, int nrows,
+__device__ ORTHROS_RARE void shift_key_rows(uint8_t *blk, int slab_bytes, int mirror, int rsub, int rstep, int nrows,
                                             int c8, int8_t *kexp, bool &bad)
 {
 #pragma unroll 1
@@ -250,7 +250,7 @@ __device__ __noinline__ void shift_key_rows(uint8_t *blk, int slab_bytes, int mi
 // wmask is set (the converter warp owning the row has shifted some of its rows), else 0.  A logit that is
 // no longer finite sets bad, unless its column lies behind the last that counts (it is masked later).
 // Called by the whole warp; the caller reloads the chunk afterwards.
-static __device__ __noinline__ void unshift_chunk32(uint32_t taddr, const int8_t *ke, int row0, uint32_t wmask, int period,
+static __device__ ORTHROS_RARE void unshift_chunk32(uint32_t taddr, const int8_t *ke, int row0, uint32_t wmask, int period,
                                              int per, bool &bad, int last = 31)
 {
     uint32_t v[32];

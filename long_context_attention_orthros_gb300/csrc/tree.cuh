@@ -39,7 +39,7 @@ cudaError_t launch_tree(int D, const TreeMaps &maps, TreeParams p, void *workspa
 
 // the tensor-memory kernel; tr: rows of a tile, 128 or 256
 constexpr int TREE_TC_CTAS = 152;  // one on each of 152 SMs
-constexpr int TREE_TC_COST = 5;    // what a segment costs it beside its blocks
+constexpr int TREE_TC_COST = 10;   // what a segment costs it beside its blocks
 cudaError_t launch_tree_tc(int D, int tr, const TreeMaps &maps, const TreeParams &p, int ctas, cudaStream_t stream);
 
 struct TreeAcceptParams {

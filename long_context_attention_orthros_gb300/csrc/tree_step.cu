@@ -1,10 +1,10 @@
-// tree_step.cu -- both streams of a tree of drafted tokens over a KV cache, on warp MMAs: the form for few
-// query rows a KV head (a node's single token, short chains), and the join of partial results.
+// tree_step.cu -- both streams of a tree of drafted tokens over a KV cache, on warp MMAs: the form for up to 8
+// query rows a KV head (a node's single token, a short chain), and the join of partial results.
 //
 // Bound by the cache's bytes (4 d a row and KV head).  The list of key blocks (tree.cuh) is shared alike by all
 // CTAs, two an SM; a CTA's blocks arrive by TMA through a ring that runs on across segment borders (one
-// producer warp); four warps take 32 keys of every other block each (16 of every block with 16 query rows), the
-// rows on the MMA's N side, and their results meet in shared memory.  A segment that one CTA holds whole is
+// producer warp); four warps take 32 keys of every other block each, the rows on the MMA's N side, and their
+// results meet in shared memory.  A segment that one CTA holds whole is
 // written at once, the others as one partial (max, sum, o) a CTA, which tree_join_kernel joins.
 //
 // The block that holds the last cached row is patched in shared memory: V rows that no query of the segment
@@ -18,13 +18,13 @@ namespace orthros {
 constexpr int TREE_CTAS = 304;  // two on each of 152 SMs
 constexpr int TREE_COST = 4;
 
-template <int D, int NT>
+template <int D>
 struct TsCfg {
-    static constexpr int TR = 8 * NT;
+    static constexpr int TR = 8;
     static constexpr int KB = TREE_KB;
     static constexpr int SLAB = KB * 128;
     static constexpr int KV_BYTES = KB * D * 2;
-    static constexpr int KT = NT == 1 ? 2 : 1;
+    static constexpr int KT = 2;  // a warp's step: two chunks of 16 keys
     static constexpr int CWARPS = 4;
     static constexpr int GROUP = 4 / KT;  // warps that share a block
     static constexpr int STAGES = D == 128 ? 2 : 4;  // a slot belongs to one group of warps: a multiple of KT
@@ -38,11 +38,11 @@ struct TsCfg {
     static_assert(2 * (SMEM + 1024) <= 233472, "two CTAs an SM");
 };
 
-template <int D, int NT>
-__global__ void __launch_bounds__(TsCfg<D, NT>::THREADS, 2)
+template <int D>
+__global__ void __launch_bounds__(TsCfg<D>::THREADS, 2)
     tree_step_kernel(const __grid_constant__ TreeMaps maps, const TreeParams p)
 {
-    using C = TsCfg<D, NT>;
+    using C = TsCfg<D>;
     extern __shared__ uint8_t smem_raw[];
     const uint32_t raw_s = smem_u32(smem_raw);
     const uint32_t pad = ((raw_s + 1023u) & ~1023u) - raw_s;
@@ -123,38 +123,33 @@ __global__ void __launch_bounds__(TsCfg<D, NT>::THREADS, 2)
             paths = tree_paths(p.parent + static_cast<long long>(b) * p.N, s.n);
             paths_b = b;
         }
-        // the lane's two rows of each eight: what they see
-        TreeRow rows[NT][2];
+        // the lane's two rows: what they see
+        TreeRow rows[2];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int e = 0; e < 2; ++e)
-                rows[nt][e] = tree_row(p, s, paths, base, (cur.tile * C::TR + 8 * nt + 2 * (lane & 3) + e) / G);
-        WarpB16<D, NT> st;
+        for (int e = 0; e < 2; ++e)
+            rows[e] = tree_row(p, s, paths, base, (cur.tile * C::TR + 2 * (lane & 3) + e) / G);
+        WarpB16<D, 1> st;
         {
             const orthros_bf16 *q = base ? p.q_new : p.qc_new;
             const float *al = base ? p.alpha : p.alpha_c, *be = base ? p.beta : p.beta_c;
+            const int row = cur.tile * C::TR + (lane >> 2), node = row / G, h = g * G + row % G;
+            const bool live = node < s.n;
+            const orthros_bf16 *x = q + ((static_cast<long long>(b) * p.N + (live ? node : 0)) * p.Hq + h) * D;
 #pragma unroll
-            for (int nt = 0; nt < NT; ++nt) {
-                const int row = cur.tile * C::TR + 8 * nt + (lane >> 2), node = row / G, h = g * G + row % G;
-                const bool live = node < s.n;
-                const orthros_bf16 *x = q + ((static_cast<long long>(b) * p.N + (live ? node : 0)) * p.Hq + h) * D;
+            for (int kt = 0; kt < D / 16; ++kt)
 #pragma unroll
-                for (int kt = 0; kt < D / 16; ++kt)
-#pragma unroll
-                    for (int hf = 0; hf < 2; ++hf) {
-                        const int d = kt * 16 + 2 * (lane & 3) + 8 * hf;
-                        uint32_t hi = 0, lo = 0;
-                        if (live) {
-                            const float2 v = unpack_bf16x2(__ldg(reinterpret_cast<const uint32_t *>(x + d)));
-                            const float2 a = __ldg(reinterpret_cast<const float2 *>(al + h * D + d));
-                            const float2 z = __ldg(reinterpret_cast<const float2 *>(be + h * D + d));
-                            split_q_pair(fmaf(v.x, a.x, z.x) * p.qscale, fmaf(v.y, a.y, z.y) * p.qscale, hi, lo);
-                        }
-                        st.qb[nt][kt][hf] = hi;
-                        st.ql[nt][kt][hf] = lo;
+                for (int hf = 0; hf < 2; ++hf) {
+                    const int d = kt * 16 + 2 * (lane & 3) + 8 * hf;
+                    uint32_t hi = 0, lo = 0;
+                    if (live) {
+                        const float2 v = unpack_bf16x2(__ldg(reinterpret_cast<const uint32_t *>(x + d)));
+                        const float2 a = __ldg(reinterpret_cast<const float2 *>(al + h * D + d));
+                        const float2 z = __ldg(reinterpret_cast<const float2 *>(be + h * D + d));
+                        split_q_pair(fmaf(v.x, a.x, z.x) * p.qscale, fmaf(v.y, a.y, z.y) * p.qscale, hi, lo);
                     }
-            }
+                    st.qb[0][kt][hf] = hi;
+                    st.ql[0][kt][hf] = lo;
+                }
         }
         st.reset();
         int span_lo, span_first;
@@ -188,14 +183,14 @@ __global__ void __launch_bounds__(TsCfg<D, NT>::THREADS, 2)
                 }
                 const uint32_t ks = sbase + slot * 2 * C::KV_BYTES;
                 if (j0 < 0) {
-                    st.template step_where<C::KT>(ks, ks + C::KV_BYTES, C::SLAB, r0, false, [&](int y, int nt, int e) {
-                        return ((rows[nt][e].mask >> y) & 1) != 0;
+                    st.template step_where<C::KT>(ks, ks + C::KV_BYTES, C::SLAB, r0, false, [&](int y, int, int e) {
+                        return ((rows[e].mask >> y) & 1) != 0;
                     });
                 } else {
                     st.template step_where<C::KT>(ks, ks + C::KV_BYTES, C::SLAB, r0, !base && r0 + WK <= end,
-                                                  [&](int y, int nt, int e) {
+                                                  [&](int y, int, int e) {
                         const int j = j0 + y;
-                        return y < end && (j >= rows[nt][e].lo || j < rows[nt][e].first);
+                        return y < end && (j >= rows[e].lo || j < rows[e].first);
                     });
                 }
                 if (patch)
@@ -210,21 +205,19 @@ __global__ void __launch_bounds__(TsCfg<D, NT>::THREADS, 2)
         // ---- the four warps' results meet in shared memory
         named_barrier(1, C::CTHREADS);  // the segment before has been read
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-            for (int r2 = 0; r2 < 2; ++r2) {
-                const int row = 8 * nt + 2 * (lane & 3) + r2, gq = lane >> 2;
-                if (gq == 0) {
-                    ms[warp * C::TR + row] = st.m[nt][r2];
-                    ls[warp * C::TR + row] = st.l[nt][r2];
-                }
-                float *po = os + (warp * C::TR + row) * D;
-#pragma unroll
-                for (int mt = 0; mt < D / 16; ++mt) {
-                    po[16 * mt + gq] = st.o[nt][mt][r2];
-                    po[16 * mt + gq + 8] = st.o[nt][mt][2 + r2];
-                }
+        for (int r2 = 0; r2 < 2; ++r2) {
+            const int row = 2 * (lane & 3) + r2, gq = lane >> 2;
+            if (gq == 0) {
+                ms[warp * C::TR + row] = st.m[0][r2];
+                ls[warp * C::TR + row] = st.l[0][r2];
             }
+            float *po = os + (warp * C::TR + row) * D;
+#pragma unroll
+            for (int mt = 0; mt < D / 16; ++mt) {
+                po[16 * mt + gq] = st.o[0][mt][r2];
+                po[16 * mt + gq + 8] = st.o[0][mt][2 + r2];
+            }
+        }
         named_barrier(1, C::CTHREADS);
         // segment bounds in the list, and who else has a share
         const long long s0 = it - cur.r + TREE_COST, s1 = it - cur.r + seg_places;
@@ -393,16 +386,17 @@ struct TreePlan {
     size_t part_ml, total;
 };
 
-// Warp MMAs keep up with memory for up to 16 query rows a KV head, and start sooner; more go to tensor memory, in
-// tiles of 128 rows or, where one does not hold them, two at a time.
+// Warp MMAs keep up with memory for up to 8 query rows a KV head (2 x 131072 rows of 32/8 heads, d = 128: 167 us; two
+// tiles of 8 would be 16 rows, which took 233 with a step of 16 keys, and 185 on tensor memory); more go to tensor
+// memory, in tiles of 128 rows or, where one does not hold them, two at a time.
 static TreePlan tree_plan(int B, int N, int L_max, int Hq, int Hkv, int D)
 {
     TreePlan pl;
     const long long R = static_cast<long long>(N) * (Hq / Hkv);
-    pl.tr = R <= 8 ? 8 : (R <= 16 ? 16 : (R <= 128 ? 128 : 256));
+    pl.tr = R <= 8 ? 8 : (R <= 128 ? 128 : 256);
     // never more CTAs than the longest caches could give places
     const long long tiles = (R + pl.tr - 1) / pl.tr;
-    const long long most = 2 * tiles * B * Hkv * (TREE_COST + 2 + (L_max + 63LL) / 64), ctas = pl.tr <= 16 ? TREE_CTAS : TREE_TC_CTAS;
+    const long long most = 2 * tiles * B * Hkv * (TREE_COST + 2 + (L_max + 63LL) / 64), ctas = pl.tr == 8 ? TREE_CTAS : TREE_TC_CTAS;
     pl.ctas = static_cast<int>(most < ctas ? most : ctas);
     const size_t slots = 2 * static_cast<size_t>(pl.ctas) * pl.tr;
     pl.part_ml = (slots * D * sizeof(float) + 255) / 256 * 256;
@@ -415,11 +409,11 @@ size_t tree_workspace_bytes(int B, int N, int L_max, int Hq, int Hkv, int D)
     return tree_plan(B, N, L_max, Hq, Hkv, D).total;
 }
 
-template <int D, int NT>
+template <int D>
 static cudaError_t launch_tree_step(const TreeMaps &maps, const TreeParams &p, int ctas, cudaStream_t stream)
 {
-    using C = TsCfg<D, NT>;
-    auto kern = tree_step_kernel<D, NT>;
+    using C = TsCfg<D>;
+    auto kern = tree_step_kernel<D>;
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess)
         return e;
@@ -439,10 +433,10 @@ static cudaError_t launch_tree_step(const TreeMaps &maps, const TreeParams &p, i
 template <int D, int TR>
 static cudaError_t launch_tree_t(const TreeMaps &maps, const TreeParams &p, int ctas, cudaStream_t stream)
 {
-    constexpr int COST = TR <= 16 ? TREE_COST : TREE_TC_COST;
+    constexpr int COST = TR == 8 ? TREE_COST : TREE_TC_COST;
     cudaError_t e;
-    if constexpr (TR <= 16)
-        e = launch_tree_step<D, TR / 8>(maps, p, ctas, stream);
+    if constexpr (TR == 8)
+        e = launch_tree_step<D>(maps, p, ctas, stream);
     else
         e = launch_tree_tc(D, TR, maps, p, ctas, stream);
     if (e != cudaSuccess)
@@ -470,11 +464,9 @@ cudaError_t launch_tree(int D, const TreeMaps &maps, TreeParams p, void *workspa
     if (D == DD && pl.tr == RR)   \
         return launch_tree_t<DD, RR>(maps, p, pl.ctas, stream);
     ORTHROS_TREE_CASE(128, 8)
-    ORTHROS_TREE_CASE(128, 16)
     ORTHROS_TREE_CASE(128, 128)
     ORTHROS_TREE_CASE(128, 256)
     ORTHROS_TREE_CASE(64, 8)
-    ORTHROS_TREE_CASE(64, 16)
     ORTHROS_TREE_CASE(64, 128)
     ORTHROS_TREE_CASE(64, 256)
 #undef ORTHROS_TREE_CASE

@@ -141,13 +141,13 @@ def test_strides_streams_and_graphs():
 @pytest.mark.parametrize("Hq,Hkv,window", [(8, 2, 128), (2, 2, 128), (8, 2, 500)])
 @pytest.mark.parametrize("value", [float("nan"), float("inf")])
 def test_rows_behind_the_sinks_do_not_reach_far(Hq, Hkv, window, value):
-    """Row 20 shares its key block with the sinks but is none: rows more than window + 128 away do not see it."""
+    """Row 20 shares its key block with the sinks but is none: it does not reach rows more than window + 256 away."""
     s = Stream(1, 1000, Hq, Hkv, 128, window, 4, seed=6)
     clean = s.run()
     v = bf(s.v)
     v[:, 20] = value
     got = orth.swa_sink_fwd(bf(s.x), bf(s.k), v, f32(s.alpha), f32(s.beta), 4, window=window)
-    far = 20 + window + 128
+    far = 20 + window + 256
     np.testing.assert_array_equal(bits(got[:, far:]), bits(clean[:, far:]))
     assert not torch.isfinite(got[:, 20].float()).any()
 
