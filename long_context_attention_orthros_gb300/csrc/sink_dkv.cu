@@ -10,11 +10,12 @@
 //   dV += P^T dO (two products), dK += dS^T q (three: the residuals' product is below fp32's rounding here)
 // The MMA's fp32 accumulators are truncated at every step, not rounded: dk of 4800 rows a key (1284 steps) came out
 // 1.9e-5 off.  So every 24 rounds (1536 rows, 288 steps) dV and dK are added to memory and begin anew.
-// Two warpgroups take 32 rows (columns) of the round each, so that a round's exponentials end while the next
-// round's S^T, dP^T run.
+// Four warpgroups take 16 rows (columns) of the round each: a warp's chain of loads, exponentials and stores is what a
+// round waits for (two warpgroups of 32 columns: 2.3 us a round).
 // Bound by the MMAs: 44 a round of 16 x (64 or 128) x 128, some 2050 cycles at d = 128.
-// Roles (384 threads, one CTA an SM): warp 0 TMA producer; warp 1 tensor memory and MMA issue; warps 2-3 the rows'
-// log-sum-exp, D and token; warps 4-7, 8-11 P^T, dS^T (lane = key) of columns 0-31, 32-63, and at the end dK, dV.
+// Roles (640 threads, one CTA an SM): warp 0 TMA producer; warp 1 tensor memory and the issue of S^T, dP^T; warp 3 that of
+// dV, dK (one thread for both spends some 90 cycles an MMA, as long as a round takes); warp 2 the rows' log-sum-exp
+// and D; warps 4-19 P^T, dS^T (lane = key), 16 columns a warpgroup, and at the end dK, dV.
 // Tensor memory: S^T at 64 u, dP^T at 128 + 64 u (buffer u), dK at 256, dV at 256 + D.  Every wait is bounded.
 #include "bwd_util.cuh"
 #include "kernels.cuh"
@@ -48,11 +49,11 @@ struct SdCfg {
     static constexpr int SMEM = USED > 120 * 1024 ? USED : 120 * 1024;  // one CTA an SM: it takes all of tensor memory
     static_assert(SMEM <= 232448, "shared memory budget");
     static constexpr uint32_t TM_S = 0, TM_DP = 128, TM_DK = 256, TM_DV = 256 + D;
-    static constexpr int THREADS = 384;
+    static constexpr int THREADS = 640;
 };
 
 template <int D, int G>
-__global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_constant__ SinkBwdMaps maps, const SinkBwdParams p)
+__global__ void __launch_bounds__(640, 1) sink_dkv_tc_kernel(const __grid_constant__ SinkBwdMaps maps, const SinkBwdParams p)
 {
     using C = SdCfg<D>;
     constexpr int TOK = C::RB / G;  // tokens of a round
@@ -85,16 +86,16 @@ __global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_consta
         mbar_init(kv_full, 1);
         for (int s = 0; s < C::STG; ++s) {
             mbar_init(&st_full[s], 1);
-            mbar_init(&meta_full[s], 2);
+            mbar_init(&meta_full[s], 1);
             mbar_init(&st_empty[s], 1);
         }
         for (int u = 0; u < 2; ++u) {
             mbar_init(&s_full[u], 1);
-            mbar_init(&p_full[u], 8);
+            mbar_init(&p_full[u], 16);
             mbar_init(&pv_done[u], 1);
         }
         mbar_init(acc_final, 1);
-        mbar_init(acc_free, 8);
+        mbar_init(acc_free, 16);
         fence_barrier_init();
     }
     if (warp == 1)
@@ -131,45 +132,11 @@ __global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_consta
             }
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        // ------------------------------------------------------------------ S^T, dP^T
+        if (elect_one()) {
             constexpr uint32_t IDESC_S = umma_idesc(128, C::RB, true, false);
-            constexpr uint32_t IDESC_D = umma_idesc(128, D, true, true);
             const uint64_t kdesc = umma_desc_sw128(sbase + C::K_OFF, 16, 1024);
             const uint64_t vdesc = umma_desc_sw128(sbase + C::V_OFF, 16, 1024);
-            // dV += P^T dO and dK += dS^T q of round j; 16 rows of P^T (dS^T) are 8 columns of its half's high
-            // parts, or of the residuals 16 columns further
-            auto accumulate = [&](int j) -> bool {
-                const int u = j & 1, s = j % C::STG;
-                if (!mbar_wait(&p_full[u], static_cast<uint32_t>((j >> 1) & 1)) ||
-                    (j > 0 && j % C::RUN == 0 && !mbar_wait(acc_free, static_cast<uint32_t>((j / C::RUN - 1) & 1))))
-                    return false;
-                tc_fence_after();
-                const uint32_t st = sbase + C::ST_OFF + s * C::ST_BYTES;
-                const uint64_t hdesc = umma_desc_sw128(st, C::RSLAB, 1024);
-                const uint64_t ldesc = umma_desc_sw128(st + C::TILE, C::RSLAB, 1024);
-                const uint64_t odesc = umma_desc_sw128(st + 2 * C::TILE, C::RSLAB, 1024);
-#pragma unroll
-                for (int kk = 0; kk < C::RB / 16; ++kk) {
-                    const uint32_t acc = (j % C::RUN > 0 || kk > 0) ? 1u : 0u;
-                    const uint64_t at = static_cast<uint64_t>(kk * (2048 >> 4));
-                    const uint32_t ph = tbase + C::TM_S + 64 * u + 32 * (kk >> 1) + 8 * (kk & 1);
-                    const uint32_t sh = ph + (C::TM_DP - C::TM_S);
-                    umma_ts(tbase + C::TM_DV, ph, odesc + at, IDESC_D, acc);
-                    umma_ts(tbase + C::TM_DV, ph + 16, odesc + at, IDESC_D, 1);
-                    umma_ts(tbase + C::TM_DK, sh, hdesc + at, IDESC_D, acc);
-                    umma_ts(tbase + C::TM_DK, sh + 16, hdesc + at, IDESC_D, 1);
-                    umma_ts(tbase + C::TM_DK, sh, ldesc + at, IDESC_D, 1);
-                }
-                // no commit that nothing waits for: round j + 2 waits for pv_done
-                if (j == rounds - 1 || j % C::RUN == C::RUN - 1)
-                    umma_commit(acc_final);
-                if (j + 2 < rounds)
-                    umma_commit(&pv_done[u]);
-                if (j + C::STG < rounds)  // the producer waits for it
-                    umma_commit(&st_empty[s]);
-                return true;
-            };
             ok = mbar_wait(kv_full, 0);
             for (int i = 0; ok && i < rounds; ++i) {
                 const int s = i % C::STG, u = i & 1;
@@ -190,36 +157,78 @@ __global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_consta
                     umma_ss(tbase + C::TM_DP + 64 * u, vdesc + ko, odesc + ro, IDESC_S, kk != 0);
                 }
                 umma_commit(&s_full[u]);
-                if (i >= 1)
-                    ok = accumulate(i - 1);
             }
-            ok = ok && accumulate(rounds - 1) && mbar_wait(acc_final, static_cast<uint32_t>(((rounds - 1) / C::RUN) & 1));
         }
-    } else if (warp < 4) {
+    } else if (warp == 3) {
+        // ------------------------------------------------------------------ dV += P^T dO, dK += dS^T q
+        if (elect_one()) {
+            constexpr uint32_t IDESC_D = umma_idesc(128, D, true, true);
+            for (int j = 0; ok && j < rounds; ++j) {
+                const int u = j & 1, s = j % C::STG;
+                if (!(ok = mbar_wait(&p_full[u], static_cast<uint32_t>((j >> 1) & 1)) &&
+                           (j == 0 || j % C::RUN != 0 || mbar_wait(acc_free, static_cast<uint32_t>((j / C::RUN - 1) & 1)))))
+                    break;
+                tc_fence_after();
+                const uint32_t st = sbase + C::ST_OFF + s * C::ST_BYTES;
+                const uint64_t hdesc = umma_desc_sw128(st, C::RSLAB, 1024);
+                const uint64_t ldesc = umma_desc_sw128(st + C::TILE, C::RSLAB, 1024);
+                const uint64_t odesc = umma_desc_sw128(st + 2 * C::TILE, C::RSLAB, 1024);
+                // 16 rows of P^T (dS^T) are 8 columns of high parts and 8 of residuals
+#pragma unroll
+                for (int kk = 0; kk < C::RB / 16; ++kk) {
+                    const uint32_t acc = (j % C::RUN > 0 || kk > 0) ? 1u : 0u;
+                    const uint64_t at = static_cast<uint64_t>(kk * (2048 >> 4));
+                    const uint32_t ph = tbase + C::TM_S + 64 * u + 16 * kk;
+                    const uint32_t sh = ph + (C::TM_DP - C::TM_S);
+                    umma_ts(tbase + C::TM_DV, ph, odesc + at, IDESC_D, acc);
+                    umma_ts(tbase + C::TM_DV, ph + 8, odesc + at, IDESC_D, 1);
+                    umma_ts(tbase + C::TM_DK, sh, hdesc + at, IDESC_D, acc);
+                    umma_ts(tbase + C::TM_DK, sh + 8, hdesc + at, IDESC_D, 1);
+                    umma_ts(tbase + C::TM_DK, sh, ldesc + at, IDESC_D, 1);
+                }
+                // no commit that nothing waits for: round j + 2 waits for pv_done
+                if (j == rounds - 1 || j % C::RUN == C::RUN - 1)
+                    umma_commit(acc_final);
+                if (j + 2 < rounds)
+                    umma_commit(&pv_done[u]);
+                if (j + C::STG < rounds)  // the producer waits for it
+                    umma_commit(&st_empty[s]);
+            }
+            ok = ok && mbar_wait(acc_final, static_cast<uint32_t>(((rounds - 1) / C::RUN) & 1));
+        }
+    } else if (warp == 2) {
         // ------------------------------------------------------------------ the rows' numbers
-        const int ct = threadIdx.x - 64;  // 0..63: one row of the round each
         for (int i = 0; ok && i < rounds; ++i) {
-            const int s = i % C::STG, t = (r0 + i) * TOK + ct / G;
-            float m_lse = -__int_as_float(0x7f800000), m_d = 0.f;  // behind the last token: weights of zero
-            if (t < p.T) {
-                const long long ri = (static_cast<long long>(b) * p.T + t) * p.Hq + g * G + ct % G;
-                m_lse = -p.lse[ri];
-                m_d = -p.Drow[ri];
+            const int s = i % C::STG;
+            float m_lse[2], m_d[2];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int ct = lane + 32 * h, t = (r0 + i) * TOK + ct / G;
+                m_lse[h] = -__int_as_float(0x7f800000);  // behind the last token: weights of zero
+                m_d[h] = 0.f;
+                if (t < p.T) {
+                    const long long ri = (static_cast<long long>(b) * p.T + t) * p.Hq + g * G + ct % G;
+                    m_lse[h] = -p.lse[ri];
+                    m_d[h] = -p.Drow[ri];
+                }
             }
             // the place is free once the stage of this round has landed: its producer waited for the MMAs of round
             // i - STG, which waited for that round's softmax
             if (!(ok = warp_wait(&st_full[s], static_cast<uint32_t>((i / C::STG) & 1))))
                 break;
             float *m = meta + s * 2 * C::RB;
-            m[ct] = m_lse;
-            m[C::RB + ct] = m_d;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                m[lane + 32 * h] = m_lse[h];
+                m[C::RB + lane + 32 * h] = m_d[h];
+            }
             __syncwarp();
             if (lane == 0)
                 mbar_arrive(&meta_full[s]);
         }
     } else {
         // ------------------------------------------------------------------ P^T, dS^T, then dK, dV
-        const int rw = warp & 3, half = (warp - 4) >> 2;
+        const int rw = warp & 3, part = (warp - 4) >> 2;  // columns 16 part .. of a round
         const int key = kt0 + rw * 32 + lane;
         const uint32_t tl = tbase + (static_cast<uint32_t>(rw * 32) << 16);
         const float2 c22 = make_float2(p.scale * kLog2eF, p.scale * kLog2eF);
@@ -229,51 +238,48 @@ __global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_consta
                        warp_wait(&meta_full[s], static_cast<uint32_t>((i / C::STG) & 1))))
                 break;
             tc_fence_after();
-            const float *m = meta + s * 2 * C::RB + 32 * half;
-            const uint32_t s_at = tl + C::TM_S + 64 * u + 32 * half, d_at = tl + C::TM_DP + 64 * u + 32 * half;
-            // what the warp's 32 keys are to the 32 rows: seen by all of them, by none, or by some
-            const int t0 = (r0 + i) * TOK + 32 * half / G, t1 = (r0 + i) * TOK + (32 * half + 31) / G;
+            const float *m = meta + s * 2 * C::RB + 16 * part;
+            const uint32_t s_at = tl + C::TM_S + 64 * u + 16 * part, d_at = tl + C::TM_DP + 64 * u + 16 * part;
+            // what the warp's 32 keys are to the 16 rows: seen by all of them, by none, or by some
+            const int t0 = (r0 + i) * TOK + 16 * part / G, t1 = (r0 + i) * TOK + (16 * part + 15) / G;
             const int k0 = kt0 + rw * 32;
             if (t1 < k0 || k0 + 31 <= t0 - p.window) {
-                const uint32_t zero[32] = {};
-                tmem_st32(s_at, zero);
-                tmem_st32(d_at, zero);
+                const uint32_t zero[16] = {};
+                tmem_st16(s_at, zero);
+                tmem_st16(d_at, zero);
             } else {
                 const bool whole = k0 + 31 <= t0 && k0 > t1 - p.window;
-                uint32_t sv[32], dv[32];
-                tmem_ld32(s_at, sv);
-                tmem_ld32(d_at, dv);
+                uint32_t sv[16], dv[16];
+                tmem_ld16(s_at, sv);
+                tmem_ld16(d_at, dv);
                 tmem_wait_ld();
+                uint32_t ph[8], pl[8], sh[8], sl[8];
 #pragma unroll
-                for (int x = 0; x < 2; ++x) {
-                    uint32_t ph[8], pl[8], sh[8], sl[8];
+                for (int e4 = 0; e4 < 4; ++e4) {
+                    const float4 nl = *reinterpret_cast<const float4 *>(m + 4 * e4);
+                    const float4 nd = *reinterpret_cast<const float4 *>(m + C::RB + 4 * e4);
 #pragma unroll
-                    for (int e4 = 0; e4 < 4; ++e4) {
-                        const float4 nl = *reinterpret_cast<const float4 *>(m + 16 * x + 4 * e4);
-                        const float4 nd = *reinterpret_cast<const float4 *>(m + C::RB + 16 * x + 4 * e4);
-#pragma unroll
-                        for (int y = 0; y < 2; ++y) {
-                            const int c = 16 * x + 4 * e4 + 2 * y, e = 2 * e4 + y;
-                            float2 pr = ffma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), c22,
-                                              y ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y));
-                            pr = make_float2(fast_exp2(pr.x), fast_exp2(pr.y));
-                            float2 ds = fmul2(pr, fadd2(make_float2(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1])),
-                                                        y ? make_float2(nd.z, nd.w) : make_float2(nd.x, nd.y)));
-                            if (!whole) {
-                                const int ta = (r0 + i) * TOK + (32 * half + c) / G, tb = (r0 + i) * TOK + (32 * half + c + 1) / G;
-                                const bool sa = key <= ta && key > ta - p.window, sb = key <= tb && key > tb - p.window;
-                                pr = make_float2(sa ? pr.x : 0.f, sb ? pr.y : 0.f);
-                                ds = make_float2(sa ? ds.x : 0.f, sb ? ds.y : 0.f);
-                            }
-                            split_pair2(pr, ph[e], pl[e]);
-                            split_pair2(ds, sh[e], sl[e]);
+                    for (int y = 0; y < 2; ++y) {
+                        const int c = 4 * e4 + 2 * y, e = 2 * e4 + y;
+                        float2 pr = ffma2(make_float2(__uint_as_float(sv[c]), __uint_as_float(sv[c + 1])), c22,
+                                          y ? make_float2(nl.z, nl.w) : make_float2(nl.x, nl.y));
+                        pr = make_float2(fast_exp2(pr.x), fast_exp2(pr.y));
+                        float2 ds = fmul2(pr, fadd2(make_float2(__uint_as_float(dv[c]), __uint_as_float(dv[c + 1])),
+                                                    y ? make_float2(nd.z, nd.w) : make_float2(nd.x, nd.y)));
+                        if (!whole) {
+                            const int ta = (r0 + i) * TOK + (16 * part + c) / G, tb = (r0 + i) * TOK + (16 * part + c + 1) / G;
+                            const bool sa = key <= ta && key > ta - p.window, sb = key <= tb && key > tb - p.window;
+                            pr = make_float2(sa ? pr.x : 0.f, sb ? pr.y : 0.f);
+                            ds = make_float2(sa ? ds.x : 0.f, sb ? ds.y : 0.f);
                         }
+                        split_pair2(pr, ph[e], pl[e]);
+                        split_pair2(ds, sh[e], sl[e]);
                     }
-                    tmem_st8(s_at + 8 * x, ph);
-                    tmem_st8(s_at + 16 + 8 * x, pl);
-                    tmem_st8(d_at + 8 * x, sh);
-                    tmem_st8(d_at + 16 + 8 * x, sl);
                 }
+                tmem_st8(s_at, ph);
+                tmem_st8(s_at + 8, pl);
+                tmem_st8(d_at, sh);
+                tmem_st8(d_at + 8, sl);
             }
             tmem_wait_st();
             tc_fence_before();
@@ -282,16 +288,17 @@ __global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_consta
                 mbar_arrive(&p_full[u]);
             if (i < rounds - 1 && i % C::RUN < C::RUN - 1)
                 continue;
-            // a run's end: dK (scaled) by the first group, dV by the second
+            // a run's end: dK (scaled) by the first two groups, dV by the others, half of the columns each
             if (!(ok = warp_wait(acc_final, static_cast<uint32_t>((i / C::RUN) & 1))))
                 break;
             tc_fence_after();
-            const float f = half ? 1.f : p.scale;
-            float *dst = (half ? p.dv : p.dk) + ((static_cast<long long>(b) * p.T + key) * p.Hkv + g) * D;
+            const bool val = part >= 2;
+            const float f = val ? 1.f : p.scale;
+            float *dst = (val ? p.dv : p.dk) + ((static_cast<long long>(b) * p.T + key) * p.Hkv + g) * D;
 #pragma unroll 1
-            for (int c = 0; c < D; c += 32) {
+            for (int c = D / 2 * (part & 1); c < D / 2 * (part & 1) + D / 2; c += 32) {
                 uint32_t w[32];
-                tmem_ld32(tl + (half ? C::TM_DV : C::TM_DK) + c, w);
+                tmem_ld32(tl + (val ? C::TM_DV : C::TM_DK) + c, w);
                 tmem_wait_ld();
                 if (key < p.T) {
 #pragma unroll
@@ -313,9 +320,9 @@ __global__ void __launch_bounds__(384, 1) sink_dkv_tc_kernel(const __grid_consta
                 mbar_arrive(acc_free);
         }
     }
-    if (!ok) {
+    if (!ok) {  // of an issuing warp its elected lane alone
         s_abort = 1;
-        if (lane == 0)
+        if (lane == 0 || warp == 1 || warp == 3)
             record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
     }
     tc_fence_before();

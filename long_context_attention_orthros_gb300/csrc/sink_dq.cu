@@ -12,7 +12,8 @@
 // one's rows arrive.  The MMA's accumulators are truncated at every step: every 32 rounds (2048 keys) dQ is added to
 // memory and begins anew.
 // Bound by memory and MMAs alike: 96 KB of rows in and 64 KB of fp32 out a tile (d = 128), 40 MMAs a round.
-// Roles (512 threads): warps 0, 2 TMA producers of rows, of keys; warp 1 tensor memory and MMA issue; warps 4-7, 8-11 dS of
+// Roles (512 threads): warps 0, 2 TMA producers of rows, of keys; warp 1 tensor memory and the issue of S, dP; warp 3 that
+// of dQ; warps 4-7, 8-11 dS of
 // a round's columns 0-31, 32-63 (lane = row); warps 12-15 dq_raw and the sums over a tile's rows: 16 columns at a
 // time x dq and dq go through a transposing buffer, where a thread sums one column of one head over its rows (loads
 // of x in that order, 2 bytes a lane, took 10 us a tile).  Every wait is bounded.
@@ -136,6 +137,15 @@ __global__ void __launch_bounds__(512, 1) sink_dq_tc_kernel(const __grid_constan
                     tma_load_4d(dst + C::QTILE, &maps.q_lo, q_full, sl * 64, g * G, tl.u0, b);
                     tma_load_4d(dst + 2 * C::QTILE, &maps.dO, q_full, sl * 64, g * G, tl.u0, b);
                 }
+                if (tau + 1 < t_end) {  // the next tile's rows on their way to L2: there is one buffer for them here
+                    const SqTile nx = sq_tile<D, G>(p, tau + 1, per_stream);
+#pragma unroll
+                    for (int sl = 0; sl < C::SLABS; ++sl) {
+                        tma_prefetch_4d(&maps.q_hi, sl * 64, nx.bh % p.Hkv * G, nx.u0, nx.bh / p.Hkv);
+                        tma_prefetch_4d(&maps.q_lo, sl * 64, nx.bh % p.Hkv * G, nx.u0, nx.bh / p.Hkv);
+                        tma_prefetch_4d(&maps.dO, sl * 64, nx.bh % p.Hkv * G, nx.u0, nx.bh / p.Hkv);
+                    }
+                }
             }
         }
     } else if (warp == 2) {
@@ -165,58 +175,28 @@ __global__ void __launch_bounds__(512, 1) sink_dq_tc_kernel(const __grid_constan
             }
         }
     } else if (warp == 1) {
-        // ------------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        // ------------------------------------------------------------------ S, dP
+        if (elect_one()) {
             constexpr uint32_t IDESC_S = umma_idesc(128, C::KB, true, false), IDESC_S32 = umma_idesc(128, 32, true, false);
-            constexpr uint32_t IDESC_Q = umma_idesc(128, D, true, true);
             const uint64_t hdesc = umma_desc_sw128(sbase + C::Q_OFF, 16, 1024);
             const uint64_t ldesc = umma_desc_sw128(sbase + C::Q_OFF + C::QTILE, 16, 1024);
             const uint64_t odesc = umma_desc_sw128(sbase + C::Q_OFF + 2 * C::QTILE, 16, 1024);
             long long i = 0;
             int j = 0;
-            // the round before, whose dQ is issued after this round's S, dP
-            bool have = false, before_sink = false, run_first = false, run_last = false;
-            int run = 0;  // runs begun
-            auto accumulate = [&](long long k) -> bool {
-                const int u = static_cast<int>(k & 1), s = static_cast<int>(k % C::STG);
-                if (run_first)
-                    ++run;
-                const int buf = (run - 1) & 1;
-                if (!mbar_wait(&p_full[u], static_cast<uint32_t>((k >> 1) & 1)) ||
-                    (run_first && run > 2 && !mbar_wait(&dq_free[buf], static_cast<uint32_t>(((run - 1) / 2 - 1) & 1))))
-                    return false;
-                tc_fence_after();
-                const uint64_t kdesc = umma_desc_sw128(sbase + C::ST_OFF + s * 2 * C::KTILE, C::KSLAB, 1024);
-                const uint32_t to = tbase + C::TM_DQ + D * buf;
-                for (int kk = 0; kk < (before_sink ? 2 : 4); ++kk) {
-                    const uint32_t a = tbase + C::TM_DP + 64 * u + 32 * (kk >> 1) + 8 * (kk & 1);
-                    const uint64_t bd = kdesc + static_cast<uint64_t>(kk * (2048 >> 4));
-                    umma_ts(to, a, bd, IDESC_Q, run_first && kk == 0 ? 0u : 1u);
-                    umma_ts(to, a + 16, bd, IDESC_Q, 1);
-                }
-                umma_commit(&ds_free[u]);
-                umma_commit(&kv_empty[s]);
-                if (run_last)
-                    umma_commit(&dq_full[buf]);
-                return true;
-            };
             for (long long tau = t_begin; ok && tau < t_end; ++tau, ++j) {
                 const SqTile tl = sq_tile<D, G>(p, tau, per_stream);
-                if (have)  // the tile before ends while this one's rows arrive
-                    ok = accumulate(i - 1);
-                have = false;
-                if (!(ok = ok && mbar_wait(q_full, static_cast<uint32_t>(j & 1))))
+                if (!(ok = mbar_wait(q_full, static_cast<uint32_t>(j & 1))))
                     break;
                 for (int r = 0; ok && r < tl.rounds; ++r, ++i) {
                     const int s = static_cast<int>(i % C::STG), u = static_cast<int>(i & 1);
-                    const bool sink = r < tl.far;
+                    // S / dP buffer u is free once dQ of round i - 2 has read dS from it
                     if (!(ok = mbar_wait(&kv_full[s], static_cast<uint32_t>((i / C::STG) & 1)) &&
                                (i < 2 || mbar_wait(&ds_free[u], static_cast<uint32_t>(((i - 2) >> 1) & 1)))))
                         break;
                     tc_fence_after();
                     const uint32_t st = sbase + C::ST_OFF + s * 2 * C::KTILE;
                     const uint64_t kdesc = umma_desc_sw128(st, 16, 1024), vdesc = umma_desc_sw128(st + C::KTILE, 16, 1024);
-                    const uint32_t idesc = sink ? IDESC_S32 : IDESC_S;
+                    const uint32_t idesc = r < tl.far ? IDESC_S32 : IDESC_S;
 #pragma unroll
                     for (int kk = 0; kk < D / 16; ++kk) {
                         const uint32_t qo = static_cast<uint32_t>((kk >> 2) * C::QSLAB + (kk & 3) * 32) >> 4;
@@ -228,23 +208,51 @@ __global__ void __launch_bounds__(512, 1) sink_dq_tc_kernel(const __grid_constan
                     umma_commit(&s_full[u]);
                     if (r == tl.rounds - 1)
                         umma_commit(q_free);
-                    if (have)
-                        ok = accumulate(i - 1);
-                    have = true;
-                    before_sink = sink;
-                    run_first = r % C::RUN == 0;
-                    run_last = r == tl.rounds - 1 || r % C::RUN == C::RUN - 1;
                 }
             }
-            if (ok && have)
-                ok = accumulate(i - 1);
+            // no commit is in flight when the CTA ends
+            if (ok && j > 0)
+                ok = mbar_wait(q_free, static_cast<uint32_t>((j - 1) & 1));
+        }
+    } else if (warp == 3) {
+        // ------------------------------------------------------------------ dQ += dS K
+        if (elect_one()) {
+            constexpr uint32_t IDESC_Q = umma_idesc(128, D, true, true);
+            long long i = 0;
+            int run = 0;
+            for (long long tau = t_begin; ok && tau < t_end; ++tau) {
+                const SqTile tl = sq_tile<D, G>(p, tau, per_stream);
+                for (int r = 0; ok && r < tl.rounds; ++r, ++i) {
+                    const int s = static_cast<int>(i % C::STG), u = static_cast<int>(i & 1), buf = run & 1;
+                    const bool begin = r % C::RUN == 0, end = r == tl.rounds - 1 || r % C::RUN == C::RUN - 1;
+                    if (!(ok = mbar_wait(&p_full[u], static_cast<uint32_t>((i >> 1) & 1)) &&
+                               (!begin || run < 2 || mbar_wait(&dq_free[buf], static_cast<uint32_t>((run / 2 - 1) & 1)))))
+                        break;
+                    tc_fence_after();
+                    const uint64_t kdesc = umma_desc_sw128(sbase + C::ST_OFF + s * 2 * C::KTILE, C::KSLAB, 1024);
+                    const uint32_t to = tbase + C::TM_DQ + D * buf;
+                    const int steps = r < tl.far ? 2 : 4;  // 16 keys each
+#pragma unroll
+                    for (int kk = 0; kk < 4; ++kk)
+                        if (kk < steps) {
+                            const uint32_t a = tbase + C::TM_DP + 64 * u + 32 * (kk >> 1) + 8 * (kk & 1);
+                            const uint64_t bd = kdesc + static_cast<uint64_t>(kk * (2048 >> 4));
+                            umma_ts(to, a, bd, IDESC_Q, begin && kk == 0 ? 0u : 1u);
+                            umma_ts(to, a + 16, bd, IDESC_Q, 1);
+                        }
+                    umma_commit(&ds_free[u]);
+                    umma_commit(&kv_empty[s]);
+                    if (end) {
+                        umma_commit(&dq_full[buf]);
+                        ++run;
+                    }
+                }
+            }
             // no commit is in flight when the CTA ends
             for (long long k = i > 2 ? i - 2 : 0; ok && k < i; ++k)
                 ok = mbar_wait(&ds_free[k & 1], static_cast<uint32_t>((k >> 1) & 1));
             for (long long k = i > C::STG ? i - C::STG : 0; ok && k < i; ++k)
                 ok = mbar_wait(&kv_empty[k % C::STG], static_cast<uint32_t>((k / C::STG) & 1));
-            if (ok && j > 0)
-                ok = mbar_wait(q_free, static_cast<uint32_t>((j - 1) & 1));
         }
     } else if (warp >= 4 && warp < 12) {
         // ------------------------------------------------------------------ dS (lane = row)
@@ -439,9 +447,9 @@ __global__ void __launch_bounds__(512, 1) sink_dq_tc_kernel(const __grid_constan
         if (ok && cur_g >= 0)
             flush(cur_g);
     }
-    if (!ok) {
+    if (!ok) {  // of an issuing warp its elected lane alone
         s_abort = 1;
-        if (lane == 0)
+        if (lane == 0 || warp == 1 || warp == 3)
             record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
     }
     tc_fence_before();

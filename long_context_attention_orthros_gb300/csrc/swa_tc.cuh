@@ -42,6 +42,9 @@
 // left it behind; its logits follow the band's in tensor memory (8 more MMAs of N = 32, and
 // 2 more of P V), its keys count for row t where j < sinks and j <= t - window, so that a key
 // never counts twice.  One ring slot and the spare columns of tensor memory pay for it.
+// The 28 MMAs of such a tile are more than one thread issues in the time that the tile's bytes
+// take (some 75 cycles each: 2 x 131072 tokens of 32/8 heads, d = 128 took 1115 us): warp 16
+// issues those of O = P V beside warp 1's of S.
 #pragma once
 
 #include <cuda_fp16.h>
@@ -61,7 +64,7 @@ struct TcCfg {
     static constexpr int STAGES = SINK ? 7 : 8;
     static constexpr int SLOTS = STAGES + (SINK ? 1 : 0);  // the last one for the sinks' block
     static constexpr int MIRROR = NB - 1;
-    static constexpr int THREADS = 512;
+    static constexpr int THREADS = SINK ? 544 : 512;  // warp 16 issues P V
     static constexpr int SLOT = KB * 128;                   // one slot of one slab array
     static constexpr int K_SLAB = (SLOTS + MIRROR) * SLOT;  // one K slab array (with mirrors)
     static constexpr int V_SLAB = SLOTS * SLOT;
@@ -106,7 +109,7 @@ __device__ __forceinline__ int tc_kb_hi(int n, int TOK, int T)
 // LSE: also store each row's log-sum-exp (p.lse); a separate instance, so that the
 // inference path carries no trace of it
 template <int D, int G, bool RANGE, bool LSE, bool SINK>
-__global__ void __launch_bounds__(512, 1)
+__global__ void __launch_bounds__(SINK ? 544 : 512, 1)
     swa_tc_kernel(const __grid_constant__ CUtensorMap qmap, const __grid_constant__ CUtensorMap kmap,
                   const __grid_constant__ CUtensorMap vmap, const SwaParams p)
 {
@@ -252,7 +255,7 @@ __global__ void __launch_bounds__(512, 1)
         }
     } else if (warp == 1) {
         // ------------------------------------------------------------------ MMA issuer
-        if (lane == 0) {
+        if (SINK ? elect_one() : lane == 0) {
             bool ok = true;
             constexpr uint32_t IDESC_PV = umma_idesc(128, D, true, true);
             // ring position (count of K/V blocks loaded before) of the current stream segment's first block
@@ -260,11 +263,10 @@ __global__ void __launch_bounds__(512, 1)
             // the previous tile, whose PV is issued after this tile's QK
             bool have_prev = false;
             int p_nb = 0, p_klo = 0, p_seg = -1, p_idx0 = 0;
-            bool p_sink = false;                   // it has the sinks' columns
-            int sink_seg = -1, sink_count = -1;    // segment whose sinks were waited for, and how many before
+            int sink_seg = -1, sink_count = -1;  // segment whose sinks were waited for, and how many before
             int n = static_cast<int>(gt_begin % tps) - 1;  // relative to the range; na = n + p.n_base
             // O = P V for tile pit; the first `rel` blocks of its band go back to the ring
-            auto issue_pv = [&](int pit, int rel, bool rel_sink) -> bool {
+            auto issue_pv = [&](int pit, int rel) -> bool {
                 const int pbuf = pit & 1;
                 ok = mbar_wait(&p_full[pbuf], static_cast<uint32_t>((pit >> 1) & 1)) &&
                      (pit < 1 || mbar_wait(o_free, static_cast<uint32_t>((pit - 1) & 1)));
@@ -279,14 +281,7 @@ __global__ void __launch_bounds__(512, 1)
                     umma_ts(tbase + C::TM_O, s_col + 16 * j, vdesc, IDESC_PV, j != 0);
                     umma_ts(tbase + C::TM_O, s_col + 16 * j + 8, vdesc + (2048 >> 4), IDESC_PV, 1);
                 }
-                if (SINK && p_sink) {
-                    const uint64_t vdesc = umma_desc_sw128(sbase + C::V_OFF + C::STAGES * C::SLOT, C::V_SLAB, 1024);
-                    umma_ts(tbase + C::TM_O, s_col + 16 * p_nb, vdesc, IDESC_PV, 1);
-                    umma_ts(tbase + C::TM_O, s_col + 16 * p_nb + 8, vdesc + (2048 >> 4), IDESC_PV, 1);
-                }
                 umma_commit(&o_full[pbuf]);
-                if (SINK && rel_sink && p_sink)
-                    umma_commit(&empty[C::STAGES]);
 #pragma unroll 1
                 for (int r = 0; r < rel; ++r)
                     umma_commit(&empty[(p_idx0 + r) % C::STAGES]);
@@ -314,8 +309,8 @@ __global__ void __launch_bounds__(512, 1)
                     sink = SINK && na >= n_sink;
                     // a new segment's first band (a row range that starts mid-sequence) may not fit
                     // the ring next to the previous segment's last band: release that tile first
-                    if (have_prev && p_seg != seg && (p_nb + nb > C::STAGES || (SINK && sink && p_sink))) {
-                        if (!issue_pv(static_cast<int>(it - 1), p_nb, true))
+                    if (!SINK && have_prev && p_seg != seg && p_nb + nb > C::STAGES) {
+                        if (!issue_pv(static_cast<int>(it - 1), p_nb))
                             break;
                         have_prev = false;
                     }
@@ -383,8 +378,7 @@ __global__ void __launch_bounds__(512, 1)
                 }
                 // ---- O = P V for the previous tile: within a segment it keeps the blocks this tile
                 // still uses; at a segment change or after the last tile it releases its whole band
-                if (have_prev && !issue_pv(static_cast<int>(it - 1), (have && p_seg == seg) ? klo - p_klo : p_nb,
-                                           have && p_seg != seg))
+                if (!SINK && have_prev && !issue_pv(static_cast<int>(it - 1), (have && p_seg == seg) ? klo - p_klo : p_nb))
                     break;
                 if (!have)
                     break;
@@ -393,7 +387,49 @@ __global__ void __launch_bounds__(512, 1)
                 p_klo = klo;
                 p_seg = seg;
                 p_idx0 = idx0;
-                p_sink = sink;
+            }
+            if (!ok)
+                record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
+        }
+    } else if (SINK && warp == 16) {
+        // ------------------------------------------------------------------ O = P V (SINK)
+        if (elect_one()) {
+            constexpr uint32_t IDESC_PV = umma_idesc(128, D, true, true);
+            bool ok = true;
+            long long idx0 = 0;  // ring position of the tile's first block
+            int it = 0;
+            for (long long gt = gt_begin; gt < gt_end && ok;) {
+                const int n0 = seg_begin(gt), n1 = seg_end(gt, n0);
+                const bool more = gt + (n1 - n0) < gt_end;  // another segment follows
+                for (int n = n0; n < n1; ++n, ++it) {
+                    const int klo = tc_kb_lo(n, TOK, p.window), nb = tc_kb_hi(n, TOK, p.T) - klo + 1;
+                    const bool sink = n >= n_sink;
+                    const int buf = it & 1;
+                    // P is written, and O of the tile before read
+                    ok = mbar_wait(&p_full[buf], static_cast<uint32_t>((it >> 1) & 1)) &&
+                         (it < 1 || mbar_wait(o_free, static_cast<uint32_t>((it - 1) & 1)));
+                    if (!ok)
+                        break;
+                    tc_fence_after();
+                    const uint32_t s_col = tbase + buf * C::TM_SSTRIDE;
+#pragma unroll 1
+                    for (int j = 0; j < nb + (sink ? 1 : 0); ++j) {
+                        const uint32_t slot = j < nb ? static_cast<uint32_t>((idx0 + j) % C::STAGES) : C::STAGES;
+                        const uint64_t vdesc = umma_desc_sw128(sbase + C::V_OFF + slot * C::SLOT, C::V_SLAB, 1024);
+                        umma_ts(tbase + C::TM_O, s_col + 16 * j, vdesc, IDESC_PV, j != 0);
+                        umma_ts(tbase + C::TM_O, s_col + 16 * j + 8, vdesc + (2048 >> 4), IDESC_PV, 1);
+                    }
+                    umma_commit(&o_full[buf]);
+                    // blocks that the next tile does not use go back to the ring (its S has read their K: P is written);
+                    // after the CTA's last tile nothing waits for them
+                    const int rel = n + 1 < n1 ? tc_kb_lo(n + 1, TOK, p.window) - klo : (more ? nb : 0);
+                    for (int r = 0; r < rel; ++r)
+                        umma_commit(&empty[(idx0 + r) % C::STAGES]);
+                    if (sink && n + 1 == n1 && more)
+                        umma_commit(&empty[C::STAGES]);
+                    idx0 += n + 1 < n1 ? tc_kb_lo(n + 1, TOK, p.window) - klo : nb;
+                }
+                gt += n1 - n0;
             }
             if (!ok)
                 record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
@@ -698,7 +734,7 @@ __global__ void __launch_bounds__(512, 1)
             record_error(p.dev_err, ORTHROS_DEVERR_RANGE);
         if (!ok && lane == 0)
             record_error(p.dev_err, ORTHROS_DEVERR_TIMEOUT);
-    } else {
+    } else if (warp < 16) {
         // ------------------------------------------------------------------ query preparation
         const int tid = threadIdx.x - 384;  // 0..127
         const int cr = tid % C::CPR;        // this thread's 16-byte chunk within a query row
