@@ -553,7 +553,7 @@ def _word(t, dev: int):
 def _invoke(name: str, dev: int, *args) -> None:
     """Call an entry point on device `dev` and its current stream (the last argument of each)."""
     fn = getattr(_lib or lib(), name)
-    if torch.cuda.current_device() == dev:
+    if torch._C._cuda_getDevice() == dev:  # CUDA is initialised: there are tensors on it
         st = fn(*args, torch._C._cuda_getCurrentRawStream(dev))
     else:
         with torch.cuda.device(dev):
@@ -732,24 +732,29 @@ def swa_sink_fwd(q_raw, k, v, alpha, beta, sinks: int, window: int = 128, scale=
     (0 <= sinks <= 32).  Only rows row_begin..row_end-1 (default all T) are computed, by swa_fwd_rows'
     rules.  With lse (fp32 [B, T, Hq], or True for a fresh one) each row's log-sum-exp is written too,
     for swa_sink_bwd, and (out, lse) is returned."""
-    B, T, Hkv, d = k.shape
+    B, T, Hkv, d = kv_shape = k.shape
     dev = k.get_device()
     if dev < 0:
         _refuse(k, "k", "bf16 CUDA tensor [B, T, Hkv, d]")
-    _, ks, kv = _kv_pair(k, v, B, Hkv, d, dev)
-    if q_raw.dim() != 4 or q_raw.shape[0] != B or q_raw.shape[1] < T or q_raw.shape[3] != d:
+    ka, ks = _rows(k, "k", kv_shape, dev)
+    va, vs = _rows(v, "v", kv_shape, dev)
+    if vs != ks:
+        raise OrthrosError("k and v must have the same shape and strides")
+    q_shape = q_raw.shape
+    if len(q_shape) != 4 or q_shape[0] != B or q_shape[1] < T or q_shape[3] != d:
         raise OrthrosError("q_raw shape does not match k")
-    Hq = q_raw.shape[2]
-    qa, qs = _rows(q_raw, "q_raw", q_raw.shape, dev)
+    Tq, Hq = q_shape[1], q_shape[2]
+    qa, qs = _rows(q_raw, "q_raw", q_shape, dev)
     if qs == 0:  # dense, but it may hold appended copies
-        qs = _bf16_rows(q_raw, "q_raw")
+        qs = Tq * Hq * d
     shape = (B, T, Hq, d)
     if out is None:
-        out = torch.empty(shape, dtype=torch.bfloat16, device=k.device)
+        out = torch.empty_like(q_raw) if Tq == T and q_raw.is_contiguous() else torch.empty(
+            shape, dtype=torch.bfloat16, device=k.device)
     oa, os_ = _rows(out, "out", shape, dev)
     if lse is True:
         lse = torch.empty((B, T, Hq), dtype=torch.float32, device=k.device)
-    _invoke("orthros_swa_sink_fwd", dev, qa, *kv, _dense(alpha, "alpha", torch.float32, (Hq, d), dev),
+    _invoke("orthros_swa_sink_fwd", dev, qa, ka, va, _dense(alpha, "alpha", torch.float32, (Hq, d), dev),
             _dense(beta, "beta", torch.float32, (Hq, d), dev), oa,
             _optional(lse, "lse", torch.float32, (B, T, Hq), dev), B, T, Hq, Hkv, d, int(window), int(sinks),
             _scale(scale, d), qs, ks, os_, int(row_begin), T if row_end is None else int(row_end), _word(dev_err, dev))

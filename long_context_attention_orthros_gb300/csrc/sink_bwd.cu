@@ -6,11 +6,13 @@
 // Everything leaves in fp32 and is computed to match: k, v, x and dO are bf16 and enter the products as they are;
 // q, dS and P enter as a bf16 high part plus residual (their product's relative error some 2^-17, where one
 // bf16 would give 2^-9); sums, exponents and D are fp32.  Launches:
-//   sink_rows_kernel    q's two parts, D and the log-sum-exp in log2 units, one pass over x, o, dO
+//   sink_keys_kernel    q's two parts, D and the log-sum-exp in log2 units, one pass over x, o, dO; in the same pass
+//                       the sinks' share of dk, dv from the rows behind their window: every row adds to the same few
+//                       keys, so the tokens are split over CTAs, which leave partial sums
+//   sink_rows_kernel    the pass alone, where no row has a sink behind its window
 //   sink_dq_tc_kernel   dq over a row's window and the sinks; dalpha, dbeta by atomics (sink_dq.cu)
 //   sink_dkv_tc_kernel  dk, dv of the window's part (sink_dkv.cu)
-//   sink_keys_kernel    the sinks' share of the rows behind their window: every row adds to the same few keys, so
-//                       the tokens are split over CTAs, whose partial sums sink_join_kernel adds to dk, dv in order
+//   sink_join_kernel    adds the partial sums to dk, dv in order
 #include "bwd_util.cuh"
 #include "kernels.cuh"
 #include "xattn.cuh"
@@ -62,10 +64,11 @@ __global__ void __launch_bounds__(256) sink_rows_kernel(const SinkBwdParams p)
 
 // ------------------------------------------------------------------ the sinks' dk, dv
 
-// Rows t and sinks j <= t - window.  A CTA has one (sequence, query head) and a run of tokens, a warp 16 tokens at a
+// The prepared rows, and rows t against sinks j <= t - window.  A CTA has one (sequence, query head) and a run of tokens, a warp 16 tokens at a
 // time: the (up to 16) sinks on M and the tokens on N for S^T = K q^T and dP^T = V dO^T, whose fragments are then the
 // operands of Y = dS^T q and dV = P^T dO (tokens on K).  Operands come straight from global memory, 16 bytes a
-// lane, with the head dimension in the order in which they lie there.  More than 16 sinks: blockIdx.z.
+// lane, with the head dimension in the order in which they lie there.  More than 16 sinks: blockIdx.z (the first
+// 16 write the prepared rows).
 constexpr int SK_M = 16;
 
 template <int D>
@@ -73,7 +76,7 @@ __global__ void __launch_bounds__(128, 2) sink_keys_kernel(const SinkBwdParams p
 {
     constexpr int KK = D / 32;  // runs of 32 values: a lane has 8 of each row
     __shared__ __align__(16) uint4 ka_s[D / 16][32], va_s[D / 16][32];  // K, V as A fragments
-    __shared__ __align__(16) float red[SK_M][2 * D];
+    __shared__ __align__(16) float red[SK_M][2 * D], ab[2 * D];
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3, rq = lane >> 2;
     const int chunk = blockIdx.x, bh = blockIdx.y, b = bh / p.Hq, h = bh % p.Hq, g = h / (p.Hq / p.Hkv);
     const int s0 = SK_M * blockIdx.z, ns = min(SK_M, count - s0);
@@ -87,6 +90,12 @@ __global__ void __launch_bounds__(128, 2) sink_keys_kernel(const SinkBwdParams p
         const int kt = x / 32, l = x % 32, d = 32 * (kt / 2) + 8 * (l & 3) + 4 * (kt & 1), j = l >> 2;
         ka_s[kt][l] = make_uint4(pair(p.k, j, d), pair(p.k, j + 8, d), pair(p.k, j, d + 2), pair(p.k, j + 8, d + 2));
         va_s[kt][l] = make_uint4(pair(p.v, j, d), pair(p.v, j + 8, d), pair(p.v, j, d + 2), pair(p.v, j + 8, d + 2));
+    }
+    for (int x = threadIdx.x; x < D; x += 128) {
+        ab[x] = p.alpha[h * D + x];
+        ab[D + x] = p.beta[h * D + x];
+        if (blockIdx.x == 0 && b == 0 && blockIdx.z == 0)
+            p.dalpha[h * D + x] = p.dbeta[h * D + x] = 0.f;
     }
     __syncthreads();
 
@@ -102,20 +111,48 @@ __global__ void __launch_bounds__(128, 2) sink_keys_kernel(const SinkBwdParams p
     const long long stride = static_cast<long long>(p.Hq) * D;  // between tokens
     const long long row0 = static_cast<long long>(b) * T * p.Hq + h;
     for (int t0 = t_begin + 16 * warp; t0 < t_end; t0 += 64) {
-        if (t0 + 15 - p.window < s0)
-            continue;  // no row of these sees a sink behind its window
+        const bool used = t0 + 15 - p.window >= s0;  // else no row of these sees a sink behind its window
+        if (!used && blockIdx.z)
+            continue;
         uint4 Q[2][KK], L[2][KK], O[2][KK];
+        float Dq[2];  // D of row rq + 8 r
 #pragma unroll
-        for (int r = 0; r < 2; ++r)
+        for (int r = 0; r < 2; ++r) {
+            const int t = t0 + rq + 8 * r;
+            const bool in = t < t_end;
+            const long long at = row0 * D + t * stride + 8 * c;
+            uint4 X[KK], F[KK];
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
-                const int t = t0 + rq + 8 * r;
-                const long long off = row0 * D + t * stride + 32 * kk + 8 * c;
-                const bool in = t < t_end;
-                Q[r][kk] = in ? __ldg(reinterpret_cast<const uint4 *>(p.q_hi + off)) : make_uint4(0, 0, 0, 0);
-                L[r][kk] = in ? __ldg(reinterpret_cast<const uint4 *>(p.q_lo + off)) : make_uint4(0, 0, 0, 0);
-                O[r][kk] = in ? __ldg(reinterpret_cast<const uint4 *>(p.dO + off)) : make_uint4(0, 0, 0, 0);
+                X[kk] = in ? __ldg(reinterpret_cast<const uint4 *>(p.q + at + 32 * kk)) : make_uint4(0, 0, 0, 0);
+                F[kk] = in ? __ldg(reinterpret_cast<const uint4 *>(p.o + at + 32 * kk)) : make_uint4(0, 0, 0, 0);
+                O[r][kk] = in ? __ldg(reinterpret_cast<const uint4 *>(p.dO + at + 32 * kk)) : make_uint4(0, 0, 0, 0);
             }
+            float acc = 0.f;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+                const uint32_t xw[4] = {X[kk].x, X[kk].y, X[kk].z, X[kk].w}, ow[4] = {F[kk].x, F[kk].y, F[kk].z, F[kk].w};
+                const uint32_t gw[4] = {O[r][kk].x, O[r][kk].y, O[r][kk].z, O[r][kk].w};
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float2 al = *reinterpret_cast<const float2 *>(ab + 32 * kk + 8 * c + 2 * e);
+                    const float2 be = *reinterpret_cast<const float2 *>(ab + D + 32 * kk + 8 * c + 2 * e);
+                    const float2 x = unpack_bf16x2(xw[e]), u = unpack_bf16x2(ow[e]), v = unpack_bf16x2(gw[e]);
+                    split_q_pair(fmaf(x.x, al.x, be.x), fmaf(x.y, al.y, be.y), hi[e], lo[e]);
+                    acc = fmaf(u.x, v.x, fmaf(u.y, v.y, acc));
+                }
+                // a row behind the last would be beta, which may be infinite: zero, as its weight
+                Q[r][kk] = in ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(0, 0, 0, 0);
+                L[r][kk] = in ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(0, 0, 0, 0);
+                if (in && blockIdx.z == 0) {
+                    *reinterpret_cast<uint4 *>(p.q_hi + at + 32 * kk) = Q[r][kk];
+                    *reinterpret_cast<uint4 *>(p.q_lo + at + 32 * kk) = L[r][kk];
+                }
+            }
+            acc += __shfl_xor_sync(0xffffffffu, acc, 1);
+            Dq[r] = acc + __shfl_xor_sync(0xffffffffu, acc, 2);
+        }
         float s[2][4], dp[2][4], lse[2][2], Dr[2][2];
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
@@ -125,10 +162,16 @@ __global__ void __launch_bounds__(128, 2) sink_keys_kernel(const SinkBwdParams p
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = t0 + 8 * r + 2 * c + i;
-                lse[r][i] = t < t_end ? p.lse[row0 + static_cast<long long>(t) * p.Hq] : 0.f;
-                Dr[r][i] = t < t_end ? p.Drow[row0 + static_cast<long long>(t) * p.Hq] : 0.f;
+                lse[r][i] = t < t_end ? p.lse_in[row0 + static_cast<long long>(t) * p.Hq] * kLog2eF : 0.f;
+                Dr[r][i] = __shfl_sync(0xffffffffu, Dq[r], 4 * (2 * c + i));
+                if (rq == 0 && t < t_end && blockIdx.z == 0) {
+                    p.lse[row0 + static_cast<long long>(t) * p.Hq] = lse[r][i];
+                    p.Drow[row0 + static_cast<long long>(t) * p.Hq] = Dr[r][i];
+                }
             }
         }
+        if (!used)
+            continue;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
             const uint4 k0 = ka_s[2 * kk][lane], k1 = ka_s[2 * kk + 1][lane];
@@ -230,18 +273,20 @@ int sink_chunks(int B, int T, int Hq)
 template <int D>
 cudaError_t launch_t(const SinkDqMaps &qmaps, const SinkBwdMaps &maps, const SinkBwdParams &p, cudaStream_t stream)
 {
-    const long long lanes = static_cast<long long>(p.B) * p.T * p.Hq * (D / 8);
-    sink_rows_kernel<D><<<static_cast<unsigned>((lanes + 255) / 256), 256, 0, stream>>>(p);
+    const int count = p.sinks < p.T - p.window ? p.sinks : p.T - p.window;  // sinks that some row sees behind its window
+    const int chunks = sink_chunks(p.B, p.T, p.Hq);
+    if (count > 0) {
+        sink_keys_kernel<D><<<dim3(chunks, p.B * p.Hq, (count + SK_M - 1) / SK_M), 128, 0, stream>>>(p, chunks, count);
+    } else {
+        const long long lanes = static_cast<long long>(p.B) * p.T * p.Hq * (D / 8);
+        sink_rows_kernel<D><<<static_cast<unsigned>((lanes + 255) / 256), 256, 0, stream>>>(p);
+    }
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess)
         return e;
-    if ((e = launch_sink_dq(D, qmaps, p, stream)) != cudaSuccess || (e = launch_sink_dkv(D, maps, p, stream)) != cudaSuccess)
+    if ((e = launch_sink_dq(D, qmaps, p, stream)) != cudaSuccess || (e = launch_sink_dkv(D, maps, p, stream)) != cudaSuccess ||
+        count <= 0)
         return e;
-    const int count = p.sinks < p.T - p.window ? p.sinks : p.T - p.window;  // sinks that some row sees behind its window
-    if (count <= 0)
-        return cudaSuccess;
-    const int chunks = sink_chunks(p.B, p.T, p.Hq);
-    sink_keys_kernel<D><<<dim3(chunks, p.B * p.Hq, (count + SK_M - 1) / SK_M), 128, 0, stream>>>(p, chunks, count);
     sink_join_kernel<D><<<dim3(count, p.B * p.Hkv), 2 * D, 0, stream>>>(p, chunks);
     return cudaGetLastError();
 }
