@@ -66,20 +66,28 @@ __global__ void __launch_bounds__(256) sink_rows_kernel(const SinkBwdParams p)
 
 // The prepared rows, and rows t against sinks j <= t - window.  A CTA has one (sequence, query head) and a run of tokens, a warp 16 tokens at a
 // time: the (up to 16) sinks on M and the tokens on N for S^T = K q^T and dP^T = V dO^T, whose fragments are then the
-// operands of Y = dS^T q and dV = P^T dO (tokens on K).  Operands come straight from global memory, 16 bytes a
-// lane, with the head dimension in the order in which they lie there.  More than 16 sinks: blockIdx.z (the first
-// 16 write the prepared rows).
+// operands of Y = dS^T q and dV = P^T dO (tokens on K).  Operands are taken 16 bytes a lane, with the head dimension
+// in the order in which it lies in memory; a lane copies what it will itself use into its places of a ring while the
+// 16 tokens before are worked on (two CTAs an SM hold some 100 KB on their way).  A token's heads lie
+// together in memory, so their CTAs follow one another.  More than 16 sinks: blockIdx.y (the first 16 write the
+// prepared rows).
 constexpr int SK_M = 16;
+
+template <int D>
+constexpr int sk_ring = 2 * 4 * (3 * 2 * D / 32) * 32 * 16;  // stages, warps, pieces of x, o and dO, lanes, bytes
 
 template <int D>
 __global__ void __launch_bounds__(128, 2) sink_keys_kernel(const SinkBwdParams p, int chunks, int count)
 {
     constexpr int KK = D / 32;  // runs of 32 values: a lane has 8 of each row
     __shared__ __align__(16) uint4 ka_s[D / 16][32], va_s[D / 16][32];  // K, V as A fragments
-    __shared__ __align__(16) float red[SK_M][2 * D], ab[2 * D];
+    __shared__ __align__(16) float ab[2 * D];
+    extern __shared__ __align__(16) uint8_t ring[];  // sk_ring<D> bytes, at the end the warps' sums
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3, rq = lane >> 2;
-    const int chunk = blockIdx.x, bh = blockIdx.y, b = bh / p.Hq, h = bh % p.Hq, g = h / (p.Hq / p.Hkv);
-    const int s0 = SK_M * blockIdx.z, ns = min(SK_M, count - s0);
+    const int h = blockIdx.x % p.Hq, chunk = blockIdx.x / p.Hq % chunks, b = blockIdx.x / p.Hq / chunks;
+    const int bh = b * p.Hq + h, g = h / (p.Hq / p.Hkv);
+    const int s0 = SK_M * blockIdx.y, ns = min(SK_M, count - s0);
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     const int T = p.T;
 
     auto pair = [&](const orthros_bf16 *src, int j, int d) -> uint32_t {  // two values of a sink (zero behind the last)
@@ -94,7 +102,7 @@ __global__ void __launch_bounds__(128, 2) sink_keys_kernel(const SinkBwdParams p
     for (int x = threadIdx.x; x < D; x += 128) {
         ab[x] = p.alpha[h * D + x];
         ab[D + x] = p.beta[h * D + x];
-        if (blockIdx.x == 0 && b == 0 && blockIdx.z == 0)
+        if (chunk == 0 && b == 0 && blockIdx.y == 0)
             p.dalpha[h * D + x] = p.dbeta[h * D + x] = 0.f;
     }
     __syncthreads();
@@ -110,29 +118,52 @@ __global__ void __launch_bounds__(128, 2) sink_keys_kernel(const SinkBwdParams p
             y[i][e] = dv[i][e] = 0.f;
     const long long stride = static_cast<long long>(p.Hq) * D;  // between tokens
     const long long row0 = static_cast<long long>(b) * T * p.Hq + h;
-    for (int t0 = t_begin + 16 * warp; t0 < t_end; t0 += 64) {
+    const uint4 *mine = reinterpret_cast<const uint4 *>(ring) + (warp * 2 * 3 * 2 * KK) * 32 + lane;  // [stage][array][r][kk][lane]
+    const uint32_t mine_at = smem_u32(mine);
+    float lse_next = 0.f;  // of token t0 + lane, log2 units
+    auto fetch = [&](int t0, int s) {
+#pragma unroll
+        for (int r = 0; r < 2; ++r) {
+            const int t = t0 + rq + 8 * r;
+            const long long at = row0 * D + (t < t_end ? t * stride : 0) + 8 * c;
+            const uint32_t to = mine_at + (s * 3 * 2 * KK + r * KK) * 512;
+#pragma unroll
+            for (int kk = 0; kk < KK; ++kk) {
+                cp_async16(to + kk * 512, p.q + at + 32 * kk, t < t_end);
+                cp_async16(to + (2 * KK + kk) * 512, p.o + at + 32 * kk, t < t_end);
+                cp_async16(to + (4 * KK + kk) * 512, p.dO + at + 32 * kk, t < t_end);
+            }
+        }
+        cp_async_commit();
+        lse_next = lane < 16 && t0 + lane < t_end ? p.lse_in[row0 + static_cast<long long>(t0 + lane) * p.Hq] * kLog2eF : 0.f;
+    };
+    int st = 0;
+    if (t_begin + 16 * warp < t_end)
+        fetch(t_begin + 16 * warp, 0);
+    for (int t0 = t_begin + 16 * warp; t0 < t_end; t0 += 64, st ^= 1) {
+        const float lse_now = lse_next;
+        if (t0 + 64 < t_end) {
+            fetch(t0 + 64, st ^ 1);
+            cp_async_wait<1>();
+        } else {
+            cp_async_wait<0>();
+        }
         const bool used = t0 + 15 - p.window >= s0;  // else no row of these sees a sink behind its window
-        if (!used && blockIdx.z)
-            continue;
-        uint4 Q[2][KK], L[2][KK], O[2][KK];
+        uint4 Q[2][KK], L[2][KK];
+        const uint4 *O[2] = {mine + (st * 3 + 2) * 2 * KK * 32, mine + ((st * 3 + 2) * 2 + 1) * KK * 32};
         float Dq[2];  // D of row rq + 8 r
 #pragma unroll
         for (int r = 0; r < 2; ++r) {
             const int t = t0 + rq + 8 * r;
             const bool in = t < t_end;
             const long long at = row0 * D + t * stride + 8 * c;
-            uint4 X[KK], F[KK];
-#pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                X[kk] = in ? __ldg(reinterpret_cast<const uint4 *>(p.q + at + 32 * kk)) : make_uint4(0, 0, 0, 0);
-                F[kk] = in ? __ldg(reinterpret_cast<const uint4 *>(p.o + at + 32 * kk)) : make_uint4(0, 0, 0, 0);
-                O[r][kk] = in ? __ldg(reinterpret_cast<const uint4 *>(p.dO + at + 32 * kk)) : make_uint4(0, 0, 0, 0);
-            }
+            const uint4 *from = mine + (st * 3 * 2 * KK + r * KK) * 32;
             float acc = 0.f;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
-                const uint32_t xw[4] = {X[kk].x, X[kk].y, X[kk].z, X[kk].w}, ow[4] = {F[kk].x, F[kk].y, F[kk].z, F[kk].w};
-                const uint32_t gw[4] = {O[r][kk].x, O[r][kk].y, O[r][kk].z, O[r][kk].w};
+                const uint4 X = from[kk * 32], F = from[(2 * KK + kk) * 32], G = O[r][kk * 32];
+                const uint32_t xw[4] = {X.x, X.y, X.z, X.w}, ow[4] = {F.x, F.y, F.z, F.w};
+                const uint32_t gw[4] = {G.x, G.y, G.z, G.w};
                 uint32_t hi[4], lo[4];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
@@ -145,7 +176,7 @@ __global__ void __launch_bounds__(128, 2) sink_keys_kernel(const SinkBwdParams p
                 // a row behind the last would be beta, which may be infinite: zero, as its weight
                 Q[r][kk] = in ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(0, 0, 0, 0);
                 L[r][kk] = in ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(0, 0, 0, 0);
-                if (in && blockIdx.z == 0) {
+                if (in && blockIdx.y == 0) {
                     *reinterpret_cast<uint4 *>(p.q_hi + at + 32 * kk) = Q[r][kk];
                     *reinterpret_cast<uint4 *>(p.q_lo + at + 32 * kk) = L[r][kk];
                 }
@@ -162,9 +193,9 @@ __global__ void __launch_bounds__(128, 2) sink_keys_kernel(const SinkBwdParams p
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
                 const int t = t0 + 8 * r + 2 * c + i;
-                lse[r][i] = t < t_end ? p.lse_in[row0 + static_cast<long long>(t) * p.Hq] * kLog2eF : 0.f;
+                lse[r][i] = __shfl_sync(0xffffffffu, lse_now, 8 * r + 2 * c + i);
                 Dr[r][i] = __shfl_sync(0xffffffffu, Dq[r], 4 * (2 * c + i));
-                if (rq == 0 && t < t_end && blockIdx.z == 0) {
+                if (rq == 0 && t < t_end && blockIdx.y == 0) {
                     p.lse[row0 + static_cast<long long>(t) * p.Hq] = lse[r][i];
                     p.Drow[row0 + static_cast<long long>(t) * p.Hq] = Dr[r][i];
                 }
@@ -184,8 +215,9 @@ __global__ void __launch_bounds__(128, 2) sink_keys_kernel(const SinkBwdParams p
                 mma_16816(s[r], ka1, Q[r][kk].z, Q[r][kk].w);
                 mma_16816(s[r], ka0, L[r][kk].x, L[r][kk].y);
                 mma_16816(s[r], ka1, L[r][kk].z, L[r][kk].w);
-                mma_16816(dp[r], va0, O[r][kk].x, O[r][kk].y);
-                mma_16816(dp[r], va1, O[r][kk].z, O[r][kk].w);
+                const uint4 G = O[r][kk * 32];
+                mma_16816(dp[r], va0, G.x, G.y);
+                mma_16816(dp[r], va1, G.z, G.w);
             }
         }
         uint32_t ph[4], pl[4], sh[4], sl[4];  // P and dS with the sinks on M, tokens on K
@@ -207,7 +239,8 @@ __global__ void __launch_bounds__(128, 2) sink_keys_kernel(const SinkBwdParams p
                 split_q_pair(ds[0], ds[1], sh[2 * r + hf], sl[2 * r + hf]);
             }
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
+        for (int kk = 0; kk < KK; ++kk) {
+            const uint4 G0 = O[0][kk * 32], G1 = O[1][kk * 32];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 auto word = [e](uint4 u) { return e == 0 ? u.x : e == 1 ? u.y : e == 2 ? u.z : u.w; };
@@ -215,32 +248,33 @@ __global__ void __launch_bounds__(128, 2) sink_keys_kernel(const SinkBwdParams p
                 mma_16816(y[4 * kk + e], sh, x0, x1);
                 mma_16816(y[4 * kk + e], sl, x0, x1);
                 mma_16816(y[4 * kk + e], sh, movmatrix_trans(word(L[0][kk])), movmatrix_trans(word(L[1][kk])));
-                const uint32_t g0 = movmatrix_trans(word(O[0][kk])), g1 = movmatrix_trans(word(O[1][kk]));
+                const uint32_t g0 = movmatrix_trans(word(G0)), g1 = movmatrix_trans(word(G1));
                 mma_16816(dv[4 * kk + e], ph, g0, g1);
                 mma_16816(dv[4 * kk + e], pl, g0, g1);
             }
+        }
     }
     // the four warps' sums, added up in order
-    for (int w = 0; w < 4; ++w) {
-        if (warp == w)
+    __syncthreads();
+    constexpr int PITCH = 2 * D + 8;  // the eight rows of a store in banks of their own
+    static_assert(4 * SK_M * PITCH * 4 <= sk_ring<D>);
+    float *red = reinterpret_cast<float *>(ring);  // [warp][SK_M][PITCH]: dk, dv
 #pragma unroll
-            for (int hf = 0; hf < 2; ++hf) {
-                float *row = red[rq + 8 * hf];
+    for (int hf = 0; hf < 2; ++hf) {
+        float *row = red + (warp * SK_M + rq + 8 * hf) * PITCH;
 #pragma unroll
-                for (int i = 0; i < D / 8; ++i) {
-                    const int d = 32 * (i / 4) + 8 * c + 2 * (i % 4);
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        row[d + e] = (w ? row[d + e] : 0.f) + y[i][2 * hf + e];
-                        row[D + d + e] = (w ? row[D + d + e] : 0.f) + dv[i][2 * hf + e];
-                    }
-                }
-            }
-        __syncthreads();
+        for (int i = 0; i < D / 8; ++i) {
+            const int d = 32 * (i / 4) + 8 * c + 2 * (i % 4);
+            *reinterpret_cast<float2 *>(row + d) = make_float2(y[i][2 * hf], y[i][2 * hf + 1]);
+            *reinterpret_cast<float2 *>(row + D + d) = make_float2(dv[i][2 * hf], dv[i][2 * hf + 1]);
+        }
     }
-    float *out = p.part + ((static_cast<long long>(blockIdx.z) * p.B * p.Hq + bh) * chunks + chunk) * SK_M * 2 * D;
-    for (int x = threadIdx.x; x < SK_M * 2 * D; x += 128)
-        out[x] = red[x / (2 * D)][x % (2 * D)];
+    __syncthreads();
+    float *out = p.part + ((static_cast<long long>(blockIdx.y) * p.B * p.Hq + bh) * chunks + chunk) * SK_M * 2 * D;
+    for (int x = threadIdx.x; x < ns * 2 * D; x += 128) {
+        const float *at = red + x / (2 * D) * PITCH + x % (2 * D);
+        out[x] = ((at[0] + at[SK_M * PITCH]) + at[2 * SK_M * PITCH]) + at[3 * SK_M * PITCH];
+    }
 }
 
 // one CTA a sink of a (sequence, KV head), a thread a column of dk and of dv
@@ -249,10 +283,17 @@ __global__ void __launch_bounds__(2 * D) sink_join_kernel(const SinkBwdParams p,
 {
     const int j = blockIdx.x, bg = blockIdx.y, b = bg / p.Hkv, g = bg % p.Hkv, G = p.Hq / p.Hkv, d = threadIdx.x;
     const float *src = p.part + (((static_cast<long long>(j / SK_M) * p.B + b) * p.Hq + g * G) * chunks * SK_M + j % SK_M) * 2 * D + d;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // it waits for all grids before it
     float sum = 0.f;
-#pragma unroll 8
-    for (int i = 0; i < G * chunks; ++i)  // the heads' chunks follow one another
-        sum += src[static_cast<long long>(i) * SK_M * 2 * D];
+    for (int i0 = 0; i0 < G * chunks; i0 += 16) {  // the heads' chunks follow one another
+        float x[16];
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            x[i] = i0 + i < G * chunks ? src[static_cast<long long>(i0 + i) * SK_M * 2 * D] : 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            sum += x[i];
+    }
     const long long at = ((static_cast<long long>(b) * p.T + j) * p.Hkv + g) * D;
     if (d < D)
         p.dk[at + d] += p.scale * sum;
@@ -276,7 +317,10 @@ cudaError_t launch_t(const SinkDqMaps &qmaps, const SinkBwdMaps &maps, const Sin
     const int count = p.sinks < p.T - p.window ? p.sinks : p.T - p.window;  // sinks that some row sees behind its window
     const int chunks = sink_chunks(p.B, p.T, p.Hq);
     if (count > 0) {
-        sink_keys_kernel<D><<<dim3(chunks, p.B * p.Hq, (count + SK_M - 1) / SK_M), 128, 0, stream>>>(p, chunks, count);
+        const cudaError_t e = cudaFuncSetAttribute(sink_keys_kernel<D>, cudaFuncAttributeMaxDynamicSharedMemorySize, sk_ring<D>);
+        if (e != cudaSuccess)
+            return e;
+        sink_keys_kernel<D><<<dim3(chunks * p.B * p.Hq, (count + SK_M - 1) / SK_M), 128, sk_ring<D>, stream>>>(p, chunks, count);
     } else {
         const long long lanes = static_cast<long long>(p.B) * p.T * p.Hq * (D / 8);
         sink_rows_kernel<D><<<static_cast<unsigned>((lanes + 255) / 256), 256, 0, stream>>>(p);
@@ -287,8 +331,7 @@ cudaError_t launch_t(const SinkDqMaps &qmaps, const SinkBwdMaps &maps, const Sin
     if ((e = launch_sink_dq(D, qmaps, p, stream)) != cudaSuccess || (e = launch_sink_dkv(D, maps, p, stream)) != cudaSuccess ||
         count <= 0)
         return e;
-    sink_join_kernel<D><<<dim3(count, p.B * p.Hkv), 2 * D, 0, stream>>>(p, chunks);
-    return cudaGetLastError();
+    return launch_dependent(sink_join_kernel<D>, dim3(count, p.B * p.Hkv), 2 * D, 0, stream, p, chunks);
 }
 
 size_t up256(size_t n) { return (n + 255) & ~static_cast<size_t>(255); }

@@ -105,6 +105,7 @@ __global__ void __launch_bounds__(640, 1) sink_dkv_tc_kernel(const __grid_consta
     tc_fence_after();
     const uint32_t tbase = *tmem_holder;
     bool ok = true;
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == 0) {
         // ------------------------------------------------------------------ producer
@@ -335,6 +336,9 @@ __global__ void __launch_bounds__(640, 1) sink_dkv_tc_kernel(const __grid_consta
         tc_fence_after();
         tmem_dealloc(tbase, 512);
     }
+    // This grid starts once every CTA of dq's has seen the prepared rows complete, and uses nothing of dq's: the two
+    // run side by side where SMs are left.  What comes after this grid comes after dq's too.
+    asm volatile("griddepcontrol.wait;" ::: "memory");
 }
 
 template <int D, int G>
@@ -345,8 +349,7 @@ cudaError_t launch_dkv(const SinkBwdMaps &maps, const SinkBwdParams &p, cudaStre
     const cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess)
         return e;
-    kern<<<dim3((p.T + C::KEYS - 1) / C::KEYS, p.B * p.Hkv), C::THREADS, C::SMEM, stream>>>(maps, p);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3((p.T + C::KEYS - 1) / C::KEYS, p.B * p.Hkv), C::THREADS, C::SMEM, stream, maps, p);
 }
 
 }  // namespace

@@ -117,6 +117,8 @@ __global__ void __launch_bounds__(512, 1) sink_dq_tc_kernel(const __grid_constan
     tc_fence_after();
     const uint32_t tbase = *tmem_holder;
     bool ok = true;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // for the prepared rows
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
 
     if (warp == 0) {
         // ------------------------------------------------------------------ rows
@@ -474,8 +476,7 @@ cudaError_t launch_dq(const SinkDqMaps &maps, const SinkBwdParams &p, cudaStream
         return e;
     constexpr int TOK = C::ROWS / G;
     const long long tiles = static_cast<long long>(p.B) * p.Hkv * ((p.T + TOK - 1) / TOK);
-    kern<<<static_cast<unsigned>(tiles < 152 ? tiles : 152), C::THREADS, C::SMEM, stream>>>(maps, p);
-    return cudaGetLastError();
+    return launch_dependent(kern, dim3(static_cast<unsigned>(tiles < 152 ? tiles : 152)), C::THREADS, C::SMEM, stream, maps, p);
 }
 
 }  // namespace
