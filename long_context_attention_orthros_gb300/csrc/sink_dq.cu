@@ -14,9 +14,11 @@
 // Bound by memory and MMAs alike: 96 KB of rows in and 64 KB of fp32 out a tile (d = 128), 40 MMAs a round.
 // Roles (512 threads): warps 0, 2 TMA producers of rows, of keys; warp 1 tensor memory and the issue of S, dP; warp 3 that
 // of dQ; warps 4-7, 8-11 dS of
-// a round's columns 0-31, 32-63 (lane = row); warps 12-15 dq_raw and the sums over a tile's rows: 16 columns at a
-// time x dq and dq go through a transposing buffer, where a thread sums one column of one head over its rows (loads
-// of x in that order, 2 bytes a lane, took 10 us a tile).  Every wait is bounded.
+// a round's columns 0-31, 32-63 (lane = row); warps 12-15 dq_raw and the sums over a tile's rows, 16 columns at a
+// time: up to four heads by shuffles that halve a lane's columns as they double its rows; more heads, whose sums
+// would take too many registers, through a transposing buffer, where a thread sums one column of one head over its
+// rows (the buffer for four heads, with its two barriers a step, bound the kernel: 10 us a tile).  Every wait is
+// bounded.
 #include "bwd_util.cuh"
 #include "kernels.cuh"
 #include "serve.cuh"
@@ -330,22 +332,40 @@ __global__ void __launch_bounds__(512, 1) sink_dq_tc_kernel(const __grid_constan
         const int rw = warp & 3, row = rw * 32 + lane, tid = threadIdx.x - 384;
         float *tp = reinterpret_cast<float *>(smem + C::TP_OFF);
         const bool v8 = (reinterpret_cast<uintptr_t>(p.dq) & 31) == 0;
-        // A thread sums column tid % 16 of each 16 over rows of one head: one of 8 groups of threads, 8 / G of them a
-        // head, every 8 / G-th token each (G <= 8), or two heads a group
-        constexpr int PER = G == 16 ? 2 : 1, SPLIT = G >= 8 ? 1 : 8 / G;
+        // Without shuffles a thread sums column tid % 16 of each 16 over a head's rows, or over those of two heads
+        constexpr bool FOLD = G <= 4;  // by shuffles; PER: sums of 16 columns that a thread has in the end
+        constexpr int PER = G == 16 || G == 4 ? 2 : 1;
         float sa[D / 16][PER], sb[D / 16][PER];
 #pragma unroll
         for (int c = 0; c < D / 16; ++c)
 #pragma unroll
             for (int e = 0; e < PER; ++e)
                 sa[c][e] = sb[c][e] = 0.f;
-        const int grp = tid >> 4, col = tid & 15, h0 = G == 16 ? 2 * grp : grp % G, first = G == 16 ? 0 : grp / G;
+        const int grp = tid >> 4, col = tid & 15, h0 = G == 16 ? 2 * grp : grp % G;
+        // sum of t[16] over the warp's rows of this lane's head: PER columns from fold_col on, a lane
+        const int fold_col = (lane & 16) / 2 + (G <= 8 ? (lane & 8) / 2 : 0) + (G <= 4 ? (lane & 4) / 2 : 0) + (G <= 2 ? (lane & 2) / 2 : 0);
+        auto fold = [&](float(&t)[16]) {
+#pragma unroll
+            for (int bit = 16, n = 8; bit >= G; bit >>= 1, n >>= 1) {
+                if (n == 0) {
+                    t[0] += __shfl_xor_sync(0xffffffffu, t[0], bit);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < n; ++i) {
+                        const float give = lane & bit ? t[i] : t[i + n];
+                        t[i] = (lane & bit ? t[i + n] : t[i]) + __shfl_xor_sync(0xffffffffu, give, bit);
+                    }
+                }
+            }
+        };
         auto flush = [&](int g) {
+            if (FOLD && G == 1 && (lane & 1))  // the last of five steps left both lanes the same sum
+                return;
 #pragma unroll
             for (int c = 0; c < D / 16; ++c)
 #pragma unroll
                 for (int e = 0; e < PER; ++e) {
-                    const int at = (g * G + h0 + e) * D + 16 * c + col;
+                    const int at = FOLD ? (g * G + lane % G) * D + 16 * c + fold_col + e : (g * G + h0 + e) * D + 16 * c + col;
                     atomicAdd(p.dalpha + at, sa[c][e]);
                     atomicAdd(p.dbeta + at, sb[c][e]);
                     sa[c][e] = sb[c][e] = 0.f;
@@ -370,7 +390,7 @@ __global__ void __launch_bounds__(512, 1) sink_dq_tc_kernel(const __grid_constan
                 const int buf = run & 1;
                 uint4 xa = __ldg(xrow), xb = __ldg(xrow + 1);  // 16 values of x, a step ahead
                 const bool got = warp_wait(&dq_full[buf], static_cast<uint32_t>((run >> 1) & 1));
-                if (!(ok = bar_red_and(1, 128, got)))
+                if (!(ok = FOLD ? got : bar_red_and(1, 128, got)))
                     break;
                 tc_fence_after();
                 const uint32_t at = tbase + (static_cast<uint32_t>(rw * 32) << 16) + C::TM_DQ + D * buf;
@@ -400,6 +420,7 @@ __global__ void __launch_bounds__(512, 1) sink_dq_tc_kernel(const __grid_constan
                             w[e + 3] = __float_as_uint(__uint_as_float(w[e + 3]) + y.w);
                         }
                     if (last) {
+                        float ta[16], tb[16];
 #pragma unroll
                         for (int e = 0; e < 16; e += 4) {
                             const float4 a = __ldg(reinterpret_cast<const float4 *>(p.alpha + h * D + 16 * c + e));
@@ -408,9 +429,24 @@ __global__ void __launch_bounds__(512, 1) sink_dq_tc_kernel(const __grid_constan
 #pragma unroll
                             for (int q = 0; q < 4; ++q) {
                                 const float y = live ? __uint_as_float(w[e + q]) * p.scale : 0.f;
-                                tp[row * 17 + e + q] = live ? xv[q] * y : 0.f;
-                                tp[(C::ROWS + row) * 17 + e + q] = y;
+                                ta[e + q] = live ? xv[q] * y : 0.f;
+                                tb[e + q] = y;
                                 w[e + q] = __float_as_uint(y * av[q]);
+                            }
+                        }
+                        if (FOLD) {
+                            fold(ta);
+                            fold(tb);
+#pragma unroll
+                            for (int e = 0; e < PER; ++e) {
+                                sa[c][e] += ta[e];
+                                sb[c][e] += tb[e];
+                            }
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                tp[row * 17 + e] = ta[e];
+                                tp[(C::ROWS + row) * 17 + e] = tb[e];
                             }
                         }
                     }
@@ -427,14 +463,14 @@ __global__ void __launch_bounds__(512, 1) sink_dq_tc_kernel(const __grid_constan
                             }
                         }
                     }
-                    if (last) {
+                    if (last && !FOLD) {
                         named_barrier(2, 128);
 #pragma unroll
                         for (int e = 0; e < PER; ++e) {
                             float ya = 0.f, yb = 0.f;
 #pragma unroll
-                            for (int k = 0; k < TOK / SPLIT; ++k) {
-                                const int r = (first + k * SPLIT) * G + h0 + e;
+                            for (int k = 0; k < TOK; ++k) {
+                                const int r = k * G + h0 + e;
                                 ya += tp[r * 17 + col];
                                 yb += tp[(C::ROWS + r) * 17 + col];
                             }
