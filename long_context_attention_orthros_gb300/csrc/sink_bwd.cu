@@ -64,15 +64,16 @@ __global__ void __launch_bounds__(256) sink_rows_kernel(const SinkBwdParams p)
 
 // ------------------------------------------------------------------ the sinks' dk, dv
 
-// The prepared rows, and rows t against sinks j <= t - window.  A CTA has one (sequence, query head) and a run of tokens, a warp 16 tokens at a
-// time: the (up to 16) sinks on M and the tokens on N for S^T = K q^T and dP^T = V dO^T, whose fragments are then the
-// operands of Y = dS^T q and dV = P^T dO (tokens on K).  Operands are taken 16 bytes a lane, with the head dimension
-// in the order in which it lies in memory; a lane copies what it will itself use into its places of a ring while the
-// 16 tokens before are worked on (two CTAs an SM hold some 100 KB on their way).  A token's heads lie
-// together in memory, so their CTAs follow one another.  More than 16 sinks: blockIdx.y (the first 16 write the
-// prepared rows).
-// It moves 670 MB for 1 x 16384 tokens of 32/8 heads, d = 128, in 172 us (3.9 TB/s; with loads a step ahead in registers
-// 220): what it waits for is the chain of a warp's 16 tokens, two warps a scheduler.
+// The prepared rows, and rows t against sinks j <= t - window.  A CTA has one (sequence, query head) and a run of
+// tokens, a warp 16 tokens at a time: the (up to 16) sinks on M and the tokens on N for S^T = K q^T and dP^T = V dO^T,
+// whose fragments are then the operands of Y = dS^T q and dV = P^T dO (tokens on K).  Operands are taken 16 bytes a
+// lane, with the head dimension in the order in which it lies in memory; a lane copies what it will itself use into
+// its places of a ring while the 16 tokens before are worked on (two CTAs an SM hold some 100 KB on their way).  A
+// token's heads lie together in memory, so their CTAs follow one another.  More than 16 sinks: blockIdx.y (the first
+// 16 write the prepared rows).
+// It moves 670 MB for 1 x 16384 tokens of 32/8 heads, d = 128, in 172 us (3.9 TB/s; 220 with loads where they are used
+// and the warps' sums one after the other).  What it waits for is the chain of a warp's 16 tokens, two warps a
+// scheduler.
 constexpr int SK_M = 16;
 
 template <int D>

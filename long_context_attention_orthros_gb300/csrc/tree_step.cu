@@ -519,7 +519,7 @@ __global__ void __cluster_dims__(ACCEPT_CTAS, 1, 1) __launch_bounds__(256) tree_
             *reinterpret_cast<uint4 *>((v ? p.v_cache : p.k_cache) + to + e) = y;
         }
     }
-    asm volatile("barrier.cluster.arrive.aligned;\n\tbarrier.cluster.wait.aligned;" ::: "memory");
+    asm volatile("barrier.cluster.arrive;\n\tbarrier.cluster.wait;" ::: "memory");
     if (rank == 0 && threadIdx.x == 0 && count > 0)
         p.cache_len[b] = len + count;
 }

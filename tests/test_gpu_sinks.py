@@ -256,3 +256,60 @@ def test_gradient_in_a_graph():
                 assert torch.equal(g, e), NAMES[i]
             else:
                 grad_parity(g, e.cpu().numpy().astype(np.float64), NAMES[i])
+
+
+@pytest.mark.parametrize("sinks", [4, 0])
+def test_gradients_one_after_the_other(sinks):
+    """Calls of different sizes that share a workspace, whose last kernels run side by side: what follows a call in its
+    stream (here the workspace is overwritten, the outputs are copied) finds it complete."""
+    sizes = [(4, 1500, 8, 2), (1, 140, 4, 4), (2, 4000, 16, 2)]
+    streams = [Stream(B, T, Hq, Hkv, 128, 128, sinks, seed=T) for B, T, Hq, Hkv in sizes]
+    n = max(orth.swa_sink_bwd_workspace_size(B, T, Hq, Hkv, 128) for B, T, Hq, Hkv in sizes)
+    calls = []
+    for s in streams:
+        o, lse = s.run(lse=True)
+        calls.append((bf(s.x), bf(s.k), bf(s.v), f32(s.alpha), f32(s.beta), o, bf(s.dO), lse, sinks))
+    alone = []
+    for c in calls:
+        alone.append(orth.swa_sink_bwd(*c))
+        torch.cuda.synchronize()
+    ws = torch.empty(n, dtype=torch.uint8, device=dev())
+    got = []
+    for c in calls + calls[::-1]:
+        y = orth.swa_sink_bwd(*c, workspace=ws)
+        ws.fill_(0xFF)
+        got.append([t.clone() for t in y])
+        for t in y:
+            t.fill_(float("nan"))
+    for y, ref in zip(got, alone + alone[::-1]):
+        for i in range(5):
+            if i < 3:  # dalpha, dbeta are summed with atomics
+                assert torch.equal(y[i], ref[i]), NAMES[i]
+            else:
+                grad_parity(y[i], ref[i].cpu().numpy().astype(np.float64), NAMES[i])
+
+
+def test_offsets_beyond_32_bits():
+    """Five sequences of 131072 rows of 32 heads: the last one's values lie beyond 2^31.  It comes out as alone (the
+    sinks' dk and dv are sums of another number of parts, 32 or 38 runs of tokens: a part's sum is truncated at up to
+    5 products of 64 steps, 320 2^-23 < 2^-14 of its size, random signs make that size a sixth of the whole's, and
+    38 such errors of one sign come to 38/6 2^-14 < 2^-11 of the largest)."""
+    B, T, Hq, Hkv, d = 5, 131072, 32, 8, 128
+    gen = torch.Generator(device=dev()).manual_seed(3)
+    x, dO = (torch.empty((B, T, Hq, d), dtype=torch.bfloat16, device=dev()) for _ in range(2))
+    k, v = (torch.empty((B, T, Hkv, d), dtype=torch.bfloat16, device=dev()) for _ in range(2))
+    for t in (x, dO, k, v):
+        for b in range(B):
+            t[b].copy_(torch.randn(t.shape[1:], generator=gen, device=dev()))
+    alpha, beta = (f32(a) for a in scale_offset(3, Hq, d))
+    o, lse = orth.swa_sink_fwd(x, k, v, alpha, beta, 4, lse=True)
+    y = orth.swa_sink_bwd(x, k, v, alpha, beta, o, dO, lse, 4)
+    one = [t[4:].contiguous() for t in (x, k, v, dO)]
+    o1, lse1 = orth.swa_sink_fwd(one[0], one[1], one[2], alpha, beta, 4, lse=True)
+    assert torch.equal(o[4:], o1) and torch.equal(lse[4:], lse1)
+    y1 = orth.swa_sink_bwd(one[0], one[1], one[2], alpha, beta, o1, one[3], lse1, 4)
+    assert torch.equal(y[0][4:], y1[0])
+    for i in (1, 2):
+        assert torch.equal(y[i][4:, 4:], y1[i][:, 4:]), NAMES[i]
+        far = (y[i][4:, :4] - y1[i][:, :4]).abs().max()
+        assert far <= 2.0 ** -11 * y1[i][:, :4].abs().max(), NAMES[i]

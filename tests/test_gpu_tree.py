@@ -314,3 +314,27 @@ def test_prompt_draft_accept_draft(Hq, Hkv, d, sinks):
                                  f32(ac), f32(bc), window=window)
         assert_parity(val(o)[:, None], ref[:, step], "decode step")
         assert_parity(val(oc)[:, None], refc[:, step], "decode step's copies")
+
+
+@pytest.mark.parametrize("N,Hq", [(1, 8), (7, 32)])
+def test_offsets_beyond_32_bits(N, Hq):
+    """The third sequence's cache lies behind 2^31 values: as the same sequence alone, and so is what is appended."""
+    B, L, L_max, Hkv, d = 3, 400, 1 << 20, 8, 128
+    c = Tree(B, N, L, Hq, Hkv, d, sinks=4, seed=41, room=N)
+    big = [torch.empty((B, L_max, Hkv, d), dtype=torch.bfloat16, device=dev()) for _ in range(2)]
+    for t, small in zip(big, (c.k, c.v)):
+        t[:, :L + N] = bf(small)
+    a = list(c.args())
+    a[5], a[6] = big
+    ref = c.run()
+    got = orth.decode_tree(*a, window=c.window, sinks=c.sinks)
+    c.check(got)
+    for y, r in zip(got, ref):
+        assert_bounded(val(y), val(r).astype(np.float64), np.abs(val(r)) * 2.0 ** -7 + 1e-2, "as in a small cache")
+    node = np.full(B, N - 1, np.int32)
+    path, k, v, lens = accept_reference(c, node)
+    got = orth.decode_tree_accept(a[2], a[3], a[4], i32(node), *big, a[7])
+    np.testing.assert_array_equal(got.cpu().numpy(), path)
+    np.testing.assert_array_equal(bits(big[0][:, :L + N]), k)
+    np.testing.assert_array_equal(bits(big[1][:, :L + N]), v)
+    np.testing.assert_array_equal(a[7].cpu().numpy(), lens)
