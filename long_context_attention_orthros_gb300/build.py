@@ -20,7 +20,7 @@ LIB = os.path.join(OUT_DIR, "liborthros.so")
 SOURCES = ["swa_fwd.cu", "swa_tc.cu", "swa_sink_tc.cu", "swa_wide.cu",
            "xattn_fwd.cu", "xattn_tc.cu", "decode_step.cu", "orthros_api.cu",
            "xattn_noalloc.cu", "kv_q8.cu", "serve_step.cu", "xattn_prefix.cu", "prefix_attn.cu", "prefix_tc.cu",
-           "attn_bwd.cu", "attn_bwd_d128.cu", "attn_bwd_d64.cu", "sink_bwd.cu", "sink_dq.cu", "sink_dkv.cu",
+           "attn_bwd.cu", "attn_bwd_d128.cu", "attn_bwd_d64.cu", "sink_bwd.cu", "sink_dq.cu", "sink_dkv.cu", "sink_lse.cu",
            "tree_step.cu", "tree_tc.cu"]
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-std=c++17", "-lineinfo", "-Xcompiler", "-fPIC", "--expt-relaxed-constexpr"]

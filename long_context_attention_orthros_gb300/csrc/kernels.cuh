@@ -165,6 +165,17 @@ struct SwaWideMaps {
 cudaError_t launch_swa_wide(int D, const SwaWideMaps &maps, const SwaWideParams &p, cudaStream_t stream);
 // the same with p.sinks > 0
 bool swa_sink_tc_supported(int D, int G, int window);
+
+// the log-sum-exp of rows with few keys (sink_lse.cu); strides between sequences, in values
+struct SinkLseParams {
+    const orthros_bf16 *q, *k;
+    const float *alpha, *beta;
+    float *lse;  // [B, T, Hq]
+    long long q_bstride, kv_bstride;
+    int B, T, Hq, Hkv, window, sinks, row_begin, row_end;
+    float qscale;  // scale log2(e)
+};
+cudaError_t launch_sink_lse(int D, SinkLseParams p, cudaStream_t stream);
 cudaError_t launch_swa_sink_tc(int D, int G, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                                const SwaParams &p, int num_sms, cudaStream_t stream);
 

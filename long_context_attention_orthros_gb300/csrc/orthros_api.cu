@@ -296,8 +296,30 @@ orthros_status orthros_swa_sink_fwd(const orthros_bf16 *q_raw, const orthros_bf1
     if (sinks > orthros::SWA_MAX_SINKS)
         return ORTHROS_ERR_UNSUPPORTED;
     // a window over the whole sequence leaves nothing to the sinks
-    return swa_fwd_impl(q_raw, k, v, alpha, beta, o, lse, B, T, Hq, Hkv, d, window, scale, q_bstride, kv_bstride,
-                        o_bstride, row_begin, row_end, dev_err, stream, 0, window < T ? sinks : 0);
+    const orthros_status st = swa_fwd_impl(q_raw, k, v, alpha, beta, o, lse, B, T, Hq, Hkv, d, window, scale, q_bstride,
+                                           kv_bstride, o_bstride, row_begin, row_end, dev_err, stream, 0,
+                                           window < T ? sinks : 0);
+    if (st != ORTHROS_OK || lse == nullptr)
+        return st;
+    orthros::SinkLseParams w{};
+    w.q = q_raw;
+    w.k = k;
+    w.alpha = alpha;
+    w.beta = beta;
+    w.lse = lse;
+    w.q_bstride = q_bstride ? q_bstride : static_cast<long long>(T) * Hq * d;
+    w.kv_bstride = kv_bstride ? kv_bstride : static_cast<long long>(T) * Hkv * d;
+    w.B = B;
+    w.T = T;
+    w.Hq = Hq;
+    w.Hkv = Hkv;
+    w.window = window;
+    w.sinks = window < T ? sinks : 0;
+    w.row_begin = row_begin;
+    w.row_end = row_end;
+    w.qscale = scale * kLog2e;
+    const cudaError_t e = orthros::launch_sink_lse(d, w, static_cast<cudaStream_t>(stream));
+    return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
 }
 
 size_t orthros_xattn_workspace_size(int B, int T_out, int T_kv, int Hq, int Hkv, int d)

@@ -181,6 +181,25 @@ def grad_parity(got, ref, what):
 NAMES = ("dq", "dk", "dv", "dalpha", "dbeta")
 
 
+@pytest.mark.parametrize("B,T,Hq,Hkv,d,window,sinks", CASES + [(2, 64, 8, 2, 64, 128, 4), (3, 5, 16, 1, 128, 77, 1),
+                                                              (1, 200, 4, 2, 64, 200, 0), (2, 100, 8, 1, 128, 33, 31)])
+def test_log_sum_exp_of_few_keys(B, T, Hq, Hkv, d, window, sinks):
+    """Rows that see at most 64 keys.  q enters as a bf16 part and a bf16 residual: 2^-9 2^-9 of each value off at most,
+    so a logit, and with it the sum's logarithm, by 2^-18 of the sum of its products' sizes; fp32 sums, exponents and
+    the logarithm add a few 2^-22 of it and of the result (at least 1 counted)."""
+    s = Stream(B, T, Hq, Hkv, d, window, sinks, seed=T + 3)
+    _, lse = s.run(lse=True)
+    ref = s.reference()[2]
+    q = np.abs(f64(s.x) * s.alpha.astype(np.float64) + s.beta.astype(np.float64)) / np.sqrt(d)
+    size = np.stack([q[:, :, h] @ np.abs(f64(s.k)[:, :, h * Hkv // Hq]).max(1)[..., None] for h in range(Hq)], 2)[..., 0]
+    t = np.arange(T)
+    few = np.minimum(t + 1, window) + np.minimum(sinks, np.maximum(0, t + 1 - window)) <= 64
+    if window + sinks > 64:
+        few &= t < 64
+    off = np.abs(lse.cpu().numpy() - ref)[:, few]
+    assert (off <= (2.0 ** -18 + 2.0 ** -20) * size[:, few] + 2.0 ** -20 * np.maximum(1, np.abs(ref[:, few]))).all()
+
+
 @pytest.mark.parametrize("B,T,Hq,Hkv,d,window,sinks", CASES)
 def test_gradient_matches(B, T, Hq, Hkv, d, window, sinks):
     s = Stream(B, T, Hq, Hkv, d, window, sinks, seed=T + 1)
