@@ -6,7 +6,8 @@
 // residual, on warp MMAs: a CTA has 32 tokens of a KV head, their keys in shared memory (at most 32 sinks and
 // 64 + 31 window rows), a warp 16 query rows on M at a time and 8 keys on N, with the head dimension in the order in
 // which it lies in memory (16 bytes a lane).  Rows with few keys are all rows, or the first 64 of each sequence,
-// where this is one short launch behind the forward's.
+// where this is one short launch behind the forward's (4 x 16384 tokens of 32/8 heads, d = 128: 10 us).  For all rows of
+// the same at window 33 it takes 410 us: a warp's chain of fragments, which the queries' two parts mostly are.
 #include "bwd_util.cuh"
 #include "kernels.cuh"
 #include "xattn.cuh"
@@ -18,7 +19,7 @@ namespace {
 constexpr int SL_TOK = 32, SL_SLOTS = 128;
 
 template <int D>
-__global__ void __launch_bounds__(256) sink_lse_kernel(const SinkLseParams p)
+__global__ void __launch_bounds__(256, 2) sink_lse_kernel(const SinkLseParams p)
 {
     constexpr int KK = D / 32, PITCH = D + 32;  // the pitch keeps eight lanes' 16 bytes in banks of their own
     __shared__ __align__(16) uint16_t ks[SL_SLOTS * PITCH];
@@ -43,24 +44,35 @@ __global__ void __launch_bounds__(256) sink_lse_kernel(const SinkLseParams p)
     for (int r0 = 16 * warp; r0 < rows; r0 += 128) {
         uint32_t hi[2 * KK][4], lo[2 * KK][4];  // A fragments of rows r0 + rq and r0 + rq + 8
         int t[2], h[2];
+        const orthros_bf16 *x[2];
 #pragma unroll
         for (int y = 0; y < 2; ++y) {
             const int r = min(r0 + rq + 8 * y, rows - 1);
             t[y] = t0 + r / G;
             h[y] = g * G + r % G;
-            const orthros_bf16 *x = p.q + b * p.q_bstride + (static_cast<long long>(t[y]) * p.Hq + h[y]) * D + 8 * c;
-            const float *al = p.alpha + h[y] * D + 8 * c, *be = p.beta + h[y] * D + 8 * c;
+            x[y] = p.q + b * p.q_bstride + (static_cast<long long>(t[y]) * p.Hq + h[y]) * D + 8 * c;
+        }
 #pragma unroll
-            for (int kk = 0; kk < KK; ++kk) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(x + 32 * kk));
+        for (int kk = 0; kk < KK; ++kk) {
+            __align__(16) float al[8], be[8];
+#pragma unroll
+            for (int y = 0; y < 2; ++y) {
+                if (y == 0 || h[1] != h[0]) {  // eight rows further it is the same head but for G = 16 and the last row
+                    const float *a = p.alpha + h[y] * D + 8 * c + 32 * kk, *s = p.beta + h[y] * D + 8 * c + 32 * kk;
+#pragma unroll
+                    for (int e = 0; e < 8; e += 4) {
+                        *reinterpret_cast<float4 *>(al + e) = __ldg(reinterpret_cast<const float4 *>(a + e));
+                        *reinterpret_cast<float4 *>(be + e) = __ldg(reinterpret_cast<const float4 *>(s + e));
+                    }
+                }
+                const uint4 u = __ldg(reinterpret_cast<const uint4 *>(x[y] + 32 * kk));
                 const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const float2 a = __ldg(reinterpret_cast<const float2 *>(al + 32 * kk) + e);
-                    const float2 s = __ldg(reinterpret_cast<const float2 *>(be + 32 * kk) + e);
                     const float2 v = unpack_bf16x2(w[e]);
                     const int kt = 2 * kk + e / 2, at = y + 2 * (e & 1);
-                    split_q_pair(fmaf(v.x, a.x, s.x), fmaf(v.y, a.y, s.y), hi[kt][at], lo[kt][at]);
+                    split_q_pair(fmaf(v.x, al[2 * e], be[2 * e]), fmaf(v.y, al[2 * e + 1], be[2 * e + 1]), hi[kt][at],
+                                 lo[kt][at]);
                 }
             }
         }
@@ -71,15 +83,15 @@ __global__ void __launch_bounds__(256) sink_lse_kernel(const SinkLseParams p)
             const int key = lo0 + n - ns;  // of slot n, behind the sinks' slots
             if (n >= ns && (key > tb || (key + 7 < first && key >= p.sinks)))
                 continue;
-            float acc[4] = {0.f, 0.f, 0.f, 0.f};
+            float part[4][4] = {};  // four chains of MMAs
             const uint16_t *kr = ks + min(n + rq, count - 1) * PITCH + 8 * c;
 #pragma unroll
             for (int kk = 0; kk < KK; ++kk) {
                 const uint4 u = *reinterpret_cast<const uint4 *>(kr + 32 * kk);
-                mma_16816(acc, hi[2 * kk], u.x, u.y);
-                mma_16816(acc, lo[2 * kk], u.x, u.y);
-                mma_16816(acc, hi[2 * kk + 1], u.z, u.w);
-                mma_16816(acc, lo[2 * kk + 1], u.z, u.w);
+                mma_16816(part[0], hi[2 * kk], u.x, u.y);
+                mma_16816(part[1], lo[2 * kk], u.x, u.y);
+                mma_16816(part[2], hi[2 * kk + 1], u.z, u.w);
+                mma_16816(part[3], lo[2 * kk + 1], u.z, u.w);
             }
 #pragma unroll
             for (int y = 0; y < 2; ++y)
@@ -87,7 +99,9 @@ __global__ void __launch_bounds__(256) sink_lse_kernel(const SinkLseParams p)
                 for (int e = 0; e < 2; ++e) {
                     const int slot = n + 2 * c + e, j = slot < ns ? slot : lo0 + slot - ns;
                     if (slot < count && j <= t[y] && (j > t[y] - p.window || j < p.sinks)) {
-                        const float x = acc[2 * y + e] * p.qscale, big = fmaxf(m[y], x);
+                        const int at = 2 * y + e;
+                        const float x = ((part[0][at] + part[2][at]) + (part[1][at] + part[3][at])) * p.qscale;
+                        const float big = fmaxf(m[y], x);
                         sum[y] = fmaf(sum[y], fast_exp2(m[y] - big), fast_exp2(x - big));
                         m[y] = big;
                     }
