@@ -135,8 +135,8 @@ orthros_status orthros_swa_fwd_lse(const orthros_bf16 *q_raw, const orthros_bf16
  * sequence stay visible to every row behind them, beside the window:
  *   row t attends over keys j <= t with j > t - window or j < sinks
  * 0 <= sinks <= 32 (0: as orthros_swa_fwd).  lse (optional, NULL: none) gets each row's log-sum-exp
- * over those keys, fp32 [B, T, Hq], for orthros_swa_sink_bwd; rows of at most 64 keys, where one fp16 of q
- * would show, to fp32 (orthros_swa_fwd_lse's others are some 1e-5 off).  Only output rows row_begin ..
+ * over those keys, fp32 [B, T, Hq], for orthros_swa_sink_bwd; some 1e-5 of itself off (q is rounded to fp16
+ * once), for rows of at most 64 keys, where that would not even out, some 1e-6.  Only output rows row_begin ..
  * row_end-1 are computed (0 and T for all; rules and reads as orthros_swa_fwd_rows, and key rows
  * 0 .. sinks-1 have to be in place).  Values of V are finite; one that is not reaches, beside the rows
  * that see it, only rows up to window + 256 away.  Other arguments, arithmetic and errors as
