@@ -26,10 +26,10 @@ __global__ void __launch_bounds__(256, 2) sink_lse_kernel(const SinkLseParams p)
     asm volatile("griddepcontrol.wait;" ::: "memory");  // for the forward's kernel, which writes lse too
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, c = lane & 3, rq = lane >> 2;
     const int G = p.Hq / p.Hkv;
-    const int skip = p.row_begin / SL_TOK;  // tiles begin at multiples of 32 tokens: a row's bits do not depend on the range
-    const long long per = (p.row_end + SL_TOK - 1) / SL_TOK - skip, bg = blockIdx.x / per;
+    // ranges begin at multiples of 128, so a row's tile, and its bits, do not depend on them
+    const long long per = (p.row_end - p.row_begin + SL_TOK - 1) / SL_TOK, bg = blockIdx.x / per;
     const int g = static_cast<int>(bg % p.Hkv), b = static_cast<int>(bg / p.Hkv);
-    const int t0 = (skip + static_cast<int>(blockIdx.x % per)) * SL_TOK, t1 = min(t0 + SL_TOK, p.row_end) - 1;
+    const int t0 = p.row_begin + static_cast<int>(blockIdx.x % per) * SL_TOK, t1 = min(t0 + SL_TOK, p.row_end) - 1;
     const int lo0 = max(0, t0 - p.window + 1);    // the first window key of token t0
     const int ns = min(p.sinks, lo0);             // sinks before it
     const int count = ns + t1 - lo0 + 1;          // slots: sinks 0 .. ns - 1, keys lo0 .. t1
@@ -116,7 +116,7 @@ __global__ void __launch_bounds__(256, 2) sink_lse_kernel(const SinkLseParams p)
                 sum[y] = sum[y] * fast_exp2(m[y] - big) + os * fast_exp2(om - big);
                 m[y] = big;
             }
-            if (c == 0 && r0 + rq + 8 * y < rows && t[y] >= p.row_begin)
+            if (c == 0 && r0 + rq + 8 * y < rows)
                 p.lse[(static_cast<long long>(b) * p.T + t[y]) * p.Hq + h[y]] = (m[y] + log2f(sum[y])) * 0.6931471805599453f;
         }
     }
@@ -125,7 +125,7 @@ __global__ void __launch_bounds__(256, 2) sink_lse_kernel(const SinkLseParams p)
 template <int D>
 cudaError_t launch_t(const SinkLseParams &p, cudaStream_t stream)
 {
-    const long long per = (p.row_end + SL_TOK - 1) / SL_TOK - p.row_begin / SL_TOK;
+    const long long per = (p.row_end - p.row_begin + SL_TOK - 1) / SL_TOK;
     return launch_dependent(sink_lse_kernel<D>, dim3(static_cast<unsigned>(per * p.B * p.Hkv)), 256, 0, stream, p);
 }
 

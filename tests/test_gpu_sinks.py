@@ -332,3 +332,15 @@ def test_offsets_beyond_32_bits():
         assert torch.equal(y[i][4:, 4:], y1[i][:, 4:]), NAMES[i]
         far = (y[i][4:, :4] - y1[i][:, :4]).abs().max()
         assert far <= 2.0 ** -11 * y1[i][:, :4].abs().max(), NAMES[i]
+
+
+@pytest.mark.parametrize("Hq,Hkv,window", [(8, 2, 9), (16, 1, 40), (2, 2, 128)])
+def test_log_sum_exp_of_row_ranges(Hq, Hkv, window):
+    """A range gives a row the bits that the whole stream gives it, and writes no other."""
+    s = Stream(2, 300, Hq, Hkv, 128, window, 3, seed=15)
+    _, whole = s.run(lse=True)
+    for begin, end in ((0, 128), (128, 300), (128, 256), (256, 300), (256, 256)):
+        lse = torch.full((2, 300, Hq), 7.0, device=dev())
+        s.run(lse=lse, row_begin=begin, row_end=end)
+        assert torch.equal(lse[:, begin:end], whole[:, begin:end])
+        assert (lse[:, :begin] == 7.0).all() and (lse[:, end:] == 7.0).all()
