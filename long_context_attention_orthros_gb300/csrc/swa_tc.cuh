@@ -807,21 +807,16 @@ __global__ void __launch_bounds__(SINK ? 544 : 512, 1)
     }
 }
 
-// an instance of the kernel for this launch; the log-sum-exp without sinks is asked for on full calls only
+// an instance of the kernel for this launch; with sinks every launch takes the one for ranges
 template <int D, int G, bool SINK>
 static cudaError_t launch_swa_tc_t(const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                                    const SwaParams &p, int num_sms, cudaStream_t stream)
 {
     using C = TcCfg<D, SINK>;
-    if (!SINK && p.lse != nullptr && p.n_base > 0)
-        return cudaErrorInvalidValue;
-    auto kern = swa_tc_kernel<D, G, SINK, true, SINK>;
-    if (p.lse == nullptr) {
-        kern = swa_tc_kernel<D, G, SINK, false, SINK>;
-        if constexpr (!SINK)
-            if (p.n_base > 0)
-                kern = swa_tc_kernel<D, G, true, false, false>;
-    }
+    auto kern = p.lse != nullptr ? swa_tc_kernel<D, G, true, true, SINK> : swa_tc_kernel<D, G, true, false, SINK>;
+    if constexpr (!SINK)
+        if (p.n_base == 0)
+            kern = p.lse != nullptr ? swa_tc_kernel<D, G, false, true, false> : swa_tc_kernel<D, G, false, false, false>;
     cudaError_t e = cudaFuncSetAttribute(kern, cudaFuncAttributeMaxDynamicSharedMemorySize, C::SMEM);
     if (e != cudaSuccess)
         return e;

@@ -1,0 +1,41 @@
+"""GPU tests of row ranges of the base stream with sinks: a range gives its rows the bits that a call for all rows
+gives them, log-sum-exp included, whatever kernel the sizes select for either call."""
+import numpy as np
+import pytest
+import torch
+
+import long_context_attention_orthros_gb300 as orth
+from tests.gpu_util import bf, bits, dev, f32
+from tests.test_gpu_sinks import Stream, error_word
+
+pytestmark = pytest.mark.gpu
+
+
+def same_as_whole(s, cuts):
+    """Each range of cuts alone: its rows as in the whole, no other row written."""
+    B, T, Hq, d = s.x.shape
+    err = error_word()
+    whole, whole_lse = s.run(lse=True, dev_err=err)
+    for begin, end in cuts:
+        out = torch.full((B, T, Hq, d), 7.0, dtype=torch.bfloat16, device=dev())
+        lse = torch.full((B, T, Hq), 7.0, device=dev())
+        s.run(out=out, lse=lse, row_begin=begin, row_end=end, dev_err=err)
+        np.testing.assert_array_equal(bits(out[:, begin:end]), bits(whole[:, begin:end]), f"{begin} .. {end}")
+        assert torch.equal(lse[:, begin:end], whole_lse[:, begin:end]), (begin, end)
+        for y in (out, lse):
+            assert (y[:, :begin] == 7.0).all() and (y[:, end:] == 7.0).all(), (begin, end)
+    assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,d,window,sinks", [
+    (2, 500, 8, 2, 128, 128, 0),    # no sinks, the band in tensor memory
+    (1, 400, 8, 4, 64, 128, 0),
+    (2, 300, 8, 1, 128, 40, 0),
+    (1, 300, 16, 1, 128, 128, 0),
+    (1, 140, 16, 1, 64, 140, 4),    # a window over everything leaves nothing to the sinks
+    (2, 500, 4, 4, 64, 128, 0),     # ungrouped heads and a wide window
+    (1, 600, 8, 2, 128, 500, 0),
+])
+def test_log_sum_exp_of_a_range_without_sinks(B, T, Hq, Hkv, d, window, sinks):
+    s = Stream(B, T, Hq, Hkv, d, window, sinks, seed=T + Hq)
+    same_as_whole(s, [(0, 128), (128, T)] + ([(128, 256), (256, T)] if T > 256 else []))
