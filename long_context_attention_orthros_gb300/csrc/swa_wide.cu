@@ -9,6 +9,10 @@
 // are worked on at once (1 x 2000 tokens of 8/2 heads, d = 64, window 300: 13.6 us against 18.6; 1 x 1024 of 32/8 heads,
 // d = 128, window 640: 34.5 against 26.5; 1 x 8192 of 8/2 heads, d = 64, window 1024: 68 against 54; 2 x 16384 of 32/8,
 // d = 128: 1151 against 852, a third of the MMAs' rate).  Bound by the chain S -> softmax -> P V.
+// A row's bits depend on the form and on where its piece begins, so both are those of the whole sequence: a range of
+// rows takes the form that all rows would, in pieces cut at the same tokens.  Ranges begin at multiples of 128 tokens; a
+// ROWS2 piece of 256 tokens (heads that do not share K and V) that one cuts has no query in its other half.  That costs
+// short ranges of long sequences time (512 rows of 1 x 8192 of 8/2 heads, d = 64, window 1024: 27.8 us, as KEYS2 18.5).
 #include "rows_tc.cuh"
 
 namespace orthros {
@@ -23,7 +27,7 @@ struct WideJob {
         long long it, it1;
     };
     struct Piece {
-        int g, b, t0, t1;     // tokens t0 .. t1 - 1
+        int g, b, t0, t1;     // tokens t0 .. t1 - 1, of which the range has those from row_begin on
         int lo, far;          // first block of the windows; the sinks' block comes before it
         int m, plain0, plain1;
     };
@@ -45,7 +49,7 @@ struct WideJob {
         const long long stream = where.it / p.per_stream;
         to.b = static_cast<int>(stream / p.Hkv);
         to.g = static_cast<int>(stream % p.Hkv);
-        to.t0 = p.row_begin + static_cast<int>(where.it % p.per_stream) * tok;
+        to.t0 = p.row_begin / tok * tok + static_cast<int>(where.it % p.per_stream) * tok;
         to.t1 = min(p.row_end, to.t0 + tok);
         to.lo = max(0, to.t0 - p.window + 1) / 64;
         to.far = p.sinks > 0 && to.lo > 0;
@@ -71,13 +75,13 @@ struct WideJob {
     static __device__ __forceinline__ void span(const Params &p, const Piece &c, int j0, int &end, int &lo, int &first)
     {
         end = c.t1 - j0;
-        lo = c.t0 - p.window + 1;
+        lo = max(c.t0, p.row_begin) - p.window + 1;  // what only rows before the range see may not be in place
         first = p.sinks;
     }
     static __device__ __forceinline__ const orthros_bf16 *query(const Params &p, const Piece &c, int r)
     {
         const int G = p.Hq / p.Hkv, t = c.t0 + r / G;
-        return t < c.t1 ? p.q + c.b * p.q_bstride + (static_cast<long long>(t) * p.Hq + c.g * G + r % G) * D : nullptr;
+        return t >= p.row_begin && t < c.t1 ? p.q + c.b * p.q_bstride + (static_cast<long long>(t) * p.Hq + c.g * G + r % G) * D : nullptr;
     }
     static __device__ __forceinline__ void vectors(const Params &p, const Piece &, const float *&alpha, const float *&beta)
     {
@@ -98,7 +102,7 @@ struct WideJob {
     {
         const int G = p.Hq / p.Hkv, t = c.t0 + r / G, h = c.g * G + r % G;
         RowOut o = {nullptr, nullptr, nullptr, nullptr, false};
-        if (t < c.t1) {
+        if (t >= p.row_begin && t < c.t1) {
             o.row = p.o + c.b * p.o_bstride + (static_cast<long long>(t) * p.Hq + h) * D;
             if (p.lse != nullptr)
                 o.lse = p.lse + (static_cast<long long>(c.b) * p.T + t) * p.Hq + h;
@@ -110,17 +114,13 @@ struct WideJob {
 template <int D>
 cudaError_t launch_t(const SwaWideMaps &maps, SwaWideParams p, cudaStream_t stream)
 {
-    const int G = p.Hq / p.Hkv, rows = p.row_end - p.row_begin;
-    auto pieces = [&](int tr) {
-        p.per_stream = (rows + tr / G - 1) / (tr / G);
-        p.pieces = static_cast<long long>(p.B) * p.Hkv * p.per_stream;
-        return p.pieces;
-    };
-    if (pieces(128) > 152) {
-        const long long n = pieces(256);
-        return launch_rows_tc<D, true, WideJob>(maps, p, static_cast<int>(n < 152 ? n : 152), stream);
-    }
-    return launch_rows_tc<D, false, WideJob>(maps, p, static_cast<int>(p.pieces), stream);
+    const int G = p.Hq / p.Hkv;
+    const bool two = static_cast<long long>(p.B) * p.Hkv * ((p.T + 128 / G - 1) / (128 / G)) > 152;  // tiles of all rows
+    const int tok = (two ? 256 : 128) / G;
+    p.per_stream = (p.row_end + tok - 1) / tok - p.row_begin / tok;
+    p.pieces = static_cast<long long>(p.B) * p.Hkv * p.per_stream;
+    const int ctas = static_cast<int>(p.pieces < 152 ? p.pieces : 152);
+    return two ? launch_rows_tc<D, true, WideJob>(maps, p, ctas, stream) : launch_rows_tc<D, false, WideJob>(maps, p, ctas, stream);
 }
 
 }  // namespace

@@ -39,3 +39,17 @@ def same_as_whole(s, cuts):
 def test_log_sum_exp_of_a_range_without_sinks(B, T, Hq, Hkv, d, window, sinks):
     s = Stream(B, T, Hq, Hkv, d, window, sinks, seed=T + Hq)
     same_as_whole(s, [(0, 128), (128, T)] + ([(128, 256), (256, T)] if T > 256 else []))
+
+
+@pytest.mark.parametrize("B,T,Hq,Hkv,d,window,sinks", [
+    (1, 5000, 4, 4, 64, 300, 4),     # 160 tiles of 128 tokens, which go by pairs: a range may begin inside a pair
+    (2, 2600, 4, 4, 128, 70, 3),
+    (1, 2600, 8, 4, 128, 300, 4),    # tiles of 64 tokens
+    (1, 1300, 16, 1, 64, 300, 5),    # tiles of 8 tokens
+    (3, 1700, 16, 2, 128, 1000, 32),
+])
+def test_ranges_of_streams_of_many_tiles(B, T, Hq, Hkv, d, window, sinks):
+    """More tiles than SMs in the whole, few in the range."""
+    s = Stream(B, T, Hq, Hkv, d, window, sinks, seed=T + Hkv)
+    last = T // 128 * 128
+    same_as_whole(s, [(0, 128), (128, 256), (128, 384), (256, 640), (640, 1024), (last, T), (last - 128, T), (384, T)])
