@@ -464,13 +464,16 @@ __global__ void __launch_bounds__(SINK ? 544 : 512, 1)
                     break;
                 }
                 if (SINK && second) {
-                    // V rows of the block that are no sinks have no weight, but may hold anything: zeros
+                    // rows of the block that are no sinks have no weight, but may hold anything (in a row range they need
+                    // not be in place): zeros in K, where they would be out of range, and in V
                     for (int r = rsub; r < C::KB; r += 4 * NCW)
                         if (r >= p.sinks)
 #pragma unroll
-                            for (int sl = 0; sl < C::SLABS; ++sl)
-                                *reinterpret_cast<uint4 *>(smem + C::V_OFF + sl * C::V_SLAB + s * C::SLOT + r * 128 +
-                                                           c8 * 16) = make_uint4(0, 0, 0, 0);
+                            for (int sl = 0; sl < C::SLABS; ++sl) {
+                                const int at = r * 128 + c8 * 16;
+                                *reinterpret_cast<uint4 *>(smem + C::K_OFF + sl * C::K_SLAB + ks * C::SLOT + at) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4 *>(smem + C::V_OFF + sl * C::V_SLAB + s * C::SLOT + at) = make_uint4(0, 0, 0, 0);
+                            }
                 }
                 // common case: every chunk below 65520 converts as is; when a chunk of the warp's
                 // rows reaches it, the warp shifts those rows instead (rare)

@@ -1,0 +1,30 @@
+"""GPU tests of what the base stream with sinks reports: the error word names what a row's result depends on and
+nothing else, and the log-sum-exp of a row that is not a number is none."""
+import numpy as np
+import pytest
+import torch
+
+import long_context_attention_orthros_gb300 as orth
+from tests.attend_util import assert_bounded
+from tests.gpu_util import bf, bits, dev, f32, val
+from tests.test_gpu_sinks import Stream, error_word
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("value", [float("inf"), float("-inf"), float("nan")])
+@pytest.mark.parametrize("Hq,Hkv,d,window,sinks", [(8, 2, 128, 128, 4), (8, 4, 64, 77, 1), (16, 1, 128, 33, 31),
+                                                   (2, 2, 128, 128, 4), (8, 2, 128, 500, 4)])
+def test_keys_behind_the_sinks_that_no_row_sees(Hq, Hkv, d, window, sinks, value):
+    """In a range only the sinks themselves have to be in place before its windows: the rows that share their key
+    block may hold anything."""
+    begin = 640
+    s = Stream(2, 900, Hq, Hkv, d, window, sinks, seed=window)
+    clean = s.run()
+    k = bf(s.k)
+    k[:, sinks:32] = value
+    err = error_word()
+    got = orth.swa_sink_fwd(bf(s.x), k, bf(s.v), f32(s.alpha), f32(s.beta), sinks, window=window, row_begin=begin,
+                            dev_err=err)
+    np.testing.assert_array_equal(bits(got[:, begin:]), bits(clean[:, begin:]))
+    assert int(err.item()) == 0
