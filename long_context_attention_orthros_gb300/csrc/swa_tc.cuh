@@ -635,13 +635,15 @@ __global__ void __launch_bounds__(SINK ? 544 : 512, 1)
                     if (__all_sync(0xffffffffu, key0 >= lo_key && key0 + 31 <= hi_key))
                         inner |= 1u << q;
                 }
-                // logits of shifted key rows times 2^e_j (rare): rewritten in tensor memory first
+                // logits of shifted key rows times 2^e_j (rare): rewritten in tensor memory first; out of range are
+                // those alone that the row sees
 #pragma unroll 1
                 for (int q = 0; q < nbs && smask != 0; ++q) {
                     const uint32_t wm = (smask >> (2 * q)) & 3u;
+                    const bool far = SINK && q == nb;  // the sinks' columns
                     if (wm != 0)
-                        unshift_chunk32(s_col + 32 * q, kexp + (SINK && q == nb ? C::STAGES : (slot0 + q) % C::STAGES) * C::KB,
-                                        0, wm, 8, 4, range_bad);
+                        unshift_chunk32(s_col + 32 * q, kexp + (far ? C::STAGES : (slot0 + q) % C::STAGES) * C::KB, 0, wm, 8, 4,
+                                        range_bad, far ? sink_last : hi_key - bs - 32 * q, far ? 0 : lo_key - bs - 32 * q);
                 }
                 // The band is read in 16-column halves, the next half's load in flight while the
                 // current one is processed (tcgen05.wait::ld waits for every load of the thread).

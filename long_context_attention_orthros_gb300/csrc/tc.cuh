@@ -256,10 +256,11 @@ __device__ ORTHROS_RARE void shift_key_rows(uint8_t *blk, int slab_bytes, int mi
 // this warp's 32 tensor-memory lanes at taddr; key rows row0 .. row0 + 31 of their block) times
 // 2^e_j, read back and stored in place.  Row r's shift is ke[r] when bit ((r % period) / per) of
 // wmask is set (the converter warp owning the row has shifted some of its rows), else 0.  A logit that is
-// no longer finite sets bad, unless its column lies behind the last that counts (it is masked later).
+// no longer finite sets bad, unless its column lies before the first or behind the last that counts for the lane's row
+// (it is masked later).
 // Called by the whole warp; the caller reloads the chunk afterwards.
 static __device__ ORTHROS_RARE void unshift_chunk32(uint32_t taddr, const int8_t *ke, int row0, uint32_t wmask, int period,
-                                             int per, bool &bad, int last = 31)
+                                             int per, bool &bad, int last = 31, int first = 0)
 {
     uint32_t v[32];
     tmem_ld32(taddr, v);
@@ -270,7 +271,7 @@ static __device__ ORTHROS_RARE void unshift_chunk32(uint32_t taddr, const int8_t
         const int x = ((wmask >> ((r % period) / per)) & 1u) ? ke[r] : 0;
         if (x != 0) {
             const float y = __uint_as_float(v[e]) * exp2i(x);
-            bad |= isinf(y) && e <= last;
+            bad |= isinf(y) && e >= first && e <= last;
             v[e] = __float_as_uint(y);
         }
     }

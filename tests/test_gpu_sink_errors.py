@@ -28,3 +28,23 @@ def test_keys_behind_the_sinks_that_no_row_sees(Hq, Hkv, d, window, sinks, value
                             dev_err=err)
     np.testing.assert_array_equal(bits(got[:, begin:]), bits(clean[:, begin:]))
     assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("Hq,Hkv,d,window,sinks", [(8, 2, 128, 128, 4), (8, 4, 64, 77, 5), (16, 1, 128, 33, 4),
+                                                   (8, 2, 128, 128, 0), (2, 2, 128, 128, 4), (8, 2, 128, 500, 4)])
+@pytest.mark.parametrize("row", [3, 20, 555])
+def test_products_beyond_fp32_that_no_row_sees(Hq, Hkv, d, window, sinks, row):
+    """A key of 3e38 in one column and zeros else, against queries that are zero in that column where they see the key
+    and 64 where they do not, so that scale log2(e) q.k would be some 3e39: no logit that counts is out of range."""
+    s = Stream(1, 1000, Hq, Hkv, d, window, sinks, seed=row)
+    t = np.arange(1000)
+    seen = (t >= row) & ((t < row + window) | (row < sinks))
+    s.alpha[:, 5], s.beta[:, 5] = 1, 0
+    s.x[0, :, :, 5] = np.where(seen, 0, 0x4280)[:, None]  # 64
+    s.k[0, row] = 0
+    s.k[0, row, :, 5] = 0x7F62  # 3.0e38
+    ref, bound, _ = s.reference()
+    err = error_word()
+    got = s.run(dev_err=err)
+    assert int(err.item()) == 0
+    assert_bounded(val(got), ref, bound, "o")
