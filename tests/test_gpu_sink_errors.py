@@ -48,3 +48,27 @@ def test_products_beyond_fp32_that_no_row_sees(Hq, Hkv, d, window, sinks, row):
     got = s.run(dev_err=err)
     assert int(err.item()) == 0
     assert_bounded(val(got), ref, bound, "o")
+
+
+@pytest.mark.parametrize("T", [500, 60])
+@pytest.mark.parametrize("Hq,Hkv,d,window,sinks", [(8, 2, 128, 128, 4), (8, 2, 64, 128, 0), (8, 2, 128, 33, 4),
+                                                   (2, 2, 128, 128, 4), (8, 2, 128, 400, 4), (8, 2, 128, 400, 0),
+                                                   (2, 2, 64, 128, 0)])
+def test_log_sum_exp_of_a_query_that_is_no_number(Hq, Hkv, d, window, sinks, T):
+    """Nothing of the buffer is left as it was."""
+    s = Stream(2, T, Hq, Hkv, d, window, sinks, seed=T)
+    ref, ref_lse = s.run(lse=True)
+    at = [(0, 0, 0), (0, T // 2, 1), (1, T - 1, Hq - 1)]
+    for b, t, h in at:
+        s.x[b, t, h, 7] = 0x7FC0
+    lse = torch.full((2, T, Hq), 7.0, device=dev())
+    got, _ = s.run(lse=lse)
+    row = torch.zeros((2, T, Hq), dtype=torch.bool, device=dev())
+    for i in at:
+        row[i] = True
+    assert torch.isnan(lse[row]).all() and torch.isnan(got.float()[row]).all()
+    assert torch.equal(lse[~row], ref_lse[~row]) and torch.equal(got[~row], ref[~row])
+    if sinks == 0:
+        lse.fill_(7.0)
+        orth.swa_fwd_lse(bf(s.x), bf(s.k), bf(s.v), f32(s.alpha), f32(s.beta), window=window, lse=lse)
+        assert torch.isnan(lse[row]).all() and torch.isfinite(lse[~row]).all()
