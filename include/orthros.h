@@ -631,13 +631,26 @@ orthros_status orthros_decode_tree(const orthros_bf16 *q_new, const orthros_bf16
  *   other arguments as orthros_decode_tree
  * A sequence whose node is outside [-1, N) or hangs below a bad parent is left as it is and sets
  * ORTHROS_DEVERR_POSITION; one whose rows do not fit, or whose cache_len is out of range, likewise with
- * ORTHROS_DEVERR_CACHE_FULL (its path is all -1).
+ * ORTHROS_DEVERR_CACHE_FULL (its path is all -1).  All trees have N nodes: for those that orthros_decode_tree
+ * was given with fewer, call orthros_decode_tree_accept_nodes.
  */
 orthros_status orthros_decode_tree_accept(const orthros_bf16 *k_new, const orthros_bf16 *v_new,
                                           const int32_t *parent, const int32_t *node,
                                           orthros_bf16 *k_cache, orthros_bf16 *v_cache,
                                           int32_t *cache_len, int L_max, int32_t *path, int B, int N,
                                           int Hkv, int d, int32_t *dev_err, void *stream);
+
+/*
+ * orthros_decode_tree_accept for trees of nodes[b] nodes (as given to orthros_decode_tree; NULL: N): node[b] in
+ * [-1, nodes[b]), and what lies behind a tree's last node may hold anything.  A node out of that range, or nodes[b]
+ * outside [0, N], leaves the sequence as it is and sets ORTHROS_DEVERR_POSITION.
+ */
+orthros_status orthros_decode_tree_accept_nodes(const orthros_bf16 *k_new, const orthros_bf16 *v_new,
+                                                const int32_t *parent, const int32_t *nodes,
+                                                const int32_t *node, orthros_bf16 *k_cache,
+                                                orthros_bf16 *v_cache, int32_t *cache_len, int L_max,
+                                                int32_t *path, int B, int N, int Hkv, int d,
+                                                int32_t *dev_err, void *stream);
 
 #ifdef __cplusplus
 }

@@ -114,6 +114,8 @@ def lib() -> ctypes.CDLL:
             L.orthros_decode_tree.argtypes = [P] * 9 + [I] + [P] * 6 + [I] * 7 + [F, P, SZ, P, P]
             L.orthros_decode_tree_accept.restype = I
             L.orthros_decode_tree_accept.argtypes = [P] * 7 + [I, P] + [I] * 4 + [P, P]
+            L.orthros_decode_tree_accept_nodes.restype = I
+            L.orthros_decode_tree_accept_nodes.argtypes = [P] * 8 + [I, P] + [I] * 4 + [P, P]
             _lib = L
     return _lib
 
@@ -825,9 +827,10 @@ def decode_tree(q_new, qc_new, k_new, v_new, parent, k_cache, v_cache, cache_len
     return o, oc
 
 
-def decode_tree_accept(k_new, v_new, parent, node, k_cache, v_cache, cache_len, path=None, dev_err=None):
+def decode_tree_accept(k_new, v_new, parent, node, k_cache, v_cache, cache_len, path=None, dev_err=None, nodes=None):
     """Append what the check of a drafted tree accepted: the rows of k_new, v_new [B, N, Hkv, d] on the path to
-    node[b] (int32 [B]; -1: none) go to cache rows cache_len[b].., and cache_len[b] grows by their number.
+    node[b] (int32 [B]; -1: none) go to cache rows cache_len[b].., and cache_len[b] grows by their number.  nodes as
+    given to decode_tree: node[b] is one of its tree's, 0..nodes[b]-1 (default N), or -1.
     Returns path, int32 [B, N]: the path's nodes in order, -1 behind the last."""
     B, L_max, Hkv, d = shape = k_cache.shape
     dev = k_cache.get_device()
@@ -837,9 +840,9 @@ def decode_tree_accept(k_new, v_new, parent, node, k_cache, v_cache, cache_len, 
     new, bf16, i32 = (B, N, Hkv, d), torch.bfloat16, torch.int32
     if path is None:
         path = torch.empty((B, N), dtype=i32, device=k_cache.device)
-    _invoke("orthros_decode_tree_accept", dev, _dense(k_new, "k_new", bf16, new, dev),
+    _invoke("orthros_decode_tree_accept_nodes", dev, _dense(k_new, "k_new", bf16, new, dev),
             _dense(v_new, "v_new", bf16, new, dev), _dense(parent, "parent", i32, (B, N), dev),
-            _dense(node, "node", i32, (B,), dev), _dense(k_cache, "k_cache", bf16, shape, dev),
+            _optional(nodes, "nodes", i32, (B,), dev), _dense(node, "node", i32, (B,), dev), _dense(k_cache, "k_cache", bf16, shape, dev),
             _dense(v_cache, "v_cache", bf16, shape, dev), _dense(cache_len, "cache_len", i32, (B,), dev), L_max,
             _dense(path, "path", i32, (B, N), dev), B, N, Hkv, d, _word(dev_err, dev))
     return path

@@ -1202,10 +1202,11 @@ orthros_status orthros_decode_tree(const orthros_bf16 *q_new, const orthros_bf16
     return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
 }
 
-orthros_status orthros_decode_tree_accept(const orthros_bf16 *k_new, const orthros_bf16 *v_new, const int32_t *parent,
-                                          const int32_t *node, orthros_bf16 *k_cache, orthros_bf16 *v_cache,
-                                          int32_t *cache_len, int L_max, int32_t *path, int B, int N, int Hkv, int d,
-                                          int32_t *dev_err, void *stream)
+orthros_status orthros_decode_tree_accept_nodes(const orthros_bf16 *k_new, const orthros_bf16 *v_new,
+                                                const int32_t *parent, const int32_t *nodes, const int32_t *node,
+                                                orthros_bf16 *k_cache, orthros_bf16 *v_cache, int32_t *cache_len,
+                                                int L_max, int32_t *path, int B, int N, int Hkv, int d,
+                                                int32_t *dev_err, void *stream)
 {
     if (!aligned16(k_new) || !aligned16(v_new) || !parent || !node || !aligned16(k_cache) || !aligned16(v_cache) ||
         !cache_len || !path || Hkv < 1 || !tree_sizes_ok(B, N, L_max, Hkv))
@@ -1216,6 +1217,7 @@ orthros_status orthros_decode_tree_accept(const orthros_bf16 *k_new, const orthr
     p.k_new = k_new;
     p.v_new = v_new;
     p.parent = parent;
+    p.nodes = nodes;
     p.node = node;
     p.k_cache = k_cache;
     p.v_cache = v_cache;
@@ -1228,6 +1230,15 @@ orthros_status orthros_decode_tree_accept(const orthros_bf16 *k_new, const orthr
     p.row = Hkv * d;
     const cudaError_t e = orthros::launch_tree_accept(p, static_cast<cudaStream_t>(stream));
     return e == cudaSuccess ? ORTHROS_OK : ORTHROS_ERR_CUDA;
+}
+
+orthros_status orthros_decode_tree_accept(const orthros_bf16 *k_new, const orthros_bf16 *v_new, const int32_t *parent,
+                                          const int32_t *node, orthros_bf16 *k_cache, orthros_bf16 *v_cache,
+                                          int32_t *cache_len, int L_max, int32_t *path, int B, int N, int Hkv, int d,
+                                          int32_t *dev_err, void *stream)
+{
+    return orthros_decode_tree_accept_nodes(k_new, v_new, parent, nullptr, node, k_cache, v_cache, cache_len, L_max, path, B,
+                                            N, Hkv, d, dev_err, stream);
 }
 
 }  // extern "C"

@@ -45,6 +45,7 @@ cudaError_t launch_tree_tc(int D, int tr, const TreeMaps &maps, const TreeParams
 struct TreeAcceptParams {
     const orthros_bf16 *k_new, *v_new;  // [B, N, Hkv, d]
     const int32_t *parent, *node;       // [B, N], [B]
+    const int32_t *nodes;               // [B] or NULL (N)
     orthros_bf16 *k_cache, *v_cache;    // [B, L_max, Hkv, d]
     int32_t *cache_len, *path;          // [B], [B, N]
     int32_t *dev_err;

@@ -485,11 +485,12 @@ __global__ void __cluster_dims__(ACCEPT_CTAS, 1, 1) __launch_bounds__(256) tree_
 {
     const int b = blockIdx.y, rank = blockIdx.x;
     const int node = __ldg(p.node + b), len = __ldcg(p.cache_len + b);
-    const bool inside = node >= 0 && node < p.N;
+    const int n = p.nodes != nullptr ? __ldg(p.nodes + b) : p.N;
+    const bool sized = n >= 0 && n <= p.N, inside = sized && node >= 0 && node < n;
     // every warp finds the path by itself
     const TreePaths t = tree_paths(p.parent + static_cast<long long>(b) * p.N, inside ? node + 1 : 0);
     unsigned long long path = inside ? t.of(node) : 0;
-    int err = node < -1 || node >= p.N || (inside && ((t.bad >> node) & 1)) ? ORTHROS_DEVERR_POSITION : 0;
+    int err = !sized || node < -1 || node >= n || (inside && ((t.bad >> node) & 1)) ? ORTHROS_DEVERR_POSITION : 0;
     if (err == 0 && (len < 0 || len > p.L_max || __popcll(path) > p.L_max - len))
         err = ORTHROS_DEVERR_CACHE_FULL;
     if (err != 0)
