@@ -113,7 +113,7 @@ __device__ __forceinline__ TreePaths tree_paths(const int32_t *parent, int n)
 // what a sequence's length and number of nodes make of it
 struct TreeSeq {
     int len, n;      // cached rows, live nodes
-    int full;        // a length or a number of nodes out of range: all its rows become zeros
+    int full;        // a length or a number of nodes out of range: its rows (all N, where the number is) become zeros
     int tiles;       // of query rows
     int nc, nb;      // blocks of a copy's segment, of a base segment: the tree's block is the last of each
     int sink;        // a base segment begins with the sinks' block (block 0 of the cache)
@@ -126,12 +126,12 @@ __device__ __forceinline__ TreeSeq tree_seq(const TreeParams &p, int b)
     TreeSeq s;
     s.len = __ldcg(p.cache_len + b);
     s.n = p.nodes != nullptr ? __ldcg(p.nodes + b) : p.N;
-    s.full = s.len < 0 || s.len > p.L_max || s.n < 0 || s.n > p.N;
-    if (s.full) {
-        s.n = p.N;
-        s.len = 0;
-    }
+    const bool sized = s.n >= 0 && s.n <= p.N;
+    s.n = sized ? s.n : p.N;
+    s.full = s.len < 0 || s.len > p.L_max || !sized;
+    s.len = s.full ? 0 : s.len;
     s.tiles = (s.n * (p.Hq / p.Hkv) + TR - 1) / TR;
+    s.tiles = s.full ? max(s.tiles, 1) : s.tiles;  // a tree without nodes has a tile all the same, which reports the length
     const int blocks = (s.len + TREE_KB - 1) / TREE_KB;
     const int lo = s.len - p.window + 1;  // first row of the window of a node at depth 0 (window >= 1: no overflow)
     s.wb0 = lo > 0 ? lo / TREE_KB : 0;

@@ -42,3 +42,21 @@ def test_accept_with_nodes(N, d):
     np.testing.assert_array_equal(bits(v), want[2])
     np.testing.assert_array_equal(lens.cpu().numpy(), want[3])
     assert int(err.item()) == 0
+
+
+@pytest.mark.parametrize("N,Hq,Hkv", [(2, 8, 2), (20, 8, 2), (64, 8, 1)])
+def test_a_bad_length_writes_no_row_behind_a_tree(N, Hq, Hkv):
+    """Zeros for the tree's nodes, the error bit for a tree without any too, and every row behind them as it was."""
+    c = Tree(5, N, 200, Hq, Hkv, 64, sinks=4, seed=37)
+    c.nodes = np.array([N - 1, N // 2, 0, N, 0], np.int32)
+    for lens in ([-1, 201, 200, 201, 200], [200, 200, 201, 200, -5]):
+        c.lens[:] = lens
+        o, oc = (torch.full((5, N, Hq, 64), 5.0, dtype=torch.bfloat16, device=dev()) for _ in range(2))
+        err = error_word()
+        got = [val(y) for y in c.run(o=o, oc=oc, dev_err=err)]
+        assert int(err.item()) == orth.DEVERR_CACHE_FULL
+        for y in got:
+            for b in range(5):
+                n = c.nodes[b]
+                assert (y[b, n:] == 5).all(), b
+                assert (y[b, :n] == 0).all() if not 0 <= lens[b] <= 200 else y[b, :n].any() or n == 0, b
