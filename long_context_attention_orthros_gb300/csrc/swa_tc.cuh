@@ -463,11 +463,15 @@ __global__ void __launch_bounds__(SINK ? 544 : 512, 1)
                     ok = false;
                     break;
                 }
-                if (SINK && second) {
-                    // rows of the block that are no sinks have no weight, but may hold anything (in a row range they need
-                    // not be in place): zeros in K, where they would be out of range, and in V
+                if (RANGE && (second || i == 0)) {
+                    // rows of the sinks' block that are no sinks, and rows of the first block before the first window, have
+                    // no weight, but may hold anything (in a row range they need not be in place): zeros in K, where they
+                    // would be out of range, and in V
+                    const int from = second ? 0 : n0 * TOK - p.window + 1 - 32 * tc_kb_lo(n0, TOK, p.window);
+                    const int to = second ? p.sinks : C::KB;
+#pragma unroll 1
                     for (int r = rsub; r < C::KB; r += 4 * NCW)
-                        if (r >= p.sinks)
+                        if (r < from || r >= to)
 #pragma unroll
                             for (int sl = 0; sl < C::SLABS; ++sl) {
                                 const int at = r * 128 + c8 * 16;

@@ -53,3 +53,36 @@ def test_ranges_of_streams_of_many_tiles(B, T, Hq, Hkv, d, window, sinks):
     s = Stream(B, T, Hq, Hkv, d, window, sinks, seed=T + Hkv)
     last = T // 128 * 128
     same_as_whole(s, [(0, 128), (128, 256), (128, 384), (256, 640), (640, 1024), (last, T), (last - 128, T), (384, T)])
+
+
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), -3e38])
+@pytest.mark.parametrize("B,T,Hq,Hkv,d,window,sinks,begin,end", [
+    (2, 900, 8, 2, 128, 128, 4, 384, 640),    # the band in tensor memory
+    (1, 700, 8, 4, 64, 100, 17, 256, 512),
+    (2, 500, 16, 1, 128, 33, 4, 256, 384),
+    (2, 900, 8, 2, 128, 128, 0, 384, 640),
+    (1, 700, 2, 2, 64, 128, 4, 384, 512),     # tiles of rows
+    (1, 5000, 4, 4, 64, 300, 4, 640, 768),
+    (1, 1300, 8, 2, 128, 400, 4, 640, 1024),
+    (2, 900, 8, 2, 128, 400, 0, 640, 900),    # on warp MMAs
+    (1, 700, 2, 2, 64, 120, 0, 384, 512),
+    (1, 700, 16, 1, 128, 250, 0, 256, 384),
+])
+def test_what_a_range_does_not_read(B, T, Hq, Hkv, d, window, sinks, begin, end, value):
+    """Keys before the range's first window that are no sinks, and keys, values and queries behind or before the range:
+    not in place yet, or not any more."""
+    s = Stream(B, T, Hq, Hkv, d, window, sinks, seed=T + window)
+    whole, whole_lse = s.run(lse=True)
+    q, k, v = bf(s.x), bf(s.k), bf(s.v)
+    q[:, :begin], q[:, end:] = value, value
+    for t in (k, v):
+        t[:, sinks:begin - window + 1], t[:, end:] = value, value
+    err = error_word()
+    o, lse = orth.swa_sink_fwd(q, k, v, f32(s.alpha), f32(s.beta), sinks, window=window, lse=True, row_begin=begin,
+                               row_end=end, dev_err=err)
+    np.testing.assert_array_equal(bits(o[:, begin:end]), bits(whole[:, begin:end]))
+    assert torch.equal(lse[:, begin:end], whole_lse[:, begin:end])
+    if sinks == 0:
+        o = orth.swa_fwd_rows(q, k, v, f32(s.alpha), f32(s.beta), begin, end, window=window, dev_err=err)
+        np.testing.assert_array_equal(bits(o[:, begin:end]), bits(whole[:, begin:end]))
+    assert int(err.item()) == 0
