@@ -135,9 +135,11 @@ orthros_status orthros_swa_fwd_lse(const orthros_bf16 *q_raw, const orthros_bf16
  * sequence stay visible to every row behind them, beside the window:
  *   row t attends over keys j <= t with j > t - window or j < sinks
  * 0 <= sinks <= 32 (0: as orthros_swa_fwd).  lse (optional, NULL: none) gets each row's log-sum-exp
- * over those keys, fp32 [B, T, Hq], for orthros_swa_sink_bwd; some 1e-5 of itself off (q is rounded to fp16
- * once), for rows of at most 64 keys, where that would not even out, some 1e-6.  Only output rows row_begin ..
- * row_end-1 are computed (0 and T for all; rules and reads as orthros_swa_fwd_rows, and key rows
+ * over those keys, fp32 [B, T, Hq], for orthros_swa_sink_bwd, where its error is a relative one of the row's
+ * weights.  q is rounded to fp16 once, which moves it by up to 2^-11 sum_i |scale q_i kbar_i|, kbar the keys' mean
+ * by the row's weights: some 1e-5 of itself (root mean square) at 128 keys of like weight, up to 1e-4 where one key
+ * has all of it.  Rows that see at most 64 keys take q as a bf16 high part plus residual: some 1e-6.  Only output
+ * rows row_begin .. row_end-1 are computed (0 and T for all; rules and reads as orthros_swa_fwd_rows, and key rows
  * 0 .. sinks-1 have to be in place).  Values of V are finite; one that is not reaches, beside the rows
  * that see it, only rows up to window + 256 away.  Other arguments, arithmetic and errors as
  * orthros_swa_fwd.
