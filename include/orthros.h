@@ -610,9 +610,9 @@ size_t orthros_decode_tree_workspace_size(int B, int N, int L_max, int Hq, int H
  *   rows behind them are left as they are, inputs behind them may hold anything
  *   k_cache, v_cache [B, L_max, Hkv, d] bf16; cache_len [B], each in [0, L_max]; rows at or beyond it
  *   may hold anything
- * A node below a parent that is not -1 or an earlier node, and every node of a sequence with nodes
- * out of range, gets zeros and sets ORTHROS_DEVERR_POSITION; a sequence with cache_len out of range
- * gets zeros and sets ORTHROS_DEVERR_CACHE_FULL.  A V row that is not finite reaches every node of its
+ * A node below a parent that is not -1 or an earlier node, and every one of the N of a sequence with nodes
+ * out of range, gets zeros and sets ORTHROS_DEVERR_POSITION; the nodes of a sequence with cache_len out of
+ * range get zeros, and it sets ORTHROS_DEVERR_CACHE_FULL.  A V row that is not finite reaches every node of its
  * tree's rows of a KV head that are computed together, whether they see it or not; rows that no node
  * sees do not count.  workspace: orthros_decode_tree_workspace_size(...) bytes, 256-byte aligned.
  */

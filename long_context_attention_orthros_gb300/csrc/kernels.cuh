@@ -145,6 +145,10 @@ cudaError_t launch_swa(int D, int G, const CUtensorMap &q, const CUtensorMap &k,
 bool swa_tc_supported(int D, int G, int window);
 cudaError_t launch_swa_tc(int D, int G, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
                           const CUtensorMap &o, const SwaParams &p, int num_sms, cudaStream_t stream);
+// the same with p.sinks > 0
+bool swa_sink_tc_supported(int D, int G, int window);
+cudaError_t launch_swa_sink_tc(int D, int G, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
+                               const SwaParams &p, int num_sms, cudaStream_t stream);
 
 // base stream with sinks, any window and grouping, over blocks of 64 keys (swa_wide.cu)
 struct SwaWideParams {
@@ -163,8 +167,6 @@ struct SwaWideMaps {
     CUtensorMap k, v;  // boxes of 64 x 1 x 64
 };
 cudaError_t launch_swa_wide(int D, const SwaWideMaps &maps, const SwaWideParams &p, cudaStream_t stream);
-// the same with p.sinks > 0
-bool swa_sink_tc_supported(int D, int G, int window);
 
 // the log-sum-exp of rows with few keys (sink_lse.cu); strides between sequences, in values
 struct SinkLseParams {
@@ -176,8 +178,6 @@ struct SinkLseParams {
     float qscale;  // scale log2(e)
 };
 cudaError_t launch_sink_lse(int D, SinkLseParams p, cudaStream_t stream);
-cudaError_t launch_swa_sink_tc(int D, int G, const CUtensorMap &q, const CUtensorMap &k, const CUtensorMap &v,
-                               const SwaParams &p, int num_sms, cudaStream_t stream);
 
 size_t xattn_workspace_bytes(int B, int T_out, int T_kv, int Hq, int Hkv, int D);
 // ctas > 0: at most 8 copy rows per (batch, KV head) run on exactly `ctas` CTAs of one SM each

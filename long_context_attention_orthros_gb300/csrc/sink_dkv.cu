@@ -12,9 +12,9 @@
 // 1.9e-5 off.  So every 24 rounds (1536 rows, 288 steps) dV and dK are added to memory and begin anew.
 // Four warpgroups take 16 rows (columns) of the round each: a warp's chain of loads, exponentials and stores is what a
 // round waits for beside the MMAs.  4 x 16384 tokens of 32/8 heads, window 128: some 1000 us; 1 x 16384 280.
-// Bound by the MMAs: 44 a round of 16 x (64 or 128) x 128, some 2050 cycles of the pipe at d = 128 and some 95 each as
-// they come, 4200 a round.  Without the residuals' products, or without the exponentials, a round would take 1.6 us
-// instead of 2.2.
+// Bound by a round's chain, MMAs and exponentials by turns: the 44 MMAs of 16 x (64 or 128) x 128 occupy the pipe for
+// some 2050 of its 4200 cycles at d = 128, and without the residuals' products, or without the exponentials, a round
+// would take 1.6 us instead of 2.2 either way.
 // Roles (640 threads, one CTA an SM): warp 0 TMA producer; warp 1 tensor memory and the issue of S^T, dP^T; warp 3 that of
 // dV, dK (one thread for both spends some 90 cycles an MMA, as long as a round takes); warp 2 the rows' log-sum-exp
 // and D; warps 4-19 P^T, dS^T (lane = key), 16 columns a warpgroup, and at the end dK, dV.

@@ -2,12 +2,13 @@
 // q_t . k_j), computed to its fp32.
 //
 // The forward kernels' logits take q as one fp16 (2^-12 off), which the sum over many keys evens out: at 128 keys the
-// log-sum-exp is some 1e-5 of itself off, but 1.4e-4 where a row sees one or two.  Here q enters as a bf16 high part plus
-// residual, on warp MMAs: a CTA has 32 tokens of a KV head, their keys in shared memory (at most 32 sinks and
-// 64 + 31 window rows), a warp 16 query rows on M at a time and 8 keys on N, with the head dimension in the order in
-// which it lies in memory (16 bytes a lane).  Rows with few keys are all rows, or the first 64 of each sequence,
-// where this is one short launch behind the forward's (4 x 16384 tokens of 32/8 heads, d = 128: 10 us).  For all rows of
-// the same at window 33 it takes 410 us: a warp's chain of fragments, which the queries' two parts mostly are.
+// log-sum-exp is some 1e-5 of itself off, but 1.4e-4 where a row sees one or two (and 1e-4 where one of many has all the
+// weight, which is left so).  Here q enters as a bf16 high part plus residual, on warp MMAs: a CTA has 32 tokens of a KV
+// head, their keys in shared memory (at most 32 sinks and 64 + 31 window rows), a warp 16 query rows on M at a time and 8
+// keys on N, with the head dimension in the order in which it lies in memory (16 bytes a lane).  Rows with few keys are
+// all rows, or the first 64 of each sequence, where this is one short launch behind the forward's (4 x 16384 tokens of
+// 32/8 heads, d = 128: 10 us).  For all rows of the same at window 33 it takes 410 us: a warp's chain of fragments, which
+// the queries' two parts mostly are.
 #include "bwd_util.cuh"
 #include "kernels.cuh"
 #include "xattn.cuh"

@@ -42,9 +42,12 @@
 // left it behind; its logits follow the band's in tensor memory (8 more MMAs of N = 32, and
 // 2 more of P V), its keys count for row t where j < sinks and j <= t - window, so that a key
 // never counts twice.  One ring slot and the spare columns of tensor memory pay for it.
-// The 28 MMAs of such a tile are more than one thread issues in the time that the tile's bytes
-// take (some 75 cycles each: 2 x 131072 tokens of 32/8 heads, d = 128 took 1115 us): warp 16
-// issues those of O = P V beside warp 1's of S.
+// Warp 16 issues the MMAs of O = P V beside warp 1's of S (2 x 131072 tokens of 32/8 heads,
+// d = 128: 1093 us, from one warp 1115).  What bounds it is a tile's chain S -> maximum -> P ->
+// P V -> result, some 5250 cycles a tile, where its bytes take 3850 and the issue of its 28 MMAs
+// 2100: 1 x 65536 tokens take 284 us; without the softmax of the sinks' columns 275, without their
+// MMAs 279, without both 270, without the maximum's pass 258; the instance without sinks 242
+// (d = 64: 230; 209, 228, 207, 184; 203).
 #pragma once
 
 #include <cuda_fp16.h>
