@@ -842,7 +842,8 @@ def decode_tree_accept(k_new, v_new, parent, node, k_cache, v_cache, cache_len, 
         path = torch.empty((B, N), dtype=i32, device=k_cache.device)
     _invoke("orthros_decode_tree_accept_nodes", dev, _dense(k_new, "k_new", bf16, new, dev),
             _dense(v_new, "v_new", bf16, new, dev), _dense(parent, "parent", i32, (B, N), dev),
-            _optional(nodes, "nodes", i32, (B,), dev), _dense(node, "node", i32, (B,), dev), _dense(k_cache, "k_cache", bf16, shape, dev),
+            _optional(nodes, "nodes", i32, (B,), dev), _dense(node, "node", i32, (B,), dev),
+            _dense(k_cache, "k_cache", bf16, shape, dev),
             _dense(v_cache, "v_cache", bf16, shape, dev), _dense(cache_len, "cache_len", i32, (B,), dev), L_max,
             _dense(path, "path", i32, (B, N), dev), B, N, Hkv, d, _word(dev_err, dev))
     return path

@@ -477,9 +477,10 @@ __global__ void __launch_bounds__(SINK ? 544 : 512, 1)
                         if (r < from || r >= to)
 #pragma unroll
                             for (int sl = 0; sl < C::SLABS; ++sl) {
-                                const int at = r * 128 + c8 * 16;
-                                *reinterpret_cast<uint4 *>(smem + C::K_OFF + sl * C::K_SLAB + ks * C::SLOT + at) = make_uint4(0, 0, 0, 0);
-                                *reinterpret_cast<uint4 *>(smem + C::V_OFF + sl * C::V_SLAB + s * C::SLOT + at) = make_uint4(0, 0, 0, 0);
+                                uint8_t *k_row = smem + C::K_OFF + sl * C::K_SLAB + ks * C::SLOT + r * 128;
+                                uint8_t *v_row = smem + C::V_OFF + sl * C::V_SLAB + s * C::SLOT + r * 128;
+                                *reinterpret_cast<uint4 *>(k_row + c8 * 16) = make_uint4(0, 0, 0, 0);
+                                *reinterpret_cast<uint4 *>(v_row + c8 * 16) = make_uint4(0, 0, 0, 0);
                             }
                 }
                 // common case: every chunk below 65520 converts as is; when a chunk of the warp's

@@ -81,7 +81,9 @@ struct WideJob {
     static __device__ __forceinline__ const orthros_bf16 *query(const Params &p, const Piece &c, int r)
     {
         const int G = p.Hq / p.Hkv, t = c.t0 + r / G;
-        return t >= p.row_begin && t < c.t1 ? p.q + c.b * p.q_bstride + (static_cast<long long>(t) * p.Hq + c.g * G + r % G) * D : nullptr;
+        if (t < p.row_begin || t >= c.t1)
+            return nullptr;
+        return p.q + c.b * p.q_bstride + (static_cast<long long>(t) * p.Hq + c.g * G + r % G) * D;
     }
     static __device__ __forceinline__ void vectors(const Params &p, const Piece &, const float *&alpha, const float *&beta)
     {
@@ -120,7 +122,8 @@ cudaError_t launch_t(const SwaWideMaps &maps, SwaWideParams p, cudaStream_t stre
     p.per_stream = (p.row_end + tok - 1) / tok - p.row_begin / tok;
     p.pieces = static_cast<long long>(p.B) * p.Hkv * p.per_stream;
     const int ctas = static_cast<int>(p.pieces < 152 ? p.pieces : 152);
-    return two ? launch_rows_tc<D, true, WideJob>(maps, p, ctas, stream) : launch_rows_tc<D, false, WideJob>(maps, p, ctas, stream);
+    return two ? launch_rows_tc<D, true, WideJob>(maps, p, ctas, stream)
+               : launch_rows_tc<D, false, WideJob>(maps, p, ctas, stream);
 }
 
 }  // namespace
